@@ -18,6 +18,9 @@ missing they raise instead of computing anything elsewhere.
   gdn_cp_windows(...)         per-boundary CP decision (warmup window, or 0 for exact)
   gdn_recurrent_fwd(...)      token-by-token form from a given state (decoding after a prefill)
   chunk_gated_delta_rule(...) autograd wrapper over gdn_chunk_fwd / gdn_chunk_bwd
+
+The operators around the rule in a layer (layer.py): gated scan, short convolution, RMS norm with
+residual addition and 8-bit output, each with its gradient and an autograd wrapper.
 """
 from __future__ import annotations
 
@@ -30,10 +33,15 @@ import torch
 from ._abi import (CP_MODES, EXPORTS, GDN_DTYPE_BF16, GDN_DTYPE_FP32, GDN_FLAG_BWD_ADJOINT_PASS,  # noqa: F401
                    GDN_FLAG_FWD_FUSED, GDN_FLAG_FWD_SPLIT, GDN_FLAG_KEEP_FORWARD, GDN_FLAG_QK_L2NORM, GDN_NOALLOC_SCRATCH_BYTES, GDN_FLAG_REUSE_FORWARD, GDN_FLAG_REUSE_CP, GdnDesc, GdnError, GdnKernelTime, GdnPlanInfo, check,
                    load_library, status_string)
+from .layer import (gated_scan, gdn_gated_scan_bwd, gdn_gated_scan_fwd, gdn_gated_scan_states,  # noqa: F401
+                    gdn_rmsnorm_bwd, gdn_rmsnorm_fwd, gdn_short_conv_bwd, gdn_short_conv_fwd, rms_norm, short_conv)
 
 __all__ = ["gdn_plan", "gdn_chunk_fwd", "gdn_chunk_fwd_noalloc", "gdn_chunk_bwd", "gdn_workspace", "gdn_cp_states", "gdn_intra_chunk", "gdn_cp_modes",
            "gdn_cp_windows", "gdn_recurrent_fwd", "gdn_profile_enable", "gdn_profile_read", "chunk_gated_delta_rule", "load_library",
-           "make_desc", "GdnError"]
+           "make_desc", "GdnError",
+           "gdn_gated_scan_fwd", "gdn_gated_scan_bwd", "gdn_gated_scan_states", "gated_scan",
+           "gdn_short_conv_fwd", "gdn_short_conv_bwd", "short_conv",
+           "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd", "rms_norm"]
 
 
 def _ptr(t: Optional[torch.Tensor]):

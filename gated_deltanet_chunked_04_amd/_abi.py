@@ -23,7 +23,13 @@ GDN_NOALLOC_SCRATCH_BYTES = 128 << 20
 # Declared entry points of include/gdn.h (checked by the ABI test).
 EXPORTS = ("gdn_abi_version", "gdn_status_string", "gdn_plan", "gdn_chunk_fwd_workspace_size",
            "gdn_chunk_fwd", "gdn_chunk_fwd_noalloc", "gdn_chunk_bwd_workspace_size", "gdn_chunk_bwd", "gdn_intra_chunk",
-           "gdn_cp_modes", "gdn_cp_windows", "gdn_recurrent_fwd", "gdn_profile_enable", "gdn_profile_read")
+           "gdn_cp_modes", "gdn_cp_windows", "gdn_recurrent_fwd", "gdn_profile_enable", "gdn_profile_read",
+           "gdn_gated_scan_fwd_workspace_size", "gdn_gated_scan_bwd_workspace_size", "gdn_gated_scan_states_size",
+           "gdn_gated_scan_fwd", "gdn_gated_scan_bwd", "gdn_short_conv_bwd_workspace_size", "gdn_short_conv_fwd",
+           "gdn_short_conv_bwd", "gdn_rmsnorm_bwd_workspace_size", "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd")
+GDN_ACT_NONE, GDN_ACT_SILU = 0, 1
+GDN_OUT_SAME, GDN_OUT_E4M3 = 0, 1
+GDN_CONV_INPLACE_T = 16
 
 
 class GdnDesc(ctypes.Structure):
@@ -53,6 +59,25 @@ class GdnPlanInfo(ctypes.Structure):
         ("fused_fwd", ctypes.c_int32), ("bwd_carried", ctypes.c_int32),
         ("reserved_out", ctypes.c_int32 * 2),
     ]
+
+
+class GdnScanDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("flags", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p), ("reserved", ctypes.c_int32 * 4)]
+
+
+class GdnConvDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("width", ctypes.c_int32), ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("num_seqs", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("cu_seqlens", ctypes.c_void_p), ("reserved", ctypes.c_int32 * 4)]
+
+
+class GdnRmsnormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("w_dtype", ctypes.c_int32), ("out_type", ctypes.c_int32), ("scale_group", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("flags", ctypes.c_int32), ("reserved", ctypes.c_int32 * 4)]
 
 
 class GdnKernelTime(ctypes.Structure):
@@ -102,6 +127,20 @@ def load_library(path: str = LIB_PATH):
     lib.gdn_cp_windows.argtypes = [dp] + [vp] * 6 + [vp, sz, vp]
     lib.gdn_recurrent_fwd.restype = i32
     lib.gdn_recurrent_fwd.argtypes = [dp] + [vp] * 8 + [vp]
+    sp, cp, rp = ctypes.POINTER(GdnScanDesc), ctypes.POINTER(GdnConvDesc), ctypes.POINTER(GdnRmsnormDesc)
+    for name, args in (("gdn_gated_scan_fwd_workspace_size", [sp, ctypes.POINTER(sz)]),
+                       ("gdn_gated_scan_bwd_workspace_size", [sp, ctypes.POINTER(sz)]),
+                       ("gdn_gated_scan_states_size", [sp, ctypes.POINTER(sz)]),
+                       ("gdn_gated_scan_fwd", [sp] + [vp] * 7 + [sz, vp]),
+                       ("gdn_gated_scan_bwd", [sp] + [vp] * 10 + [sz, vp]),
+                       ("gdn_short_conv_bwd_workspace_size", [cp, ctypes.POINTER(sz)]),
+                       ("gdn_short_conv_fwd", [cp] + [vp] * 7),
+                       ("gdn_short_conv_bwd", [cp] + [vp] * 11 + [sz, vp]),
+                       ("gdn_rmsnorm_bwd_workspace_size", [rp, ctypes.POINTER(sz)]),
+                       ("gdn_rmsnorm_fwd", [rp] + [vp] * 7),
+                       ("gdn_rmsnorm_bwd", [rp] + [vp] * 7 + [sz, vp])):
+        getattr(lib, name).restype = i32
+        getattr(lib, name).argtypes = args
     lib.gdn_profile_enable.restype = i32
     lib.gdn_profile_enable.argtypes = [i32]
     lib.gdn_profile_read.restype = i32

@@ -298,11 +298,11 @@ Geo make_geo(const gdn_desc* d, const Plan& p, unsigned char* ws) {
 
 // ---------------------------------------------------------------------------
 // Kernel timing (gdn_profile_enable / gdn_profile_read).
-enum KernelId { kKTables = 0, kKIntra, kKDecide, kKPrepass, kKScan, kKRecurOut, kKRecurStates,
-                kKBwdPrepass, kKBwdScan, kKBwdReverse, kKBwdChunk, kKDecode, kKL2NormBwd, kKFused, kKCount };
 const char* const kKernelNames[kKCount] = {"tables", "intra", "cp_decide", "cp_prepass", "cp_scan",
                                            "recur_out", "recur_states", "bwd_cp_prepass", "bwd_cp_scan",
-                                           "bwd_reverse", "bwd_chunk", "recurrent", "qk_l2norm_bwd", "fused_fwd"};
+                                           "bwd_reverse", "bwd_chunk", "recurrent", "qk_l2norm_bwd", "fused_fwd",
+                                           "gated_scan_fwd", "gated_scan_bwd", "short_conv_fwd", "short_conv_bwd",
+                                           "rmsnorm_fwd", "rmsnorm_bwd"};
 struct Pending {
     int kid;
     hipEvent_t start, stop;
@@ -330,27 +330,25 @@ Profiler& profiler() {
     return p;
 }
 
-// Brackets one launch with events when profiling is on.
-struct ProfScope {
-    int kid;
-    hipStream_t st;
-    hipEvent_t a = nullptr, b = nullptr;
-    ProfScope(int k, hipStream_t s) : kid(k), st(s) {
-        Profiler& p = profiler();
-        std::lock_guard<std::mutex> g(p.mu);
-        if (!p.on) return;
-        a = p.get();
-        b = p.get();
-        if (a && b) (void)hipEventRecord(a, st);
-    }
-    ~ProfScope() {
-        if (!a || !b) return;
-        (void)hipEventRecord(b, st);
-        Profiler& p = profiler();
-        std::lock_guard<std::mutex> g(p.mu);
-        p.pending.push_back(Pending{kid, a, b});
-    }
-};
+}  // namespace
+
+ProfScope::ProfScope(int k, hipStream_t s) : kid(k), st(s) {
+    Profiler& p = profiler();
+    std::lock_guard<std::mutex> g(p.mu);
+    if (!p.on) return;
+    a = p.get();
+    b = p.get();
+    if (a && b) (void)hipEventRecord(a, st);
+}
+ProfScope::~ProfScope() {
+    if (!a || !b) return;
+    (void)hipEventRecord(b, st);
+    Profiler& p = profiler();
+    std::lock_guard<std::mutex> g(p.mu);
+    p.pending.push_back(Pending{kid, a, b});
+}
+
+namespace {
 
 #define GDN_LAUNCH(kid, st, call)         \
     do {                                  \

@@ -385,4 +385,19 @@ struct DecodeArgs {
 };
 hipError_t launch_decode(const DecodeArgs& a, int dtype, int K, int V, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// Kernel timing (gdn_profile_enable / gdn_profile_read, in gdn_api.hip): what a launch, or the few
+// launches of one operator, count under.
+enum KernelId { kKTables = 0, kKIntra, kKDecide, kKPrepass, kKScan, kKRecurOut, kKRecurStates,
+                kKBwdPrepass, kKBwdScan, kKBwdReverse, kKBwdChunk, kKDecode, kKL2NormBwd, kKFused,
+                kKGScanFwd, kKGScanBwd, kKConvFwd, kKConvBwd, kKRmsFwd, kKRmsBwd, kKCount };
+// Brackets the launches in its scope with two events on `st` while profiling is on.
+struct ProfScope {
+    int kid;
+    hipStream_t st;
+    hipEvent_t a = nullptr, b = nullptr;
+    ProfScope(int k, hipStream_t s);
+    ~ProfScope();
+};
+
 }  // namespace gdn

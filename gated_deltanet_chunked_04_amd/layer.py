@@ -1,0 +1,444 @@
+"""The operators around the gated delta rule in a layer: gated scan, short convolution and RMS norm.
+
+Like the rest of the package these functions carry the C ABI's names (include/gdn.h) and only marshal
+tensors into it; every step of the computation runs in the HIP library. Tensors are contiguous, on one
+device; work runs on that device's current stream.
+
+  gdn_gated_scan_fwd / _bwd     h_t = exp(g_t) h_{t-1} + x_t per channel, and its gradients
+  gdn_gated_scan_states(x)      the buffer that carries the forward's states to the backward
+  gdn_short_conv_fwd / _bwd     causal convolution of 2 to 4 taps per channel, silu or none behind it
+  gdn_rmsnorm_fwd / _bwd        RMS norm, residual addition in front, 8-bit output with scales behind
+  gated_scan, short_conv, rms_norm   the same with autograd
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from ._abi import (GDN_ACT_NONE, GDN_ACT_SILU, GDN_DTYPE_BF16, GDN_DTYPE_FP32, GDN_OUT_E4M3, GDN_OUT_SAME,
+                   GdnConvDesc, GdnRmsnormDesc, GdnScanDesc, check, load_library)
+
+_DTYPES = {torch.bfloat16: GDN_DTYPE_BF16, torch.float32: GDN_DTYPE_FP32}
+_ACTIVATIONS = {None: GDN_ACT_NONE, "silu": GDN_ACT_SILU}
+_QUANT = {"row": 0, "group": 128}
+SCAN_TILE = 64  # tokens between two kept states of the gated scan
+
+
+def _dtype(t) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported input dtype {t.dtype} (bf16 or fp32)")
+    return code
+
+
+def _lead(name, x, dims):
+    if not isinstance(x, torch.Tensor) or x.dim() != dims or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous device tensor of {dims} dimensions")
+
+
+def _like(name, t, shape, dtype, device):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {tuple(shape)} {dtype} tensor on {device}")
+    return t.data_ptr()
+
+
+def _second_type(name, t, x) -> int:
+    if not isinstance(t, torch.Tensor) or (t.dtype != x.dtype and t.dtype != torch.float32):
+        raise ValueError(f"{name}: expected {x.dtype} or fp32")
+    return _DTYPES[t.dtype]
+
+
+def _sequences(desc, x, cu_seqlens) -> int:
+    """Fills B, T, D and the packing; returns N."""
+    desc.B, desc.T, desc.D = x.shape
+    if cu_seqlens is None:
+        return x.shape[0]
+    if (not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype != torch.int32 or cu_seqlens.device != x.device
+            or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or cu_seqlens.numel() < 2):
+        raise TypeError(f"cu_seqlens must be a contiguous int32 tensor [N+1], N >= 1, on {x.device}")
+    if x.shape[0] != 1:
+        raise ValueError("cu_seqlens needs B = 1")
+    desc.num_seqs = cu_seqlens.numel() - 1
+    desc.cu_seqlens = cu_seqlens.data_ptr()
+    return desc.num_seqs
+
+
+@contextlib.contextmanager
+def _other_device(device):
+    with torch.cuda.device(device):
+        yield
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device):
+    """Makes `device` current for the launches of a call, if it is not."""
+    return _HERE if torch.cuda.current_device() == device.index else _other_device(device)
+
+
+def _stream_of(device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _scratch(nbytes, device, workspace):
+    """(pointer, bytes, the tensor to keep alive) of a caller's workspace or of a new one."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif (not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous()
+          or workspace.data_ptr() % 256):
+        raise ValueError(f"workspace must be a contiguous tensor on {device} at a 256-byte aligned address")
+    size = workspace.numel() * workspace.element_size()
+    if size < nbytes:
+        raise ValueError(f"workspace too small: {size} bytes, {nbytes} needed")
+    return workspace.data_ptr(), size, workspace
+
+
+def _bytes(fn, desc, where) -> int:
+    n = ctypes.c_size_t()
+    check(fn(ctypes.byref(desc), ctypes.byref(n)), where)
+    return n.value
+
+
+# ---- gated scan ---------------------------------------------------------------------------------
+
+
+def _scan_desc(x, g, cu_seqlens):
+    _lead("x", x, 3)
+    desc = GdnScanDesc()
+    desc.dtype = _dtype(x)
+    desc.g_dtype = _second_type("g", g, x)
+    return desc, _sequences(desc, x, cu_seqlens)
+
+
+def gdn_gated_scan_states(x):
+    """The buffer (fp32 device tensor) in which gdn_gated_scan_fwd(states=...) leaves the state that
+    enters every 64th token, for gdn_gated_scan_bwd(states=...) on the same inputs."""
+    _lead("x", x, 3)
+    B, T, D = x.shape
+    return torch.empty((-(-B * T // SCAN_TILE), D), dtype=torch.float32, device=x.device)
+
+
+def _check_states(states, x):
+    if states is None:
+        return None
+    B, T, D = x.shape
+    p = _like("states", states, (-(-B * T // SCAN_TILE), D), torch.float32, x.device)
+    if p % 256:
+        raise ValueError("states must start at a 256-byte aligned address")
+    return p or None
+
+
+def gdn_gated_scan_fwd(x, g, initial_state=None, *, cu_seqlens=None, output_final_state=True, h=None,
+                       final_state=None, states=None, workspace=None):
+    """h_t = exp(g_t) h_{t-1} + x_t per sequence and channel. Returns (h, final_state or None).
+
+    x [B,T,D] bf16 or fp32; g [B,T,D] natural-log decay, in x's type or fp32; initial_state [N,D] fp32
+    or None (zeros); cu_seqlens int32 device tensor [N+1] (B = 1), no host copy needed. final_state may be
+    initial_state itself (updated in place). states (see gdn_gated_scan_states) receives what
+    gdn_gated_scan_bwd needs of the forward."""
+    desc, N = _scan_desc(x, g, cu_seqlens)
+    shape, dev = x.shape, x.device
+    pg = _like("g", g, shape, g.dtype, dev)
+    p0 = _like("initial_state", initial_state, (N, shape[2]), torch.float32, dev)
+    if h is None:
+        h = torch.empty_like(x)
+    ph = _like("h", h, shape, x.dtype, dev)
+    if not output_final_state:
+        final_state = None
+    elif final_state is None:
+        final_state = torch.empty((N, shape[2]), dtype=torch.float32, device=dev)
+    pT = _like("final_state", final_state, (N, shape[2]), torch.float32, dev)
+    ps = _check_states(states, x)
+    lib = load_library()
+    with _on(dev):
+        need = _bytes(lib.gdn_gated_scan_fwd_workspace_size, desc, "gdn_gated_scan_fwd_workspace_size")
+        pw, wb, ws = _scratch(need, dev, workspace)
+        check(lib.gdn_gated_scan_fwd(ctypes.byref(desc), x.data_ptr(), pg, p0, ph, pT, ps, pw, wb, _stream_of(dev)),
+              "gdn_gated_scan_fwd")
+    return h, final_state
+
+
+def gdn_gated_scan_bwd(x, g, d_h, initial_state=None, d_final_state=None, *, cu_seqlens=None, states=None,
+                       need_d_initial_state=True, workspace=None, out=None):
+    """Gradients of <d_h, h> + <d_final_state, final_state>: dict(dx, dg, d_initial_state); `out` may hold
+    them preallocated. states: what gdn_gated_scan_fwd(states=...) wrote for these inputs, or None (the
+    states are recomputed)."""
+    desc, N = _scan_desc(x, g, cu_seqlens)
+    shape, dev = x.shape, x.device
+    if d_h is None:
+        raise ValueError("d_h is required")
+    pg = _like("g", g, shape, g.dtype, dev)
+    p0 = _like("initial_state", initial_state, (N, shape[2]), torch.float32, dev)
+    pd = _like("d_h", d_h, shape, x.dtype, dev)
+    pT = _like("d_final_state", d_final_state, (N, shape[2]), torch.float32, dev)
+    if out is None:
+        out = dict(dx=torch.empty_like(x), dg=torch.empty_like(g),
+                   d_initial_state=(torch.empty((N, shape[2]), dtype=torch.float32, device=dev)
+                                    if need_d_initial_state else None))
+    for name in ("dx", "dg"):
+        if out.get(name) is None:
+            raise ValueError(f"out[{name!r}] is required")
+    px = _like("out['dx']", out["dx"], shape, x.dtype, dev)
+    pdg = _like("out['dg']", out["dg"], shape, g.dtype, dev)
+    pd0 = _like("out['d_initial_state']", out.get("d_initial_state"), (N, shape[2]), torch.float32, dev)
+    ps = _check_states(states, x)
+    lib = load_library()
+    with _on(dev):
+        need = _bytes(lib.gdn_gated_scan_bwd_workspace_size, desc, "gdn_gated_scan_bwd_workspace_size")
+        pw, wb, ws = _scratch(need, dev, workspace)
+        check(lib.gdn_gated_scan_bwd(ctypes.byref(desc), x.data_ptr(), pg, p0, pd, pT, ps, px, pdg, pd0, pw, wb,
+                                     _stream_of(dev)), "gdn_gated_scan_bwd")
+    return out
+
+
+# ---- short convolution --------------------------------------------------------------------------
+
+
+def _conv_desc(x, weight, bias, activation, cu_seqlens):
+    _lead("x", x, 3)
+    desc = GdnConvDesc()
+    desc.dtype = _dtype(x)
+    desc.w_dtype = _second_type("weight", weight, x)
+    if activation not in _ACTIVATIONS:
+        raise ValueError("activation: expected 'silu' or None")
+    desc.activation = _ACTIVATIONS[activation]
+    D = x.shape[2]
+    if weight.dim() != 2:
+        raise ValueError("weight: expected [D, W]")
+    desc.width = W = weight.shape[1]
+    pw = _like("weight", weight, (D, W), weight.dtype, x.device)
+    pb = _like("bias", bias, (D,), weight.dtype, x.device)
+    return desc, _sequences(desc, x, cu_seqlens), W, pw, pb
+
+
+def gdn_short_conv_fwd(x, weight, bias=None, initial_state=None, *, activation="silu", cu_seqlens=None,
+                       output_final_state=False, y=None, final_state=None):
+    """y_t = act(bias + sum_j weight[:, j] x_{t-W+1+j}). Returns (y, final_state or None).
+
+    x [B,T,D] bf16 or fp32; weight [D,W], W in {2, 3, 4}, and bias [D] in x's type or fp32; activation
+    'silu' or None; initial_state [N,W-1,D] in x's type: the inputs before each sequence's first token,
+    oldest first (zeros if None). The final state is a sequence's last W-1 inputs; a final_state tensor
+    asks for it, and may be initial_state itself for up to 16 tokens per row (decoding)."""
+    desc, N, W, pw, pb = _conv_desc(x, weight, bias, activation, cu_seqlens)
+    shape, dev = x.shape, x.device
+    sshape = (N, W - 1, shape[2])
+    p0 = _like("initial_state", initial_state, sshape, x.dtype, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    py = _like("y", y, shape, x.dtype, dev)
+    if final_state is None and output_final_state:
+        final_state = torch.empty(sshape, dtype=x.dtype, device=dev)
+    pT = _like("final_state", final_state, sshape, x.dtype, dev)
+    lib = load_library()
+    with _on(dev):
+        check(lib.gdn_short_conv_fwd(ctypes.byref(desc), x.data_ptr(), pw, pb, p0, py, pT, _stream_of(dev)),
+              "gdn_short_conv_fwd")
+    return y, final_state
+
+
+def gdn_short_conv_bwd(x, weight, d_y, bias=None, initial_state=None, d_final_state=None, *, activation="silu",
+                       cu_seqlens=None, need_d_initial_state=True, workspace=None, out=None):
+    """Gradients of <d_y, y> + <d_final_state, final_state>: dict(dx, dweight, dbias, d_initial_state), dweight
+    and dbias in fp32, dbias None without a bias; `out` may hold them preallocated."""
+    desc, N, W, pw, pb = _conv_desc(x, weight, bias, activation, cu_seqlens)
+    shape, dev = x.shape, x.device
+    D = shape[2]
+    sshape = (N, W - 1, D)
+    if d_y is None:
+        raise ValueError("d_y is required")
+    p0 = _like("initial_state", initial_state, sshape, x.dtype, dev)
+    pd = _like("d_y", d_y, shape, x.dtype, dev)
+    pT = _like("d_final_state", d_final_state, sshape, x.dtype, dev)
+    if out is None:
+        out = dict(dx=torch.empty_like(x), dweight=torch.empty((D, W), dtype=torch.float32, device=dev),
+                   dbias=None if bias is None else torch.empty((D,), dtype=torch.float32, device=dev),
+                   d_initial_state=torch.empty(sshape, dtype=x.dtype, device=dev) if need_d_initial_state else None)
+    for name in ("dx", "dweight"):
+        if out.get(name) is None:
+            raise ValueError(f"out[{name!r}] is required")
+    px = _like("out['dx']", out["dx"], shape, x.dtype, dev)
+    pdw = _like("out['dweight']", out["dweight"], (D, W), torch.float32, dev)
+    pdb = _like("out['dbias']", out.get("dbias"), (D,), torch.float32, dev)
+    pd0 = _like("out['d_initial_state']", out.get("d_initial_state"), sshape, x.dtype, dev)
+    lib = load_library()
+    with _on(dev):
+        need = _bytes(lib.gdn_short_conv_bwd_workspace_size, desc, "gdn_short_conv_bwd_workspace_size")
+        ws_p, wb, ws = _scratch(need, dev, workspace)
+        check(lib.gdn_short_conv_bwd(ctypes.byref(desc), x.data_ptr(), pw, pb, p0, pd, pT, px, pdw, pdb, pd0, ws_p, wb,
+                                     _stream_of(dev)), "gdn_short_conv_bwd")
+    return out
+
+
+# ---- RMS norm -----------------------------------------------------------------------------------
+
+
+def _rms_desc(name, x, weight, eps):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous device tensor [..., D]")
+    desc = GdnRmsnormDesc()
+    desc.dtype = _dtype(x)
+    desc.w_dtype = _second_type("weight", weight, x)
+    desc.D = D = x.shape[-1]
+    desc.rows = x.numel() // D if D else 0
+    desc.eps = eps
+    return desc, _like("weight", weight, (D,), weight.dtype, x.device)
+
+
+def gdn_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, quant=None, y=None, residual_out=None, scale=None):
+    """r = x + residual, y = r weight / sqrt(mean(r^2) + eps) over the last dimension. Returns
+    (y, residual_out or None, scale or None).
+
+    x [..., D] bf16 or fp32; weight [D] in x's type or fp32; residual like x or None. residual_out receives r
+    in x's type (it may be residual or x itself). quant None gives y in x's type; 'row' and 'group' give
+    it as torch.float8_e4m3fn with fp32 scales of every row ([..., 1]) or of every 128 columns
+    ([..., ceil(D/128)]): y stands for y.float() * scale."""
+    desc, pw = _rms_desc("x", x, weight, eps)
+    shape, dev, D = x.shape, x.device, x.shape[-1]
+    pr = _like("residual", residual, shape, x.dtype, dev)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without a residual")
+    elif residual_out is None:
+        residual_out = torch.empty_like(x)
+    po = _like("residual_out", residual_out, shape, x.dtype, dev)
+    if quant is None:
+        if scale is not None:
+            raise ValueError("scale without quant")
+        ydt, psc = x.dtype, None
+    else:
+        if quant not in _QUANT:
+            raise ValueError("quant: expected None, 'row' or 'group'")
+        desc.out_type, desc.scale_group, ydt = GDN_OUT_E4M3, _QUANT[quant], torch.float8_e4m3fn
+        sshape = (*shape[:-1], 1 if quant == "row" else -(-D // 128))
+        if scale is None:
+            scale = torch.empty(sshape, dtype=torch.float32, device=dev)
+        psc = _like("scale", scale, sshape, torch.float32, dev)
+    if y is None:
+        y = torch.empty(shape, dtype=ydt, device=dev)
+    py = _like("y", y, shape, ydt, dev)
+    lib = load_library()
+    with _on(dev):
+        check(lib.gdn_rmsnorm_fwd(ctypes.byref(desc), x.data_ptr(), pr, pw, py, psc, po, _stream_of(dev)),
+              "gdn_rmsnorm_fwd")
+    return y, residual_out, scale
+
+
+def gdn_rmsnorm_bwd(r, weight, d_y, d_residual=None, *, eps=1e-6, need_dweight=True, workspace=None, out=None):
+    """Gradients of <d_y, y> + <d_residual, residual_out> from r (the forward's residual_out, or x where there
+    was no residual): dict(dx, dweight), dx being the gradient of x and of residual alike, dweight fp32;
+    `out` may hold them preallocated."""
+    desc, pw = _rms_desc("r", r, weight, eps)
+    shape, dev, D = r.shape, r.device, r.shape[-1]
+    if d_y is None:
+        raise ValueError("d_y is required")
+    pd = _like("d_y", d_y, shape, r.dtype, dev)
+    pr = _like("d_residual", d_residual, shape, r.dtype, dev)
+    if out is None:
+        out = dict(dx=torch.empty_like(r),
+                   dweight=torch.empty((D,), dtype=torch.float32, device=dev) if need_dweight else None)
+    if out.get("dx") is None:
+        raise ValueError("out['dx'] is required")
+    px = _like("out['dx']", out["dx"], shape, r.dtype, dev)
+    pdw = _like("out['dweight']", out.get("dweight"), (D,), torch.float32, dev)
+    lib = load_library()
+    with _on(dev):
+        need = _bytes(lib.gdn_rmsnorm_bwd_workspace_size, desc, "gdn_rmsnorm_bwd_workspace_size")
+        ws_p, wb, ws = _scratch(need, dev, workspace)
+        check(lib.gdn_rmsnorm_bwd(ctypes.byref(desc), r.data_ptr(), pw, pd, pr, px, pdw, ws_p, wb, _stream_of(dev)),
+              "gdn_rmsnorm_bwd")
+    return out
+
+
+# ---- autograd -----------------------------------------------------------------------------------
+
+
+def _dense(t: Optional[torch.Tensor]):
+    return None if t is None else t.contiguous()
+
+
+class _GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, g, initial_state, cu_seqlens, grad):
+        states = gdn_gated_scan_states(x) if grad else None
+        h, final = gdn_gated_scan_fwd(x, g, initial_state, cu_seqlens=cu_seqlens, states=states)
+        ctx.save_for_backward(x, g, initial_state, cu_seqlens, states)
+        ctx.set_materialize_grads(False)
+        return h, final
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_h, d_final):
+        x, g, s0, cu, states = ctx.saved_tensors
+        gr = gdn_gated_scan_bwd(x, g, torch.zeros_like(x) if d_h is None else _dense(d_h), s0, _dense(d_final),
+                                cu_seqlens=cu, states=states, need_d_initial_state=s0 is not None)
+        return gr["dx"], gr["dg"], gr["d_initial_state"], None, None
+
+
+def gated_scan(x, g, initial_state=None, *, cu_seqlens=None, output_final_state=True):
+    """gdn_gated_scan_fwd with autograd (x, g, initial_state): (h, final_state or None). The state entering
+    every 64th token is held for the backward, which recomputes h from there."""
+    grad = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, g, initial_state))
+    h, final = _GatedScan.apply(x, g, initial_state, cu_seqlens, grad)
+    return h, (final if output_final_state else None)
+
+
+class _ShortConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, initial_state, activation, cu_seqlens, output_final_state):
+        y, final = gdn_short_conv_fwd(x, weight, bias, initial_state, activation=activation, cu_seqlens=cu_seqlens,
+                                      output_final_state=output_final_state)
+        ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens)
+        ctx.activation = activation
+        ctx.set_materialize_grads(False)
+        return y, final
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_y, d_final):
+        x, w, b, s0, cu = ctx.saved_tensors
+        gr = gdn_short_conv_bwd(x, w, torch.zeros_like(x) if d_y is None else _dense(d_y), b, s0, _dense(d_final),
+                                activation=ctx.activation, cu_seqlens=cu, need_d_initial_state=s0 is not None)
+        return (gr["dx"], gr["dweight"].to(w.dtype), None if b is None else gr["dbias"].to(b.dtype),
+                gr["d_initial_state"], None, None, None)
+
+
+def short_conv(x, weight, bias=None, initial_state=None, *, activation="silu", cu_seqlens=None,
+               output_final_state=False):
+    """gdn_short_conv_fwd with autograd (x, weight, bias, initial_state): (y, final_state or None)."""
+    return _ShortConv.apply(x, weight, bias, initial_state, activation, cu_seqlens, output_final_state)
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        y, kept, _ = gdn_rmsnorm_fwd(x, weight, residual, eps=eps)
+        ctx.save_for_backward(x if residual is None else kept, weight)
+        ctx.eps = eps
+        ctx.added = residual is not None
+        ctx.set_materialize_grads(False)
+        return y, kept
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_y, d_kept):
+        r, w = ctx.saved_tensors
+        gr = gdn_rmsnorm_bwd(r, w, torch.zeros_like(r) if d_y is None else _dense(d_y), _dense(d_kept), eps=ctx.eps,
+                             need_dweight=ctx.needs_input_grad[1])
+        dw = None if gr["dweight"] is None else gr["dweight"].to(w.dtype)
+        return gr["dx"], dw, gr["dx"] if ctx.added else None, None
+
+
+def rms_norm(x, weight, residual=None, *, eps=1e-6):
+    """gdn_rmsnorm_fwd (in x's type) with autograd (x, weight, residual): y, or (y, residual_out) with a
+    residual."""
+    y, kept = _RmsNorm.apply(x, weight, residual, eps)
+    return y if residual is None else (y, kept)

@@ -329,6 +329,137 @@ gdn_status gdn_cp_windows(const gdn_desc* desc, const void* k, const void* v,
                           int32_t* rev_windows, void* workspace, size_t workspace_bytes,
                           void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators that stand around the gated delta rule in a layer. Same conventions as above:
+ * row-major contiguous device buffers of the caller, the caller's stream, argument checks before
+ * any launch, no allocation, no host synchronisation, deterministic results, outputs overwritten.
+ * Descriptors are zero-initialised, then filled; `reserved` must be zero. They take channels in
+ * any number; rows whose length or buffers whose address do not fit 16-byte vectors take a slower
+ * path of the same results within rounding.
+ *
+ * Sequences: without cu_seqlens, row b of [B, T, D] is sequence b (N = B). With cu_seqlens (device
+ * int32 [N+1], not decreasing), B is 1 and sequence n owns tokens [cu_seqlens[n], cu_seqlens[n+1]);
+ * tokens before cu_seqlens[0] and from cu_seqlens[N] on belong to no sequence and their outputs are
+ * left as they were. No host copy is needed. Offsets are read clamped into [0, T]: an array that
+ * decreases gives unspecified values, never an access out of range.
+ * An empty sequence passes its entering state on as its final state (and the final state's
+ * gradient on as the entering state's). */
+
+/* Gated scan: the recurrence with a gate per channel,
+ *     h_t = exp(g_t) h_{t-1} + x_t,    h_0 = initial_state (zeros when NULL),
+ * per sequence and channel; g is a natural-log decay (usually <= 0; -inf forgets). */
+typedef struct gdn_scan_desc {
+    int64_t B, T, D;
+    int32_t dtype;             /* gdn_dtype of x, h and their gradients */
+    int32_t g_dtype;           /* gdn_dtype of g and dg: dtype's, or GDN_DTYPE_FP32 */
+    int32_t num_seqs;          /* with cu_seqlens: N (>= 1); ignored otherwise */
+    int32_t flags;             /* must be zero */
+    const int32_t* cu_seqlens; /* device [N+1], or NULL */
+    int32_t reserved[4];       /* must be zero */
+} gdn_scan_desc;
+
+/* Bytes of the workspaces (256-byte aligned) and of the kept states. The sizes depend on B*T, D
+ * alone. */
+gdn_status gdn_gated_scan_fwd_workspace_size(const gdn_scan_desc* desc, size_t* bytes);
+gdn_status gdn_gated_scan_bwd_workspace_size(const gdn_scan_desc* desc, size_t* bytes);
+gdn_status gdn_gated_scan_states_size(const gdn_scan_desc* desc, size_t* bytes);
+
+/* Forward.
+ *   x, h  [B,T,D] (dtype); g [B,T,D] (g_dtype); initial_state, final_state [N,D] fp32
+ *   initial_state may be NULL (zeros); final_state may be NULL (not written) or initial_state
+ *   itself (updated in place, for decoding)
+ *   states: NULL, or a buffer of gdn_gated_scan_states_size bytes (256-byte aligned) that receives
+ *   the fp32 state entering every 64th token, for gdn_gated_scan_bwd
+ * A call of a few tokens per sequence (decoding) is one launch and touches no workspace; the
+ * workspace argument is checked all the same. */
+gdn_status gdn_gated_scan_fwd(const gdn_scan_desc* desc, const void* x, const void* g,
+                              const float* initial_state, void* h, float* final_state, void* states,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of <d_h, h> + <d_final_state, final_state>.
+ *   d_h, dx [B,T,D] (dtype); dg [B,T,D] (g_dtype; with respect to the log-decay)
+ *   d_final_state [N,D] fp32 or NULL (zeros); d_initial_state [N,D] fp32 or NULL (not written)
+ *   states: what the forward of the same inputs wrote, or NULL (recomputed here) */
+gdn_status gdn_gated_scan_bwd(const gdn_scan_desc* desc, const void* x, const void* g,
+                              const float* initial_state, const void* d_h,
+                              const float* d_final_state, const void* states, void* dx, void* dg,
+                              float* d_initial_state, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Short causal convolution, one filter of W taps per channel:
+ *     z_t = bias + sum_j weight[:, j] x_{t-W+1+j},    y = z or silu(z),
+ * the inputs before a sequence's first token being its initial_state (zeros when NULL). */
+typedef enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation;
+typedef struct gdn_conv_desc {
+    int64_t B, T, D;
+    int32_t width;             /* W: 2, 3 or 4 taps */
+    int32_t dtype;             /* gdn_dtype of x, y, the states and their gradients */
+    int32_t w_dtype;           /* gdn_dtype of weight and bias: dtype's, or GDN_DTYPE_FP32 */
+    int32_t activation;        /* gdn_activation */
+    int32_t num_seqs;          /* with cu_seqlens: N (>= 1); ignored otherwise */
+    int32_t flags;             /* must be zero */
+    const int32_t* cu_seqlens; /* device [N+1], or NULL */
+    int32_t reserved[4];       /* must be zero */
+} gdn_conv_desc;
+
+gdn_status gdn_short_conv_bwd_workspace_size(const gdn_conv_desc* desc, size_t* bytes);
+
+/* Forward.
+ *   x, y [B,T,D]; weight [D,W]; bias [D] or NULL
+ *   initial_state, final_state [N, W-1, D], oldest input first: the last W-1 inputs of a sequence,
+ *   its initial_state in front of them where it is shorter. initial_state may be NULL (zeros);
+ *   final_state may be NULL (not written), or initial_state itself where T <= GDN_CONV_INPLACE_T
+ *   without cu_seqlens (updated in place, for decoding; otherwise GDN_ERR_INVALID_ARG) */
+#define GDN_CONV_INPLACE_T 16
+gdn_status gdn_short_conv_fwd(const gdn_conv_desc* desc, const void* x, const void* weight,
+                              const void* bias, const void* initial_state, void* y,
+                              void* final_state, void* stream);
+
+/* Gradients of <d_y, y> + <d_final_state, final_state>; the forward is recomputed inside.
+ *   d_y, dx [B,T,D]; dweight [D,W] fp32; dbias [D] fp32 or NULL (not written)
+ *   d_final_state, d_initial_state [N, W-1, D] (dtype) or NULL (zeros; not written) */
+gdn_status gdn_short_conv_bwd(const gdn_conv_desc* desc, const void* x, const void* weight,
+                              const void* bias, const void* initial_state, const void* d_y,
+                              const void* d_final_state, void* dx, float* dweight, float* dbias,
+                              void* d_initial_state, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* RMS norm of rows of D values, the residual stream's addition in front:
+ *     r = x + residual (rounded to dtype: what residual_out receives is what is normed),
+ *     y = r weight / sqrt(mean(r^2) + eps).
+ * With out_type GDN_OUT_E4M3, y holds 8-bit floats (OCP e4m3) and scale their fp32 scales, of a
+ * whole row (scale_group 0; scale [rows]) or of every 128 columns (scale_group 128; scale
+ * [rows, ceil(D/128)]): scale = max|y| / 448, or 1 where every y is zero, and the 8-bit value is
+ * y / scale to nearest even, formed from the fp32 y. A row with NaN or infinity in it gets what
+ * the formulas give: NaN scales where a NaN is among their columns. */
+typedef enum gdn_out_type { GDN_OUT_SAME = 0, GDN_OUT_E4M3 = 1 } gdn_out_type;
+typedef struct gdn_rmsnorm_desc {
+    int64_t rows, D;
+    int32_t dtype;       /* gdn_dtype of x, residual, residual_out, y and their gradients */
+    int32_t w_dtype;     /* gdn_dtype of weight: dtype's, or GDN_DTYPE_FP32 */
+    int32_t out_type;    /* gdn_out_type (the backward ignores it) */
+    int32_t scale_group; /* with GDN_OUT_E4M3: 0 (a row) or 128 columns per scale; else 0 */
+    float eps;           /* >= 0 */
+    int32_t flags;       /* must be zero */
+    int32_t reserved[4]; /* must be zero */
+} gdn_rmsnorm_desc;
+
+/* Forward. residual and residual_out are both given or both NULL; residual_out may be x or residual
+ * itself (in place). scale only with GDN_OUT_E4M3. */
+gdn_status gdn_rmsnorm_fwd(const gdn_rmsnorm_desc* desc, const void* x, const void* residual,
+                           const void* weight, void* y, float* scale, void* residual_out,
+                           void* stream);
+
+gdn_status gdn_rmsnorm_bwd_workspace_size(const gdn_rmsnorm_desc* desc, size_t* bytes);
+
+/* Gradients of <d_y, y> + <d_residual, residual_out> (of the unquantised y), from r: residual_out,
+ * or x where there was no residual.
+ *   dx [rows, D]: the gradient of x and, being the same, of residual; d_residual or NULL (zeros)
+ *   dweight [D] fp32, or NULL (not written) */
+gdn_status gdn_rmsnorm_bwd(const gdn_rmsnorm_desc* desc, const void* r, const void* weight,
+                           const void* d_y, const void* d_residual, void* dx, float* dweight,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
 /* Per-kernel timing, for measurement tools (off by default). While enabled, each kernel
  * launch of the calls above is bracketed by two HIP events recorded on the call's stream
  * (this adds a few microseconds per launch). gdn_profile_read waits for the recorded
