@@ -4,169 +4,453 @@
 // final state. Gradient: dz = dy act'(z), z recomputed;
 //   dx_s = sum_i w_{W-1-i} dz_{s+i},  dw_j = sum_t dz_t x_{t-W+1+j},  dbias = sum_t dz_t,
 // positions before the first token giving the entering state's gradient.
+//
+// Bound by memory: 2W + 5 operations per element forward and 6W + 10 backward, against 4 and 6 bytes
+// in bf16. So every input is read once: a wave walks a run of tokens down its block of channels (a
+// lane holds a few neighbouring ones, so a wave reads whole cache lines of a token's row) with the
+// last W-1 inputs, and in the gradient the last W-1 dz, in registers; only the W-1 tokens around the
+// ends of a run are read by two waves. The next tokens' loads are issued before the present ones
+// are used. Runs that lie inside one sequence take a path without any test per token.
 #include "gdn_layer.h"
+#include "gdn_vec.h"
 
 namespace gdn {
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSumTokens = 512;  // tokens per partial sum of dw and dbias
+constexpr int kWaves = kThreads / kWave;
 
-// Input at position t of sequence s: a token, or before its first one a row of the entering state.
-template <typename T>
-__device__ __forceinline__ float input_at(const ConvArgs& p, const SeqPos& s, int32_t t, int64_t c) {
-    if (t >= s.start) return Elem<T>::to_f(static_cast<const T*>(p.x)[(int64_t)t * p.D + c]);
-    if (!p.s0) return 0.f;
-    const int64_t row = (int64_t)s.n * (p.W - 1) + (t - s.start + p.W - 1);
-    return Elem<T>::to_f(static_cast<const T*>(p.s0)[row * p.D + c]);
-}
-
-template <typename T, typename TW>
-__device__ __forceinline__ float pre_act(const ConvArgs& p, const SeqPos& s, int32_t t, int64_t c) {
-    float z = p.bias ? Elem<TW>::to_f(static_cast<const TW*>(p.bias)[c]) : 0.f;
-    for (int j = 0; j < p.W; ++j)
-        z = fmaf(Elem<TW>::to_f(static_cast<const TW*>(p.w)[c * p.W + j]), input_at<T>(p, s, t - p.W + 1 + j, c), z);
-    return z;
-}
-
-template <typename T, typename TW>
-__device__ __forceinline__ float d_pre_act(const ConvArgs& p, const SeqPos& s, int32_t t, int64_t c) {
-    const float dy = Elem<T>::to_f(static_cast<const T*>(p.d_y)[(int64_t)t * p.D + c]);
-    if (!p.silu) return dy;
-    const float z = pre_act<T, TW>(p, s, t, c);
-    const float sg = 1.f / (1.f + fast_exp(-z));
-    return dy * sg * (1.f + z * (1.f - sg));
-}
-
-template <typename T, typename TW>
-__global__ __launch_bounds__(kThreads) void k_conv_fwd(ConvArgs p) {
-    const int64_t c = (int64_t)blockIdx.y * kThreads + threadIdx.x;
-    const int32_t t = blockIdx.x;
-    if (c >= p.D) return;
-    const SeqPos s = seq_find(p.seq, t);
-    if (t < s.start || t >= s.end) return;
-    float z = pre_act<T, TW>(p, s, t, c);
-    if (p.silu) z = z / (1.f + fast_exp(-z));
-    static_cast<T*>(p.y)[(int64_t)t * p.D + c] = Elem<T>::from_f(z);
-}
-
-// Final states: a thread reads all W-1 rows of its channel before it writes them, so that the
-// entering states may be overwritten in place.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_conv_final(ConvArgs p) {
-    const int64_t c = (int64_t)blockIdx.y * kThreads + threadIdx.x;
-    if (c >= p.D) return;
-    const SeqPos s = seq_at(p.seq, blockIdx.x);
-    float v[3];
-    const int32_t end = s.end > s.start ? s.end : s.start;
-    for (int r = 0; r < p.W - 1; ++r) v[r] = input_at<T>(p, s, end - p.W + 1 + r, c);
-    for (int r = 0; r < p.W - 1; ++r)
-        static_cast<T*>(p.sT)[((int64_t)s.n * (p.W - 1) + r) * p.D + c] = Elem<T>::from_f(v[r]);
-}
-
-// dL/d(input at position t), t from W-1 before the sequence's first token to its last token.
-template <typename T, typename TW>
-__device__ __forceinline__ float d_input(const ConvArgs& p, const SeqPos& s, int32_t t, int64_t c) {
-    float d = 0.f;
-    for (int i = 0; i < p.W; ++i)
-        if (t + i >= s.start && t + i < s.end)
-            d = fmaf(Elem<TW>::to_f(static_cast<const TW*>(p.w)[c * p.W + p.W - 1 - i]),
-                     d_pre_act<T, TW>(p, s, t + i, c), d);
-    const int32_t end = s.end > s.start ? s.end : s.start;
-    const int32_t r = t - (end - p.W + 1);
-    if (p.d_sT && r >= 0)
-        d += Elem<T>::to_f(static_cast<const T*>(p.d_sT)[((int64_t)s.n * (p.W - 1) + r) * p.D + c]);
-    return d;
-}
-
-template <typename T, typename TW>
-__global__ __launch_bounds__(kThreads) void k_conv_dx(ConvArgs p) {
-    const int64_t c = (int64_t)blockIdx.y * kThreads + threadIdx.x;
-    const int32_t t = blockIdx.x;
-    if (c >= p.D) return;
-    const SeqPos s = seq_find(p.seq, t);
-    if (t < s.start || t >= s.end) return;
-    static_cast<T*>(p.dx)[(int64_t)t * p.D + c] = Elem<T>::from_f(d_input<T, TW>(p, s, t, c));
-}
-
-template <typename T, typename TW>
-__global__ __launch_bounds__(kThreads) void k_conv_dstate(ConvArgs p) {
-    const int64_t c = (int64_t)blockIdx.y * kThreads + threadIdx.x;
-    if (c >= p.D) return;
-    const SeqPos s = seq_at(p.seq, blockIdx.x);
-    for (int r = 0; r < p.W - 1; ++r)
-        static_cast<T*>(p.ds0)[((int64_t)s.n * (p.W - 1) + r) * p.D + c] =
-            Elem<T>::from_f(d_input<T, TW>(p, s, s.start - p.W + 1 + r, c));
-}
-
-// Partial sums over kSumTokens tokens, [parts, W + 1, D] (the taps, then the bias).
-template <typename T, typename TW>
-__global__ __launch_bounds__(kThreads) void k_conv_dw(ConvArgs p, float* part) {
-    const int64_t c = (int64_t)blockIdx.y * kThreads + threadIdx.x;
-    if (c >= p.D) return;
-    const int32_t t0 = blockIdx.x * kSumTokens, t1 = min(t0 + kSumTokens, p.seq.total);
-    float acc[5] = {};
-    SeqPos s = seq_find(p.seq, t0);
-    for (int32_t t = t0; t < t1; ++t) {
-        seq_advance(p.seq, s, t);
-        if (t < s.start || t >= s.end) continue;
-        const float dz = d_pre_act<T, TW>(p, s, t, c);
-        for (int j = 0; j < p.W; ++j) acc[j] = fmaf(dz, input_at<T>(p, s, t - p.W + 1 + j, c), acc[j]);
-        acc[4] += dz;
+// The lane's filter, tap by tap, and its bias.
+template <typename TW, int W, int VEC>
+struct Filter {
+    float w[W][VEC], b[VEC];
+    __device__ __forceinline__ void load(const ConvArgs& p, int64_t c0) {
+        const Raw<TW, VEC * W> r = load_raw<TW, VEC * W>(static_cast<const TW*>(p.w) + c0 * W);
+        Raw<TW, VEC> rb;
+        rb.clear();
+        if (p.bias) rb = load_raw<TW, VEC>(static_cast<const TW*>(p.bias) + c0);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][v] = r.get(v * W + j);
+            b[v] = rb.get(v);
+        }
     }
-    float* out = part + (int64_t)blockIdx.x * (p.W + 1) * p.D + c;
-    for (int j = 0; j < p.W; ++j) out[j * p.D] = acc[j];
-    out[p.W * p.D] = acc[4];
+};
+
+// Row t of a [tokens, D] array, the lane's channels.
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> row(const void* a, int64_t t, const ConvArgs& p, int64_t c0) {
+    return load_raw<T, VEC>(static_cast<const T*>(a) + t * p.D + c0);
+}
+// Row r of sequence n's state [W-1, D], zeros where there is none.
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> state_row(const void* a, int32_t n, int r, const ConvArgs& p, int64_t c0) {
+    if (!a) {
+        Raw<T, VEC> z;
+        z.clear();
+        return z;
+    }
+    return row<T, VEC>(a, (int64_t)n * (p.W - 1) + r, p, c0);
 }
 
-__global__ __launch_bounds__(kThreads) void k_conv_dw_sum(const float* part, int parts, int W, int64_t D, float* dw, float* db) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int j = blockIdx.y;
-    if (c >= D) return;
-    float s = 0.f;
-    for (int i = 0; i < parts; ++i) s += part[((int64_t)i * (W + 1) + j) * D + c];
+template <int W, int VEC>
+__device__ __forceinline__ void shift_in(float (&win)[W - 1][VEC], const float (&x)[VEC]) {
+#pragma unroll
+    for (int r = 0; r + 1 < W - 1; ++r)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) win[r][v] = win[r + 1][v];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) win[W - 2][v] = x[v];
+}
+
+template <typename TW, int W, int VEC>
+__device__ __forceinline__ void pre_act(const Filter<TW, W, VEC>& f, const float (&win)[W - 1][VEC], const float (&x)[VEC], float (&z)[VEC]) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        z[v] = f.b[v];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) z[v] = fmaf(f.w[j][v], win[j][v], z[v]);
+        z[v] = fmaf(f.w[W - 1][v], x[v], z[v]);
+    }
+}
+// 1 / (1 + exp(-z)); 0 where exp(-z) is infinite
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + fast_exp(-z)); }
+
+// Sequences without tokens: their state (or its gradient) passes through, by the workgroups of the
+// grid's last row.
+template <bool kOdd, typename T, int VEC>
+__device__ void pass_empty(const ConvArgs& p, const void* in, void* out, int64_t c0, int skip) {
+    for (int32_t s = wave_id(); s < p.seq.N; s += kWaves) {
+        const SeqPos q = seq_at(p.seq, s);
+        if (q.start < q.end) continue;
+        for (int r = 0; r < p.W - 1; ++r)
+            store_own<kOdd, T, VEC>(static_cast<T*>(out) + ((int64_t)s * (p.W - 1) + r) * p.D + c0,
+                                    state_row<T, VEC>(in, s, r, p, c0), skip);
+    }
+}
+
+// U: tokens loaded ahead. `run`: tokens per wave.
+template <bool kOdd, typename T, typename TW, int W, int VEC, int U>
+__global__ __launch_bounds__(kThreads) void k_conv_fwd(ConvArgs p, int run, int token_blocks) {
+    const int64_t ch = ((int64_t)blockIdx.x * kWave + (threadIdx.x & 63)) * VEC;
+    if (ch >= p.D) return;
+    const Lane ln(ch, p.D, VEC);
+    const int64_t c0 = ln.at;
+    if ((int)blockIdx.y == token_blocks) return pass_empty<kOdd, T, VEC>(p, p.s0, p.sT, c0, ln.skip);
+    const int64_t w0l = ((int64_t)blockIdx.y * kWaves + wave_id()) * run;
+    if (w0l >= p.seq.total) return;
+    const int32_t w0 = (int32_t)w0l;
+    const int32_t w1 = w0l + run < p.seq.total ? w0 + run : p.seq.total;
+    Raw<T, VEC> nx[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) nx[u] = row<T, VEC>(p.x, min(w0 + u, w1 - 1), p, c0);
+    Filter<TW, W, VEC> f;
+    f.load(p, c0);
+    SeqPos s = seq_find(p.seq, w0);
+    float win[W - 1][VEC];
+#pragma unroll
+    for (int r = 0; r < W - 1; ++r) {
+        const int32_t at = w0 - (W - 1) + r;
+        Raw<T, VEC> h;
+        h.clear();
+        if (w0 >= s.start && w0 < s.end)
+            h = at >= s.start ? row<T, VEC>(p.x, at, p, c0) : state_row<T, VEC>(p.s0, s.n, at - s.start + W - 1, p, c0);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) win[r][v] = h.get(v);
+    }
+    T* y = static_cast<T*>(p.y);
+    auto token = [&](int32_t t, const Raw<T, VEC>& raw) {
+        float x[VEC], z[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) x[v] = raw.get(v);
+        pre_act<TW, W, VEC>(f, win, x, z);
+        if (p.silu)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) z[v] *= sigmoid(z[v]);
+        store_own<kOdd, T, VEC>(y + (int64_t)t * p.D + c0, z, ln.skip);
+        shift_in<W, VEC>(win, x);
+    };
+    const bool inside = w0 >= s.start && w1 < s.end;
+    for (int32_t t0 = w0; t0 < w1; t0 += U) {
+        Raw<T, VEC> x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = nx[u];
+        if (t0 + U < w1)
+#pragma unroll
+            for (int u = 0; u < U; ++u) nx[u] = row<T, VEC>(p.x, min(t0 + U + u, w1 - 1), p, c0);
+        if (inside && t0 + U <= w1) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) token(t0 + u, x[u]);
+            continue;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int32_t t = t0 + u;
+            if (t >= w1) break;
+            seq_advance(p.seq, s, t);
+            if (t < s.start || t >= s.end) continue;
+            if (t == s.start && t > w0)
+#pragma unroll
+                for (int r = 0; r < W - 1; ++r) {
+                    const Raw<T, VEC> h = state_row<T, VEC>(p.s0, s.n, r, p, c0);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) win[r][v] = h.get(v);
+                }
+            token(t, x[u]);
+            // the window now holds the last W-1 inputs, exactly as they were read
+            if (p.sT && t + 1 == s.end)
+#pragma unroll
+                for (int r = 0; r < W - 1; ++r)
+                    store_own<kOdd, T, VEC>(static_cast<T*>(p.sT) + ((int64_t)s.n * (W - 1) + r) * p.D + c0, win[r], ln.skip);
+        }
+    }
+}
+
+// One workgroup: kWaves runs of `run` tokens and 64 VEC channels; the partial sums of dw and dbias over
+// its tokens go to part[blockIdx.y], [W + 1, D] (the taps, then the bias).
+template <bool kOdd, typename T, typename TW, int W, int VEC, int U>
+__global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int token_blocks, float* part) {
+    __shared__ float sh[kWaves - 1][(W + 1) * VEC][kWave];
+    const int lane = threadIdx.x & 63;
+    const int wave = wave_id();
+    const int64_t ch = ((int64_t)blockIdx.x * kWave + lane) * VEC;
+    const bool live = ch < p.D;
+    const Lane ln(ch, p.D, VEC);
+    const int64_t c0 = ln.at;
+    if ((int)blockIdx.y == token_blocks) {
+        if (live) pass_empty<kOdd, T, VEC>(p, p.d_sT, p.ds0, c0, ln.skip);
+        return;
+    }
+    float dw[W][VEC] = {}, db[VEC] = {};
+    const int64_t w0l = ((int64_t)blockIdx.y * kWaves + wave) * run;
+    if (live && w0l < p.seq.total) {
+        const int32_t w0 = (int32_t)w0l;
+        const int32_t w1 = w0l + run < p.seq.total ? w0 + run : p.seq.total;
+        const int32_t w2 = min(w1 + W - 1, p.seq.total);  // dx of the run's last tokens needs dz up to here
+        Raw<T, VEC> nx[U], nd[U];
+        auto fetch = [&](int32_t t0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int32_t t = min(t0 + u, w2 - 1);
+                nx[u] = row<T, VEC>(p.x, t, p, c0);
+                nd[u] = row<T, VEC>(p.d_y, t, p, c0);
+            }
+        };
+        fetch(w0);
+        Filter<TW, W, VEC> f;
+        f.load(p, c0);
+        SeqPos s = seq_find(p.seq, w0);
+        float win[W - 1][VEC], dzw[W - 1][VEC];  // x and dz of the W-1 tokens before the present one
+#pragma unroll
+        for (int r = 0; r < W - 1; ++r) {
+            const int32_t at = w0 - (W - 1) + r;
+            Raw<T, VEC> h;
+            h.clear();
+            if (w0 >= s.start && w0 < s.end)
+                h = at >= s.start ? row<T, VEC>(p.x, at, p, c0) : state_row<T, VEC>(p.s0, s.n, at - s.start + W - 1, p, c0);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                win[r][v] = h.get(v);
+                dzw[r][v] = 0.f;
+            }
+        }
+        T* dx = static_cast<T*>(p.dx);
+        // dz of a token, its part of the sums (own: the token is one of the run's), and the gradient of the
+        // input W-1 positions back, which is whole now
+        auto token = [&](const Raw<T, VEC>& rx, const Raw<T, VEC>& rd, bool own, float (&back)[VEC]) {
+            float x[VEC], z[VEC], dz[VEC];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) x[v] = rx.get(v);
+            if (p.silu) {
+                pre_act<TW, W, VEC>(f, win, x, z);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float sg = sigmoid(z[v]);
+                    dz[v] = rd.get(v) * (sg * (1.f + z[v] * (1.f - sg)));
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) dz[v] = rd.get(v);
+            }
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                back[v] = f.w[0][v] * dz[v];
+#pragma unroll
+                for (int i = 0; i < W - 1; ++i) back[v] = fmaf(f.w[W - 1 - i][v], dzw[i][v], back[v]);
+            }
+            if (own) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) dw[j][v] = fmaf(dz[v], win[j][v], dw[j][v]);
+                    dw[W - 1][v] = fmaf(dz[v], x[v], dw[W - 1][v]);
+                    db[v] += dz[v];
+                }
+            }
+            shift_in<W, VEC>(win, x);
+            shift_in<W, VEC>(dzw, dz);
+        };
+        // where the gradient of position t of sequence s goes: the token's owner stores it, positions before
+        // the first token (rows of the entering state) go by the first token's owner
+        auto put = [&](int32_t t, const float (&d)[VEC]) {
+            if (t >= s.start) {
+                if (t >= w0 && t < w1) store_own<kOdd, T, VEC>(dx + (int64_t)t * p.D + c0, d, ln.skip);
+            } else if (p.ds0 && s.start >= w0 && s.start < w1) {
+                store_own<kOdd, T, VEC>(static_cast<T*>(p.ds0) + ((int64_t)s.n * (W - 1) + t - s.start + W - 1) * p.D + c0, d, ln.skip);
+            }
+        };
+        const bool inside = w0 - (W - 1) >= s.start && w2 < s.end;
+        for (int32_t t0 = w0; t0 < w2; t0 += U) {
+            Raw<T, VEC> x[U], d[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                x[u] = nx[u];
+                d[u] = nd[u];
+            }
+            if (t0 + U < w2) fetch(t0 + U);
+            if (inside && t0 + U <= w1) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float back[VEC];
+                    token(x[u], d[u], true, back);
+                    const int32_t at = t0 + u - (W - 1);
+                    if (at >= w0) store_own<kOdd, T, VEC>(dx + (int64_t)at * p.D + c0, back, ln.skip);
+                }
+                continue;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int32_t t = t0 + u;
+                if (t >= w2) break;
+                // behind the run only the sequence that its last token is in matters
+                if (t < w1) seq_advance(p.seq, s, t);
+                if (t < s.start || t >= s.end) continue;
+                if (t == s.start && t > w0)
+#pragma unroll
+                    for (int r = 0; r < W - 1; ++r) {
+                        const Raw<T, VEC> h = state_row<T, VEC>(p.s0, s.n, r, p, c0);
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) {
+                            win[r][v] = h.get(v);
+                            dzw[r][v] = 0.f;
+                        }
+                    }
+                float back[VEC];
+                token(x[u], d[u], t < w1, back);
+                put(t - (W - 1), back);
+                if (t + 1 == s.end) {
+                    // the last W-1 positions: no tokens behind them, but the final state's gradient
+#pragma unroll
+                    for (int r = 0; r < W - 1; ++r) {
+                        const Raw<T, VEC> g = state_row<T, VEC>(p.d_sT, s.n, r, p, c0);
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) {
+                            back[v] = g.get(v);
+#pragma unroll
+                            for (int i = 0; i + r < W - 1; ++i) back[v] = fmaf(f.w[W - 1 - i][v], dzw[r + i][v], back[v]);
+                        }
+                        put(s.end - (W - 1) + r, back);
+                    }
+                }
+            }
+        }
+    }
+    if (wave > 0)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) sh[wave - 1][j * VEC + v][lane] = dw[j][v];
+            sh[wave - 1][W * VEC + v][lane] = db[v];
+        }
+    __syncthreads();
+    if (wave > 0 || !live) return;
+#pragma unroll
+    for (int i = 0; i < kWaves - 1; ++i)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) dw[j][v] += sh[i][j * VEC + v][lane];
+            db[v] += sh[i][W * VEC + v][lane];
+        }
+    float* out = part + (int64_t)blockIdx.y * (W + 1) * p.D + c0;
+#pragma unroll
+    for (int j = 0; j < W; ++j) store_own<kOdd, float, VEC>(out + j * p.D, dw[j], ln.skip);
+    store_own<kOdd, float, VEC>(out + W * p.D, db, ln.skip);
+}
+
+__global__ __launch_bounds__(1024) void k_conv_dw_sum(const float* part, int parts, int W, int64_t D, float* dw, float* db) {
+    __shared__ float sh[256];
+    const int64_t c0 = (int64_t)blockIdx.x * 16;
+    const float s = sum_parts16(part, parts, (W + 1) * D, c0, sh);
+    const int64_t i = c0 + threadIdx.x;
+    if (threadIdx.x >= 16 || i >= (W + 1) * D) return;
+    const int64_t j = i / D, c = i % D;
     if (j < W) dw[c * W + j] = s;
     else if (db) db[c] = s;
 }
 
-template <typename T, typename TW>
-hipError_t fwd_t(const ConvArgs& a, hipStream_t st) {
-    const unsigned cb = (unsigned)((a.D + kThreads - 1) / kThreads);
-    if (a.seq.total)
-        hipLaunchKernelGGL((k_conv_fwd<T, TW>), dim3((unsigned)a.seq.total, cb), dim3(kThreads), 0, st, a);
-    if (a.sT) hipLaunchKernelGGL((k_conv_final<T>), dim3((unsigned)a.seq.N, cb), dim3(kThreads), 0, st, a);
-    return hipGetLastError();
+unsigned blocks_of(int64_t D, int vec) { return (unsigned)((D + (int64_t)kWave * vec - 1) / ((int64_t)kWave * vec)); }
+
+// Channels per lane forward: 16 bytes of them; in rows of fewer than 64 such vectors 4 bytes, so that
+// short rows still use a wave's lanes; one where a row has less than that.
+template <typename T> int fwd_vec(int64_t D) {
+    constexpr int wide = 16 / sizeof(T), slim = 4 / sizeof(T);
+    return D >= 64 * wide ? wide : (D >= slim ? slim : 1);
+}
+// The gradient's: 4 (8 or 16 bytes), for its filter, its sums and two windows stay in registers beside
+// the loads in flight.
+template <typename T> int bwd_vec(int64_t D) {
+    constexpr int wide = 4, slim = 4 / sizeof(T);
+    return D >= 64 * wide ? wide : (D >= slim ? slim : 1);
 }
 
-int parts_of(int64_t total) { return (int)((total + kSumTokens - 1) / kSumTokens); }
+// Tokens per wave: rows of at most 16 tokens go to one wave each (which makes their state's update in
+// place safe: one wave reads it before it writes it). Longer axes take 32, or 8 where 32 would leave
+// the chip's 1,024 SIMDs without two waves each: fewer tokens re-read against more waves in flight.
+int fwd_run(const SeqView& s, unsigned cblocks) {
+    if (!s.cu && s.T <= 16) return s.T > 0 ? s.T : 1;
+    return (int64_t)s.total * cblocks >= 2048 * 32 ? 32 : 8;
+}
+
+template <typename T, typename TW, int W, int VEC>
+hipError_t fwd_v(const ConvArgs& a, hipStream_t st) {
+    const unsigned cb = blocks_of(a.D, VEC);
+    const int run = fwd_run(a.seq, cb);
+    const int tb = (int)(((int64_t)a.seq.total + (int64_t)run * kWaves - 1) / ((int64_t)run * kWaves));
+    const int extra = a.sT && (a.seq.cu || a.seq.T == 0);
+    if (tb + extra == 0) return hipSuccess;
+    const dim3 grid(cb, (unsigned)(tb + extra));
+    constexpr bool kMayOdd = VEC > 1;
+    const bool odd = a.D % VEC;
+    if (run < 8 && odd) hipLaunchKernelGGL((k_conv_fwd<kMayOdd, T, TW, W, VEC, 1>), grid, dim3(kThreads), 0, st, a, run, tb);
+    else if (run < 8) hipLaunchKernelGGL((k_conv_fwd<false, T, TW, W, VEC, 1>), grid, dim3(kThreads), 0, st, a, run, tb);
+    else if (odd) hipLaunchKernelGGL((k_conv_fwd<kMayOdd, T, TW, W, VEC, 8>), grid, dim3(kThreads), 0, st, a, run, tb);
+    else hipLaunchKernelGGL((k_conv_fwd<false, T, TW, W, VEC, 8>), grid, dim3(kThreads), 0, st, a, run, tb);
+    return hipGetLastError();
+}
+template <typename T, typename TW, int W>
+hipError_t fwd_t(const ConvArgs& a, hipStream_t st) {
+    constexpr int wide = 16 / sizeof(T), slim = 4 / sizeof(T);
+    const int v = fwd_vec<T>(a.D);
+    return v == wide ? fwd_v<T, TW, W, wide>(a, st) : (v == slim ? fwd_v<T, TW, W, slim>(a, st) : fwd_v<T, TW, W, 1>(a, st));
+}
+
+// Tokens per wave in the gradient: about 4,096 waves in all, in steps of 8 tokens from 16 to 256: longer
+// runs re-read less and leave fewer partial sums.
+int bwd_run(int64_t total, unsigned cblocks) {
+    const int64_t r = (total * cblocks / 4096 + 7) / 8 * 8;
+    return (int)(r < 16 ? 16 : (r > 256 ? 256 : r));
+}
+int bwd_parts(int64_t total, int run) { return (int)((total + (int64_t)run * kWaves - 1) / ((int64_t)run * kWaves)); }
+
+template <typename T, typename TW, int W, int VEC>
+hipError_t bwd_v(const ConvArgs& a, hipStream_t st) {
+    const unsigned cb = blocks_of(a.D, VEC);
+    const int run = bwd_run(a.seq.total, cb);
+    const int parts = bwd_parts(a.seq.total, run);
+    const int extra = a.ds0 && (a.seq.cu || a.seq.T == 0);
+    float* part = reinterpret_cast<float*>(a.ws);
+    const dim3 grid(cb, (unsigned)(parts + extra));
+    if (parts + extra) {
+        if (a.D % VEC) hipLaunchKernelGGL((k_conv_bwd<(VEC > 1), T, TW, W, VEC, 4>), grid, dim3(kThreads), 0, st, a, run, parts, part);
+        else hipLaunchKernelGGL((k_conv_bwd<false, T, TW, W, VEC, 4>), grid, dim3(kThreads), 0, st, a, run, parts, part);
+    }
+    hipLaunchKernelGGL(k_conv_dw_sum, dim3((unsigned)(((W + 1) * a.D + 15) / 16)), dim3(1024), 0, st, part, parts, W, a.D, a.dw, a.db);
+    return hipGetLastError();
+}
+template <typename T, typename TW, int W>
+hipError_t bwd_t(const ConvArgs& a, hipStream_t st) {
+    constexpr int slim = 4 / sizeof(T);
+    const int v = bwd_vec<T>(a.D);
+    return v == 4 ? bwd_v<T, TW, W, 4>(a, st) : (v == slim ? bwd_v<T, TW, W, slim>(a, st) : bwd_v<T, TW, W, 1>(a, st));
+}
 
 template <typename T, typename TW>
-hipError_t bwd_t(const ConvArgs& a, hipStream_t st) {
-    const unsigned cb = (unsigned)((a.D + kThreads - 1) / kThreads);
-    const int parts = parts_of(a.seq.total);
-    float* part = reinterpret_cast<float*>(a.ws);
-    if (a.seq.total) {
-        hipLaunchKernelGGL((k_conv_dx<T, TW>), dim3((unsigned)a.seq.total, cb), dim3(kThreads), 0, st, a);
-        hipLaunchKernelGGL((k_conv_dw<T, TW>), dim3((unsigned)parts, cb), dim3(kThreads), 0, st, a, part);
-    }
-    if (a.ds0) hipLaunchKernelGGL((k_conv_dstate<T, TW>), dim3((unsigned)a.seq.N, cb), dim3(kThreads), 0, st, a);
-    hipLaunchKernelGGL(k_conv_dw_sum, dim3(cb, (unsigned)a.W + 1), dim3(kThreads), 0, st, part, parts, a.W, a.D, a.dw, a.db);
-    return hipGetLastError();
+hipError_t fwd_w(const ConvArgs& a, hipStream_t st) {
+    return a.W == 2 ? fwd_t<T, TW, 2>(a, st) : (a.W == 3 ? fwd_t<T, TW, 3>(a, st) : fwd_t<T, TW, 4>(a, st));
+}
+template <typename T, typename TW>
+hipError_t bwd_w(const ConvArgs& a, hipStream_t st) {
+    return a.W == 2 ? bwd_t<T, TW, 2>(a, st) : (a.W == 3 ? bwd_t<T, TW, 3>(a, st) : bwd_t<T, TW, 4>(a, st));
 }
 
 }  // namespace
 
-size_t conv_bwd_ws(int64_t total, int64_t D, int W) { return (size_t)parts_of(total) * (W + 1) * D * 4; }
+size_t conv_bwd_ws(int64_t total, int64_t D, int W, int dtype) {
+    const unsigned cb = blocks_of(D, dtype == 1 ? bwd_vec<float>(D) : bwd_vec<bf16_t>(D));
+    return (size_t)bwd_parts(total, bwd_run(total, cb)) * (W + 1) * D * 4;
+}
 
 // dtype, w_dtype: gdn_dtype (0 bf16, 1 fp32); the filter in the type of x or fp32
 hipError_t launch_conv_fwd(const ConvArgs& a, int dtype, int w_dtype, hipStream_t st) {
-    if (dtype == 1) return fwd_t<float, float>(a, st);
-    return w_dtype == 1 ? fwd_t<bf16_t, float>(a, st) : fwd_t<bf16_t, bf16_t>(a, st);
+    if (dtype == 1) return fwd_w<float, float>(a, st);
+    return w_dtype == 1 ? fwd_w<bf16_t, float>(a, st) : fwd_w<bf16_t, bf16_t>(a, st);
 }
 hipError_t launch_conv_bwd(const ConvArgs& a, int dtype, int w_dtype, hipStream_t st) {
-    if (dtype == 1) return bwd_t<float, float>(a, st);
-    return w_dtype == 1 ? bwd_t<bf16_t, float>(a, st) : bwd_t<bf16_t, bf16_t>(a, st);
+    if (dtype == 1) return bwd_w<float, float>(a, st);
+    return w_dtype == 1 ? bwd_w<bf16_t, float>(a, st) : bwd_w<bf16_t, bf16_t>(a, st);
 }
 
 }  // namespace gdn

@@ -94,7 +94,7 @@ struct ConvArgs {
     void* ds0;
     unsigned char* ws;
 };
-size_t conv_bwd_ws(int64_t total, int64_t D, int W);
+size_t conv_bwd_ws(int64_t total, int64_t D, int W, int dtype);
 hipError_t launch_conv_fwd(const ConvArgs& a, int dtype, int w_dtype, hipStream_t st);
 hipError_t launch_conv_bwd(const ConvArgs& a, int dtype, int w_dtype, hipStream_t st);
 

@@ -147,7 +147,7 @@ gdn_status gdn_short_conv_bwd_workspace_size(const gdn_conv_desc* desc, size_t* 
     SeqView seq;
     if (!bytes) return GDN_ERR_INVALID_ARG;
     if (gdn_status s = check_conv(desc, seq)) return s;
-    *bytes = conv_bwd_ws(seq.total, desc->D, desc->width);
+    *bytes = conv_bwd_ws(seq.total, desc->D, desc->width, desc->dtype);
     return GDN_OK;
 }
 
@@ -179,7 +179,7 @@ gdn_status gdn_short_conv_bwd(const gdn_conv_desc* desc, const void* x, const vo
     if (gdn_status s = check_conv(desc, a.seq)) return s;
     if (!weight || !dweight || (a.seq.total && (!x || !d_y || !dx || dx == x || dx == d_y))) return GDN_ERR_INVALID_ARG;
     if (d_initial_state && (d_initial_state == initial_state || d_initial_state == d_final_state)) return GDN_ERR_INVALID_ARG;
-    const size_t need = conv_bwd_ws(a.seq.total, desc->D, desc->width);
+    const size_t need = conv_bwd_ws(a.seq.total, desc->D, desc->width, desc->dtype);
     if (need)
         if (gdn_status s = check_buf(workspace, need, workspace_bytes)) return s;
     a.D = desc->D;

@@ -1,0 +1,103 @@
+// gdn_vec.h -- vectors of consecutive channels held by one lane, in storage form, for the streaming
+// kernels of the layer operators. Rows of any length and buffers at any element-aligned address take
+// the same code: a vector moves by one load or store at whatever alignment it has (the hardware takes
+// any; 16-byte aligned ones are the fast case). Where a row does not end on a vector, its last lane's
+// vector is moved back to end with the row (Lane::at), reads its neighbour's channels again and
+// stores its own only (Lane::skip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdn_common.h"
+
+namespace gdn {
+
+template <typename T, int N>
+struct Raw {
+    static constexpr int kWords = (N * (int)sizeof(T) + 3) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void set(const float (&x)[N]) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = __float_as_uint(x[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = pack_bf2(x[2 * i], 2 * i + 1 < N ? x[(2 * i + 1) % N] : 0.f);
+        }
+    }
+};
+
+// A lane's channels at .. at + N - 1 of a row of D >= N, of which it owns those from at + skip on.
+struct Lane {
+    int64_t at;
+    int skip;
+    __device__ __forceinline__ Lane(int64_t c0, int64_t D, int N) : at(c0 + N <= D ? c0 : D - N), skip((int)(c0 - at)) {}
+};
+
+template <typename T, int N>
+__device__ __forceinline__ Raw<T, N> load_raw(const T* p) {
+    Raw<T, N> r;
+    if constexpr (N * sizeof(T) < 4) r.w[0] = p[0];
+    else __builtin_memcpy(r.w, p, N * sizeof(T));
+    return r;
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_raw(T* p, const Raw<T, N>& r) {
+    if constexpr (N * sizeof(T) < 4) p[0] = (T)r.w[0];
+    else __builtin_memcpy(p, r.w, N * sizeof(T));
+}
+// kOdd: rows that may not end on a vector (skip may be above zero).
+template <bool kOdd, typename T, int N>
+__device__ __forceinline__ void store_own(T* p, const Raw<T, N>& r, int skip) {
+    if (!kOdd || skip == 0) return store_raw<T, N>(p, r);
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+        if (i >= skip) {
+            if constexpr (sizeof(T) == 4) p[i] = __uint_as_float(r.w[i]);
+            else p[i] = (T)(r.w[i / 2] >> (16 * (i & 1)));
+        }
+}
+template <bool kOdd, typename T, int N>
+__device__ __forceinline__ void store_own(T* p, const float (&x)[N], int skip) {
+    Raw<T, N> r;
+    r.set(x);
+    store_own<kOdd, T, N>(p, r, skip);
+}
+
+// Sum over `parts` rows of partial sums [parts, n] for columns c0 .. c0+15, by a workgroup of 1024
+// threads: 64 rows at a time, 16 lanes on the columns of each, then a tree over the rows in LDS. The
+// order of the additions depends on `parts` alone. Threads 0..15 get the sums of columns c0 + threadIdx.x.
+__device__ __forceinline__ float sum_parts16(const float* part, int parts, int64_t n, int64_t c0, float* sh) {
+    const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
+    float s[4] = {};
+    if (c0 + col < n) {
+        const float* p = part + c0 + col;
+        int i = row;
+        for (; i + 192 < parts; i += 256)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s[u] += p[(int64_t)(i + 64 * u) * n];
+        for (; i < parts; i += 64) s[0] += p[(int64_t)i * n];
+    }
+    float v = (s[0] + s[1]) + (s[2] + s[3]);
+    // a wave holds 4 rows of 16 columns
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    if ((threadIdx.x & 63) < 16) sh[(threadIdx.x >> 6) * 16 + col] = v;
+    __syncthreads();
+    float t = 0.f;
+    if (threadIdx.x < 16)
+#pragma unroll
+        for (int w = 0; w < 16; ++w) t += sh[w * 16 + threadIdx.x];
+    return t;
+}
+
+}  // namespace gdn
