@@ -340,8 +340,8 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
     store_own<kOdd, float, VEC>(out + W * p.D, db, ln.skip);
 }
 
-__global__ __launch_bounds__(1024) void k_conv_dw_sum(const float* part, int parts, int W, int64_t D, float* dw, float* db) {
-    __shared__ float sh[256];
+__global__ __launch_bounds__(kThreads) void k_conv_dw_sum(const float* part, int parts, int W, int64_t D, float* dw, float* db) {
+    __shared__ float sh[64];
     const int64_t c0 = (int64_t)blockIdx.x * 16;
     const float s = sum_parts16(part, parts, (W + 1) * D, c0, sh);
     const int64_t i = c0 + threadIdx.x;
@@ -371,7 +371,7 @@ template <typename T> int bwd_vec(int64_t D) {
 // the chip's 1,024 SIMDs without two waves each: fewer tokens re-read against more waves in flight.
 int fwd_run(const SeqView& s, unsigned cblocks) {
     if (!s.cu && s.T <= 16) return s.T > 0 ? s.T : 1;
-    return (int64_t)s.total * cblocks >= 2048 * 32 ? 32 : 8;
+    return (int64_t)s.total * cblocks >= 2048 * 16 ? 16 : 8;
 }
 
 template <typename T, typename TW, int W, int VEC>
@@ -400,7 +400,7 @@ hipError_t fwd_t(const ConvArgs& a, hipStream_t st) {
 // Tokens per wave in the gradient: about 4,096 waves in all, in steps of 8 tokens from 16 to 256: longer
 // runs re-read less and leave fewer partial sums.
 int bwd_run(int64_t total, unsigned cblocks) {
-    const int64_t r = (total * cblocks / 4096 + 7) / 8 * 8;
+    const int64_t r = (total * cblocks / 16384 + 7) / 8 * 8;
     return (int)(r < 16 ? 16 : (r > 256 ? 256 : r));
 }
 int bwd_parts(int64_t total, int run) { return (int)((total + (int64_t)run * kWaves - 1) / ((int64_t)run * kWaves)); }
@@ -417,7 +417,7 @@ hipError_t bwd_v(const ConvArgs& a, hipStream_t st) {
         if (a.D % VEC) hipLaunchKernelGGL((k_conv_bwd<(VEC > 1), T, TW, W, VEC, 4>), grid, dim3(kThreads), 0, st, a, run, parts, part);
         else hipLaunchKernelGGL((k_conv_bwd<false, T, TW, W, VEC, 4>), grid, dim3(kThreads), 0, st, a, run, parts, part);
     }
-    hipLaunchKernelGGL(k_conv_dw_sum, dim3((unsigned)(((W + 1) * a.D + 15) / 16)), dim3(1024), 0, st, part, parts, W, a.D, a.dw, a.db);
+    hipLaunchKernelGGL(k_conv_dw_sum, dim3((unsigned)(((W + 1) * a.D + 15) / 16)), dim3(kThreads), 0, st, part, parts, W, a.D, a.dw, a.db);
     return hipGetLastError();
 }
 template <typename T, typename TW, int W>
