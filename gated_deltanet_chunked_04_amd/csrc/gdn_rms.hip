@@ -3,68 +3,319 @@
 //   r = x + residual (rounded to the input's type: the value the stream keeps is the value that is
 //       normed, so the gradient sees what the forward saw),
 //   y = r w / sqrt(mean(r^2) + eps),
-//   8 bits: scale = max|y| / 448 over a row or over 128 columns (1 where all are zero),
+//   8 bits: scale = max|y| / 448 over a row or over 128 columns (at least 2^-126; 1 where all are zero),
 //           q = e4m3(y / scale), from the fp32 y.
 // Gradient, with rh = r / sqrt(mean(r^2) + eps) and u = w dy:
 //   dr = (u - rh mean(u rh)) / sqrt(mean(r^2) + eps) + d_residual,  dw = sum over rows of dy rh.
+//
+// Bound by memory (about 6 operations per element forward and 10 backward against 7 or 8 bytes in
+// bf16), so a row is read once and stays in registers between its sum and its output: a lane owns
+// vectors of 8 neighbouring columns, a row belongs to one wave (up to 2,048 columns) or to one
+// workgroup. 16 lanes that sit side by side own 128 columns, so the maximum behind a scale of 128 columns is
+// taken inside a row of 16 lanes. Rows too long for a workgroup's registers are read again.
 #include "gdn_layer.h"
+#include "gdn_vec.h"
 
 namespace gdn {
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSumRows = 64;  // rows per partial sum of dw
 constexpr float kE4m3Max = 448.f;
 
-// Sum over the workgroup, the same bits for every thread.
-__device__ __forceinline__ float block_sum(float v, float* sh) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float s = 0.f;
-    for (int i = 0; i < kThreads / 64; ++i) s += sh[i];
-    return s;
-}
-// Largest bit pattern over the workgroup (of absolute values: NaN above infinity above the rest).
-__device__ __forceinline__ uint32_t block_umax(uint32_t v, uint32_t* sh) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-    __syncthreads();
-    uint32_t s = 0;
-    for (int i = 0; i < kThreads / 64; ++i) s = max(s, sh[i]);
-    return s;
-}
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-// e4m3 (OCP) of v, to nearest even, clamped to +-448; NaN stays NaN.
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-    v = v > kE4m3Max ? kE4m3Max : (v < -kE4m3Max ? -kE4m3Max : v);
-    return (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xFF);
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, kCtrl, 0xF, 0xF, true);
+}
+// Largest over the 16 lanes of a row, to each of them (bit patterns of absolute values: NaN above
+// infinity above the rest).
+__device__ __forceinline__ uint32_t umax_ln(uint32_t x) {
+    x = max(x, dpp_u<0xB1>(x));
+    x = max(x, dpp_u<0x4E>(x));
+    x = max(x, dpp_u<0x141>(x));
+    return max(x, dpp_u<0x140>(x));
+}
+
+// Sum (or largest) over the lanes of a row: a wave, or the workgroup's LANES / 64 waves through LDS. The
+// same bits in every lane. `slot`: which of the kernel's LDS words this call uses (two calls in a row use
+// different ones, so one barrier per call is enough).
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v, float (*sh)[LANES / 64], int slot) {
+    v = sum_rows(sum_ln(v));
+    if constexpr (LANES > 64) {
+        if ((threadIdx.x & 63) == 0) sh[slot][threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < LANES / 64; ++i) v += sh[slot][i];
+    }
+    return v;
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t row_umax(uint32_t v, float (*sh)[LANES / 64], int slot) {
+    v = umax_ln(v);
+    v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+    v = max(v, (uint32_t)__shfl_xor((int)v, 32));
+    if constexpr (LANES > 64) {
+        if ((threadIdx.x & 63) == 0) sh[slot][threadIdx.x >> 6] = __uint_as_float(v);
+        __syncthreads();
+        v = 0;
+#pragma unroll
+        for (int i = 0; i < LANES / 64; ++i) v = max(v, __float_as_uint(sh[slot][i]));
+    }
+    return v;
+}
+
+// Two values in e4m3 (OCP), to nearest even, clamped to +-448; NaN stays NaN.
+__device__ __forceinline__ float clamp_e4m3(float v) {
+    return v > kE4m3Max ? kE4m3Max : (v < -kE4m3Max ? -kE4m3Max : v);
+}
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(a), clamp_e4m3(b), 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(c), clamp_e4m3(d), w, true);
+}
+__device__ __forceinline__ float scale_of(uint32_t amax_bits) {
+    if (amax_bits == 0) return 1.f;
+    const float s = __uint_as_float(amax_bits) / kE4m3Max;
+    return s < 0x1p-126f ? 0x1p-126f : s;  // its reciprocal stays finite (NaN stays NaN)
+}
+
+// 8 bytes of 8-bit values, of which the lane owns those from `skip` on.
+template <bool kOdd>
+__device__ __forceinline__ void store_e4m3(uint8_t* p, uint32_t lo, uint32_t hi, int skip) {
+    if (!kOdd || skip == 0) {
+        typedef uint32_t words __attribute__((ext_vector_type(2), aligned(1)));
+        __builtin_nontemporal_store(words{lo, hi}, reinterpret_cast<words*>(p));
+        return;
+    }
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+        if (i >= skip) p[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+}
+
+// A row's lane holds vectors at columns 8 (v LANES + lane), v < NV. Its first columns may belong to the
+// lane before (Lane): they count for nothing in sums and maxima.
+template <bool kOdd>
+__device__ __forceinline__ float own(float x, int i, int skip) { return kOdd && i < skip ? 0.f : x; }
+
+enum { kPlain = 0, kRowScale = 1, kGroupScale = 2 };
+
+// One row per LANES threads; LANES = 64 puts four rows in a workgroup of 256, else a row has the workgroup.
+template <bool kOdd, typename T, typename TW, int LANES, int NV, int OUT>
+__global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_fwd(RmsArgs p) {
+    __shared__ float sh[2][LANES / 64];
+    constexpr int kRows = LANES == 64 ? kThreads / 64 : 1;
+    const int lane = threadIdx.x % LANES;
+    const int64_t row = LANES == 64 ? (int64_t)blockIdx.x * kRows + wave_id() : (int64_t)blockIdx.x;
+    if (row >= p.rows) return;  // whole waves, and with LANES > 64 never
+    const int64_t base = row * p.D;
+    Raw<T, 8> r[NV], s[NV];
+    Raw<TW, 8> w[NV];
+    int skip[NV];
+    int64_t at[NV];
+    bool live[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int64_t c0 = 8 * ((int64_t)v * LANES + lane);
+        const Lane ln(c0, p.D, 8);
+        live[v] = c0 < p.D;
+        at[v] = ln.at;
+        skip[v] = ln.skip;
+        r[v].clear();
+        s[v].clear();
+        w[v].clear();
+        if (live[v]) {
+            r[v] = load_raw<T, 8>(static_cast<const T*>(p.x) + base + at[v]);
+            if (p.res) s[v] = load_raw<T, 8>(static_cast<const T*>(p.res) + base + at[v]);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        if (live[v]) w[v] = load_raw<TW, 8>(static_cast<const TW*>(p.w) + at[v]);
+    float ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        float a[8];
+        if (p.res) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = r[v].get(i) + s[v].get(i);
+            r[v].set(a);
+            if (live[v]) store_own<kOdd, T, 8>(static_cast<T*>(p.res_out) + base + at[v], r[v], skip[v]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = own<kOdd>(r[v].get(i), i, skip[v]);
+            ss = fmaf(x, x, ss);
+        }
+    }
+    const float rstd = 1.f / sqrtf(row_sum<LANES>(ss, sh, 0) / (float)p.D + p.eps);
+    if constexpr (OUT == kPlain) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = r[v].get(i) * rstd * w[v].get(i);
+            if (live[v]) store_own<kOdd, T, 8>(static_cast<T*>(p.y) + base + at[v], y, skip[v]);
+        }
+    } else {
+        float scale[NV];
+        uint32_t top = 0;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            uint32_t m = 0;
+            if (live[v])
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = max(m, abs_bits(own<kOdd>(r[v].get(i) * rstd * w[v].get(i), i, skip[v])));
+            if constexpr (OUT == kGroupScale) {
+                scale[v] = scale_of(umax_ln(m));
+                if (live[v] && (lane & 15) == 0)
+                    p.scale[row * ((p.D + 127) / 128) + (v * LANES + lane) / 16] = scale[v];
+            } else {
+                top = max(top, m);
+            }
+        }
+        if constexpr (OUT == kRowScale) {
+            const float sc = scale_of(row_umax<LANES>(top, sh, 1));
+#pragma unroll
+            for (int v = 0; v < NV; ++v) scale[v] = sc;
+            if (lane == 0) p.scale[row] = sc;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            // one quotient and eight products: off from eight quotients by half a step of the fp32 y, far
+            // below the 8-bit values' steps
+            const float inv = 1.f / scale[v];
+            float q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = r[v].get(i) * rstd * w[v].get(i) * inv;
+            if (live[v])
+                store_e4m3<kOdd>(static_cast<uint8_t*>(p.y) + base + at[v], pack_e4m3(q[0], q[1], q[2], q[3]),
+                                 pack_e4m3(q[4], q[5], q[6], q[7]), skip[v]);
+        }
+    }
+}
+
+// Gradient: the workgroup's rows one after the other (a row per wave, or per workgroup), each lane adding its
+// columns' dy rh in registers; at the end the workgroup's waves add theirs in LDS where they hold the same
+// columns, and part[blockIdx.x] gets them.
+template <bool kOdd, typename T, typename TW, int LANES, int NV>
+__global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_bwd(RmsArgs p, float* part) {
+    constexpr int kRows = LANES == 64 ? kThreads / 64 : 1;
+    __shared__ float sh[4][LANES / 64];
+    __shared__ float shw[LANES == 64 ? (kRows - 1) * 64 * 8 * NV : 1];
+    const int lane = threadIdx.x % LANES;
+    int skip[NV];
+    int64_t at[NV];
+    bool live[NV];
+    Raw<TW, 8> w[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int64_t c0 = 8 * ((int64_t)v * LANES + lane);
+        const Lane ln(c0, p.D, 8);
+        live[v] = c0 < p.D;
+        at[v] = live[v] ? ln.at : 0;
+        skip[v] = ln.skip;
+        w[v].clear();
+        if (live[v]) w[v] = load_raw<TW, 8>(static_cast<const TW*>(p.w) + at[v]);
+    }
+    float dw[NV][8] = {};
+    int slot = 0;
+    const int64_t first = LANES == 64 ? (int64_t)blockIdx.x * kRows + wave_id() : (int64_t)blockIdx.x;
+    for (int64_t row = first; row < p.rows; row += (int64_t)gridDim.x * kRows) {
+        const int64_t base = row * p.D;
+        Raw<T, 8> r[NV], d[NV], s[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            r[v].clear();
+            d[v].clear();
+            s[v].clear();
+            if (live[v]) {
+                r[v] = load_raw<T, 8>(static_cast<const T*>(p.x) + base + at[v]);
+                d[v] = load_raw<T, 8>(static_cast<const T*>(p.d_y) + base + at[v]);
+                if (p.d_res) s[v] = load_raw<T, 8>(static_cast<const T*>(p.d_res) + base + at[v]);
+            }
+        }
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float x = own<kOdd>(r[v].get(i), i, skip[v]);
+                ss = fmaf(x, x, ss);
+                dot = fmaf(d[v].get(i) * w[v].get(i), x, dot);
+            }
+        ss = row_sum<LANES>(ss, sh, slot);
+        dot = row_sum<LANES>(dot, sh, slot + 1);
+        slot ^= 2;
+        const float rstd = 1.f / sqrtf(ss / (float)p.D + p.eps);
+        const float m = dot * rstd / (float)p.D;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float rh = r[v].get(i) * rstd;
+                dw[v][i] = fmaf(d[v].get(i), rh, dw[v][i]);
+                o[i] = rstd * (d[v].get(i) * w[v].get(i) - rh * m);
+            }
+            if (p.d_res)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] += s[v].get(i);
+            if (live[v]) store_own<kOdd, T, 8>(static_cast<T*>(p.dx) + base + at[v], o, skip[v]);
+        }
+    }
+    if (!p.dw) return;
+    if constexpr (LANES == 64) {
+        const int wave = wave_id();
+        if (wave > 0)
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) shw[(((wave - 1) * NV + v) * 8 + i) * 64 + lane] = dw[v][i];
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int k = 0; k < kRows - 1; ++k)
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dw[v][i] += shw[((k * NV + v) * 8 + i) * 64 + lane];
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        if (live[v]) store_own<kOdd, float, 8>(part + (int64_t)blockIdx.x * p.D + at[v], dw[v], skip[v]);
+}
+
+__global__ __launch_bounds__(kThreads) void k_rms_dw_sum(const float* part, int parts, int64_t D, float* dw) {
+    __shared__ float sh[64];
+    const int64_t c0 = (int64_t)blockIdx.x * 16;
+    const float s = sum_parts16(part, parts, D, c0, sh);
+    if (threadIdx.x < 16 && c0 + threadIdx.x < D) dw[c0 + threadIdx.x] = s;
+}
+
+// ---- rows of any length, element by element: fewer than 8 columns, or more than a workgroup's registers hold.
+constexpr int kLoopThreads = 1024;
+constexpr int kSlots = kLoopThreads / 64;
+
+__device__ __forceinline__ float loop_sum(float v, float (*sh)[kSlots]) {
+    const float s = row_sum<kLoopThreads>(v, sh, 0);
+    __syncthreads();
+    return s;
 }
 
 template <typename T, typename TW, bool kQuant>
-__global__ __launch_bounds__(kThreads) void k_rms_fwd(RmsArgs p) {
-    __shared__ float sh[kThreads / 64];
-    __shared__ uint32_t shu[kThreads / 64];
+__global__ __launch_bounds__(kLoopThreads) void k_rms_fwd_loop(RmsArgs p) {
+    __shared__ float sh[1][kSlots];
     const int64_t base = (int64_t)blockIdx.x * p.D;
     const T* x = static_cast<const T*>(p.x) + base;
     const T* res = p.res ? static_cast<const T*>(p.res) + base : nullptr;
     const TW* w = static_cast<const TW*>(p.w);
-    T* keep = p.res_out ? static_cast<T*>(p.res_out) + base : nullptr;
-    auto value = [&](int64_t c) {
-        float v = Elem<T>::to_f(x[c]);
-        return v;
-    };
-    // the sum is formed once and kept: later reads come from the stream's new value
-    const T* r = keep ? keep : x;
+    T* keep = p.res ? static_cast<T*>(p.res_out) + base : nullptr;
     float ss = 0.f;
-    for (int64_t c = threadIdx.x; c < p.D; c += kThreads) {
-        float v = value(c);
+    for (int64_t c = threadIdx.x; c < p.D; c += kLoopThreads) {
+        float v = Elem<T>::to_f(x[c]);
         if (res) {
             const T q = Elem<T>::from_f(v + Elem<T>::to_f(res[c]));
             keep[c] = q;
@@ -72,29 +323,36 @@ __global__ __launch_bounds__(kThreads) void k_rms_fwd(RmsArgs p) {
         }
         ss = fmaf(v, v, ss);
     }
-    const float rstd = 1.f / sqrtf(block_sum(ss, sh) / (float)p.D + p.eps);
+    const float rstd = 1.f / sqrtf(loop_sum(ss, sh) / (float)p.D + p.eps);  // (a barrier: keep is complete)
+    const T* r = res ? keep : x;
     auto norm = [&](int64_t c) { return Elem<T>::to_f(r[c]) * rstd * Elem<TW>::to_f(w[c]); };
     if constexpr (!kQuant) {
         T* y = static_cast<T*>(p.y) + base;
-        for (int64_t c = threadIdx.x; c < p.D; c += kThreads) y[c] = Elem<T>::from_f(norm(c));
+        for (int64_t c = threadIdx.x; c < p.D; c += kLoopThreads) y[c] = Elem<T>::from_f(norm(c));
     } else {
         uint8_t* y = static_cast<uint8_t*>(p.y) + base;
         const int64_t G = p.group, groups = (p.D + G - 1) / G;
-        for (int64_t i = 0; i < groups; ++i) {
-            const int64_t c1 = (i + 1) * G < p.D ? (i + 1) * G : p.D;
+        // a wave per group of 128 columns; a whole row by the workgroup
+        const bool by_wave = G == 128;
+        const int n = by_wave ? 64 : kLoopThreads, id = by_wave ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+        for (int64_t g = by_wave ? wave_id() : 0; g < groups; g += by_wave ? kSlots : 1) {
+            const int64_t c1 = (g + 1) * G < p.D ? (g + 1) * G : p.D;
             uint32_t m = 0;
-            for (int64_t c = i * G + threadIdx.x; c < c1; c += kThreads) m = max(m, abs_bits(norm(c)));
-            const float amax = __uint_as_float(block_umax(m, shu));
-            const float scale = amax == 0.f ? 1.f : amax / kE4m3Max;
-            for (int64_t c = i * G + threadIdx.x; c < c1; c += kThreads) y[c] = to_e4m3(norm(c) / scale);
-            if (threadIdx.x == 0) p.scale[(int64_t)blockIdx.x * groups + i] = scale;
+            for (int64_t c = g * G + id; c < c1; c += n) m = max(m, abs_bits(norm(c)));
+            m = by_wave ? row_umax<64>(m, nullptr, 0) : row_umax<kLoopThreads>(m, sh, 0);
+            const float scale = scale_of(m), inv = 1.f / scale;
+            for (int64_t c = g * G + id; c < c1; c += n) {
+                const float q = norm(c) * inv;
+                y[c] = (uint8_t)pack_e4m3(q, q, q, q);
+            }
+            if (id == 0) p.scale[(int64_t)blockIdx.x * groups + g] = scale;
         }
     }
 }
 
 template <typename T, typename TW>
-__global__ __launch_bounds__(kThreads) void k_rms_dx(RmsArgs p, float* rstds) {
-    __shared__ float sh[kThreads / 64];
+__global__ __launch_bounds__(kLoopThreads) void k_rms_dx_loop(RmsArgs p, float* rstds) {
+    __shared__ float sh[1][kSlots];
     const int64_t base = (int64_t)blockIdx.x * p.D;
     const T* r = static_cast<const T*>(p.x) + base;
     const T* dy = static_cast<const T*>(p.d_y) + base;
@@ -102,14 +360,14 @@ __global__ __launch_bounds__(kThreads) void k_rms_dx(RmsArgs p, float* rstds) {
     const TW* w = static_cast<const TW*>(p.w);
     T* dx = static_cast<T*>(p.dx) + base;
     float ss = 0.f, dot = 0.f;
-    for (int64_t c = threadIdx.x; c < p.D; c += kThreads) {
+    for (int64_t c = threadIdx.x; c < p.D; c += kLoopThreads) {
         const float v = Elem<T>::to_f(r[c]);
         ss = fmaf(v, v, ss);
         dot = fmaf(Elem<T>::to_f(dy[c]) * Elem<TW>::to_f(w[c]), v, dot);
     }
-    const float rstd = 1.f / sqrtf(block_sum(ss, sh) / (float)p.D + p.eps);
-    const float m = block_sum(dot, sh) * rstd / (float)p.D;
-    for (int64_t c = threadIdx.x; c < p.D; c += kThreads) {
+    const float rstd = 1.f / sqrtf(loop_sum(ss, sh) / (float)p.D + p.eps);
+    const float m = loop_sum(dot, sh) * rstd / (float)p.D;
+    for (int64_t c = threadIdx.x; c < p.D; c += kLoopThreads) {
         const float rh = Elem<T>::to_f(r[c]) * rstd;
         float d = rstd * (Elem<T>::to_f(dy[c]) * Elem<TW>::to_f(w[c]) - rh * m);
         if (dres) d += Elem<T>::to_f(dres[c]);
@@ -118,54 +376,129 @@ __global__ __launch_bounds__(kThreads) void k_rms_dx(RmsArgs p, float* rstds) {
     if (threadIdx.x == 0) rstds[blockIdx.x] = rstd;
 }
 
+constexpr int kLoopSumRows = 64;  // rows per partial sum of dw behind k_rms_dx_loop
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_rms_dw(RmsArgs p, const float* rstds, float* part) {
-    const int64_t c = (int64_t)blockIdx.y * kThreads + threadIdx.x;
+__global__ __launch_bounds__(kThreads) void k_rms_dw_loop(RmsArgs p, const float* rstds, float* part) {
+    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (c >= p.D) return;
-    const int64_t r0 = (int64_t)blockIdx.x * kSumRows, r1 = r0 + kSumRows < p.rows ? r0 + kSumRows : p.rows;
+    const int64_t r0 = (int64_t)blockIdx.y * kLoopSumRows, r1 = r0 + kLoopSumRows < p.rows ? r0 + kLoopSumRows : p.rows;
     float s = 0.f;
     for (int64_t i = r0; i < r1; ++i)
         s = fmaf(Elem<T>::to_f(static_cast<const T*>(p.d_y)[i * p.D + c]),
                  Elem<T>::to_f(static_cast<const T*>(p.x)[i * p.D + c]) * rstds[i], s);
-    part[(int64_t)blockIdx.x * p.D + c] = s;
+    part[(int64_t)blockIdx.y * p.D + c] = s;
 }
 
-__global__ __launch_bounds__(kThreads) void k_rms_dw_sum(const float* part, int64_t parts, int64_t D, float* dw) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= D) return;
-    float s = 0.f;
-    for (int64_t i = 0; i < parts; ++i) s += part[i * D + c];
-    dw[c] = s;
-}
+// ---- launches -----------------------------------------------------------------------------
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-int64_t parts_of(int64_t rows) { return (rows + kSumRows - 1) / kSumRows; }
 
+// Lanes and vectors of a row: a wave up to 2,048 columns (four vectors a lane), then a workgroup of 256, then
+// of 1,024 up to 32,768 columns; 0: by elements. Few rows take the workgroup from 1,024 columns on: a row is
+// read by four waves at once, and nothing else would use them.
+struct Shape {
+    int lanes, nv;
+};
+Shape shape_of(int64_t D, int64_t rows) {
+    if (D < 8 || D > 32768) return {0, 0};
+    auto nv = [&](int lanes) { const int64_t n = (D + 8 * lanes - 1) / (8 * lanes); return (int)(n <= 1 ? 1 : (n <= 2 ? 2 : 4)); };
+    if (D <= 512 || (D <= 2048 && rows > 1024)) return {64, nv(64)};
+    if (D <= 8192) return {256, nv(256)};
+    return {1024, nv(1024)};
+}
+// The gradient's: its sums of dw double the registers a column takes, so 512 lanes and four vectors are the most.
+Shape bwd_shape_of(int64_t D, int64_t rows) {
+    if (D > 16384) return {0, 0};
+    return D > 8192 ? Shape{512, 4} : shape_of(D, rows);
+}
+
+template <bool kOdd, typename T, typename TW, int OUT>
+hipError_t fwd_o(const RmsArgs& a, hipStream_t st) {
+    const Shape s = shape_of(a.D, a.rows);
+#define GDN_RMS_FWD(LANES, NV)                                                                              \
+    if (s.lanes == LANES && s.nv == NV) {                                                                   \
+        constexpr int kRows = LANES == 64 ? kThreads / 64 : 1;                                              \
+        hipLaunchKernelGGL((k_rms_fwd<kOdd, T, TW, LANES, NV, OUT>), dim3((unsigned)((a.rows + kRows - 1) / kRows)), \
+                           dim3(LANES > kThreads ? LANES : kThreads), 0, st, a);                            \
+        return hipGetLastError();                                                                           \
+    }
+    GDN_RMS_FWD(64, 1)
+    GDN_RMS_FWD(64, 2)
+    GDN_RMS_FWD(64, 4)
+    GDN_RMS_FWD(256, 1)
+    GDN_RMS_FWD(256, 2)
+    GDN_RMS_FWD(256, 4)
+    GDN_RMS_FWD(1024, 2)
+    GDN_RMS_FWD(1024, 4)
+#undef GDN_RMS_FWD
+    hipLaunchKernelGGL((k_rms_fwd_loop<T, TW, OUT != kPlain>), dim3((unsigned)a.rows), dim3(kLoopThreads), 0, st, a);
+    return hipGetLastError();
+}
 template <typename T, typename TW>
 hipError_t fwd_t(const RmsArgs& a, int out, hipStream_t st) {
     if (a.rows == 0) return hipSuccess;
-    if (out == 0) hipLaunchKernelGGL((k_rms_fwd<T, TW, false>), dim3((unsigned)a.rows), dim3(kThreads), 0, st, a);
-    else hipLaunchKernelGGL((k_rms_fwd<T, TW, true>), dim3((unsigned)a.rows), dim3(kThreads), 0, st, a);
-    return hipGetLastError();
+    const bool odd = a.D % 8;
+    if (out == 0) return odd ? fwd_o<true, T, TW, kPlain>(a, st) : fwd_o<false, T, TW, kPlain>(a, st);
+    if (a.group == 128) return odd ? fwd_o<true, T, TW, kGroupScale>(a, st) : fwd_o<false, T, TW, kGroupScale>(a, st);
+    return odd ? fwd_o<true, T, TW, kRowScale>(a, st) : fwd_o<false, T, TW, kRowScale>(a, st);
 }
 
+// Workgroups of the gradient, each with its own partial sums of dw: four to each of the 256 compute units, or
+// fewer where there are fewer rows.
+int64_t bwd_groups(int64_t rows, const Shape& s) {
+    const int64_t per = s.lanes == 64 ? kThreads / 64 : 1, most = s.lanes == 512 ? 512 : 1024;
+    const int64_t n = (rows + per - 1) / per;
+    return n < most ? n : most;
+}
+int64_t loop_parts(int64_t rows) { return (rows + kLoopSumRows - 1) / kLoopSumRows; }
+
+template <bool kOdd, typename T, typename TW>
+hipError_t bwd_o(const RmsArgs& a, hipStream_t st) {
+    const Shape s = bwd_shape_of(a.D, a.rows);
+    int64_t parts = 0;
+    float* part = reinterpret_cast<float*>(a.ws);
+    if (a.rows && s.lanes) {
+        parts = bwd_groups(a.rows, s);
+        bool done = false;
+#define GDN_RMS_BWD(LANES, NV)                                                                              \
+        if (s.lanes == LANES && s.nv == NV) {                                                               \
+            hipLaunchKernelGGL((k_rms_bwd<kOdd, T, TW, LANES, NV>), dim3((unsigned)parts),                  \
+                               dim3(LANES > kThreads ? LANES : kThreads), 0, st, a, part);                  \
+            done = true;                                                                                    \
+        }
+        GDN_RMS_BWD(64, 1)
+        GDN_RMS_BWD(64, 2)
+        GDN_RMS_BWD(64, 4)
+        GDN_RMS_BWD(256, 1)
+        GDN_RMS_BWD(256, 2)
+        GDN_RMS_BWD(256, 4)
+        GDN_RMS_BWD(512, 4)
+#undef GDN_RMS_BWD
+        if (!done) return hipErrorInvalidValue;
+    } else if (a.rows) {
+        float* rstds = part;
+        part = reinterpret_cast<float*>(a.ws + align256((size_t)a.rows * 4));
+        parts = loop_parts(a.rows);
+        hipLaunchKernelGGL((k_rms_dx_loop<T, TW>), dim3((unsigned)a.rows), dim3(kLoopThreads), 0, st, a, rstds);
+        const unsigned cb = (unsigned)((a.D + kThreads - 1) / kThreads);
+        if (a.dw) hipLaunchKernelGGL((k_rms_dw_loop<T>), dim3(cb, (unsigned)parts), dim3(kThreads), 0, st, a, rstds, part);
+    }
+    if (a.dw)
+        hipLaunchKernelGGL(k_rms_dw_sum, dim3((unsigned)((a.D + 15) / 16)), dim3(kThreads), 0, st, part, (int)parts, a.D, a.dw);
+    return hipGetLastError();
+}
 template <typename T, typename TW>
 hipError_t bwd_t(const RmsArgs& a, hipStream_t st) {
-    float* rstds = reinterpret_cast<float*>(a.ws);
-    float* part = reinterpret_cast<float*>(a.ws + align256((size_t)a.rows * 4));
-    const int64_t parts = parts_of(a.rows);
-    const unsigned cb = (unsigned)((a.D + kThreads - 1) / kThreads);
-    if (a.rows) {
-        hipLaunchKernelGGL((k_rms_dx<T, TW>), dim3((unsigned)a.rows), dim3(kThreads), 0, st, a, rstds);
-        if (a.dw) hipLaunchKernelGGL((k_rms_dw<T>), dim3((unsigned)parts, cb), dim3(kThreads), 0, st, a, rstds, part);
-    }
-    if (a.dw) hipLaunchKernelGGL(k_rms_dw_sum, dim3(cb), dim3(kThreads), 0, st, part, parts, a.D, a.dw);
-    return hipGetLastError();
+    return a.D % 8 ? bwd_o<true, T, TW>(a, st) : bwd_o<false, T, TW>(a, st);
 }
 
 }  // namespace
 
-size_t rms_bwd_ws(int64_t rows, int64_t D) { return align256((size_t)rows * 4) + (size_t)parts_of(rows) * D * 4; }
+size_t rms_bwd_ws(int64_t rows, int64_t D) {
+    const Shape s = bwd_shape_of(D, rows);
+    if (s.lanes) return (size_t)bwd_groups(rows, s) * D * 4;
+    return align256((size_t)rows * 4) + (size_t)loop_parts(rows) * D * 4;
+}
 
 // dtype, w_dtype: gdn_dtype (0 bf16, 1 fp32); the weight in the type of x or fp32
 hipError_t launch_rms_fwd(const RmsArgs& a, int dtype, int w_dtype, int out, hipStream_t st) {

@@ -429,8 +429,8 @@ gdn_status gdn_short_conv_bwd(const gdn_conv_desc* desc, const void* x, const vo
  *     y = r weight / sqrt(mean(r^2) + eps).
  * With out_type GDN_OUT_E4M3, y holds 8-bit floats (OCP e4m3) and scale their fp32 scales, of a
  * whole row (scale_group 0; scale [rows]) or of every 128 columns (scale_group 128; scale
- * [rows, ceil(D/128)]): scale = max|y| / 448, or 1 where every y is zero, and the 8-bit value is
- * y / scale to nearest even, formed from the fp32 y. A row with NaN or infinity in it gets what
+ * [rows, ceil(D/128)]): scale = max|y| / 448 (at least 2^-126), or 1 where every y is zero, and the
+ * 8-bit value is y / scale to nearest even, formed from the fp32 y. A row with NaN or infinity in it gets what
  * the formulas give: NaN scales where a NaN is among their columns. */
 typedef enum gdn_out_type { GDN_OUT_SAME = 0, GDN_OUT_E4M3 = 1 } gdn_out_type;
 typedef struct gdn_rmsnorm_desc {
