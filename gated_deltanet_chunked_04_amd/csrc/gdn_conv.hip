@@ -340,8 +340,8 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
     store_own<kOdd, float, VEC>(out + W * p.D, db, ln.skip);
 }
 
-__global__ __launch_bounds__(kThreads) void k_conv_dw_sum(const float* part, int parts, int W, int64_t D, float* dw, float* db) {
-    __shared__ float sh[64];
+__global__ __launch_bounds__(kSumThreads) void k_conv_dw_sum(const float* part, int parts, int W, int64_t D, float* dw, float* db) {
+    __shared__ float sh[kSumThreads / 4];
     const int64_t c0 = (int64_t)blockIdx.x * 16;
     const float s = sum_parts16(part, parts, (W + 1) * D, c0, sh);
     const int64_t i = c0 + threadIdx.x;
@@ -417,7 +417,7 @@ hipError_t bwd_v(const ConvArgs& a, hipStream_t st) {
         if (a.D % VEC) hipLaunchKernelGGL((k_conv_bwd<(VEC > 1), T, TW, W, VEC, 4>), grid, dim3(kThreads), 0, st, a, run, parts, part);
         else hipLaunchKernelGGL((k_conv_bwd<false, T, TW, W, VEC, 4>), grid, dim3(kThreads), 0, st, a, run, parts, part);
     }
-    hipLaunchKernelGGL(k_conv_dw_sum, dim3((unsigned)(((W + 1) * a.D + 15) / 16)), dim3(kThreads), 0, st, part, parts, W, a.D, a.dw, a.db);
+    hipLaunchKernelGGL(k_conv_dw_sum, dim3((unsigned)(((W + 1) * a.D + 15) / 16)), dim3(kSumThreads), 0, st, part, parts, W, a.D, a.dw, a.db);
     return hipGetLastError();
 }
 template <typename T, typename TW, int W>

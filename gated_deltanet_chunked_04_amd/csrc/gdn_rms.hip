@@ -223,20 +223,36 @@ __global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_bwd
     float dw[NV][8] = {};
     int slot = 0;
     const int64_t first = LANES == 64 ? (int64_t)blockIdx.x * kRows + wave_id() : (int64_t)blockIdx.x;
-    for (int64_t row = first; row < p.rows; row += (int64_t)gridDim.x * kRows) {
+    // the next row is loaded while the present one is worked on, where both fit the registers of two waves a SIMD
+    constexpr bool kAhead = NV < 4;
+    Raw<T, 8> nr[NV], nd[NV], ns[NV];
+    auto fetch = [&](int64_t row) {
         const int64_t base = row * p.D;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            nr[v].clear();
+            nd[v].clear();
+            ns[v].clear();
+            if (live[v]) {
+                nr[v] = load_raw<T, 8>(static_cast<const T*>(p.x) + base + at[v]);
+                nd[v] = load_raw<T, 8>(static_cast<const T*>(p.d_y) + base + at[v]);
+                if (p.d_res) ns[v] = load_raw<T, 8>(static_cast<const T*>(p.d_res) + base + at[v]);
+            }
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    if (first < p.rows) fetch(first);
+    for (int64_t row = first; row < p.rows; row += step) {
+        const int64_t base = row * p.D;
+        if (!kAhead && row != first) fetch(row);
         Raw<T, 8> r[NV], d[NV], s[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            r[v].clear();
-            d[v].clear();
-            s[v].clear();
-            if (live[v]) {
-                r[v] = load_raw<T, 8>(static_cast<const T*>(p.x) + base + at[v]);
-                d[v] = load_raw<T, 8>(static_cast<const T*>(p.d_y) + base + at[v]);
-                if (p.d_res) s[v] = load_raw<T, 8>(static_cast<const T*>(p.d_res) + base + at[v]);
-            }
+            r[v] = nr[v];
+            d[v] = nd[v];
+            s[v] = ns[v];
         }
+        if (kAhead && row + step < p.rows) fetch(row + step);
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
@@ -288,8 +304,8 @@ __global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_bwd
         if (live[v]) store_own<kOdd, float, 8>(part + (int64_t)blockIdx.x * p.D + at[v], dw[v], skip[v]);
 }
 
-__global__ __launch_bounds__(kThreads) void k_rms_dw_sum(const float* part, int parts, int64_t D, float* dw) {
-    __shared__ float sh[64];
+__global__ __launch_bounds__(kSumThreads) void k_rms_dw_sum(const float* part, int parts, int64_t D, float* dw) {
+    __shared__ float sh[kSumThreads / 4];
     const int64_t c0 = (int64_t)blockIdx.x * 16;
     const float s = sum_parts16(part, parts, D, c0, sh);
     if (threadIdx.x < 16 && c0 + threadIdx.x < D) dw[c0 + threadIdx.x] = s;
@@ -393,28 +409,28 @@ __global__ __launch_bounds__(kThreads) void k_rms_dw_loop(RmsArgs p, const float
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Lanes and vectors of a row: a wave up to 2,048 columns (four vectors a lane), then a workgroup of 256, then
-// of 1,024 up to 32,768 columns; 0: by elements. Few rows take the workgroup from 1,024 columns on: a row is
-// read by four waves at once, and nothing else would use them.
+// Lanes and vectors of a row: a wave up to 512 columns, a workgroup of 256 up to 8,192, one of 1,024 up to
+// 32,768 columns; 0: by elements. (A wave for 2,048 columns, four vectors a lane, was slower: 32,768 rows of
+// them to e4m3 took 85 us against 80, and 5,003 fp32 rows of 1,001 columns 19 against 15.5.)
 struct Shape {
     int lanes, nv;
 };
-Shape shape_of(int64_t D, int64_t rows) {
+Shape shape_of(int64_t D) {
     if (D < 8 || D > 32768) return {0, 0};
     auto nv = [&](int lanes) { const int64_t n = (D + 8 * lanes - 1) / (8 * lanes); return (int)(n <= 1 ? 1 : (n <= 2 ? 2 : 4)); };
-    if (D <= 512 || (D <= 2048 && rows > 1024)) return {64, nv(64)};
+    if (D <= 512) return {64, nv(64)};
     if (D <= 8192) return {256, nv(256)};
     return {1024, nv(1024)};
 }
 // The gradient's: its sums of dw double the registers a column takes, so 512 lanes and four vectors are the most.
-Shape bwd_shape_of(int64_t D, int64_t rows) {
+Shape bwd_shape_of(int64_t D) {
     if (D > 16384) return {0, 0};
-    return D > 8192 ? Shape{512, 4} : shape_of(D, rows);
+    return D > 8192 ? Shape{512, 4} : shape_of(D);
 }
 
 template <bool kOdd, typename T, typename TW, int OUT>
 hipError_t fwd_o(const RmsArgs& a, hipStream_t st) {
-    const Shape s = shape_of(a.D, a.rows);
+    const Shape s = shape_of(a.D);
 #define GDN_RMS_FWD(LANES, NV)                                                                              \
     if (s.lanes == LANES && s.nv == NV) {                                                                   \
         constexpr int kRows = LANES == 64 ? kThreads / 64 : 1;                                              \
@@ -443,18 +459,19 @@ hipError_t fwd_t(const RmsArgs& a, int out, hipStream_t st) {
     return odd ? fwd_o<true, T, TW, kRowScale>(a, st) : fwd_o<false, T, TW, kRowScale>(a, st);
 }
 
-// Workgroups of the gradient, each with its own partial sums of dw: four to each of the 256 compute units, or
-// fewer where there are fewer rows.
+// Workgroups of the gradient, each with its own partial sums of dw: two to each of the 256 compute units, or
+// fewer where there are fewer rows (32,768 rows of 2,048: 98 us; four to each 106, eight 116, for the partial
+// sums grow with them).
 int64_t bwd_groups(int64_t rows, const Shape& s) {
-    const int64_t per = s.lanes == 64 ? kThreads / 64 : 1, most = s.lanes == 512 ? 512 : 1024;
+    const int64_t per = s.lanes == 64 ? kThreads / 64 : 1;
     const int64_t n = (rows + per - 1) / per;
-    return n < most ? n : most;
+    return n < 512 ? n : 512;
 }
 int64_t loop_parts(int64_t rows) { return (rows + kLoopSumRows - 1) / kLoopSumRows; }
 
 template <bool kOdd, typename T, typename TW>
 hipError_t bwd_o(const RmsArgs& a, hipStream_t st) {
-    const Shape s = bwd_shape_of(a.D, a.rows);
+    const Shape s = bwd_shape_of(a.D);
     int64_t parts = 0;
     float* part = reinterpret_cast<float*>(a.ws);
     if (a.rows && s.lanes) {
@@ -484,7 +501,7 @@ hipError_t bwd_o(const RmsArgs& a, hipStream_t st) {
         if (a.dw) hipLaunchKernelGGL((k_rms_dw_loop<T>), dim3(cb, (unsigned)parts), dim3(kThreads), 0, st, a, rstds, part);
     }
     if (a.dw)
-        hipLaunchKernelGGL(k_rms_dw_sum, dim3((unsigned)((a.D + 15) / 16)), dim3(kThreads), 0, st, part, (int)parts, a.D, a.dw);
+        hipLaunchKernelGGL(k_rms_dw_sum, dim3((unsigned)((a.D + 15) / 16)), dim3(kSumThreads), 0, st, part, (int)parts, a.D, a.dw);
     return hipGetLastError();
 }
 template <typename T, typename TW>
@@ -495,7 +512,7 @@ hipError_t bwd_t(const RmsArgs& a, hipStream_t st) {
 }  // namespace
 
 size_t rms_bwd_ws(int64_t rows, int64_t D) {
-    const Shape s = bwd_shape_of(D, rows);
+    const Shape s = bwd_shape_of(D);
     if (s.lanes) return (size_t)bwd_groups(rows, s) * D * 4;
     return align256((size_t)rows * 4) + (size_t)loop_parts(rows) * D * 4;
 }

@@ -82,21 +82,24 @@ __device__ __forceinline__ void store_own(T* p, const float (&x)[N], int skip) {
     store_own<kOdd, T, N>(p, r, skip);
 }
 
-// Sum over `parts` rows of partial sums [parts, n] for columns c0 .. c0+15, by a workgroup of 256
-// threads: 16 rows at a time, 16 lanes on the columns of each, then a tree over the rows in LDS. The
-// order of the additions depends on `parts` alone. Threads 0..15 get the sums of columns c0 + threadIdx.x.
+// Sum over `parts` rows of partial sums [parts, n] for columns c0 .. c0+15, by a workgroup of
+// kSumThreads: 32 rows at a time, 16 lanes on the columns of each, eight loads in flight per lane, then a
+// tree over the rows in LDS (`sh`: kSumThreads / 4 words). The order of the additions depends on `parts`
+// alone. Threads 0..15 get the sums of columns c0 + threadIdx.x.
+constexpr int kSumThreads = 512;
 __device__ __forceinline__ float sum_parts16(const float* part, int parts, int64_t n, int64_t c0, float* sh) {
+    constexpr int kRows = kSumThreads / 16, kAhead = 8;
     const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
-    float s[4] = {};
+    float s[kAhead] = {};
     if (c0 + col < n) {
         const float* p = part + c0 + col;
         int i = row;
-        for (; i + 48 < parts; i += 64)
+        for (; i + (kAhead - 1) * kRows < parts; i += kAhead * kRows)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) s[u] += p[(int64_t)(i + 16 * u) * n];
-        for (; i < parts; i += 16) s[0] += p[(int64_t)i * n];
+            for (int u = 0; u < kAhead; ++u) s[u] += p[(int64_t)(i + kRows * u) * n];
+        for (; i < parts; i += kRows) s[0] += p[(int64_t)i * n];
     }
-    float v = (s[0] + s[1]) + (s[2] + s[3]);
+    float v = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
     // a wave holds 4 rows of 16 columns
     v += __shfl_xor(v, 16);
     v += __shfl_xor(v, 32);
@@ -105,7 +108,7 @@ __device__ __forceinline__ float sum_parts16(const float* part, int parts, int64
     float t = 0.f;
     if (threadIdx.x < 16)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) t += sh[w * 16 + threadIdx.x];
+        for (int w = 0; w < kSumThreads / 64; ++w) t += sh[w * 16 + threadIdx.x];
     return t;
 }
 
