@@ -93,13 +93,14 @@ __device__ void pass_empty(const ConvArgs& p, const void* in, void* out, int64_t
 
 // U: tokens loaded ahead. `run`: tokens per wave.
 template <bool kOdd, typename T, typename TW, int W, int VEC, int U>
-__global__ __launch_bounds__(kThreads) void k_conv_fwd(ConvArgs p, int run, int token_blocks) {
-    const int64_t ch = ((int64_t)blockIdx.x * kWave + (threadIdx.x & 63)) * VEC;
+__global__ __launch_bounds__(kThreads) void k_conv_fwd(ConvArgs p, int run, int token_blocks, int cblocks) {
+    const int block = blockIdx.x / cblocks;  // of tokens
+    const int64_t ch = ((int64_t)(blockIdx.x % cblocks) * kWave + (threadIdx.x & 63)) * VEC;
     if (ch >= p.D) return;
     const Lane ln(ch, p.D, VEC);
     const int64_t c0 = ln.at;
-    if ((int)blockIdx.y == token_blocks) return pass_empty<kOdd, T, VEC>(p, p.s0, p.sT, c0, ln.skip);
-    const int64_t w0l = ((int64_t)blockIdx.y * kWaves + wave_id()) * run;
+    if (block == token_blocks) return pass_empty<kOdd, T, VEC>(p, p.s0, p.sT, c0, ln.skip);
+    const int64_t w0l = ((int64_t)block * kWaves + wave_id()) * run;
     if (w0l >= p.seq.total) return;
     const int32_t w0 = (int32_t)w0l;
     const int32_t w1 = w0l + run < p.seq.total ? w0 + run : p.seq.total;
@@ -169,22 +170,23 @@ __global__ __launch_bounds__(kThreads) void k_conv_fwd(ConvArgs p, int run, int 
 }
 
 // One workgroup: kWaves runs of `run` tokens and 64 VEC channels; the partial sums of dw and dbias over
-// its tokens go to part[blockIdx.y], [W + 1, D] (the taps, then the bias).
+// its tokens go to part[block], [W + 1, D] (the taps, then the bias).
 template <bool kOdd, typename T, typename TW, int W, int VEC, int U>
-__global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int token_blocks, float* part) {
+__global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int token_blocks, int cblocks, float* part) {
     __shared__ float sh[kWaves - 1][(W + 1) * VEC][kWave];
     const int lane = threadIdx.x & 63;
     const int wave = wave_id();
-    const int64_t ch = ((int64_t)blockIdx.x * kWave + lane) * VEC;
+    const int block = blockIdx.x / cblocks;
+    const int64_t ch = ((int64_t)(blockIdx.x % cblocks) * kWave + lane) * VEC;
     const bool live = ch < p.D;
     const Lane ln(ch, p.D, VEC);
     const int64_t c0 = ln.at;
-    if ((int)blockIdx.y == token_blocks) {
+    if (block == token_blocks) {
         if (live) pass_empty<kOdd, T, VEC>(p, p.d_sT, p.ds0, c0, ln.skip);
         return;
     }
     float dw[W][VEC] = {}, db[VEC] = {};
-    const int64_t w0l = ((int64_t)blockIdx.y * kWaves + wave) * run;
+    const int64_t w0l = ((int64_t)block * kWaves + wave) * run;
     if (live && w0l < p.seq.total) {
         const int32_t w0 = (int32_t)w0l;
         const int32_t w1 = w0l + run < p.seq.total ? w0 + run : p.seq.total;
@@ -334,7 +336,7 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
             for (int j = 0; j < W; ++j) dw[j][v] += sh[i][j * VEC + v][lane];
             db[v] += sh[i][W * VEC + v][lane];
         }
-    float* out = part + (int64_t)blockIdx.y * (W + 1) * p.D + c0;
+    float* out = part + (int64_t)block * (W + 1) * p.D + c0;
 #pragma unroll
     for (int j = 0; j < W; ++j) store_own<kOdd, float, VEC>(out + j * p.D, dw[j], ln.skip);
     store_own<kOdd, float, VEC>(out + W * p.D, db, ln.skip);
@@ -381,13 +383,14 @@ hipError_t fwd_v(const ConvArgs& a, hipStream_t st) {
     const int tb = (int)(((int64_t)a.seq.total + (int64_t)run * kWaves - 1) / ((int64_t)run * kWaves));
     const int extra = a.sT && (a.seq.cu || a.seq.T == 0);
     if (tb + extra == 0) return hipSuccess;
-    const dim3 grid(cb, (unsigned)(tb + extra));
+    if (!grid_fits((int64_t)cb * (tb + extra), kThreads)) return hipErrorInvalidConfiguration;
+    const dim3 grid(cb * (unsigned)(tb + extra));
     constexpr bool kMayOdd = VEC > 1;
     const bool odd = a.D % VEC;
-    if (run < 8 && odd) hipLaunchKernelGGL((k_conv_fwd<kMayOdd, T, TW, W, VEC, 1>), grid, dim3(kThreads), 0, st, a, run, tb);
-    else if (run < 8) hipLaunchKernelGGL((k_conv_fwd<false, T, TW, W, VEC, 1>), grid, dim3(kThreads), 0, st, a, run, tb);
-    else if (odd) hipLaunchKernelGGL((k_conv_fwd<kMayOdd, T, TW, W, VEC, 8>), grid, dim3(kThreads), 0, st, a, run, tb);
-    else hipLaunchKernelGGL((k_conv_fwd<false, T, TW, W, VEC, 8>), grid, dim3(kThreads), 0, st, a, run, tb);
+    if (run < 8 && odd) hipLaunchKernelGGL((k_conv_fwd<kMayOdd, T, TW, W, VEC, 1>), grid, dim3(kThreads), 0, st, a, run, tb, (int)cb);
+    else if (run < 8) hipLaunchKernelGGL((k_conv_fwd<false, T, TW, W, VEC, 1>), grid, dim3(kThreads), 0, st, a, run, tb, (int)cb);
+    else if (odd) hipLaunchKernelGGL((k_conv_fwd<kMayOdd, T, TW, W, VEC, 8>), grid, dim3(kThreads), 0, st, a, run, tb, (int)cb);
+    else hipLaunchKernelGGL((k_conv_fwd<false, T, TW, W, VEC, 8>), grid, dim3(kThreads), 0, st, a, run, tb, (int)cb);
     return hipGetLastError();
 }
 template <typename T, typename TW, int W>
@@ -412,10 +415,11 @@ hipError_t bwd_v(const ConvArgs& a, hipStream_t st) {
     const int parts = bwd_parts(a.seq.total, run);
     const int extra = a.ds0 && (a.seq.cu || a.seq.T == 0);
     float* part = reinterpret_cast<float*>(a.ws);
-    const dim3 grid(cb, (unsigned)(parts + extra));
+    if (!grid_fits((int64_t)cb * (parts + extra), kThreads)) return hipErrorInvalidConfiguration;
+    const dim3 grid(cb * (unsigned)(parts + extra));
     if (parts + extra) {
-        if (a.D % VEC) hipLaunchKernelGGL((k_conv_bwd<(VEC > 1), T, TW, W, VEC, 4>), grid, dim3(kThreads), 0, st, a, run, parts, part);
-        else hipLaunchKernelGGL((k_conv_bwd<false, T, TW, W, VEC, 4>), grid, dim3(kThreads), 0, st, a, run, parts, part);
+        if (a.D % VEC) hipLaunchKernelGGL((k_conv_bwd<(VEC > 1), T, TW, W, VEC, 4>), grid, dim3(kThreads), 0, st, a, run, parts, (int)cb, part);
+        else hipLaunchKernelGGL((k_conv_bwd<false, T, TW, W, VEC, 4>), grid, dim3(kThreads), 0, st, a, run, parts, (int)cb, part);
     }
     hipLaunchKernelGGL(k_conv_dw_sum, dim3((unsigned)(((W + 1) * a.D + 15) / 16)), dim3(kSumThreads), 0, st, part, parts, W, a.D, a.dw, a.db);
     return hipGetLastError();

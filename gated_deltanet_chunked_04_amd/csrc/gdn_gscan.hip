@@ -3,212 +3,573 @@
 //   mu_t = a_t (dh_t + mu_{t+1}),  dx_t = dh_t + mu_{t+1},  dg_t = mu_t h_{t-1},  dh_0 = mu_1,
 // a = exp(g), mu behind the last token of a sequence = the gradient of its final state.
 //
-// The token axis is cut into tiles. A tile acts on the state that enters it as c -> A c + H, so
-// three launches do it: the pair (A, H) of every tile, a scan over the pairs that leaves every
-// tile's entering state, and the tiles again from their states. The gradient does the same from
-// the other end, with the forward's entering states at hand to recompute h inside a tile in fp32.
+// Bound by memory: 3 operations per element forward and 8 backward, against 8 and 14 bytes (bf16
+// with fp32 gates). So every input is read once, in a single pass over the token axis:
+//   * A workgroup of eight waves holds a tile of tokens by 64 VEC channels in registers, eight tokens
+//     to a wave. A run of tokens acts on the state that enters it as c -> A c + H; the waves' pairs
+//     (A, H) meet in LDS and make the tile's pair.
+//   * The tile publishes its pair, gathers the state that enters it from the tiles before it (look_back),
+//     and each wave runs its tokens again from its own entering state, now with their outputs.
+//   * Tiles are handed out in the order of the token axis by a counter, so a tile only ever waits for
+//     tiles that are running or done, and those publish their pairs before they wait themselves.
+//   * What is added to what is fixed by the tile's place, not by who was ready first, so results are
+//     the same bits every time: the state entering a group of 16 tiles comes from the group before it
+//     as one published value, the tiles inside the group combine the pairs since then.
+// Published words carry their own mark (all ones: not there yet), so no other ordering of memory is
+// needed; a small launch clears them first. The gradient runs the same from the other end, and
+// recomputes h inside its tile in fp32 from the state that the forward kept for every 64th token.
 #include "gdn_layer.h"
+#include "gdn_vec.h"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWaves = 8;              // waves of a tile
+constexpr int kThreads = kWaves * kWave;
+constexpr int kTokens = 8;             // tokens of a wave
+constexpr int kTile = kWaves * kTokens;
+static_assert(kTile == kScanTile, "a kept state per tile");
+constexpr int kGroup = 16;             // tiles between two published entering states
+constexpr int kMaxSpins = 1 << 20;     // (about a second) a wait gives up with NaN rather than hang
 
-// A c + H. A with its sign bit set marks a tile in which a sequence starts: nothing of c passes,
-// whatever it holds. c = 0 passes nothing either, also where growing gates took A to infinity.
+struct Chain {
+    uint32_t* ticket;
+    uint64_t* pairs;  // [tiles, D], in the order of the chain: A in the high word, H in the low one
+    uint32_t* carry;  // [groups, D]: the state that enters the group
+};
+
+// A c + H. A with its sign bit set marks a run in which a sequence starts: nothing of c passes, whatever it
+// holds. c = 0 passes nothing either, also where growing gates took A to infinity.
 __device__ __forceinline__ float pass_on(float A, float H, float c) {
     return (__float_as_int(A) < 0 || c == 0.f) ? H : fmaf(A, c, H);
 }
+// (A, H) followed by (a, h).
+__device__ __forceinline__ void then(float& A, float& H, float a, float h) {
+    H = pass_on(a, h, H);
+    A = __float_as_int(a) < 0 ? a : A * a;
+}
+// Bits that are never all ones.
+__device__ __forceinline__ uint32_t mark(float x) { return x == x ? __float_as_uint(x) : 0x7FC00000u; }
 
-template <typename TX, typename TG, bool kRev>
-__global__ __launch_bounds__(kThreads) void k_pairs(GScanArgs p, float2* pairs) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int32_t t0 = blockIdx.y * kScanTile;
-    const int32_t t1 = min(t0 + kScanTile, p.seq.total);
-    if (c >= p.D) return;
-    const TX* x = static_cast<const TX*>(kRev ? p.d_h : p.x);
-    const TG* g = static_cast<const TG*>(p.g);
+template <typename W>
+__device__ __forceinline__ W peek(const W* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename W>
+__device__ __forceinline__ void publish(W* p, W v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The state that enters place `pos` of the chain in channel c; `first`: the place in which its sequence starts
+// (uniform, < pos). Whole waves call it; `live`: this lane's channel exists.
+__device__ float look_back(const Chain& ch, int64_t D, int64_t c, int pos, int first, bool live) {
+    const int group = pos / kGroup;
+    const int from = first > group * kGroup ? first : group * kGroup;
+    const float lost = __uint_as_float(0x7FC00000u);
     float A = 1.f, H = 0.f;
-    if (!kRev) {
-        SeqPos s = seq_find(p.seq, t0);
-        for (int32_t t = t0; t < t1; ++t) {
+    int spins = 0;
+    for (int k = from; k < pos; k += 8) {
+        uint64_t v[8];
+        for (;;) {
+            bool ok = true;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (k + u < pos) v[u] = live ? peek(ch.pairs + (int64_t)(k + u) * D + c) : 0;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (k + u < pos) ok = ok && v[u] != ~0ull;
+            if (__all(ok)) break;
+            if (++spins > kMaxSpins) return lost;
+            __builtin_amdgcn_s_sleep(1);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (k + u < pos) then(A, H, __uint_as_float((uint32_t)(v[u] >> 32)), __uint_as_float((uint32_t)v[u]));
+    }
+    if (first >= group * kGroup) return H;  // (the first of these pairs holds the sequence's start)
+    for (;;) {
+        const uint32_t v = live ? peek(ch.carry + (int64_t)group * D + c) : 0;
+        if (__all(v != ~0u)) return pass_on(A, H, __uint_as_float(v));
+        if (++spins > kMaxSpins) return lost;
+        __builtin_amdgcn_s_sleep(1);
+    }
+}
+
+// The tile's pair and the state (or adjoint) that enters each of its waves, for channel `c` of the block's
+// thread: agg holds the waves' pairs in LDS, cin receives the entering values. Publishes on the way.
+template <bool kRev, bool kChain, int CH>
+__device__ __forceinline__ void enter_tile(const float2 (*agg)[CH], float (*cin)[CH], const Chain& ch, int64_t D,
+                                           int64_t c, int pos, int tiles, int first) {
+    const int t = threadIdx.x;
+    const bool live = c < D;
+    float2 q[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) q[w] = agg[kRev ? kWaves - 1 - w : w][t];
+    float s = 0.f;
+    if constexpr (kChain) {
+        float A = 1.f, H = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) then(A, H, q[w].x, q[w].y);
+        if (live && pos + 1 < tiles)
+            publish(ch.pairs + (int64_t)pos * D + c, ((uint64_t)__float_as_uint(A) << 32) | mark(H));
+        if (first < pos) s = look_back(ch, D, c, pos, first, live);
+        if (live && (pos + 1) % kGroup == 0 && pos + 1 < tiles)
+            publish(ch.carry + (int64_t)((pos + 1) / kGroup) * D + c, mark(pass_on(A, H, s)));
+    }
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        cin[kRev ? kWaves - 1 - w : w][t] = s;
+        s = pass_on(q[w].x, q[w].y, s);
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_f(const float* p, float (&x)[VEC]) {
+    const Raw<float, VEC> r = load_raw<float, VEC>(p);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) x[v] = r.get(v);
+}
+template <int VEC>
+__device__ __forceinline__ void state_of(const float* s, int32_t n, int64_t D, int64_t c, float (&x)[VEC]) {
+    if (s) {
+        load_f<VEC>(s + (int64_t)n * D + c, x);
+    } else {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) x[v] = 0.f;
+    }
+}
+
+// Sequences without tokens: their state (or its gradient) passes through, by the workgroups behind the tiles.
+template <int VEC>
+__device__ void pass_empty(const GScanArgs& p, const float* in, float* out, int64_t c) {
+    if (c >= p.D) return;
+    for (int32_t n = wave_id(); n < p.seq.N; n += kWaves) {
+        const SeqPos q = seq_at(p.seq, n);
+        if (q.start < q.end) continue;
+        float x[VEC];
+        state_of<VEC>(in, n, p.D, c, x);
+        store_own<false, float, VEC>(out + (int64_t)n * p.D + c, x, 0);
+    }
+}
+
+// This workgroup's item: tile * cblocks + channel block, in the order in which workgroups got here.
+__device__ __forceinline__ int take(const Chain& ch, bool chain, int* sh) {
+    if (!chain) return blockIdx.x;
+    if (threadIdx.x == 0) *sh = (int)__hip_atomic_fetch_add(ch.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*sh);
+}
+
+template <typename TX, typename TG, int VEC, bool kChain>
+__global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, int cblocks, Chain ch) {
+    constexpr int CH = kWave * VEC;
+    __shared__ __attribute__((aligned(16))) float2 agg[kWaves][CH];
+    __shared__ __attribute__((aligned(16))) float cin[kWaves][CH];
+    __shared__ int sh_id, sh_first;
+    const int id = take(ch, kChain, &sh_id);
+    const int tile = id / cblocks, lane = threadIdx.x & 63, wave = wave_id();
+    const int64_t cbase = (int64_t)(id % cblocks) * CH;
+    const int64_t c = cbase + lane * VEC;
+    if (tile == tiles) return pass_empty<VEC>(p, p.s0, p.sT, c);
+    const bool live = c < p.D;
+    const int64_t cl = live ? c : 0;
+    const int64_t w0l = (int64_t)tile * kTile + wave * kTokens;
+    const int32_t w0 = w0l < p.seq.total ? (int32_t)w0l : p.seq.total;
+    const int32_t w1 = p.seq.total - w0 < kTokens ? p.seq.total : w0 + kTokens;
+    Raw<TX, VEC> x[kTokens];
+    Raw<TG, VEC> g[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const int64_t at = (int64_t)min(w0 + i, p.seq.total - 1) * p.D + cl;
+        x[i] = load_raw<TX, VEC>(static_cast<const TX*>(p.x) + at);
+        g[i] = load_raw<TG, VEC>(static_cast<const TG*>(p.g) + at);
+    }
+    const SeqPos s0 = seq_find(p.seq, min(w0, p.seq.total - 1));
+    // all of the wave's tokens inside one sequence, none of them its first
+    const bool inside = w0 > s0.start && w0 + kTokens <= s0.end;
+    if (kChain && threadIdx.x == 0) sh_first = w0 >= s0.start && w0 < s0.end ? s0.start / kTile : tile;
+    float A[VEC], H[VEC], last[VEC] = {};  // last: the entering state of the last sequence that starts here
+    int32_t last_n = -1;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        A[v] = 1.f;
+        H[v] = 0.f;
+    }
+    auto feed = [&](int i) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float a = fast_exp(g[i].get(v));
+            H[v] = fmaf(a, H[v], x[i].get(v));
+            A[v] *= a;
+        }
+    };
+    if (inside) {
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) feed(i);
+    } else {
+        SeqPos s = s0;
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) {
+            const int32_t t = w0 + i;
+            if (t >= w1) break;
             seq_advance(p.seq, s, t);
             if (t < s.start || t >= s.end) continue;
-            const int64_t at = (int64_t)t * p.D + c;
-            const float a = fast_exp(Elem<TG>::to_f(g[at]));
             if (t == s.start) {
-                A = -1.f;
-                H = p.s0 ? p.s0[(int64_t)s.n * p.D + c] : 0.f;
+                last_n = s.n;
+                state_of<VEC>(p.s0, s.n, p.D, cl, last);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    A[v] = -1.f;
+                    H[v] = last[v];
+                }
             }
-            H = fmaf(a, H, Elem<TX>::to_f(x[at]));
-            A *= a;
-        }
-    } else {
-        for (int32_t t = t1 - 1; t >= t0; --t) {
-            const SeqPos s = seq_find(p.seq, t);
-            if (t < s.start || t >= s.end) continue;
-            const int64_t at = (int64_t)t * p.D + c;
-            const float a = fast_exp(Elem<TG>::to_f(g[at]));
-            if (t + 1 == s.end) {
-                A = -1.f;
-                H = p.d_sT ? p.d_sT[(int64_t)s.n * p.D + c] : 0.f;
-            }
-            H = a * (Elem<TX>::to_f(x[at]) + H);
-            A *= a;
+            feed(i);
         }
     }
-    pairs[(int64_t)blockIdx.y * p.D + c] = make_float2(A, H);
-}
-
-template <bool kRev>
-__global__ __launch_bounds__(kThreads) void k_carry(const float2* pairs, float* states, int tiles, int64_t D) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= D) return;
-    float s = 0.f;
-    for (int i = 0; i < tiles; ++i) {
-        const int64_t at = (int64_t)(kRev ? tiles - 1 - i : i) * D + c;
-        states[at] = s;
-        const float2 q = pairs[at];
-        s = pass_on(q.x, q.y, s);
-    }
-}
-
-template <typename TX, typename TG>
-__global__ __launch_bounds__(kThreads) void k_fwd(GScanArgs p) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int32_t t0 = blockIdx.y * kScanTile;
-    const int32_t t1 = min(t0 + kScanTile, p.seq.total);
-    if (c >= p.D) return;
-    const TX* x = static_cast<const TX*>(p.x);
-    const TG* g = static_cast<const TG*>(p.g);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) agg[wave][lane * VEC + v] = make_float2(A[v], H[v]);
+    __syncthreads();
+    if (threadIdx.x < CH)
+        enter_tile<false, kChain, CH>(agg, cin, ch, p.D, cbase + threadIdx.x, tile, tiles, kChain ? __builtin_amdgcn_readfirstlane(sh_first) : tile);
+    __syncthreads();
+    float h[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) h[v] = cin[wave][lane * VEC + v];
+    if (!live || w0 >= w1) return;
+    if (p.states && wave == 0) store_own<false, float, VEC>(p.states + (int64_t)tile * p.D + c, h, 0);
     TX* out = static_cast<TX*>(p.h);
-    float h = p.states[(int64_t)blockIdx.y * p.D + c];
-    SeqPos s = seq_find(p.seq, t0);
-    for (int32_t t = t0; t < t1; ++t) {
+    auto step = [&](int i) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) h[v] = fmaf(fast_exp(g[i].get(v)), h[v], x[i].get(v));
+        if (out) store_own<false, TX, VEC>(out + (int64_t)(w0 + i) * p.D + c, h, 0);
+    };
+    if (inside) {
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) step(i);
+        if (p.sT && w1 == s0.end) store_own<false, float, VEC>(p.sT + (int64_t)s0.n * p.D + c, h, 0);
+        return;
+    }
+    SeqPos s = s0;
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const int32_t t = w0 + i;
+        if (t >= w1) break;
         seq_advance(p.seq, s, t);
         if (t < s.start || t >= s.end) continue;
-        const int64_t at = (int64_t)t * p.D + c;
-        if (t == s.start) h = p.s0 ? p.s0[(int64_t)s.n * p.D + c] : 0.f;
-        h = fmaf(fast_exp(Elem<TG>::to_f(g[at])), h, Elem<TX>::to_f(x[at]));
-        out[at] = Elem<TX>::from_f(h);
-        if (t + 1 == s.end && p.sT) p.sT[(int64_t)s.n * p.D + c] = h;
+        if (t == s.start) {
+            // final_state may be initial_state: the last sequence's end may lie in another workgroup, which may
+            // have written it by now, so its start was kept; the others end in this wave, behind this read
+            if (s.n == last_n) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) h[v] = last[v];
+            } else {
+                state_of<VEC>(p.s0, s.n, p.D, c, h);
+            }
+        }
+        step(i);
+        if (p.sT && t + 1 == s.end) store_own<false, float, VEC>(p.sT + (int64_t)s.n * p.D + c, h, 0);
     }
 }
 
-template <typename TX, typename TG>
-__global__ __launch_bounds__(kThreads) void k_bwd(GScanArgs p, const float* rstates) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int32_t t0 = blockIdx.y * kScanTile;
-    if (c >= p.D) return;
-    const TX* x = static_cast<const TX*>(p.x);
-    const TX* dh = static_cast<const TX*>(p.d_h);
-    const TG* g = static_cast<const TG*>(p.g);
+template <typename TX, typename TG, int VEC, bool kChain>
+__global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, int cblocks, Chain ch) {
+    constexpr int CH = kWave * VEC;
+    __shared__ __attribute__((aligned(16))) float2 agg[kWaves][CH];  // the forward's pairs, then the adjoint's
+    __shared__ __attribute__((aligned(16))) float2 ragg[kWaves][CH];
+    __shared__ __attribute__((aligned(16))) float cin[kWaves][CH];
+    __shared__ __attribute__((aligned(16))) float rin[kWaves][CH];
+    __shared__ int sh_id, sh_first;
+    const int id = take(ch, kChain, &sh_id);
+    const int pos = id / cblocks, tile = tiles - 1 - pos, lane = threadIdx.x & 63, wave = wave_id();
+    const int64_t cbase = (int64_t)(id % cblocks) * CH;
+    const int64_t c = cbase + lane * VEC;
+    if (pos == tiles) return pass_empty<VEC>(p, p.d_sT, p.ds0, c);
+    const bool live = c < p.D;
+    const int64_t cl = live ? c : 0;
+    const int64_t w0l = (int64_t)tile * kTile + wave * kTokens;
+    const int32_t w0 = w0l < p.seq.total ? (int32_t)w0l : p.seq.total;
+    const int32_t w1 = p.seq.total - w0 < kTokens ? p.seq.total : w0 + kTokens;
+    Raw<TX, VEC> x[kTokens], d[kTokens];
+    Raw<TG, VEC> g[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const int64_t at = (int64_t)min(w0 + i, p.seq.total - 1) * p.D + cl;
+        g[i] = load_raw<TG, VEC>(static_cast<const TG*>(p.g) + at);
+        x[i] = load_raw<TX, VEC>(static_cast<const TX*>(p.x) + at);
+        d[i] = load_raw<TX, VEC>(static_cast<const TX*>(p.d_h) + at);
+    }
+    const SeqPos s0 = seq_find(p.seq, min(w0, p.seq.total - 1));
+    // all of the wave's tokens inside one sequence, neither its first nor its last among them
+    const bool inside = w0 > s0.start && w0 + kTokens < s0.end;
+    if (kChain && threadIdx.x == kThreads - kWave) {
+        // the chain comes from the sequence that goes on behind the tile
+        const int32_t t1 = min((int64_t)(tile + 1) * kTile, (int64_t)p.seq.total);
+        const SeqPos e = seq_find(p.seq, t1 - 1);
+        sh_first = t1 > e.start && t1 < e.end ? tiles - 1 - (e.end - 1) / kTile : pos;
+    }
+    float A[VEC], H[VEC], R[VEC], M[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        A[v] = R[v] = 1.f;
+        H[v] = M[v] = 0.f;
+    }
+    if (inside) {
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float a = fast_exp(g[i].get(v));
+                H[v] = fmaf(a, H[v], x[i].get(v));
+                A[v] *= a;
+            }
+#pragma unroll
+        for (int i = kTokens - 1; i >= 0; --i)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) M[v] = fast_exp(g[i].get(v)) * (d[i].get(v) + M[v]);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) R[v] = A[v];
+    } else {
+        SeqPos s = s0;
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) {
+            const int32_t t = w0 + i;
+            if (t >= w1) break;
+            seq_advance(p.seq, s, t);
+            if (t < s.start || t >= s.end) continue;
+            if (t == s.start) {
+                state_of<VEC>(p.s0, s.n, p.D, cl, H);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) A[v] = -1.f;
+            }
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float a = fast_exp(g[i].get(v));
+                H[v] = fmaf(a, H[v], x[i].get(v));
+                A[v] *= a;
+            }
+        }
+#pragma unroll
+        for (int i = kTokens - 1; i >= 0; --i) {
+            const int32_t t = w0 + i;
+            if (t >= w1) continue;
+            const SeqPos e = seq_find(p.seq, t);
+            if (t < e.start || t >= e.end) continue;
+            if (t + 1 == e.end) {
+                state_of<VEC>(p.d_sT, e.n, p.D, cl, M);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) R[v] = -1.f;
+            }
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float a = fast_exp(g[i].get(v));
+                M[v] = a * (d[i].get(v) + M[v]);
+                R[v] *= a;
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        agg[wave][lane * VEC + v] = make_float2(A[v], H[v]);
+        ragg[wave][lane * VEC + v] = make_float2(R[v], M[v]);
+    }
+    __syncthreads();
+    if (threadIdx.x < CH) {
+        const int64_t tc = cbase + threadIdx.x;
+        enter_tile<true, kChain, CH>(ragg, rin, ch, p.D, tc, pos, tiles, kChain ? __builtin_amdgcn_readfirstlane(sh_first) : pos);
+    } else if (threadIdx.x < 2 * CH) {
+        // the other threads: the states that enter the waves, from the tile's kept one
+        const int t = threadIdx.x - CH;
+        float h = cbase + t < p.D ? p.states[(int64_t)tile * p.D + cbase + t] : 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            cin[w][t] = h;
+            h = pass_on(agg[w][t].x, agg[w][t].y, h);
+        }
+    }
+    __syncthreads();
+    if (!live || w0 >= w1) return;
+    float h[VEC], mu[VEC], before[kTokens][VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        h[v] = cin[wave][lane * VEC + v];
+        mu[v] = rin[wave][lane * VEC + v];
+    }
     TX* dx = static_cast<TX*>(p.dx);
     TG* dg = static_cast<TG*>(p.dg);
-    float before[kScanTile];
-    float h = p.states[(int64_t)blockIdx.y * p.D + c];
-    SeqPos s = seq_find(p.seq, t0);
+    auto ahead = [&](int i) {
 #pragma unroll
-    for (int i = 0; i < kScanTile; ++i) {
-        const int32_t t = t0 + i;
-        if (t >= p.seq.total) continue;
+        for (int v = 0; v < VEC; ++v) {
+            before[i][v] = h[v];
+            h[v] = fmaf(fast_exp(g[i].get(v)), h[v], x[i].get(v));
+        }
+    };
+    auto back = [&](int i) {
+        float lam[VEC], dgv[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            lam[v] = d[i].get(v) + mu[v];
+            mu[v] = fast_exp(g[i].get(v)) * lam[v];
+            dgv[v] = mu[v] * before[i][v];
+        }
+        const int64_t at = (int64_t)(w0 + i) * p.D + c;
+        store_own<false, TX, VEC>(dx + at, lam, 0);
+        store_own<false, TG, VEC>(dg + at, dgv, 0);
+    };
+    if (inside) {
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) ahead(i);
+#pragma unroll
+        for (int i = kTokens - 1; i >= 0; --i) back(i);
+        return;
+    }
+    SeqPos s = s0;
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const int32_t t = w0 + i;
+        if (t >= w1) break;
         seq_advance(p.seq, s, t);
         if (t < s.start || t >= s.end) continue;
-        const int64_t at = (int64_t)t * p.D + c;
-        if (t == s.start) h = p.s0 ? p.s0[(int64_t)s.n * p.D + c] : 0.f;
-        before[i] = h;
-        h = fmaf(fast_exp(Elem<TG>::to_f(g[at])), h, Elem<TX>::to_f(x[at]));
+        if (t == s.start) state_of<VEC>(p.s0, s.n, p.D, c, h);
+        ahead(i);
     }
-    float mu = rstates[(int64_t)blockIdx.y * p.D + c];
 #pragma unroll
-    for (int i = kScanTile - 1; i >= 0; --i) {
-        const int32_t t = t0 + i;
-        if (t >= p.seq.total) continue;
-        s = seq_find(p.seq, t);
-        if (t < s.start || t >= s.end) continue;
-        const int64_t at = (int64_t)t * p.D + c;
-        if (t + 1 == s.end) mu = p.d_sT ? p.d_sT[(int64_t)s.n * p.D + c] : 0.f;
-        const float lam = Elem<TX>::to_f(dh[at]) + mu;
-        mu = fast_exp(Elem<TG>::to_f(g[at])) * lam;
-        dx[at] = Elem<TX>::from_f(lam);
-        dg[at] = Elem<TG>::from_f(mu * before[i]);
-        if (t == s.start && p.ds0) p.ds0[(int64_t)s.n * p.D + c] = mu;
+    for (int i = kTokens - 1; i >= 0; --i) {
+        const int32_t t = w0 + i;
+        if (t >= w1) continue;
+        const SeqPos e = seq_find(p.seq, t);
+        if (t < e.start || t >= e.end) continue;
+        if (t + 1 == e.end) state_of<VEC>(p.d_sT, e.n, p.D, c, mu);
+        back(i);
+        if (p.ds0 && t == e.start) store_own<false, float, VEC>(p.ds0 + (int64_t)e.n * p.D + c, mu, 0);
     }
 }
 
-// Sequences without tokens: their state (or its gradient) passes through.
-__global__ __launch_bounds__(kThreads) void k_empty(SeqView seq, int64_t D, const float* in, float* out) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    for (int32_t n = blockIdx.y; n < seq.N; n += gridDim.y) {
-        const SeqPos s = seq_at(seq, n);
-        if (s.start < s.end || c >= D) continue;
-        out[(int64_t)n * D + c] = in ? in[(int64_t)n * D + c] : 0.f;
+// Short sequences (decoding): a wave per sequence and block of channels walks the tokens; one launch, no workspace.
+constexpr int kRowThreads = 256;
+template <typename TX, typename TG, int VEC>
+__global__ __launch_bounds__(kRowThreads) void k_gscan_rows(GScanArgs p, int cblocks) {
+    const int64_t item = (int64_t)blockIdx.x * (kRowThreads / kWave) + wave_id();
+    const int64_t nl = item / cblocks;
+    if (nl >= p.seq.N) return;
+    const int64_t c = ((item % cblocks) * kWave + (threadIdx.x & 63)) * VEC;
+    if (c >= p.D) return;
+    const SeqPos s = seq_at(p.seq, (int32_t)nl);
+    float h[VEC];
+    state_of<VEC>(p.s0, s.n, p.D, c, h);
+    const TX* x = static_cast<const TX*>(p.x) + c;
+    const TG* g = static_cast<const TG*>(p.g) + c;
+    TX* out = static_cast<TX*>(p.h);
+    Raw<TX, VEC> nx;
+    Raw<TG, VEC> ng;
+    if (s.start < s.end) {
+        nx = load_raw<TX, VEC>(x + (int64_t)s.start * p.D);
+        ng = load_raw<TG, VEC>(g + (int64_t)s.start * p.D);
+    }
+    for (int32_t t = s.start; t < s.end; ++t) {
+        const Raw<TX, VEC> xt = nx;
+        const Raw<TG, VEC> gt = ng;
+        if (t + 1 < s.end) {
+            nx = load_raw<TX, VEC>(x + (int64_t)(t + 1) * p.D);
+            ng = load_raw<TG, VEC>(g + (int64_t)(t + 1) * p.D);
+        }
+        if (p.states && t % kScanTile == 0) store_own<false, float, VEC>(p.states + (int64_t)(t / kScanTile) * p.D + c, h, 0);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) h[v] = fmaf(fast_exp(gt.get(v)), h[v], xt.get(v));
+        if (out) store_own<false, TX, VEC>(out + (int64_t)t * p.D + c, h, 0);
+    }
+    if (p.sT) store_own<false, float, VEC>(p.sT + (int64_t)s.n * p.D + c, h, 0);
+}
+
+// Clears a chain: the ticket to zero, every word behind it to "not there yet".
+__global__ __launch_bounds__(256) void k_clear(u32x4* p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const uint32_t v = i < 16 ? 0u : ~0u;
+        p[i] = u32x4{v, v, v, v};
     }
 }
 
-hipError_t empties(const GScanArgs& a, const float* in, float* out, hipStream_t st) {
-    if (!out || (!a.seq.cu && a.seq.T > 0)) return hipSuccess;
-    const dim3 grid((unsigned)((a.D + kThreads - 1) / kThreads), (unsigned)(a.seq.N < 1024 ? a.seq.N : 1024));
-    hipLaunchKernelGGL(k_empty, grid, dim3(kThreads), 0, st, a.seq, a.D, in, out);
-    return hipGetLastError();
-}
-
-int tiles_of(int64_t total) { return (int)((total + kScanTile - 1) / kScanTile); }
+int tiles_of(int64_t total) { return (int)((total + kTile - 1) / kTile); }
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-template <typename TX, typename TG>
-hipError_t fwd_states(const GScanArgs& a, float2* pairs, hipStream_t st) {
-    const int tiles = tiles_of(a.seq.total);
-    const dim3 grid((unsigned)((a.D + kThreads - 1) / kThreads), (unsigned)tiles);
-    hipLaunchKernelGGL((k_pairs<TX, TG, false>), grid, dim3(kThreads), 0, st, a, pairs);
-    hipLaunchKernelGGL((k_carry<false>), dim3(grid.x), dim3(kThreads), 0, st, pairs, a.states, tiles, a.D);
+// A chain in the workspace: 256 bytes for the ticket, the pairs, the groups' states.
+size_t chain_bytes(int64_t total, int64_t D) {
+    const size_t tiles = tiles_of(total), groups = (tiles + kGroup - 1) / kGroup;
+    return tiles < 2 ? 0 : 256 + align256(tiles * D * 8) + align256(groups * D * 4);
+}
+hipError_t make_chain(unsigned char* ws, int64_t total, int64_t D, Chain& ch, hipStream_t st) {
+    const size_t bytes = chain_bytes(total, D);
+    ch.ticket = reinterpret_cast<uint32_t*>(ws);
+    ch.pairs = reinterpret_cast<uint64_t*>(ws + 256);
+    ch.carry = reinterpret_cast<uint32_t*>(ws + 256 + align256((size_t)tiles_of(total) * D * 8));
+    const int64_t n = (int64_t)(bytes / 16), blocks = (n + 1023) / 1024;
+    hipLaunchKernelGGL(k_clear, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, reinterpret_cast<u32x4*>(ws), n);
     return hipGetLastError();
 }
 
-template <typename TX, typename TG>
-hipError_t fwd_t(GScanArgs a, hipStream_t st) {
+template <typename TX, typename TG, int VEC>
+hipError_t fwd_v(const GScanArgs& a, hipStream_t st) {
     const int tiles = tiles_of(a.seq.total);
-    if (tiles) {
-        float2* pairs = reinterpret_cast<float2*>(a.ws);
-        if (!a.states) a.states = reinterpret_cast<float*>(a.ws + align256((size_t)tiles * a.D * 8));
-        if (hipError_t e = fwd_states<TX, TG>(a, pairs, st)) return e;
-        const dim3 grid((unsigned)((a.D + kThreads - 1) / kThreads), (unsigned)tiles);
-        hipLaunchKernelGGL((k_fwd<TX, TG>), grid, dim3(kThreads), 0, st, a);
-        if (hipError_t e = hipGetLastError()) return e;
+    const int cb = (int)((a.D + kWave * VEC - 1) / (kWave * VEC));
+    // sequences of up to 16 tokens, or on average up to 4 where they are packed: a wave each
+    if (a.seq.cu ? a.seq.total / a.seq.N <= 4 : a.seq.T <= 16) {
+        const int64_t items = (int64_t)a.seq.N * cb, per = kRowThreads / kWave;
+        if (!grid_fits((items + per - 1) / per, kRowThreads)) return hipErrorInvalidConfiguration;
+        hipLaunchKernelGGL((k_gscan_rows<TX, TG, VEC>), dim3((unsigned)((items + per - 1) / per)), dim3(kRowThreads), 0, st, a, cb);
+        return hipGetLastError();
     }
-    return empties(a, a.s0, a.sT, st);
+    const int extra = a.sT && a.seq.cu;
+    Chain ch{};
+    if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)(tiles + extra) * (unsigned)cb);
+    if (tiles > 1) {
+        if (hipError_t e = make_chain(a.ws, a.seq.total, a.D, ch, st)) return e;
+        hipLaunchKernelGGL((k_gscan_fwd<TX, TG, VEC, true>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
+    } else {
+        hipLaunchKernelGGL((k_gscan_fwd<TX, TG, VEC, false>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
+    }
+    return hipGetLastError();
 }
 
-template <typename TX, typename TG>
-hipError_t bwd_t(GScanArgs a, bool have, hipStream_t st) {
+template <typename TX, typename TG, int VEC>
+hipError_t bwd_v(GScanArgs a, bool have, hipStream_t st) {
     const int tiles = tiles_of(a.seq.total);
-    if (tiles) {
-        float2* pairs = reinterpret_cast<float2*>(a.ws);
-        float* rst = reinterpret_cast<float*>(a.ws + align256((size_t)tiles * a.D * 8));
-        const dim3 grid((unsigned)((a.D + kThreads - 1) / kThreads), (unsigned)tiles);
-        if (!have) {
-            a.states = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(rst) + align256((size_t)tiles * a.D * 4));
-            if (hipError_t e = fwd_states<TX, TG>(a, pairs, st)) return e;
-        }
-        hipLaunchKernelGGL((k_pairs<TX, TG, true>), grid, dim3(kThreads), 0, st, a, pairs);
-        hipLaunchKernelGGL((k_carry<true>), dim3(grid.x), dim3(kThreads), 0, st, pairs, rst, tiles, a.D);
-        hipLaunchKernelGGL((k_bwd<TX, TG>), grid, dim3(kThreads), 0, st, a, rst);
-        if (hipError_t e = hipGetLastError()) return e;
+    const int cb = (int)((a.D + kWave * VEC - 1) / (kWave * VEC));
+    const int extra = a.ds0 && (a.seq.cu || a.seq.T == 0);
+    if (tiles + extra == 0) return hipSuccess;
+    if (!have && tiles) {
+        a.states = reinterpret_cast<float*>(a.ws + chain_bytes(a.seq.total, a.D));
+        GScanArgs f = a;
+        f.h = nullptr;
+        f.sT = nullptr;
+        if (hipError_t e = fwd_v<TX, TG, VEC>(f, st)) return e;
     }
-    return empties(a, a.d_sT, a.ds0, st);
+    Chain ch{};
+    if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)(tiles + extra) * (unsigned)cb);
+    if (tiles > 1) {
+        if (hipError_t e = make_chain(a.ws, a.seq.total, a.D, ch, st)) return e;
+        hipLaunchKernelGGL((k_gscan_bwd<TX, TG, VEC, true>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
+    } else {
+        hipLaunchKernelGGL((k_gscan_bwd<TX, TG, VEC, false>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
+    }
+    return hipGetLastError();
+}
+
+// Four channels per lane where the rows are whole vectors of four, else one.
+template <typename TX, typename TG>
+hipError_t fwd_t(const GScanArgs& a, hipStream_t st) {
+    return a.D % 4 == 0 && a.D >= 128 ? fwd_v<TX, TG, 4>(a, st) : fwd_v<TX, TG, 1>(a, st);
+}
+template <typename TX, typename TG>
+hipError_t bwd_t(const GScanArgs& a, bool have, hipStream_t st) {
+    return a.D % 4 == 0 && a.D >= 128 ? bwd_v<TX, TG, 4>(a, have, st) : bwd_v<TX, TG, 1>(a, have, st);
 }
 
 }  // namespace
 
-size_t gscan_fwd_ws(int64_t total, int64_t D) {
-    const size_t n = (size_t)tiles_of(total) * D;
-    return align256(n * 8) + align256(n * 4);
-}
-size_t gscan_bwd_ws(int64_t total, int64_t D) {
-    const size_t n = (size_t)tiles_of(total) * D;
-    return align256(n * 8) + 2 * align256(n * 4);
-}
+size_t gscan_fwd_ws(int64_t total, int64_t D) { return chain_bytes(total, D); }
+size_t gscan_bwd_ws(int64_t total, int64_t D) { return chain_bytes(total, D) + (size_t)tiles_of(total) * D * 4; }
 
 // dtype, g_dtype: gdn_dtype (0 bf16, 1 fp32); g in the type of x or fp32
 hipError_t launch_gscan_fwd(const GScanArgs& a, int dtype, int g_dtype, hipStream_t st) {

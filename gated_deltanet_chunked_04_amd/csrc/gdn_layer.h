@@ -51,6 +51,9 @@ __device__ __forceinline__ void seq_advance(const SeqView& s, SeqPos& p, int32_t
     while (t >= p.end && p.n + 1 < s.N) p = seq_at(s, p.n + 1);
 }
 
+// A launch's threads are counted in 32 bits. Launchers return hipErrorInvalidConfiguration for more.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks <= (int64_t)UINT32_MAX / threads; }
+
 // ---- gated scan ---------------------------------------------------------------------------
 constexpr int kScanTile = 64;  // tokens between two entries of the kept states
 

@@ -63,7 +63,9 @@ gdn_status check_rms(const gdn_rmsnorm_desc* d) {
     return GDN_OK;
 }
 
-gdn_status launched(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_ERR_HIP; }
+gdn_status launched(hipError_t e) {
+    return e == hipSuccess ? GDN_OK : (e == hipErrorInvalidConfiguration ? GDN_ERR_UNSUPPORTED : GDN_ERR_HIP);
+}
 
 }  // namespace
 

@@ -395,14 +395,15 @@ __global__ __launch_bounds__(kLoopThreads) void k_rms_dx_loop(RmsArgs p, float* 
 constexpr int kLoopSumRows = 64;  // rows per partial sum of dw behind k_rms_dx_loop
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_rms_dw_loop(RmsArgs p, const float* rstds, float* part) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t cblocks = (p.D + kThreads - 1) / kThreads, block = blockIdx.x / cblocks;
+    const int64_t c = (blockIdx.x % cblocks) * kThreads + threadIdx.x;
     if (c >= p.D) return;
-    const int64_t r0 = (int64_t)blockIdx.y * kLoopSumRows, r1 = r0 + kLoopSumRows < p.rows ? r0 + kLoopSumRows : p.rows;
+    const int64_t r0 = block * kLoopSumRows, r1 = r0 + kLoopSumRows < p.rows ? r0 + kLoopSumRows : p.rows;
     float s = 0.f;
     for (int64_t i = r0; i < r1; ++i)
         s = fmaf(Elem<T>::to_f(static_cast<const T*>(p.d_y)[i * p.D + c]),
                  Elem<T>::to_f(static_cast<const T*>(p.x)[i * p.D + c]) * rstds[i], s);
-    part[(int64_t)blockIdx.y * p.D + c] = s;
+    part[block * p.D + c] = s;
 }
 
 // ---- launches -----------------------------------------------------------------------------
@@ -434,19 +435,20 @@ hipError_t fwd_o(const RmsArgs& a, hipStream_t st) {
 #define GDN_RMS_FWD(LANES, NV)                                                                              \
     if (s.lanes == LANES && s.nv == NV) {                                                                   \
         constexpr int kRows = LANES == 64 ? kThreads / 64 : 1;                                              \
+        if (!grid_fits((a.rows + kRows - 1) / kRows, LANES > kThreads ? LANES : kThreads))                  \
+            return hipErrorInvalidConfiguration;                                                            \
         hipLaunchKernelGGL((k_rms_fwd<kOdd, T, TW, LANES, NV, OUT>), dim3((unsigned)((a.rows + kRows - 1) / kRows)), \
                            dim3(LANES > kThreads ? LANES : kThreads), 0, st, a);                            \
         return hipGetLastError();                                                                           \
     }
     GDN_RMS_FWD(64, 1)
-    GDN_RMS_FWD(64, 2)
-    GDN_RMS_FWD(64, 4)
     GDN_RMS_FWD(256, 1)
     GDN_RMS_FWD(256, 2)
     GDN_RMS_FWD(256, 4)
     GDN_RMS_FWD(1024, 2)
     GDN_RMS_FWD(1024, 4)
 #undef GDN_RMS_FWD
+    if (!grid_fits(a.rows, kLoopThreads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((k_rms_fwd_loop<T, TW, OUT != kPlain>), dim3((unsigned)a.rows), dim3(kLoopThreads), 0, st, a);
     return hipGetLastError();
 }
@@ -484,8 +486,6 @@ hipError_t bwd_o(const RmsArgs& a, hipStream_t st) {
             done = true;                                                                                    \
         }
         GDN_RMS_BWD(64, 1)
-        GDN_RMS_BWD(64, 2)
-        GDN_RMS_BWD(64, 4)
         GDN_RMS_BWD(256, 1)
         GDN_RMS_BWD(256, 2)
         GDN_RMS_BWD(256, 4)
@@ -496,9 +496,10 @@ hipError_t bwd_o(const RmsArgs& a, hipStream_t st) {
         float* rstds = part;
         part = reinterpret_cast<float*>(a.ws + align256((size_t)a.rows * 4));
         parts = loop_parts(a.rows);
+        if (!grid_fits(a.rows, kLoopThreads)) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((k_rms_dx_loop<T, TW>), dim3((unsigned)a.rows), dim3(kLoopThreads), 0, st, a, rstds);
         const unsigned cb = (unsigned)((a.D + kThreads - 1) / kThreads);
-        if (a.dw) hipLaunchKernelGGL((k_rms_dw_loop<T>), dim3(cb, (unsigned)parts), dim3(kThreads), 0, st, a, rstds, part);
+        if (a.dw) hipLaunchKernelGGL((k_rms_dw_loop<T>), dim3(cb * (unsigned)parts), dim3(kThreads), 0, st, a, rstds, part);
     }
     if (a.dw)
         hipLaunchKernelGGL(k_rms_dw_sum, dim3((unsigned)((a.D + 15) / 16)), dim3(kSumThreads), 0, st, part, (int)parts, a.D, a.dw);

@@ -463,8 +463,9 @@ def test_refusals(gpu_lib):
         gdn.gdn_gated_scan_fwd(x, x, torch.zeros(2, 16, device="cuda"))
     with pytest.raises(ValueError):
         gdn.gdn_gated_scan_fwd(x, x, states=torch.zeros(2, 16, device="cuda"))
+    long = torch.zeros(1, 300, 16, device="cuda")
     with pytest.raises(ValueError):
-        gdn.gdn_gated_scan_fwd(x, x, workspace=torch.zeros(8, dtype=torch.uint8, device="cuda"))
+        gdn.gdn_gated_scan_fwd(long, long, workspace=torch.zeros(8, dtype=torch.uint8, device="cuda"))
     with pytest.raises(TypeError):
         gdn.gdn_gated_scan_fwd(x, x, cu_seqlens=torch.tensor([0, 8]).cuda())
     with pytest.raises(TypeError):
