@@ -8,12 +8,12 @@
 //   * A workgroup of eight waves holds a tile of tokens by 64 VEC channels in registers, eight tokens
 //     to a wave. A run of tokens acts on the state that enters it as c -> A c + H; the waves' pairs
 //     (A, H) meet in LDS and make the tile's pair.
-//   * The tile publishes its pair, gathers the state that enters it from the tiles before it (look_back),
+//   * The tile publishes its pair, gathers the state that enters it from the tiles before it (enter_tile),
 //     and each wave runs its tokens again from its own entering state, now with their outputs.
 //   * Tiles are handed out in the order of the token axis by a counter, so a tile only ever waits for
 //     tiles that are running or done, and those publish their pairs before they wait themselves.
 //   * What is added to what is fixed by the tile's place, not by who was ready first, so results are
-//     the same bits every time: the state entering a group of 16 tiles comes from the group before it
+//     the same bits every time: the state entering a group of 8 tiles comes from the group before it
 //     as one published value, the tiles inside the group combine the pairs since then.
 // Published words carry their own mark (all ones: not there yet), so no other ordering of memory is
 // needed; a small launch clears them first. The gradient runs the same from the other end, and
@@ -27,10 +27,9 @@ namespace {
 
 constexpr int kWaves = 8;              // waves of a tile
 constexpr int kThreads = kWaves * kWave;
-constexpr int kTokens = 8;             // tokens of a wave
-constexpr int kTile = kWaves * kTokens;
-static_assert(kTile == kScanTile, "a kept state per tile");
-constexpr int kGroup = 16;             // tiles between two published entering states
+constexpr int kBwdTokens = 8;          // tokens of a wave in the gradient
+static_assert(kWaves * kBwdTokens == kScanTile, "a kept state per tile of the gradient");
+constexpr int kGroup = 8;              // tiles between two published entering states
 constexpr int kMaxSpins = 1 << 20;     // (about a second) a wait gives up with NaN rather than hang
 
 struct Chain {
@@ -61,67 +60,97 @@ __device__ __forceinline__ void publish(W* p, W v) {
     __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The state that enters place `pos` of the chain in channel c; `first`: the place in which its sequence starts
-// (uniform, < pos). Whole waves call it; `live`: this lane's channel exists.
-__device__ float look_back(const Chain& ch, int64_t D, int64_t c, int pos, int first, bool live) {
-    const int group = pos / kGroup;
-    const int from = first > group * kGroup ? first : group * kGroup;
-    const float lost = __uint_as_float(0x7FC00000u);
-    float A = 1.f, H = 0.f;
-    int spins = 0;
-    for (int k = from; k < pos; k += 8) {
-        uint64_t v[8];
-        for (;;) {
+// What the places from .. to - 1 of the chain do together to a state in channel c. Whole waves call it; `live`:
+// this lane's channel exists. False if the wait was given up.
+__device__ __forceinline__ bool gather(const Chain& ch, int64_t D, int64_t c, bool live, int from, int to, float& A, float& H) {
+    constexpr int kAhead = 4;
+    for (int k = from; k < to; k += kAhead) {
+        uint64_t v[kAhead];
+        for (int spins = 0;;) {
             bool ok = true;
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (k + u < pos) v[u] = live ? peek(ch.pairs + (int64_t)(k + u) * D + c) : 0;
+            for (int u = 0; u < kAhead; ++u)
+                if (k + u < to) v[u] = live ? peek(ch.pairs + (int64_t)(k + u) * D + c) : 0;
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (k + u < pos) ok = ok && v[u] != ~0ull;
+            for (int u = 0; u < kAhead; ++u)
+                if (k + u < to) ok = ok && v[u] != ~0ull;
             if (__all(ok)) break;
-            if (++spins > kMaxSpins) return lost;
+            if (++spins > kMaxSpins) return false;
             __builtin_amdgcn_s_sleep(1);
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (k + u < pos) then(A, H, __uint_as_float((uint32_t)(v[u] >> 32)), __uint_as_float((uint32_t)v[u]));
+        for (int u = 0; u < kAhead; ++u)
+            if (k + u < to) then(A, H, __uint_as_float((uint32_t)(v[u] >> 32)), __uint_as_float((uint32_t)v[u]));
     }
-    if (first >= group * kGroup) return H;  // (the first of these pairs holds the sequence's start)
-    for (;;) {
-        const uint32_t v = live ? peek(ch.carry + (int64_t)group * D + c) : 0;
-        if (__all(v != ~0u)) return pass_on(A, H, __uint_as_float(v));
-        if (++spins > kMaxSpins) return lost;
-        __builtin_amdgcn_s_sleep(1);
-    }
+    return true;
 }
 
-// The tile's pair and the state (or adjoint) that enters each of its waves, for channel `c` of the block's
-// thread: agg holds the waves' pairs in LDS, cin receives the entering values. Publishes on the way.
+// The state (or adjoint) that enters each of the tile's waves, for all channels of the block, into `cin`, from the
+// waves' pairs in `agg`. Place `pos` of the chain; `first`: the place in which the sequence that enters it starts
+// (pos: none enters). Publishes the tile's pair before it waits for anything. All threads call it: the places to
+// look back over are split among kThreads / CH parts of the workgroup, so that each thread has few loads in flight
+// beside its tokens. Ends with a barrier.
 template <bool kRev, bool kChain, int CH>
-__device__ __forceinline__ void enter_tile(const float2 (*agg)[CH], float (*cin)[CH], const Chain& ch, int64_t D,
-                                           int64_t c, int pos, int tiles, int first) {
-    const int t = threadIdx.x;
+__device__ __forceinline__ void enter_tile(const float2 (*agg)[CH], float2 (*mid)[CH], float (*cin)[CH], const Chain& ch,
+                                           int64_t D, int64_t cbase, int pos, int tiles, int first) {
+    constexpr int kParts = kThreads / CH;
+    const int t = threadIdx.x % CH;
+    const int part = __builtin_amdgcn_readfirstlane((int)threadIdx.x / CH);
+    const int64_t c = cbase + t;
     const bool live = c < D;
-    float2 q[kWaves];
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) q[w] = agg[kRev ? kWaves - 1 - w : w][t];
-    float s = 0.f;
+    const float lost = __uint_as_float(0x7FC00000u);
+    float s = 0.f, A = 1.f, H = 0.f;
     if constexpr (kChain) {
-        float A = 1.f, H = 0.f;
+        if (part == 0) {
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) then(A, H, q[w].x, q[w].y);
-        if (live && pos + 1 < tiles)
-            publish(ch.pairs + (int64_t)pos * D + c, ((uint64_t)__float_as_uint(A) << 32) | mark(H));
-        if (first < pos) s = look_back(ch, D, c, pos, first, live);
-        if (live && (pos + 1) % kGroup == 0 && pos + 1 < tiles)
+            for (int w = 0; w < kWaves; ++w) {
+                const float2 q = agg[kRev ? kWaves - 1 - w : w][t];
+                then(A, H, q.x, q.y);
+            }
+            if (live && pos + 1 < tiles)
+                publish(ch.pairs + (int64_t)pos * D + c, ((uint64_t)__float_as_uint(A) << 32) | mark(H));
+        }
+        if (first < pos) {
+            const int group = pos / kGroup, begin = group * kGroup;
+            const bool carried = first < begin;  // the state comes from the group before
+            const int from = carried ? begin : first, each = (pos - from + kParts - 1) / kParts;
+            const uint32_t* word = ch.carry + (int64_t)group * D + c;
+            uint32_t v = 0;
+            if (part == 0 && carried && live) v = peek(word);
+            float a = 1.f, h = 0.f;
+            const int lo = min(from + part * each, pos), hi = min(lo + each, pos);
+            if (!gather(ch, D, c, live, lo, hi, a, h)) {
+                a = -1.f;
+                h = lost;
+            }
+            mid[part][t] = make_float2(a, h);
+            __syncthreads();
+            if (part == 0) {
+                for (int spins = 0; !__all(v != ~0u);) {
+                    if (++spins > kMaxSpins) {
+                        v = __float_as_uint(lost);
+                        break;
+                    }
+                    __builtin_amdgcn_s_sleep(1);
+                    if (live) v = peek(word);
+                }
+                s = __uint_as_float(v);
+#pragma unroll
+                for (int q = 0; q < kParts; ++q) s = pass_on(mid[q][t].x, mid[q][t].y, s);
+            }
+        }
+        if (part == 0 && live && (pos + 1) % kGroup == 0 && pos + 1 < tiles)
             publish(ch.carry + (int64_t)((pos + 1) / kGroup) * D + c, mark(pass_on(A, H, s)));
+        asm volatile("" ::: "memory");  // the waves' pairs are read again rather than held through the wait
     }
+    if (part == 0)
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        cin[kRev ? kWaves - 1 - w : w][t] = s;
-        s = pass_on(q[w].x, q[w].y, s);
-    }
+        for (int w = 0; w < kWaves; ++w) {
+            const float2 q = agg[kRev ? kWaves - 1 - w : w][t];
+            cin[kRev ? kWaves - 1 - w : w][t] = s;
+            s = pass_on(q.x, q.y, s);
+        }
+    __syncthreads();
 }
 
 template <int VEC>
@@ -161,11 +190,14 @@ __device__ __forceinline__ int take(const Chain& ch, bool chain, int* sh) {
     return __builtin_amdgcn_readfirstlane(*sh);
 }
 
-template <typename TX, typename TG, int VEC, bool kChain>
+template <typename TX, typename TG, int VEC, int kTokens, bool kChain>
 __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, int cblocks, Chain ch) {
+    constexpr int kTile = kWaves * kTokens;
+    constexpr int kKeep = kScanTile / kTokens;  // waves between two kept states
     constexpr int CH = kWave * VEC;
     __shared__ __attribute__((aligned(16))) float2 agg[kWaves][CH];
     __shared__ __attribute__((aligned(16))) float cin[kWaves][CH];
+    __shared__ __attribute__((aligned(16))) float2 mid[kChain ? kThreads / CH : 1][CH];
     __shared__ int sh_id, sh_first;
     const int id = take(ch, kChain, &sh_id);
     const int tile = id / cblocks, lane = threadIdx.x & 63, wave = wave_id();
@@ -179,11 +211,13 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
     const int32_t w1 = p.seq.total - w0 < kTokens ? p.seq.total : w0 + kTokens;
     Raw<TX, VEC> x[kTokens];
     Raw<TG, VEC> g[kTokens];
+    // a uniform row address and a 32-bit lane offset
+    const uint32_t lo = live ? lane * VEC : 0;
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-        const int64_t at = (int64_t)min(w0 + i, p.seq.total - 1) * p.D + cl;
-        x[i] = load_raw<TX, VEC>(static_cast<const TX*>(p.x) + at);
-        g[i] = load_raw<TG, VEC>(static_cast<const TG*>(p.g) + at);
+        const int64_t at = (int64_t)min(w0 + i, p.seq.total - 1) * p.D + cbase;
+        x[i] = load_raw<TX, VEC>(static_cast<const TX*>(p.x) + at + lo);
+        g[i] = load_raw<TG, VEC>(static_cast<const TG*>(p.g) + at + lo);
     }
     const SeqPos s0 = seq_find(p.seq, min(w0, p.seq.total - 1));
     // all of the wave's tokens inside one sequence, none of them its first
@@ -230,19 +264,18 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
 #pragma unroll
     for (int v = 0; v < VEC; ++v) agg[wave][lane * VEC + v] = make_float2(A[v], H[v]);
     __syncthreads();
-    if (threadIdx.x < CH)
-        enter_tile<false, kChain, CH>(agg, cin, ch, p.D, cbase + threadIdx.x, tile, tiles, kChain ? __builtin_amdgcn_readfirstlane(sh_first) : tile);
-    __syncthreads();
+    enter_tile<false, kChain, CH>(agg, mid, cin, ch, p.D, cbase, tile, tiles, kChain ? __builtin_amdgcn_readfirstlane(sh_first) : tile);
     float h[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h[v] = cin[wave][lane * VEC + v];
     if (!live || w0 >= w1) return;
-    if (p.states && wave == 0) store_own<false, float, VEC>(p.states + (int64_t)tile * p.D + c, h, 0);
+    if (p.states && wave % kKeep == 0)
+        store_own<false, float, VEC>(p.states + (int64_t)(w0 / kScanTile) * p.D + c, h, 0);
     TX* out = static_cast<TX*>(p.h);
     auto step = [&](int i) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) h[v] = fmaf(fast_exp(g[i].get(v)), h[v], x[i].get(v));
-        if (out) store_own<false, TX, VEC>(out + (int64_t)(w0 + i) * p.D + c, h, 0);
+        if (out) store_own<false, TX, VEC>(out + ((int64_t)(w0 + i) * p.D + cbase) + lo, h, 0);
     };
     if (inside) {
 #pragma unroll
@@ -274,11 +307,13 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
 
 template <typename TX, typename TG, int VEC, bool kChain>
 __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, int cblocks, Chain ch) {
+    constexpr int kTokens = kBwdTokens, kTile = kScanTile;
     constexpr int CH = kWave * VEC;
     __shared__ __attribute__((aligned(16))) float2 agg[kWaves][CH];  // the forward's pairs, then the adjoint's
     __shared__ __attribute__((aligned(16))) float2 ragg[kWaves][CH];
     __shared__ __attribute__((aligned(16))) float cin[kWaves][CH];
     __shared__ __attribute__((aligned(16))) float rin[kWaves][CH];
+    __shared__ __attribute__((aligned(16))) float2 mid[kChain ? kThreads / CH : 1][CH];
     __shared__ int sh_id, sh_first;
     const int id = take(ch, kChain, &sh_id);
     const int pos = id / cblocks, tile = tiles - 1 - pos, lane = threadIdx.x & 63, wave = wave_id();
@@ -292,12 +327,13 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
     const int32_t w1 = p.seq.total - w0 < kTokens ? p.seq.total : w0 + kTokens;
     Raw<TX, VEC> x[kTokens], d[kTokens];
     Raw<TG, VEC> g[kTokens];
+    const uint32_t lo = live ? lane * VEC : 0;
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-        const int64_t at = (int64_t)min(w0 + i, p.seq.total - 1) * p.D + cl;
-        g[i] = load_raw<TG, VEC>(static_cast<const TG*>(p.g) + at);
-        x[i] = load_raw<TX, VEC>(static_cast<const TX*>(p.x) + at);
-        d[i] = load_raw<TX, VEC>(static_cast<const TX*>(p.d_h) + at);
+        const int64_t at = (int64_t)min(w0 + i, p.seq.total - 1) * p.D + cbase;
+        g[i] = load_raw<TG, VEC>(static_cast<const TG*>(p.g) + at + lo);
+        x[i] = load_raw<TX, VEC>(static_cast<const TX*>(p.x) + at + lo);
+        d[i] = load_raw<TX, VEC>(static_cast<const TX*>(p.d_h) + at + lo);
     }
     const SeqPos s0 = seq_find(p.seq, min(w0, p.seq.total - 1));
     // all of the wave's tokens inside one sequence, neither its first nor its last among them
@@ -374,12 +410,9 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
         ragg[wave][lane * VEC + v] = make_float2(R[v], M[v]);
     }
     __syncthreads();
-    if (threadIdx.x < CH) {
-        const int64_t tc = cbase + threadIdx.x;
-        enter_tile<true, kChain, CH>(ragg, rin, ch, p.D, tc, pos, tiles, kChain ? __builtin_amdgcn_readfirstlane(sh_first) : pos);
-    } else if (threadIdx.x < 2 * CH) {
-        // the other threads: the states that enter the waves, from the tile's kept one
-        const int t = threadIdx.x - CH;
+    if (threadIdx.x >= kThreads - CH) {
+        // the states that enter the waves, from the tile's kept one
+        const int t = threadIdx.x - (kThreads - CH);
         float h = cbase + t < p.D ? p.states[(int64_t)tile * p.D + cbase + t] : 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
@@ -387,7 +420,7 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
             h = pass_on(agg[w][t].x, agg[w][t].y, h);
         }
     }
-    __syncthreads();
+    enter_tile<true, kChain, CH>(ragg, mid, rin, ch, p.D, cbase, pos, tiles, kChain ? __builtin_amdgcn_readfirstlane(sh_first) : pos);
     if (!live || w0 >= w1) return;
     float h[VEC], mu[VEC], before[kTokens][VEC];
 #pragma unroll
@@ -412,9 +445,9 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
             mu[v] = fast_exp(g[i].get(v)) * lam[v];
             dgv[v] = mu[v] * before[i][v];
         }
-        const int64_t at = (int64_t)(w0 + i) * p.D + c;
-        store_own<false, TX, VEC>(dx + at, lam, 0);
-        store_own<false, TG, VEC>(dg + at, dgv, 0);
+        const int64_t at = (int64_t)(w0 + i) * p.D + cbase;
+        store_own<false, TX, VEC>(dx + at + lo, lam, 0);
+        store_own<false, TG, VEC>(dg + at + lo, dgv, 0);
     };
     if (inside) {
 #pragma unroll
@@ -481,6 +514,11 @@ __global__ __launch_bounds__(kRowThreads) void k_gscan_rows(GScanArgs p, int cbl
     if (p.sT) store_own<false, float, VEC>(p.sT + (int64_t)s.n * p.D + c, h, 0);
 }
 
+// Tokens of a wave forward: 16 where x and g are both bf16 (as many registers as 8 with fp32 gates), for half as
+// many pairs to look back over (64K x 4096 packed: 309 -> 285 us).
+template <typename TX, typename TG>
+constexpr int fwd_tokens() { return sizeof(TX) + sizeof(TG) == 4 ? 16 : 8; }
+
 // Clears a chain: the ticket to zero, every word behind it to "not there yet".
 __global__ __launch_bounds__(256) void k_clear(u32x4* p, int64_t n) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
@@ -489,27 +527,42 @@ __global__ __launch_bounds__(256) void k_clear(u32x4* p, int64_t n) {
     }
 }
 
-int tiles_of(int64_t total) { return (int)((total + kTile - 1) / kTile); }
+int tiles_of(int64_t total, int tile) { return (int)((total + tile - 1) / tile); }
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // A chain in the workspace: 256 bytes for the ticket, the pairs, the groups' states.
-size_t chain_bytes(int64_t total, int64_t D) {
-    const size_t tiles = tiles_of(total), groups = (tiles + kGroup - 1) / kGroup;
+size_t chain_bytes(size_t tiles, int64_t D) {
+    const size_t groups = (tiles + kGroup - 1) / kGroup;
     return tiles < 2 ? 0 : 256 + align256(tiles * D * 8) + align256(groups * D * 4);
 }
-hipError_t make_chain(unsigned char* ws, int64_t total, int64_t D, Chain& ch, hipStream_t st) {
-    const size_t bytes = chain_bytes(total, D);
+hipError_t make_chain(unsigned char* ws, size_t tiles, int64_t D, Chain& ch, hipStream_t st) {
+    const size_t bytes = chain_bytes(tiles, D);
     ch.ticket = reinterpret_cast<uint32_t*>(ws);
     ch.pairs = reinterpret_cast<uint64_t*>(ws + 256);
-    ch.carry = reinterpret_cast<uint32_t*>(ws + 256 + align256((size_t)tiles_of(total) * D * 8));
+    ch.carry = reinterpret_cast<uint32_t*>(ws + 256 + align256(tiles * D * 8));
     const int64_t n = (int64_t)(bytes / 16), blocks = (n + 1023) / 1024;
     hipLaunchKernelGGL(k_clear, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, reinterpret_cast<u32x4*>(ws), n);
     return hipGetLastError();
 }
 
+template <typename TX, typename TG, int VEC, int TOK>
+hipError_t fwd_tiles(const GScanArgs& a, int cb, hipStream_t st) {
+    const int tiles = tiles_of(a.seq.total, kWaves * TOK);
+    const int extra = a.sT && a.seq.cu;
+    Chain ch{};
+    if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)(tiles + extra) * (unsigned)cb);
+    if (tiles > 1) {
+        if (hipError_t e = make_chain(a.ws, tiles, a.D, ch, st)) return e;
+        hipLaunchKernelGGL((k_gscan_fwd<TX, TG, VEC, TOK, true>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
+    } else {
+        hipLaunchKernelGGL((k_gscan_fwd<TX, TG, VEC, TOK, false>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
+    }
+    return hipGetLastError();
+}
+
 template <typename TX, typename TG, int VEC>
 hipError_t fwd_v(const GScanArgs& a, hipStream_t st) {
-    const int tiles = tiles_of(a.seq.total);
     const int cb = (int)((a.D + kWave * VEC - 1) / (kWave * VEC));
     // sequences of up to 16 tokens, or on average up to 4 where they are packed: a wave each
     if (a.seq.cu ? a.seq.total / a.seq.N <= 4 : a.seq.T <= 16) {
@@ -518,27 +571,17 @@ hipError_t fwd_v(const GScanArgs& a, hipStream_t st) {
         hipLaunchKernelGGL((k_gscan_rows<TX, TG, VEC>), dim3((unsigned)((items + per - 1) / per)), dim3(kRowThreads), 0, st, a, cb);
         return hipGetLastError();
     }
-    const int extra = a.sT && a.seq.cu;
-    Chain ch{};
-    if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)(tiles + extra) * (unsigned)cb);
-    if (tiles > 1) {
-        if (hipError_t e = make_chain(a.ws, a.seq.total, a.D, ch, st)) return e;
-        hipLaunchKernelGGL((k_gscan_fwd<TX, TG, VEC, true>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
-    } else {
-        hipLaunchKernelGGL((k_gscan_fwd<TX, TG, VEC, false>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
-    }
-    return hipGetLastError();
+    return fwd_tiles<TX, TG, VEC, fwd_tokens<TX, TG>()>(a, cb, st);
 }
 
 template <typename TX, typename TG, int VEC>
 hipError_t bwd_v(GScanArgs a, bool have, hipStream_t st) {
-    const int tiles = tiles_of(a.seq.total);
+    const int tiles = tiles_of(a.seq.total, kScanTile);
     const int cb = (int)((a.D + kWave * VEC - 1) / (kWave * VEC));
     const int extra = a.ds0 && (a.seq.cu || a.seq.T == 0);
     if (tiles + extra == 0) return hipSuccess;
     if (!have && tiles) {
-        a.states = reinterpret_cast<float*>(a.ws + chain_bytes(a.seq.total, a.D));
+        a.states = reinterpret_cast<float*>(a.ws + chain_bytes(tiles, a.D));
         GScanArgs f = a;
         f.h = nullptr;
         f.sT = nullptr;
@@ -548,7 +591,7 @@ hipError_t bwd_v(GScanArgs a, bool have, hipStream_t st) {
     if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)(tiles + extra) * (unsigned)cb);
     if (tiles > 1) {
-        if (hipError_t e = make_chain(a.ws, a.seq.total, a.D, ch, st)) return e;
+        if (hipError_t e = make_chain(a.ws, tiles, a.D, ch, st)) return e;
         hipLaunchKernelGGL((k_gscan_bwd<TX, TG, VEC, true>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
     } else {
         hipLaunchKernelGGL((k_gscan_bwd<TX, TG, VEC, false>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
@@ -568,8 +611,12 @@ hipError_t bwd_t(const GScanArgs& a, bool have, hipStream_t st) {
 
 }  // namespace
 
-size_t gscan_fwd_ws(int64_t total, int64_t D) { return chain_bytes(total, D); }
-size_t gscan_bwd_ws(int64_t total, int64_t D) { return chain_bytes(total, D) + (size_t)tiles_of(total) * D * 4; }
+// (sized for 64-token tiles, whatever the types)
+size_t gscan_fwd_ws(int64_t total, int64_t D) { return chain_bytes(tiles_of(total, kScanTile), D); }
+size_t gscan_bwd_ws(int64_t total, int64_t D) {
+    const size_t tiles = tiles_of(total, kScanTile);
+    return chain_bytes(tiles, D) + tiles * D * 4;
+}
 
 // dtype, g_dtype: gdn_dtype (0 bf16, 1 fp32); g in the type of x or fp32
 hipError_t launch_gscan_fwd(const GScanArgs& a, int dtype, int g_dtype, hipStream_t st) {
