@@ -48,6 +48,26 @@ def _like(name, t, shape, dtype, device):
     return t.data_ptr()
 
 
+def _out(name, t, x, shape, dtype, device):
+    """(tensor, pointer) of a caller's output, or of a new one."""
+    if t is None:
+        t = x.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    return t, _like(name, t, shape, dtype, device)
+
+
+def _outs(out, x, device, **want):
+    """(dict, its pointers in order) of a backward's outputs, name=(shape, dtype, whether a new dict has it): new
+    ones, or the caller's, which must hold all but the ones that may be left out (a state's or a bias's)."""
+    if out is None:
+        out = {k: x.new_empty(shape, dtype=dtype) if need else None for k, (shape, dtype, need) in want.items()}
+        return (out, *(None if t is None else t.data_ptr() for t in out.values()))
+    for k in ("dx", "dg", "dweight"):
+        if k in want and want[k][2] and out.get(k) is None:
+            raise ValueError(f"out[{k!r}] is required")
+    return (out, *(_like(f"out[{k!r}]", out.get(k), shape, dtype, device) for k, (shape, dtype, _) in want.items()))
+
+
 def _second_type(name, t, x) -> int:
     if not isinstance(t, torch.Tensor) or (t.dtype != x.dtype and t.dtype != torch.float32):
         raise ValueError(f"{name}: expected {x.dtype} or fp32")
@@ -83,8 +103,13 @@ def _on(device):
     return _HERE if torch.cuda.current_device() == device.index else _other_device(device)
 
 
+# The current stream's handle. The first form gives it without building a Stream object (0.1 against 1.9 us of a
+# decoding call's 10); it is not in torch's public interface, so the public one stands in where it is missing.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_of(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _scratch(nbytes, device, workspace):
@@ -149,14 +174,11 @@ def gdn_gated_scan_fwd(x, g, initial_state=None, *, cu_seqlens=None, output_fina
     shape, dev = x.shape, x.device
     pg = _like("g", g, shape, g.dtype, dev)
     p0 = _like("initial_state", initial_state, (N, shape[2]), torch.float32, dev)
-    if h is None:
-        h = torch.empty_like(x)
-    ph = _like("h", h, shape, x.dtype, dev)
-    if not output_final_state:
-        final_state = None
-    elif final_state is None:
-        final_state = torch.empty((N, shape[2]), dtype=torch.float32, device=dev)
-    pT = _like("final_state", final_state, (N, shape[2]), torch.float32, dev)
+    h, ph = _out("h", h, x, shape, x.dtype, dev)
+    if output_final_state:
+        final_state, pT = _out("final_state", final_state, x, (N, shape[2]), torch.float32, dev)
+    else:
+        final_state = pT = None
     ps = _check_states(states, x)
     lib = load_library()
     with _on(dev):
@@ -180,16 +202,8 @@ def gdn_gated_scan_bwd(x, g, d_h, initial_state=None, d_final_state=None, *, cu_
     p0 = _like("initial_state", initial_state, (N, shape[2]), torch.float32, dev)
     pd = _like("d_h", d_h, shape, x.dtype, dev)
     pT = _like("d_final_state", d_final_state, (N, shape[2]), torch.float32, dev)
-    if out is None:
-        out = dict(dx=torch.empty_like(x), dg=torch.empty_like(g),
-                   d_initial_state=(torch.empty((N, shape[2]), dtype=torch.float32, device=dev)
-                                    if need_d_initial_state else None))
-    for name in ("dx", "dg"):
-        if out.get(name) is None:
-            raise ValueError(f"out[{name!r}] is required")
-    px = _like("out['dx']", out["dx"], shape, x.dtype, dev)
-    pdg = _like("out['dg']", out["dg"], shape, g.dtype, dev)
-    pd0 = _like("out['d_initial_state']", out.get("d_initial_state"), (N, shape[2]), torch.float32, dev)
+    out, px, pdg, pd0 = _outs(out, x, dev, dx=(shape, x.dtype, True), dg=(shape, g.dtype, True),
+                              d_initial_state=((N, shape[2]), torch.float32, need_d_initial_state))
     ps = _check_states(states, x)
     lib = load_library()
     with _on(dev):
@@ -232,12 +246,10 @@ def gdn_short_conv_fwd(x, weight, bias=None, initial_state=None, *, activation="
     shape, dev = x.shape, x.device
     sshape = (N, W - 1, shape[2])
     p0 = _like("initial_state", initial_state, sshape, x.dtype, dev)
-    if y is None:
-        y = torch.empty_like(x)
-    py = _like("y", y, shape, x.dtype, dev)
-    if final_state is None and output_final_state:
-        final_state = torch.empty(sshape, dtype=x.dtype, device=dev)
-    pT = _like("final_state", final_state, sshape, x.dtype, dev)
+    y, py = _out("y", y, x, shape, x.dtype, dev)
+    pT = None
+    if final_state is not None or output_final_state:
+        final_state, pT = _out("final_state", final_state, x, sshape, x.dtype, dev)
     lib = load_library()
     with _on(dev):
         check(lib.gdn_short_conv_fwd(ctypes.byref(desc), x.data_ptr(), pw, pb, p0, py, pT, _stream_of(dev)),
@@ -258,17 +270,9 @@ def gdn_short_conv_bwd(x, weight, d_y, bias=None, initial_state=None, d_final_st
     p0 = _like("initial_state", initial_state, sshape, x.dtype, dev)
     pd = _like("d_y", d_y, shape, x.dtype, dev)
     pT = _like("d_final_state", d_final_state, sshape, x.dtype, dev)
-    if out is None:
-        out = dict(dx=torch.empty_like(x), dweight=torch.empty((D, W), dtype=torch.float32, device=dev),
-                   dbias=None if bias is None else torch.empty((D,), dtype=torch.float32, device=dev),
-                   d_initial_state=torch.empty(sshape, dtype=x.dtype, device=dev) if need_d_initial_state else None)
-    for name in ("dx", "dweight"):
-        if out.get(name) is None:
-            raise ValueError(f"out[{name!r}] is required")
-    px = _like("out['dx']", out["dx"], shape, x.dtype, dev)
-    pdw = _like("out['dweight']", out["dweight"], (D, W), torch.float32, dev)
-    pdb = _like("out['dbias']", out.get("dbias"), (D,), torch.float32, dev)
-    pd0 = _like("out['d_initial_state']", out.get("d_initial_state"), sshape, x.dtype, dev)
+    out, px, pdw, pdb, pd0 = _outs(out, x, dev, dx=(shape, x.dtype, True), dweight=((D, W), torch.float32, True),
+                                   dbias=((D,), torch.float32, bias is not None),
+                                   d_initial_state=(sshape, x.dtype, need_d_initial_state))
     lib = load_library()
     with _on(dev):
         need = _bytes(lib.gdn_short_conv_bwd_workspace_size, desc, "gdn_short_conv_bwd_workspace_size")
@@ -307,9 +311,9 @@ def gdn_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, quant=None, y=None, r
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out without a residual")
-    elif residual_out is None:
-        residual_out = torch.empty_like(x)
-    po = _like("residual_out", residual_out, shape, x.dtype, dev)
+        po = None
+    else:
+        residual_out, po = _out("residual_out", residual_out, x, shape, x.dtype, dev)
     if quant is None:
         if scale is not None:
             raise ValueError("scale without quant")
@@ -319,12 +323,8 @@ def gdn_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, quant=None, y=None, r
             raise ValueError("quant: expected None, 'row' or 'group'")
         desc.out_type, desc.scale_group, ydt = GDN_OUT_E4M3, _QUANT[quant], torch.float8_e4m3fn
         sshape = (*shape[:-1], 1 if quant == "row" else -(-D // 128))
-        if scale is None:
-            scale = torch.empty(sshape, dtype=torch.float32, device=dev)
-        psc = _like("scale", scale, sshape, torch.float32, dev)
-    if y is None:
-        y = torch.empty(shape, dtype=ydt, device=dev)
-    py = _like("y", y, shape, ydt, dev)
+        scale, psc = _out("scale", scale, x, sshape, torch.float32, dev)
+    y, py = _out("y", y, x, shape, ydt, dev)
     lib = load_library()
     with _on(dev):
         check(lib.gdn_rmsnorm_fwd(ctypes.byref(desc), x.data_ptr(), pr, pw, py, psc, po, _stream_of(dev)),
@@ -342,13 +342,9 @@ def gdn_rmsnorm_bwd(r, weight, d_y, d_residual=None, *, eps=1e-6, need_dweight=T
         raise ValueError("d_y is required")
     pd = _like("d_y", d_y, shape, r.dtype, dev)
     pr = _like("d_residual", d_residual, shape, r.dtype, dev)
-    if out is None:
-        out = dict(dx=torch.empty_like(r),
-                   dweight=torch.empty((D,), dtype=torch.float32, device=dev) if need_dweight else None)
-    if out.get("dx") is None:
-        raise ValueError("out['dx'] is required")
-    px = _like("out['dx']", out["dx"], shape, r.dtype, dev)
-    pdw = _like("out['dweight']", out.get("dweight"), (D,), torch.float32, dev)
+    if out is not None:
+        need_dweight = out.get("dweight") is not None
+    out, px, pdw = _outs(out, r, dev, dx=(shape, r.dtype, True), dweight=((D,), torch.float32, need_dweight))
     lib = load_library()
     with _on(dev):
         need = _bytes(lib.gdn_rmsnorm_bwd_workspace_size, desc, "gdn_rmsnorm_bwd_workspace_size")
