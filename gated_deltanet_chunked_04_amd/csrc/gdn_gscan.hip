@@ -13,7 +13,7 @@
 //   * Tiles are handed out in the order of the token axis by a counter, so a tile only ever waits for
 //     tiles that are running or done, and those publish their pairs before they wait themselves.
 //   * What is added to what is fixed by the tile's place, not by who was ready first, so results are
-//     the same bits every time: the state entering a group of 8 tiles comes from the group before it
+//     the same bits every time: the state entering a group of tiles comes from the group before it
 //     as one published value, the tiles inside the group combine the pairs since then.
 // Published words carry their own mark (all ones: not there yet), so no other ordering of memory is
 // needed; a small launch clears them first. The gradient runs the same from the other end, and
@@ -29,13 +29,13 @@ constexpr int kWaves = 8;              // waves of a tile
 constexpr int kThreads = kWaves * kWave;
 constexpr int kBwdTokens = 8;          // tokens of a wave in the gradient
 static_assert(kWaves * kBwdTokens == kScanTile, "a kept state per tile of the gradient");
-constexpr int kGroup = 8;              // tiles between two published entering states
 constexpr int kMaxSpins = 1 << 20;     // (about a second) a wait gives up with NaN rather than hang
 
 struct Chain {
     uint32_t* ticket;
     uint64_t* pairs;  // [tiles, D], in the order of the chain: A in the high word, H in the low one
     uint32_t* carry;  // [groups, D]: the state that enters the group
+    int group;        // tiles between two published entering states
 };
 
 // A c + H. A with its sign bit set marks a run in which a sequence starts: nothing of c passes, whatever it
@@ -111,7 +111,7 @@ __device__ __forceinline__ void enter_tile(const float2 (*agg)[CH], float2 (*mid
                 publish(ch.pairs + (int64_t)pos * D + c, ((uint64_t)__float_as_uint(A) << 32) | mark(H));
         }
         if (first < pos) {
-            const int group = pos / kGroup, begin = group * kGroup;
+            const int group = pos / ch.group, begin = group * ch.group;
             const bool carried = first < begin;  // the state comes from the group before
             const int from = carried ? begin : first, each = (pos - from + kParts - 1) / kParts;
             const uint32_t* word = ch.carry + (int64_t)group * D + c;
@@ -139,8 +139,8 @@ __device__ __forceinline__ void enter_tile(const float2 (*agg)[CH], float2 (*mid
                 for (int q = 0; q < kParts; ++q) s = pass_on(mid[q][t].x, mid[q][t].y, s);
             }
         }
-        if (part == 0 && live && (pos + 1) % kGroup == 0 && pos + 1 < tiles)
-            publish(ch.carry + (int64_t)((pos + 1) / kGroup) * D + c, mark(pass_on(A, H, s)));
+        if (part == 0 && live && (pos + 1) % ch.group == 0 && pos + 1 < tiles)
+            publish(ch.carry + (int64_t)((pos + 1) / ch.group) * D + c, mark(pass_on(A, H, s)));
         asm volatile("" ::: "memory");  // the waves' pairs are read again rather than held through the wait
     }
     if (part == 0)
@@ -170,15 +170,14 @@ __device__ __forceinline__ void state_of(const float* s, int32_t n, int64_t D, i
 }
 
 // Sequences without tokens: their state (or its gradient) passes through, by the workgroups behind the tiles.
-template <int VEC>
-__device__ void pass_empty(const GScanArgs& p, const float* in, float* out, int64_t c) {
-    if (c >= p.D) return;
+template <bool kOdd, int VEC>
+__device__ void pass_empty(const GScanArgs& p, const float* in, float* out, int64_t c, int skip) {
     for (int32_t n = wave_id(); n < p.seq.N; n += kWaves) {
         const SeqPos q = seq_at(p.seq, n);
         if (q.start < q.end) continue;
         float x[VEC];
         state_of<VEC>(in, n, p.D, c, x);
-        store_own<false, float, VEC>(out + (int64_t)n * p.D + c, x, 0);
+        store_own<kOdd, float, VEC>(out + (int64_t)n * p.D + c, x, skip);
     }
 }
 
@@ -190,7 +189,7 @@ __device__ __forceinline__ int take(const Chain& ch, bool chain, int* sh) {
     return __builtin_amdgcn_readfirstlane(*sh);
 }
 
-template <typename TX, typename TG, int VEC, int kTokens, bool kChain>
+template <bool kOdd, typename TX, typename TG, int VEC, int kTokens, bool kChain>
 __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, int cblocks, Chain ch) {
     constexpr int kTile = kWaves * kTokens;
     constexpr int kKeep = kScanTile / kTokens;  // waves between two kept states
@@ -202,17 +201,20 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
     const int id = take(ch, kChain, &sh_id);
     const int tile = id / cblocks, lane = threadIdx.x & 63, wave = wave_id();
     const int64_t cbase = (int64_t)(id % cblocks) * CH;
-    const int64_t c = cbase + lane * VEC;
-    if (tile == tiles) return pass_empty<VEC>(p, p.s0, p.sT, c);
-    const bool live = c < p.D;
-    const int64_t cl = live ? c : 0;
+    const bool live = cbase + lane * VEC < p.D;
+    const Lane ln(cbase + lane * VEC, p.D, VEC);
+    const int skip = kOdd ? ln.skip : 0;
+    const int lo = live ? lane * VEC - skip : 0;  // the lane's first channel, from the block's
+    const int64_t c = cbase + lo;
+    if (tile == tiles) {
+        if (live) pass_empty<kOdd, VEC>(p, p.s0, p.sT, c, skip);
+        return;
+    }
     const int64_t w0l = (int64_t)tile * kTile + wave * kTokens;
     const int32_t w0 = w0l < p.seq.total ? (int32_t)w0l : p.seq.total;
     const int32_t w1 = p.seq.total - w0 < kTokens ? p.seq.total : w0 + kTokens;
     Raw<TX, VEC> x[kTokens];
     Raw<TG, VEC> g[kTokens];
-    // a uniform row address and a 32-bit lane offset
-    const uint32_t lo = live ? lane * VEC : 0;
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
         const int64_t at = (int64_t)min(w0 + i, p.seq.total - 1) * p.D + cbase;
@@ -251,7 +253,7 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
             if (t < s.start || t >= s.end) continue;
             if (t == s.start) {
                 last_n = s.n;
-                state_of<VEC>(p.s0, s.n, p.D, cl, last);
+                state_of<VEC>(p.s0, s.n, p.D, c, last);
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     A[v] = -1.f;
@@ -262,25 +264,26 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
         }
     }
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) agg[wave][lane * VEC + v] = make_float2(A[v], H[v]);
+    for (int v = 0; v < VEC; ++v)
+        if (!kOdd || (live && v >= skip)) agg[wave][lo + v] = make_float2(A[v], H[v]);
     __syncthreads();
     enter_tile<false, kChain, CH>(agg, mid, cin, ch, p.D, cbase, tile, tiles, kChain ? __builtin_amdgcn_readfirstlane(sh_first) : tile);
     float h[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) h[v] = cin[wave][lane * VEC + v];
+    for (int v = 0; v < VEC; ++v) h[v] = cin[wave][kOdd ? max(lo + v, 0) : lo + v];
     if (!live || w0 >= w1) return;
     if (p.states && wave % kKeep == 0)
-        store_own<false, float, VEC>(p.states + (int64_t)(w0 / kScanTile) * p.D + c, h, 0);
+        store_own<kOdd, float, VEC>(p.states + (int64_t)(w0 / kScanTile) * p.D + c, h, skip);
     TX* out = static_cast<TX*>(p.h);
     auto step = [&](int i) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) h[v] = fmaf(fast_exp(g[i].get(v)), h[v], x[i].get(v));
-        if (out) store_own<false, TX, VEC>(out + ((int64_t)(w0 + i) * p.D + cbase) + lo, h, 0);
+        if (out) store_own<kOdd, TX, VEC>(out + ((int64_t)(w0 + i) * p.D + cbase) + lo, h, skip);
     };
     if (inside) {
 #pragma unroll
         for (int i = 0; i < kTokens; ++i) step(i);
-        if (p.sT && w1 == s0.end) store_own<false, float, VEC>(p.sT + (int64_t)s0.n * p.D + c, h, 0);
+        if (p.sT && w1 == s0.end) store_own<kOdd, float, VEC>(p.sT + (int64_t)s0.n * p.D + c, h, skip);
         return;
     }
     SeqPos s = s0;
@@ -301,11 +304,11 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
             }
         }
         step(i);
-        if (p.sT && t + 1 == s.end) store_own<false, float, VEC>(p.sT + (int64_t)s.n * p.D + c, h, 0);
+        if (p.sT && t + 1 == s.end) store_own<kOdd, float, VEC>(p.sT + (int64_t)s.n * p.D + c, h, skip);
     }
 }
 
-template <typename TX, typename TG, int VEC, bool kChain>
+template <bool kOdd, typename TX, typename TG, int VEC, bool kChain>
 __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, int cblocks, Chain ch) {
     constexpr int kTokens = kBwdTokens, kTile = kScanTile;
     constexpr int CH = kWave * VEC;
@@ -318,16 +321,20 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
     const int id = take(ch, kChain, &sh_id);
     const int pos = id / cblocks, tile = tiles - 1 - pos, lane = threadIdx.x & 63, wave = wave_id();
     const int64_t cbase = (int64_t)(id % cblocks) * CH;
-    const int64_t c = cbase + lane * VEC;
-    if (pos == tiles) return pass_empty<VEC>(p, p.d_sT, p.ds0, c);
-    const bool live = c < p.D;
-    const int64_t cl = live ? c : 0;
+    const bool live = cbase + lane * VEC < p.D;
+    const Lane ln(cbase + lane * VEC, p.D, VEC);
+    const int skip = kOdd ? ln.skip : 0;
+    const int lo = live ? lane * VEC - skip : 0;
+    const int64_t c = cbase + lo;
+    if (pos == tiles) {
+        if (live) pass_empty<kOdd, VEC>(p, p.d_sT, p.ds0, c, skip);
+        return;
+    }
     const int64_t w0l = (int64_t)tile * kTile + wave * kTokens;
     const int32_t w0 = w0l < p.seq.total ? (int32_t)w0l : p.seq.total;
     const int32_t w1 = p.seq.total - w0 < kTokens ? p.seq.total : w0 + kTokens;
     Raw<TX, VEC> x[kTokens], d[kTokens];
     Raw<TG, VEC> g[kTokens];
-    const uint32_t lo = live ? lane * VEC : 0;
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
         const int64_t at = (int64_t)min(w0 + i, p.seq.total - 1) * p.D + cbase;
@@ -374,7 +381,7 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
             seq_advance(p.seq, s, t);
             if (t < s.start || t >= s.end) continue;
             if (t == s.start) {
-                state_of<VEC>(p.s0, s.n, p.D, cl, H);
+                state_of<VEC>(p.s0, s.n, p.D, c, H);
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) A[v] = -1.f;
             }
@@ -392,7 +399,7 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
             const SeqPos e = seq_find(p.seq, t);
             if (t < e.start || t >= e.end) continue;
             if (t + 1 == e.end) {
-                state_of<VEC>(p.d_sT, e.n, p.D, cl, M);
+                state_of<VEC>(p.d_sT, e.n, p.D, c, M);
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) R[v] = -1.f;
             }
@@ -406,8 +413,10 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
     }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-        agg[wave][lane * VEC + v] = make_float2(A[v], H[v]);
-        ragg[wave][lane * VEC + v] = make_float2(R[v], M[v]);
+        if (!kOdd || (live && v >= skip)) {
+            agg[wave][lo + v] = make_float2(A[v], H[v]);
+            ragg[wave][lo + v] = make_float2(R[v], M[v]);
+        }
     }
     __syncthreads();
     if (threadIdx.x >= kThreads - CH) {
@@ -425,8 +434,8 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
     float h[VEC], mu[VEC], before[kTokens][VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-        h[v] = cin[wave][lane * VEC + v];
-        mu[v] = rin[wave][lane * VEC + v];
+        h[v] = cin[wave][kOdd ? max(lo + v, 0) : lo + v];
+        mu[v] = rin[wave][kOdd ? max(lo + v, 0) : lo + v];
     }
     TX* dx = static_cast<TX*>(p.dx);
     TG* dg = static_cast<TG*>(p.dg);
@@ -446,8 +455,8 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
             dgv[v] = mu[v] * before[i][v];
         }
         const int64_t at = (int64_t)(w0 + i) * p.D + cbase;
-        store_own<false, TX, VEC>(dx + at + lo, lam, 0);
-        store_own<false, TG, VEC>(dg + at + lo, dgv, 0);
+        store_own<kOdd, TX, VEC>(dx + at + lo, lam, skip);
+        store_own<kOdd, TG, VEC>(dg + at + lo, dgv, skip);
     };
     if (inside) {
 #pragma unroll
@@ -474,19 +483,22 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
         if (t < e.start || t >= e.end) continue;
         if (t + 1 == e.end) state_of<VEC>(p.d_sT, e.n, p.D, c, mu);
         back(i);
-        if (p.ds0 && t == e.start) store_own<false, float, VEC>(p.ds0 + (int64_t)e.n * p.D + c, mu, 0);
+        if (p.ds0 && t == e.start) store_own<kOdd, float, VEC>(p.ds0 + (int64_t)e.n * p.D + c, mu, skip);
     }
 }
 
 // Short sequences (decoding): a wave per sequence and block of channels walks the tokens; one launch, no workspace.
 constexpr int kRowThreads = 256;
-template <typename TX, typename TG, int VEC>
+template <bool kOdd, typename TX, typename TG, int VEC>
 __global__ __launch_bounds__(kRowThreads) void k_gscan_rows(GScanArgs p, int cblocks) {
     const int64_t item = (int64_t)blockIdx.x * (kRowThreads / kWave) + wave_id();
     const int64_t nl = item / cblocks;
     if (nl >= p.seq.N) return;
-    const int64_t c = ((item % cblocks) * kWave + (threadIdx.x & 63)) * VEC;
-    if (c >= p.D) return;
+    const int64_t c0 = ((item % cblocks) * kWave + (threadIdx.x & 63)) * VEC;
+    if (c0 >= p.D) return;
+    const Lane ln(c0, p.D, VEC);
+    const int64_t c = ln.at;
+    const int skip = kOdd ? ln.skip : 0;
     const SeqPos s = seq_at(p.seq, (int32_t)nl);
     float h[VEC];
     state_of<VEC>(p.s0, s.n, p.D, c, h);
@@ -506,12 +518,12 @@ __global__ __launch_bounds__(kRowThreads) void k_gscan_rows(GScanArgs p, int cbl
             nx = load_raw<TX, VEC>(x + (int64_t)(t + 1) * p.D);
             ng = load_raw<TG, VEC>(g + (int64_t)(t + 1) * p.D);
         }
-        if (p.states && t % kScanTile == 0) store_own<false, float, VEC>(p.states + (int64_t)(t / kScanTile) * p.D + c, h, 0);
+        if (p.states && t % kScanTile == 0) store_own<kOdd, float, VEC>(p.states + (int64_t)(t / kScanTile) * p.D + c, h, skip);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) h[v] = fmaf(fast_exp(gt.get(v)), h[v], xt.get(v));
-        if (out) store_own<false, TX, VEC>(out + (int64_t)t * p.D + c, h, 0);
+        if (out) store_own<kOdd, TX, VEC>(out + (int64_t)t * p.D + c, h, skip);
     }
-    if (p.sT) store_own<false, float, VEC>(p.sT + (int64_t)s.n * p.D + c, h, 0);
+    if (p.sT) store_own<kOdd, float, VEC>(p.sT + (int64_t)s.n * p.D + c, h, skip);
 }
 
 // Tokens of a wave forward: 16 where x and g are both bf16 (as many registers as 8 with fp32 gates), for half as
@@ -530,13 +542,23 @@ __global__ __launch_bounds__(256) void k_clear(u32x4* p, int64_t n) {
 int tiles_of(int64_t total, int tile) { return (int)((total + tile - 1) / tile); }
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// Four channels per lane, or one in rows so short that a wave would not be filled.
+constexpr int64_t kSlim = 128;
+
 // A chain in the workspace: 256 bytes for the ticket, the pairs, the groups' states.
+constexpr int kMinGroup = 8;
 size_t chain_bytes(size_t tiles, int64_t D) {
-    const size_t groups = (tiles + kGroup - 1) / kGroup;
+    const size_t groups = (tiles + kMinGroup - 1) / kMinGroup;
     return tiles < 2 ? 0 : 256 + align256(tiles * D * 8) + align256(groups * D * 4);
 }
-hipError_t make_chain(unsigned char* ws, size_t tiles, int64_t D, Chain& ch, hipStream_t st) {
+// A group hands its state on in about a microsecond, one group after the other, while a tile looks back over half
+// a group's pairs. With eight channel blocks or more to a tile the memory takes longer than the chain and small
+// groups read less (32K x 2048 fp32 gates: groups of 8 110 us, 16 109, 32 119; 64K x 4096 bf16 gates: 285, 288, -).
+// With fewer, longer groups keep the chain short (64K tokens of 1024 channels: 8 138 us, 16 115; of 256: 8 101,
+// 32 51, 64 49; of 64: 8 116, 32 46, 64 35).
+hipError_t make_chain(unsigned char* ws, size_t tiles, int64_t D, int cblocks, Chain& ch, hipStream_t st) {
     const size_t bytes = chain_bytes(tiles, D);
+    ch.group = cblocks >= 8 ? kMinGroup : (cblocks >= 4 ? 16 : (D >= kSlim ? 32 : 64));
     ch.ticket = reinterpret_cast<uint32_t*>(ws);
     ch.pairs = reinterpret_cast<uint64_t*>(ws + 256);
     ch.carry = reinterpret_cast<uint32_t*>(ws + 256 + align256(tiles * D * 8));
@@ -545,7 +567,7 @@ hipError_t make_chain(unsigned char* ws, size_t tiles, int64_t D, Chain& ch, hip
     return hipGetLastError();
 }
 
-template <typename TX, typename TG, int VEC, int TOK>
+template <bool kOdd, typename TX, typename TG, int VEC, int TOK>
 hipError_t fwd_tiles(const GScanArgs& a, int cb, hipStream_t st) {
     const int tiles = tiles_of(a.seq.total, kWaves * TOK);
     const int extra = a.sT && a.seq.cu;
@@ -553,28 +575,28 @@ hipError_t fwd_tiles(const GScanArgs& a, int cb, hipStream_t st) {
     if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)(tiles + extra) * (unsigned)cb);
     if (tiles > 1) {
-        if (hipError_t e = make_chain(a.ws, tiles, a.D, ch, st)) return e;
-        hipLaunchKernelGGL((k_gscan_fwd<TX, TG, VEC, TOK, true>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
+        if (hipError_t e = make_chain(a.ws, tiles, a.D, cb, ch, st)) return e;
+        hipLaunchKernelGGL((k_gscan_fwd<kOdd, TX, TG, VEC, TOK, true>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
     } else {
-        hipLaunchKernelGGL((k_gscan_fwd<TX, TG, VEC, TOK, false>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
+        hipLaunchKernelGGL((k_gscan_fwd<kOdd, TX, TG, VEC, TOK, false>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
     }
     return hipGetLastError();
 }
 
-template <typename TX, typename TG, int VEC>
+template <bool kOdd, typename TX, typename TG, int VEC>
 hipError_t fwd_v(const GScanArgs& a, hipStream_t st) {
     const int cb = (int)((a.D + kWave * VEC - 1) / (kWave * VEC));
     // sequences of up to 16 tokens, or on average up to 4 where they are packed: a wave each
     if (a.seq.cu ? a.seq.total / a.seq.N <= 4 : a.seq.T <= 16) {
         const int64_t items = (int64_t)a.seq.N * cb, per = kRowThreads / kWave;
         if (!grid_fits((items + per - 1) / per, kRowThreads)) return hipErrorInvalidConfiguration;
-        hipLaunchKernelGGL((k_gscan_rows<TX, TG, VEC>), dim3((unsigned)((items + per - 1) / per)), dim3(kRowThreads), 0, st, a, cb);
+        hipLaunchKernelGGL((k_gscan_rows<kOdd, TX, TG, VEC>), dim3((unsigned)((items + per - 1) / per)), dim3(kRowThreads), 0, st, a, cb);
         return hipGetLastError();
     }
-    return fwd_tiles<TX, TG, VEC, fwd_tokens<TX, TG>()>(a, cb, st);
+    return fwd_tiles<kOdd, TX, TG, VEC, fwd_tokens<TX, TG>()>(a, cb, st);
 }
 
-template <typename TX, typename TG, int VEC>
+template <bool kOdd, typename TX, typename TG, int VEC>
 hipError_t bwd_v(GScanArgs a, bool have, hipStream_t st) {
     const int tiles = tiles_of(a.seq.total, kScanTile);
     const int cb = (int)((a.D + kWave * VEC - 1) / (kWave * VEC));
@@ -585,28 +607,29 @@ hipError_t bwd_v(GScanArgs a, bool have, hipStream_t st) {
         GScanArgs f = a;
         f.h = nullptr;
         f.sT = nullptr;
-        if (hipError_t e = fwd_v<TX, TG, VEC>(f, st)) return e;
+        if (hipError_t e = fwd_v<kOdd, TX, TG, VEC>(f, st)) return e;
     }
     Chain ch{};
     if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)(tiles + extra) * (unsigned)cb);
     if (tiles > 1) {
-        if (hipError_t e = make_chain(a.ws, tiles, a.D, ch, st)) return e;
-        hipLaunchKernelGGL((k_gscan_bwd<TX, TG, VEC, true>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
+        if (hipError_t e = make_chain(a.ws, tiles, a.D, cb, ch, st)) return e;
+        hipLaunchKernelGGL((k_gscan_bwd<kOdd, TX, TG, VEC, true>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
     } else {
-        hipLaunchKernelGGL((k_gscan_bwd<TX, TG, VEC, false>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
+        hipLaunchKernelGGL((k_gscan_bwd<kOdd, TX, TG, VEC, false>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
     }
     return hipGetLastError();
 }
 
-// Four channels per lane where the rows are whole vectors of four, else one.
 template <typename TX, typename TG>
 hipError_t fwd_t(const GScanArgs& a, hipStream_t st) {
-    return a.D % 4 == 0 && a.D >= 128 ? fwd_v<TX, TG, 4>(a, st) : fwd_v<TX, TG, 1>(a, st);
+    if (a.D < kSlim) return fwd_v<false, TX, TG, 1>(a, st);
+    return a.D % 4 ? fwd_v<true, TX, TG, 4>(a, st) : fwd_v<false, TX, TG, 4>(a, st);
 }
 template <typename TX, typename TG>
 hipError_t bwd_t(const GScanArgs& a, bool have, hipStream_t st) {
-    return a.D % 4 == 0 && a.D >= 128 ? bwd_v<TX, TG, 4>(a, have, st) : bwd_v<TX, TG, 1>(a, have, st);
+    if (a.D < kSlim) return bwd_v<false, TX, TG, 1>(a, have, st);
+    return a.D % 4 ? bwd_v<true, TX, TG, 4>(a, have, st) : bwd_v<false, TX, TG, 4>(a, have, st);
 }
 
 }  // namespace
