@@ -11,6 +11,8 @@
 // last W-1 inputs, and in the gradient the last W-1 dz, in registers; only the W-1 tokens around the
 // ends of a run are read by two waves. The next tokens' loads are issued before the present ones
 // are used. Runs that lie inside one sequence take a path without any test per token.
+#include <type_traits>
+
 #include "gdn_layer.h"
 #include "gdn_vec.h"
 
@@ -169,7 +171,7 @@ __global__ __launch_bounds__(kThreads) void k_conv_fwd(ConvArgs p, int run, int 
     }
 }
 
-// One workgroup: kWaves runs of `run` tokens and 64 VEC channels; the partial sums of dw and dbias over
+// One workgroup: kWaves runs of `run` tokens (a multiple of 2 U) and 64 VEC channels; the partial sums of dw and dbias over
 // its tokens go to part[block], [W + 1, D] (the taps, then the bias).
 template <bool kOdd, typename T, typename TW, int W, int VEC, int U>
 __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int token_blocks, int cblocks, float* part) {
@@ -191,16 +193,19 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
         const int32_t w0 = (int32_t)w0l;
         const int32_t w1 = w0l + run < p.seq.total ? w0 + run : p.seq.total;
         const int32_t w2 = min(w1 + W - 1, p.seq.total);  // dx of the run's last tokens needs dz up to here
-        Raw<T, VEC> nx[U], nd[U];
-        auto fetch = [&](int32_t t0) {
+        struct Pair {
+            Raw<T, VEC> x, d;
+        };
+        auto fetch = [&](int32_t t, Pair (&q)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int32_t t = min(t0 + u, w2 - 1);
-                nx[u] = row<T, VEC>(p.x, t, p, c0);
-                nd[u] = row<T, VEC>(p.d_y, t, p, c0);
+                const int32_t at = min(t + u, w2 - 1);
+                q[u].x = row<T, VEC>(p.x, at, p, c0);
+                q[u].d = row<T, VEC>(p.d_y, at, p, c0);
             }
         };
-        fetch(w0);
+        Pair qa[U];
+        fetch(w0, qa);
         Filter<TW, W, VEC> f;
         f.load(p, c0);
         SeqPos s = seq_find(p.seq, w0);
@@ -221,20 +226,20 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
         T* dx = static_cast<T*>(p.dx);
         // dz of a token, its part of the sums (own: the token is one of the run's), and the gradient of the
         // input W-1 positions back, which is whole now
-        auto token = [&](const Raw<T, VEC>& rx, const Raw<T, VEC>& rd, bool own, float (&back)[VEC]) {
+        auto token = [&](const Pair& q, auto silu, bool own, float (&back)[VEC]) {
             float x[VEC], z[VEC], dz[VEC];
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) x[v] = rx.get(v);
-            if (p.silu) {
+            for (int v = 0; v < VEC; ++v) x[v] = q.x.get(v);
+            if constexpr (silu.value) {
                 pre_act<TW, W, VEC>(f, win, x, z);
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     const float sg = sigmoid(z[v]);
-                    dz[v] = rd.get(v) * (sg * (1.f + z[v] * (1.f - sg)));
+                    dz[v] = q.d.get(v) * (sg * (1.f + z[v] * (1.f - sg)));
                 }
             } else {
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) dz[v] = rd.get(v);
+                for (int v = 0; v < VEC; ++v) dz[v] = q.d.get(v);
             }
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
@@ -254,6 +259,33 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
             shift_in<W, VEC>(win, x);
             shift_in<W, VEC>(dzw, dz);
         };
+        // Inside one sequence: blocks of U tokens, the next two in flight, in two buffers that take turns. The
+        // first W-1 results belong to the wave before; W-1 tokens behind the run complete its last ones.
+        auto inside = [&](auto silu) {
+            static_assert(U >= W - 1, "the tokens behind the run fit one block");
+            auto block = [&](const Pair (&q)[U], int32_t t, int from, int to, bool own) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (u >= to) break;
+                    float back[VEC];
+                    token(q[u], silu, own, back);
+                    if (u >= from) store_own<kOdd, T, VEC>(dx + (int64_t)(t + u - (W - 1)) * p.D + c0, back, ln.skip);
+                }
+            };
+            Pair qb[U];
+            fetch(w0 + U, qb);
+            block(qa, w0, W - 1, U, true);
+            fetch(w0 + 2 * U, qa);
+            int32_t t = w0 + U;
+            for (; t + U < w1; t += 2 * U) {
+                block(qb, t, 0, U, true);
+                fetch(t + 2 * U, qb);
+                block(qa, t + U, 0, U, true);
+                fetch(t + 3 * U, qa);
+            }
+            block(qb, t, 0, U, true);
+            block(qa, w1, 0, W - 1, false);
+        };
         // where the gradient of position t of sequence s goes: the token's owner stores it, positions before
         // the first token (rows of the entering state) go by the first token's owner
         auto put = [&](int32_t t, const float (&d)[VEC]) {
@@ -263,29 +295,16 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
                 store_own<kOdd, T, VEC>(static_cast<T*>(p.ds0) + ((int64_t)s.n * (W - 1) + t - s.start + W - 1) * p.D + c0, d, ln.skip);
             }
         };
-        const bool inside = w0 - (W - 1) >= s.start && w2 < s.end;
-        for (int32_t t0 = w0; t0 < w2; t0 += U) {
-            Raw<T, VEC> x[U], d[U];
+        // Around the ends of sequences: token by token, U loads ahead.
+        auto across = [&](auto silu) {
+#pragma unroll 1
+            for (int32_t t = w0; t < w2; ++t) {
+                const Pair q = qa[0];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                x[u] = nx[u];
-                d[u] = nd[u];
-            }
-            if (t0 + U < w2) fetch(t0 + U);
-            if (inside && t0 + U <= w1) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float back[VEC];
-                    token(x[u], d[u], true, back);
-                    const int32_t at = t0 + u - (W - 1);
-                    if (at >= w0) store_own<kOdd, T, VEC>(dx + (int64_t)at * p.D + c0, back, ln.skip);
-                }
-                continue;
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int32_t t = t0 + u;
-                if (t >= w2) break;
+                for (int u = 0; u + 1 < U; ++u) qa[u] = qa[u + 1];
+                const int32_t at = min(t + U, w2 - 1);
+                qa[U - 1].x = row<T, VEC>(p.x, at, p, c0);
+                qa[U - 1].d = row<T, VEC>(p.d_y, at, p, c0);
                 // behind the run only the sequence that its last token is in matters
                 if (t < w1) seq_advance(p.seq, s, t);
                 if (t < s.start || t >= s.end) continue;
@@ -300,7 +319,7 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
                         }
                     }
                 float back[VEC];
-                token(x[u], d[u], t < w1, back);
+                token(q, silu, t < w1, back);
                 put(t - (W - 1), back);
                 if (t + 1 == s.end) {
                     // the last W-1 positions: no tokens behind them, but the final state's gradient
@@ -317,6 +336,14 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
                     }
                 }
             }
+        };
+        const bool in_one = w0 - (W - 1) >= s.start && w2 < s.end;  // (then the run is whole)
+        if (p.silu) {
+            if (in_one) inside(std::true_type{});
+            else across(std::true_type{});
+        } else {
+            if (in_one) inside(std::false_type{});
+            else across(std::false_type{});
         }
     }
     if (wave > 0)
@@ -342,12 +369,12 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
     store_own<kOdd, float, VEC>(out + W * p.D, db, ln.skip);
 }
 
+template <int COLS>
 __global__ __launch_bounds__(kSumThreads) void k_conv_dw_sum(const float* part, int parts, int W, int64_t D, float* dw, float* db) {
-    __shared__ float sh[kSumThreads / 4];
-    const int64_t c0 = (int64_t)blockIdx.x * 16;
-    const float s = sum_parts16(part, parts, (W + 1) * D, c0, sh);
-    const int64_t i = c0 + threadIdx.x;
-    if (threadIdx.x >= 16 || i >= (W + 1) * D) return;
+    __shared__ float sh[kSumThreads];
+    const int64_t c0 = (int64_t)blockIdx.x * COLS, i = c0 + threadIdx.x;
+    const float s = sum_parts<COLS>(part, parts, (W + 1) * D, c0, sh);
+    if (threadIdx.x >= COLS || i >= (W + 1) * D) return;
     const int64_t j = i / D, c = i % D;
     if (j < W) dw[c * W + j] = s;
     else if (db) db[c] = s;
@@ -400,12 +427,11 @@ hipError_t fwd_t(const ConvArgs& a, hipStream_t st) {
     return v == wide ? fwd_v<T, TW, W, wide>(a, st) : (v == slim ? fwd_v<T, TW, W, slim>(a, st) : fwd_v<T, TW, W, 1>(a, st));
 }
 
-// Tokens per wave in the gradient: about 4,096 waves in all, in steps of 8 tokens from 16 to 256: longer
-// runs re-read less and leave fewer partial sums.
-int bwd_run(int64_t total, unsigned cblocks) {
-    const int64_t r = (total * cblocks / 16384 + 7) / 8 * 8;
-    return (int)(r < 16 ? 16 : (r > 256 ? 256 : r));
-}
+// Tokens per wave in the gradient: 24, or 8 where 24 would leave fewer than 4,096 waves. Longer runs re-read less
+// and leave fewer partial sums, shorter ones put more waves in flight and lose less where sequences end inside
+// them (2 x 16384 x 6144 bf16, W = 4: 24 tokens 239 us, 32 253, 48 256, 64 271, 136 292; 30,000 tokens in 50
+// sequences: 234, 238, 247, 259, 320; 4,099 x 768 fp32, W = 3: 8 tokens 15.7 us, 16 19.9).
+int bwd_run(int64_t total, unsigned cblocks) { return total * cblocks >= 24 * 4096 ? 24 : 8; }
 int bwd_parts(int64_t total, int run) { return (int)((total + (int64_t)run * kWaves - 1) / ((int64_t)run * kWaves)); }
 
 template <typename T, typename TW, int W, int VEC>
@@ -421,7 +447,11 @@ hipError_t bwd_v(const ConvArgs& a, hipStream_t st) {
         if (a.D % VEC) hipLaunchKernelGGL((k_conv_bwd<(VEC > 1), T, TW, W, VEC, 4>), grid, dim3(kThreads), 0, st, a, run, parts, (int)cb, part);
         else hipLaunchKernelGGL((k_conv_bwd<false, T, TW, W, VEC, 4>), grid, dim3(kThreads), 0, st, a, run, parts, (int)cb, part);
     }
-    hipLaunchKernelGGL(k_conv_dw_sum, dim3((unsigned)(((W + 1) * a.D + 15) / 16)), dim3(kSumThreads), 0, st, part, parts, W, a.D, a.dw, a.db);
+    const int64_t n = (W + 1) * a.D;
+    const int cols = sum_cols(n);
+    const dim3 sums((unsigned)((n + cols - 1) / cols));
+    if (cols == 64) hipLaunchKernelGGL(k_conv_dw_sum<64>, sums, dim3(kSumThreads), 0, st, part, parts, W, a.D, a.dw, a.db);
+    else hipLaunchKernelGGL(k_conv_dw_sum<16>, sums, dim3(kSumThreads), 0, st, part, parts, W, a.D, a.dw, a.db);
     return hipGetLastError();
 }
 template <typename T, typename TW, int W>

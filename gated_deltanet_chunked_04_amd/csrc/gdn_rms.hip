@@ -304,11 +304,12 @@ __global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_bwd
         if (live[v]) store_own<kOdd, float, 8>(part + (int64_t)blockIdx.x * p.D + at[v], dw[v], skip[v]);
 }
 
+template <int COLS>
 __global__ __launch_bounds__(kSumThreads) void k_rms_dw_sum(const float* part, int parts, int64_t D, float* dw) {
-    __shared__ float sh[kSumThreads / 4];
-    const int64_t c0 = (int64_t)blockIdx.x * 16;
-    const float s = sum_parts16(part, parts, D, c0, sh);
-    if (threadIdx.x < 16 && c0 + threadIdx.x < D) dw[c0 + threadIdx.x] = s;
+    __shared__ float sh[kSumThreads];
+    const int64_t c0 = (int64_t)blockIdx.x * COLS;
+    const float s = sum_parts<COLS>(part, parts, D, c0, sh);
+    if (threadIdx.x < COLS && c0 + threadIdx.x < D) dw[c0 + threadIdx.x] = s;
 }
 
 // ---- rows of any length, element by element: fewer than 8 columns, or more than a workgroup's registers hold.
@@ -501,8 +502,12 @@ hipError_t bwd_o(const RmsArgs& a, hipStream_t st) {
         const unsigned cb = (unsigned)((a.D + kThreads - 1) / kThreads);
         if (a.dw) hipLaunchKernelGGL((k_rms_dw_loop<T>), dim3(cb * (unsigned)parts), dim3(kThreads), 0, st, a, rstds, part);
     }
-    if (a.dw)
-        hipLaunchKernelGGL(k_rms_dw_sum, dim3((unsigned)((a.D + 15) / 16)), dim3(kSumThreads), 0, st, part, (int)parts, a.D, a.dw);
+    if (a.dw) {
+        const int cols = sum_cols(a.D);
+        const dim3 sums((unsigned)((a.D + cols - 1) / cols));
+        if (cols == 64) hipLaunchKernelGGL(k_rms_dw_sum<64>, sums, dim3(kSumThreads), 0, st, part, (int)parts, a.D, a.dw);
+        else hipLaunchKernelGGL(k_rms_dw_sum<16>, sums, dim3(kSumThreads), 0, st, part, (int)parts, a.D, a.dw);
+    }
     return hipGetLastError();
 }
 template <typename T, typename TW>

@@ -82,14 +82,17 @@ __device__ __forceinline__ void store_own(T* p, const float (&x)[N], int skip) {
     store_own<kOdd, T, N>(p, r, skip);
 }
 
-// Sum over `parts` rows of partial sums [parts, n] for columns c0 .. c0+15, by a workgroup of
-// kSumThreads: 32 rows at a time, 16 lanes on the columns of each, eight loads in flight per lane, then a
-// tree over the rows in LDS (`sh`: kSumThreads / 4 words). The order of the additions depends on `parts`
-// alone. Threads 0..15 get the sums of columns c0 + threadIdx.x.
+// Sum over `parts` rows of partial sums [parts, n] for COLS columns from c0 on, by a workgroup of
+// kSumThreads: COLS lanes side by side on the columns of a row, eight loads in flight per lane, then a tree
+// over the rows in LDS (`sh`: kSumThreads words). The order of the additions depends on `parts` and COLS
+// alone. Threads 0 .. COLS-1 get the sums of columns c0 + threadIdx.x. Many columns take 64 (whole cache lines),
+// few 16, for more workgroups (171 parts of 30,720 columns: 64 6 us, 16 11; 512 of 2,048: 16 4.4 us).
 constexpr int kSumThreads = 512;
-__device__ __forceinline__ float sum_parts16(const float* part, int parts, int64_t n, int64_t c0, float* sh) {
-    constexpr int kRows = kSumThreads / 16, kAhead = 8;
-    const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
+inline int sum_cols(int64_t n) { return n >= 64 * 256 ? 64 : 16; }
+template <int COLS>
+__device__ __forceinline__ float sum_parts(const float* part, int parts, int64_t n, int64_t c0, float* sh) {
+    constexpr int kRows = kSumThreads / COLS, kAhead = 8;
+    const int col = threadIdx.x % COLS, row = threadIdx.x / COLS;
     float s[kAhead] = {};
     if (c0 + col < n) {
         const float* p = part + c0 + col;
@@ -99,16 +102,12 @@ __device__ __forceinline__ float sum_parts16(const float* part, int parts, int64
             for (int u = 0; u < kAhead; ++u) s[u] += p[(int64_t)(i + kRows * u) * n];
         for (; i < parts; i += kRows) s[0] += p[(int64_t)i * n];
     }
-    float v = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
-    // a wave holds 4 rows of 16 columns
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-    if ((threadIdx.x & 63) < 16) sh[(threadIdx.x >> 6) * 16 + col] = v;
+    sh[threadIdx.x] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
     __syncthreads();
     float t = 0.f;
-    if (threadIdx.x < 16)
+    if (threadIdx.x < COLS)
 #pragma unroll
-        for (int w = 0; w < kSumThreads / 64; ++w) t += sh[w * 16 + threadIdx.x];
+        for (int r = 0; r < kRows; ++r) t += sh[r * COLS + threadIdx.x];
     return t;
 }
 
