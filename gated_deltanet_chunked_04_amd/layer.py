@@ -12,8 +12,8 @@ device; work runs on that device's current stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -74,33 +74,14 @@ def _second_type(name, t, x) -> int:
     return _DTYPES[t.dtype]
 
 
-def _sequences(desc, x, cu_seqlens) -> int:
-    """Fills B, T, D and the packing; returns N."""
-    desc.B, desc.T, desc.D = x.shape
-    if cu_seqlens is None:
-        return x.shape[0]
+def _packing(x, cu_seqlens) -> int:
+    """N of a packed batch."""
     if (not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype != torch.int32 or cu_seqlens.device != x.device
             or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or cu_seqlens.numel() < 2):
         raise TypeError(f"cu_seqlens must be a contiguous int32 tensor [N+1], N >= 1, on {x.device}")
     if x.shape[0] != 1:
         raise ValueError("cu_seqlens needs B = 1")
-    desc.num_seqs = cu_seqlens.numel() - 1
-    desc.cu_seqlens = cu_seqlens.data_ptr()
-    return desc.num_seqs
-
-
-@contextlib.contextmanager
-def _other_device(device):
-    with torch.cuda.device(device):
-        yield
-
-
-_HERE = contextlib.nullcontext()
-
-
-def _on(device):
-    """Makes `device` current for the launches of a call, if it is not."""
-    return _HERE if torch.cuda.current_device() == device.index else _other_device(device)
+    return cu_seqlens.numel() - 1
 
 
 # The current stream's handle. The first form gives it without building a Stream object (0.1 against 1.9 us of a
@@ -112,36 +93,61 @@ def _stream_of(device) -> int:
     return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
 
 
-def _scratch(nbytes, device, workspace):
+def _run(fn, device, *args):
+    """One call of the library on `device`'s current stream, with `device` current."""
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, _stream_of(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream_of(device))
+    if status:
+        check(status, fn.__name__)
+
+
+def _scratch(nbytes, x, workspace):
     """(pointer, bytes, the tensor to keep alive) of a caller's workspace or of a new one."""
     if workspace is None:
         if nbytes == 0:
             return None, 0, None
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    elif (not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous()
-          or workspace.data_ptr() % 256):
-        raise ValueError(f"workspace must be a contiguous tensor on {device} at a 256-byte aligned address")
+        workspace = x.new_empty(nbytes, dtype=torch.uint8)
+        return workspace.data_ptr(), nbytes, workspace
+    if (not isinstance(workspace, torch.Tensor) or workspace.device != x.device or not workspace.is_contiguous()
+            or workspace.data_ptr() % 256):
+        raise ValueError(f"workspace must be a contiguous tensor on {x.device} at a 256-byte aligned address")
     size = workspace.numel() * workspace.element_size()
     if size < nbytes:
         raise ValueError(f"workspace too small: {size} bytes, {nbytes} needed")
     return workspace.data_ptr(), size, workspace
 
 
-def _bytes(fn, desc, where) -> int:
+def _bytes(name, desc) -> int:
     n = ctypes.c_size_t()
-    check(fn(ctypes.byref(desc), ctypes.byref(n)), where)
+    check(getattr(load_library(), name)(ctypes.byref(desc), ctypes.byref(n)), name)
     return n.value
 
 
 # ---- gated scan ---------------------------------------------------------------------------------
 
 
-def _scan_desc(x, g, cu_seqlens):
+@functools.lru_cache(maxsize=1024)
+def _scan_plan(B, T, D, dtype, g_dtype):
+    """(descriptor of an unpacked call, its forward's and its backward's workspace sizes): by sizes and types alone,
+    never changed afterwards."""
+    desc = GdnScanDesc(B, T, D, dtype, g_dtype)
+    return (ctypes.byref(desc), _bytes("gdn_gated_scan_fwd_workspace_size", desc),
+            _bytes("gdn_gated_scan_bwd_workspace_size", desc))
+
+
+def _scan_call(x, g, cu_seqlens):
+    """(descriptor, forward and backward workspace bytes, N)."""
     _lead("x", x, 3)
-    desc = GdnScanDesc()
-    desc.dtype = _dtype(x)
-    desc.g_dtype = _second_type("g", g, x)
-    return desc, _sequences(desc, x, cu_seqlens)
+    dtype, g_dtype = _dtype(x), _second_type("g", g, x)
+    B, T, D = x.shape
+    ref, fwd, bwd = _scan_plan(B, T, D, dtype, g_dtype)
+    if cu_seqlens is None:
+        return ref, fwd, bwd, B
+    N = _packing(x, cu_seqlens)
+    return ctypes.byref(GdnScanDesc(B, T, D, dtype, g_dtype, N, 0, cu_seqlens.data_ptr())), fwd, bwd, N
 
 
 def gdn_gated_scan_states(x):
@@ -170,7 +176,7 @@ def gdn_gated_scan_fwd(x, g, initial_state=None, *, cu_seqlens=None, output_fina
     or None (zeros); cu_seqlens int32 device tensor [N+1] (B = 1), no host copy needed. final_state may be
     initial_state itself (updated in place). states (see gdn_gated_scan_states) receives what
     gdn_gated_scan_bwd needs of the forward."""
-    desc, N = _scan_desc(x, g, cu_seqlens)
+    ref, need, _, N = _scan_call(x, g, cu_seqlens)
     shape, dev = x.shape, x.device
     pg = _like("g", g, shape, g.dtype, dev)
     p0 = _like("initial_state", initial_state, (N, shape[2]), torch.float32, dev)
@@ -180,12 +186,8 @@ def gdn_gated_scan_fwd(x, g, initial_state=None, *, cu_seqlens=None, output_fina
     else:
         final_state = pT = None
     ps = _check_states(states, x)
-    lib = load_library()
-    with _on(dev):
-        need = _bytes(lib.gdn_gated_scan_fwd_workspace_size, desc, "gdn_gated_scan_fwd_workspace_size")
-        pw, wb, ws = _scratch(need, dev, workspace)
-        check(lib.gdn_gated_scan_fwd(ctypes.byref(desc), x.data_ptr(), pg, p0, ph, pT, ps, pw, wb, _stream_of(dev)),
-              "gdn_gated_scan_fwd")
+    pw, wb, ws = _scratch(need, x, workspace)
+    _run(load_library().gdn_gated_scan_fwd, dev, ref, x.data_ptr(), pg, p0, ph, pT, ps, pw, wb)
     return h, final_state
 
 
@@ -194,7 +196,7 @@ def gdn_gated_scan_bwd(x, g, d_h, initial_state=None, d_final_state=None, *, cu_
     """Gradients of <d_h, h> + <d_final_state, final_state>: dict(dx, dg, d_initial_state); `out` may hold
     them preallocated. states: what gdn_gated_scan_fwd(states=...) wrote for these inputs, or None (the
     states are recomputed)."""
-    desc, N = _scan_desc(x, g, cu_seqlens)
+    ref, _, need, N = _scan_call(x, g, cu_seqlens)
     shape, dev = x.shape, x.device
     if d_h is None:
         raise ValueError("d_h is required")
@@ -205,33 +207,39 @@ def gdn_gated_scan_bwd(x, g, d_h, initial_state=None, d_final_state=None, *, cu_
     out, px, pdg, pd0 = _outs(out, x, dev, dx=(shape, x.dtype, True), dg=(shape, g.dtype, True),
                               d_initial_state=((N, shape[2]), torch.float32, need_d_initial_state))
     ps = _check_states(states, x)
-    lib = load_library()
-    with _on(dev):
-        need = _bytes(lib.gdn_gated_scan_bwd_workspace_size, desc, "gdn_gated_scan_bwd_workspace_size")
-        pw, wb, ws = _scratch(need, dev, workspace)
-        check(lib.gdn_gated_scan_bwd(ctypes.byref(desc), x.data_ptr(), pg, p0, pd, pT, ps, px, pdg, pd0, pw, wb,
-                                     _stream_of(dev)), "gdn_gated_scan_bwd")
+    pw, wb, ws = _scratch(need, x, workspace)
+    _run(load_library().gdn_gated_scan_bwd, dev, ref, x.data_ptr(), pg, p0, pd, pT, ps, px, pdg, pd0, pw, wb)
     return out
 
 
 # ---- short convolution --------------------------------------------------------------------------
 
 
-def _conv_desc(x, weight, bias, activation, cu_seqlens):
+@functools.lru_cache(maxsize=1024)
+def _conv_plan(B, T, D, W, dtype, w_dtype, activation):
+    """(descriptor of an unpacked call, its backward's workspace size)."""
+    desc = GdnConvDesc(B, T, D, W, dtype, w_dtype, activation)
+    return ctypes.byref(desc), _bytes("gdn_short_conv_bwd_workspace_size", desc)
+
+
+def _conv_call(x, weight, bias, activation, cu_seqlens):
+    """(descriptor, backward workspace bytes, N, W, pointers of weight and bias)."""
     _lead("x", x, 3)
-    desc = GdnConvDesc()
-    desc.dtype = _dtype(x)
-    desc.w_dtype = _second_type("weight", weight, x)
+    dtype, w_dtype = _dtype(x), _second_type("weight", weight, x)
     if activation not in _ACTIVATIONS:
         raise ValueError("activation: expected 'silu' or None")
-    desc.activation = _ACTIVATIONS[activation]
-    D = x.shape[2]
     if weight.dim() != 2:
         raise ValueError("weight: expected [D, W]")
-    desc.width = W = weight.shape[1]
+    B, T, D = x.shape
+    W = weight.shape[1]
     pw = _like("weight", weight, (D, W), weight.dtype, x.device)
     pb = _like("bias", bias, (D,), weight.dtype, x.device)
-    return desc, _sequences(desc, x, cu_seqlens), W, pw, pb
+    act = _ACTIVATIONS[activation]
+    ref, bwd = _conv_plan(B, T, D, W, dtype, w_dtype, act)
+    if cu_seqlens is None:
+        return ref, bwd, B, W, pw, pb
+    N = _packing(x, cu_seqlens)
+    return ctypes.byref(GdnConvDesc(B, T, D, W, dtype, w_dtype, act, N, 0, cu_seqlens.data_ptr())), bwd, N, W, pw, pb
 
 
 def gdn_short_conv_fwd(x, weight, bias=None, initial_state=None, *, activation="silu", cu_seqlens=None,
@@ -242,7 +250,7 @@ def gdn_short_conv_fwd(x, weight, bias=None, initial_state=None, *, activation="
     'silu' or None; initial_state [N,W-1,D] in x's type: the inputs before each sequence's first token,
     oldest first (zeros if None). The final state is a sequence's last W-1 inputs; a final_state tensor
     asks for it, and may be initial_state itself for up to 16 tokens per row (decoding)."""
-    desc, N, W, pw, pb = _conv_desc(x, weight, bias, activation, cu_seqlens)
+    ref, _, N, W, pw, pb = _conv_call(x, weight, bias, activation, cu_seqlens)
     shape, dev = x.shape, x.device
     sshape = (N, W - 1, shape[2])
     p0 = _like("initial_state", initial_state, sshape, x.dtype, dev)
@@ -250,10 +258,7 @@ def gdn_short_conv_fwd(x, weight, bias=None, initial_state=None, *, activation="
     pT = None
     if final_state is not None or output_final_state:
         final_state, pT = _out("final_state", final_state, x, sshape, x.dtype, dev)
-    lib = load_library()
-    with _on(dev):
-        check(lib.gdn_short_conv_fwd(ctypes.byref(desc), x.data_ptr(), pw, pb, p0, py, pT, _stream_of(dev)),
-              "gdn_short_conv_fwd")
+    _run(load_library().gdn_short_conv_fwd, dev, ref, x.data_ptr(), pw, pb, p0, py, pT)
     return y, final_state
 
 
@@ -261,7 +266,7 @@ def gdn_short_conv_bwd(x, weight, d_y, bias=None, initial_state=None, d_final_st
                        cu_seqlens=None, need_d_initial_state=True, workspace=None, out=None):
     """Gradients of <d_y, y> + <d_final_state, final_state>: dict(dx, dweight, dbias, d_initial_state), dweight
     and dbias in fp32, dbias None without a bias; `out` may hold them preallocated."""
-    desc, N, W, pw, pb = _conv_desc(x, weight, bias, activation, cu_seqlens)
+    ref, need, N, W, pw, pb = _conv_call(x, weight, bias, activation, cu_seqlens)
     shape, dev = x.shape, x.device
     D = shape[2]
     sshape = (N, W - 1, D)
@@ -273,28 +278,29 @@ def gdn_short_conv_bwd(x, weight, d_y, bias=None, initial_state=None, d_final_st
     out, px, pdw, pdb, pd0 = _outs(out, x, dev, dx=(shape, x.dtype, True), dweight=((D, W), torch.float32, True),
                                    dbias=((D,), torch.float32, bias is not None),
                                    d_initial_state=(sshape, x.dtype, need_d_initial_state))
-    lib = load_library()
-    with _on(dev):
-        need = _bytes(lib.gdn_short_conv_bwd_workspace_size, desc, "gdn_short_conv_bwd_workspace_size")
-        ws_p, wb, ws = _scratch(need, dev, workspace)
-        check(lib.gdn_short_conv_bwd(ctypes.byref(desc), x.data_ptr(), pw, pb, p0, pd, pT, px, pdw, pdb, pd0, ws_p, wb,
-                                     _stream_of(dev)), "gdn_short_conv_bwd")
+    ws_p, wb, ws = _scratch(need, x, workspace)
+    _run(load_library().gdn_short_conv_bwd, dev, ref, x.data_ptr(), pw, pb, p0, pd, pT, px, pdw, pdb, pd0, ws_p, wb)
     return out
 
 
 # ---- RMS norm -----------------------------------------------------------------------------------
 
 
-def _rms_desc(name, x, weight, eps):
+@functools.lru_cache(maxsize=1024)
+def _rms_plan(rows, D, dtype, w_dtype, out_type, scale_group, eps):
+    """(descriptor, the backward's workspace size)."""
+    desc = GdnRmsnormDesc(rows, D, dtype, w_dtype, out_type, scale_group, eps)
+    return ctypes.byref(desc), _bytes("gdn_rmsnorm_bwd_workspace_size", desc)
+
+
+def _rms_call(name, x, weight, eps, out_type=GDN_OUT_SAME, scale_group=0):
+    """(descriptor, backward workspace bytes, pointer of weight)."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1 or not x.is_cuda or not x.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous device tensor [..., D]")
-    desc = GdnRmsnormDesc()
-    desc.dtype = _dtype(x)
-    desc.w_dtype = _second_type("weight", weight, x)
-    desc.D = D = x.shape[-1]
-    desc.rows = x.numel() // D if D else 0
-    desc.eps = eps
-    return desc, _like("weight", weight, (D,), weight.dtype, x.device)
+    D = x.shape[-1]
+    ref, bwd = _rms_plan(x.numel() // D if D else 0, D, _dtype(x), _second_type("weight", weight, x), out_type,
+                         scale_group, eps)
+    return ref, bwd, _like("weight", weight, (D,), weight.dtype, x.device)
 
 
 def gdn_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, quant=None, y=None, residual_out=None, scale=None):
@@ -305,7 +311,9 @@ def gdn_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, quant=None, y=None, r
     in x's type (it may be residual or x itself). quant None gives y in x's type; 'row' and 'group' give
     it as torch.float8_e4m3fn with fp32 scales of every row ([..., 1]) or of every 128 columns
     ([..., ceil(D/128)]): y stands for y.float() * scale."""
-    desc, pw = _rms_desc("x", x, weight, eps)
+    if quant is not None and quant not in _QUANT:
+        raise ValueError("quant: expected None, 'row' or 'group'")
+    ref, _, pw = _rms_call("x", x, weight, eps, *((GDN_OUT_SAME, 0) if quant is None else (GDN_OUT_E4M3, _QUANT[quant])))
     shape, dev, D = x.shape, x.device, x.shape[-1]
     pr = _like("residual", residual, shape, x.dtype, dev)
     if residual is None:
@@ -319,16 +327,11 @@ def gdn_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, quant=None, y=None, r
             raise ValueError("scale without quant")
         ydt, psc = x.dtype, None
     else:
-        if quant not in _QUANT:
-            raise ValueError("quant: expected None, 'row' or 'group'")
-        desc.out_type, desc.scale_group, ydt = GDN_OUT_E4M3, _QUANT[quant], torch.float8_e4m3fn
+        ydt = torch.float8_e4m3fn
         sshape = (*shape[:-1], 1 if quant == "row" else -(-D // 128))
         scale, psc = _out("scale", scale, x, sshape, torch.float32, dev)
     y, py = _out("y", y, x, shape, ydt, dev)
-    lib = load_library()
-    with _on(dev):
-        check(lib.gdn_rmsnorm_fwd(ctypes.byref(desc), x.data_ptr(), pr, pw, py, psc, po, _stream_of(dev)),
-              "gdn_rmsnorm_fwd")
+    _run(load_library().gdn_rmsnorm_fwd, dev, ref, x.data_ptr(), pr, pw, py, psc, po)
     return y, residual_out, scale
 
 
@@ -336,7 +339,7 @@ def gdn_rmsnorm_bwd(r, weight, d_y, d_residual=None, *, eps=1e-6, need_dweight=T
     """Gradients of <d_y, y> + <d_residual, residual_out> from r (the forward's residual_out, or x where there
     was no residual): dict(dx, dweight), dx being the gradient of x and of residual alike, dweight fp32;
     `out` may hold them preallocated."""
-    desc, pw = _rms_desc("r", r, weight, eps)
+    ref, need, pw = _rms_call("r", r, weight, eps)
     shape, dev, D = r.shape, r.device, r.shape[-1]
     if d_y is None:
         raise ValueError("d_y is required")
@@ -345,12 +348,8 @@ def gdn_rmsnorm_bwd(r, weight, d_y, d_residual=None, *, eps=1e-6, need_dweight=T
     if out is not None:
         need_dweight = out.get("dweight") is not None
     out, px, pdw = _outs(out, r, dev, dx=(shape, r.dtype, True), dweight=((D,), torch.float32, need_dweight))
-    lib = load_library()
-    with _on(dev):
-        need = _bytes(lib.gdn_rmsnorm_bwd_workspace_size, desc, "gdn_rmsnorm_bwd_workspace_size")
-        ws_p, wb, ws = _scratch(need, dev, workspace)
-        check(lib.gdn_rmsnorm_bwd(ctypes.byref(desc), r.data_ptr(), pw, pd, pr, px, pdw, ws_p, wb, _stream_of(dev)),
-              "gdn_rmsnorm_bwd")
+    ws_p, wb, ws = _scratch(need, r, workspace)
+    _run(load_library().gdn_rmsnorm_bwd, dev, ref, r.data_ptr(), pw, pd, pr, px, pdw, ws_p, wb)
     return out
 
 
