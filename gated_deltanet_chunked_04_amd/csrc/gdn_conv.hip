@@ -83,14 +83,13 @@ __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf
 // Sequences without tokens: their state (or its gradient) passes through, by the workgroups of the
 // grid's last row.
 template <bool kOdd, typename T, int VEC>
-__device__ void pass_empty(const ConvArgs& p, const void* in, void* out, int64_t c0, int skip) {
-    for (int32_t s = wave_id(); s < p.seq.N; s += kWaves) {
-        const SeqPos q = seq_at(p.seq, s);
-        if (q.start < q.end) continue;
+__device__ void pass_empty(const ConvArgs& p, const void* in, void* out, int64_t c0, int skip, bool live) {
+    for_each_empty(p.seq, wave_id(), kWaves, [&](int32_t s) {
+        if (!live) return;
         for (int r = 0; r < p.W - 1; ++r)
             store_own<kOdd, T, VEC>(static_cast<T*>(out) + ((int64_t)s * (p.W - 1) + r) * p.D + c0,
                                     state_row<T, VEC>(in, s, r, p, c0), skip);
-    }
+    });
 }
 
 // U: tokens loaded ahead. `run`: tokens per wave.
@@ -98,10 +97,10 @@ template <bool kOdd, typename T, typename TW, int W, int VEC, int U>
 __global__ __launch_bounds__(kThreads) void k_conv_fwd(ConvArgs p, int run, int token_blocks, int cblocks) {
     const int block = blockIdx.x / cblocks;  // of tokens
     const int64_t ch = ((int64_t)(blockIdx.x % cblocks) * kWave + (threadIdx.x & 63)) * VEC;
-    if (ch >= p.D) return;
     const Lane ln(ch, p.D, VEC);
     const int64_t c0 = ln.at;
-    if (block == token_blocks) return pass_empty<kOdd, T, VEC>(p, p.s0, p.sT, c0, ln.skip);
+    if (block == token_blocks) return pass_empty<kOdd, T, VEC>(p, p.s0, p.sT, c0, ln.skip, ch < p.D);
+    if (ch >= p.D) return;
     const int64_t w0l = ((int64_t)block * kWaves + wave_id()) * run;
     if (w0l >= p.seq.total) return;
     const int32_t w0 = (int32_t)w0l;
@@ -183,10 +182,7 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
     const bool live = ch < p.D;
     const Lane ln(ch, p.D, VEC);
     const int64_t c0 = ln.at;
-    if (block == token_blocks) {
-        if (live) pass_empty<kOdd, T, VEC>(p, p.d_sT, p.ds0, c0, ln.skip);
-        return;
-    }
+    if (block == token_blocks) return pass_empty<kOdd, T, VEC>(p, p.d_sT, p.ds0, c0, ln.skip, live);
     float dw[W][VEC] = {}, db[VEC] = {};
     const int64_t w0l = ((int64_t)block * kWaves + wave) * run;
     if (live && w0l < p.seq.total) {

@@ -171,14 +171,13 @@ __device__ __forceinline__ void state_of(const float* s, int32_t n, int64_t D, i
 
 // Sequences without tokens: their state (or its gradient) passes through, by the workgroups behind the tiles.
 template <bool kOdd, int VEC>
-__device__ void pass_empty(const GScanArgs& p, const float* in, float* out, int64_t c, int skip) {
-    for (int32_t n = wave_id(); n < p.seq.N; n += kWaves) {
-        const SeqPos q = seq_at(p.seq, n);
-        if (q.start < q.end) continue;
+__device__ void pass_empty(const GScanArgs& p, const float* in, float* out, int64_t c, int skip, bool live) {
+    for_each_empty(p.seq, wave_id(), kWaves, [&](int32_t n) {
+        if (!live) return;
         float x[VEC];
         state_of<VEC>(in, n, p.D, c, x);
         store_own<kOdd, float, VEC>(out + (int64_t)n * p.D + c, x, skip);
-    }
+    });
 }
 
 // This workgroup's item: tile * cblocks + channel block, in the order in which workgroups got here.
@@ -206,10 +205,7 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
     const int skip = kOdd ? ln.skip : 0;
     const int lo = live ? lane * VEC - skip : 0;  // the lane's first channel, from the block's
     const int64_t c = cbase + lo;
-    if (tile == tiles) {
-        if (live) pass_empty<kOdd, VEC>(p, p.s0, p.sT, c, skip);
-        return;
-    }
+    if (tile == tiles) return pass_empty<kOdd, VEC>(p, p.s0, p.sT, c, skip, live);
     const int64_t w0l = (int64_t)tile * kTile + wave * kTokens;
     const int32_t w0 = w0l < p.seq.total ? (int32_t)w0l : p.seq.total;
     const int32_t w1 = p.seq.total - w0 < kTokens ? p.seq.total : w0 + kTokens;
@@ -326,10 +322,7 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
     const int skip = kOdd ? ln.skip : 0;
     const int lo = live ? lane * VEC - skip : 0;
     const int64_t c = cbase + lo;
-    if (pos == tiles) {
-        if (live) pass_empty<kOdd, VEC>(p, p.d_sT, p.ds0, c, skip);
-        return;
-    }
+    if (pos == tiles) return pass_empty<kOdd, VEC>(p, p.d_sT, p.ds0, c, skip, live);
     const int64_t w0l = (int64_t)tile * kTile + wave * kTokens;
     const int32_t w0 = w0l < p.seq.total ? (int32_t)w0l : p.seq.total;
     const int32_t w1 = p.seq.total - w0 < kTokens ? p.seq.total : w0 + kTokens;
@@ -526,6 +519,9 @@ __global__ __launch_bounds__(kRowThreads) void k_gscan_rows(GScanArgs p, int cbl
     if (p.sT) store_own<kOdd, float, VEC>(p.sT + (int64_t)s.n * p.D + c, h, skip);
 }
 
+// Sequences of up to 16 tokens, or on average up to 4 where they are packed, get a wave each.
+bool by_rows(const SeqView& s) { return s.cu ? s.total / s.N <= 4 : s.T <= 16; }
+
 // Tokens of a wave forward: 16 where x and g are both bf16 (as many registers as 8 with fp32 gates), for half as
 // many pairs to look back over (64K x 4096 packed: 309 -> 285 us).
 template <typename TX, typename TG>
@@ -586,8 +582,7 @@ hipError_t fwd_tiles(const GScanArgs& a, int cb, hipStream_t st) {
 template <bool kOdd, typename TX, typename TG, int VEC>
 hipError_t fwd_v(const GScanArgs& a, hipStream_t st) {
     const int cb = (int)((a.D + kWave * VEC - 1) / (kWave * VEC));
-    // sequences of up to 16 tokens, or on average up to 4 where they are packed: a wave each
-    if (a.seq.cu ? a.seq.total / a.seq.N <= 4 : a.seq.T <= 16) {
+    if (by_rows(a.seq)) {
         const int64_t items = (int64_t)a.seq.N * cb, per = kRowThreads / kWave;
         if (!grid_fits((items + per - 1) / per, kRowThreads)) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((k_gscan_rows<kOdd, TX, TG, VEC>), dim3((unsigned)((items + per - 1) / per)), dim3(kRowThreads), 0, st, a, cb);
@@ -635,7 +630,9 @@ hipError_t bwd_t(const GScanArgs& a, bool have, hipStream_t st) {
 }  // namespace
 
 // (sized for 64-token tiles, whatever the types)
-size_t gscan_fwd_ws(int64_t total, int64_t D) { return chain_bytes(tiles_of(total, kScanTile), D); }
+size_t gscan_fwd_ws(const SeqView& seq, int64_t D) {
+    return by_rows(seq) ? 0 : chain_bytes(tiles_of(seq.total, kScanTile), D);
+}
 size_t gscan_bwd_ws(int64_t total, int64_t D) {
     const size_t tiles = tiles_of(total, kScanTile);
     return chain_bytes(tiles, D) + tiles * D * 4;

@@ -46,9 +46,31 @@ __device__ __forceinline__ SeqPos seq_find(const SeqView& s, int32_t t) {
     }
     return seq_at(s, lo);
 }
-// Advance p to the sequence that holds t, t at or behind p's start.
+// Advance p to the sequence that holds t, t at or behind p's start: mostly the next one, else (behind sequences
+// without tokens) by search.
 __device__ __forceinline__ void seq_advance(const SeqView& s, SeqPos& p, int32_t t) {
-    while (t >= p.end && p.n + 1 < s.N) p = seq_at(s, p.n + 1);
+    if (t < p.end || p.n + 1 >= s.N) return;
+    p = seq_at(s, p.n + 1);
+    if (t >= p.end) p = seq_find(s, t);
+}
+// Calls f(n) (uniform) for every sequence without tokens, 64 sequences looked at together by each of `waves` waves.
+// Whole waves call it.
+template <typename F>
+__device__ __forceinline__ void for_each_empty(const SeqView& s, int wave, int waves, F f) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t base = (int64_t)wave * 64; base < s.N; base += (int64_t)waves * 64) {
+        const int64_t n = base + lane;
+        bool empty = false;
+        if (n < s.N) {
+            if (s.cu) {
+                const int32_t a = s.cu[n], b = s.cu[n + 1];
+                empty = min(max(a, 0), s.total) >= min(max(b, 0), s.total);
+            } else {
+                empty = s.T == 0;
+            }
+        }
+        for (uint64_t m = __ballot(empty); m; m &= m - 1) f((int32_t)(base + __builtin_ctzll(m)));
+    }
 }
 
 // A launch's threads are counted in 32 bits. Launchers return hipErrorInvalidConfiguration for more.
@@ -73,7 +95,7 @@ struct GScanArgs {
     float* ds0;
     unsigned char* ws;
 };
-size_t gscan_fwd_ws(int64_t total, int64_t D);
+size_t gscan_fwd_ws(const SeqView& seq, int64_t D);
 size_t gscan_bwd_ws(int64_t total, int64_t D);
 hipError_t launch_gscan_fwd(const GScanArgs& a, int dtype, int g_dtype, hipStream_t st);
 hipError_t launch_gscan_bwd(const GScanArgs& a, int dtype, int g_dtype, bool have_states, hipStream_t st);

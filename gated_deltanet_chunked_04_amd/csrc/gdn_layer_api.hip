@@ -75,7 +75,7 @@ gdn_status gdn_gated_scan_fwd_workspace_size(const gdn_scan_desc* desc, size_t* 
     SeqView seq;
     if (!bytes) return GDN_ERR_INVALID_ARG;
     if (gdn_status s = check_scan(desc, seq)) return s;
-    *bytes = gscan_fwd_ws(seq.total, desc->D);
+    *bytes = gscan_fwd_ws(seq, desc->D);
     return GDN_OK;
 }
 
@@ -102,7 +102,7 @@ gdn_status gdn_gated_scan_fwd(const gdn_scan_desc* desc, const void* x, const vo
     if (gdn_status s = check_scan(desc, a.seq)) return s;
     if (a.seq.total && (!x || !g || !h)) return GDN_ERR_INVALID_ARG;
     if (a.seq.total && (h == x || h == g)) return GDN_ERR_INVALID_ARG;
-    const size_t need = gscan_fwd_ws(a.seq.total, desc->D);
+    const size_t need = gscan_fwd_ws(a.seq, desc->D);
     if (need)
         if (gdn_status s = check_buf(workspace, need, workspace_bytes)) return s;
     if (states && reinterpret_cast<uintptr_t>(states) % 256) return GDN_ERR_WORKSPACE;

@@ -334,8 +334,8 @@ gdn_status gdn_cp_windows(const gdn_desc* desc, const void* k, const void* v,
  * row-major contiguous device buffers of the caller, the caller's stream, argument checks before
  * any launch, no allocation, no host synchronisation, deterministic results, outputs overwritten.
  * Descriptors are zero-initialised, then filled; `reserved` must be zero. They take channels in
- * any number; rows whose length or buffers whose address do not fit 16-byte vectors take a slower
- * path of the same results within rounding.
+ * any number; rows whose length or buffers whose address do not fit 16-byte vectors are slower, no
+ * more. Sizes beyond a 32-bit grid of threads return GDN_ERR_UNSUPPORTED.
  *
  * Sequences: without cu_seqlens, row b of [B, T, D] is sequence b (N = B). With cu_seqlens (device
  * int32 [N+1], not decreasing), B is 1 and sequence n owns tokens [cu_seqlens[n], cu_seqlens[n+1]);
@@ -347,7 +347,9 @@ gdn_status gdn_cp_windows(const gdn_desc* desc, const void* k, const void* v,
 
 /* Gated scan: the recurrence with a gate per channel,
  *     h_t = exp(g_t) h_{t-1} + x_t,    h_0 = initial_state (zeros when NULL),
- * per sequence and channel; g is a natural-log decay (usually <= 0; -inf forgets). */
+ * per sequence and channel; g is a natural-log decay (usually <= 0; -inf forgets). Gates above zero
+ * are taken too, but the tokens are worked on in runs of up to 128, whose gates' products must stay
+ * within fp32's range where a state other than zero enters the run. */
 typedef struct gdn_scan_desc {
     int64_t B, T, D;
     int32_t dtype;             /* gdn_dtype of x, h and their gradients */
@@ -358,8 +360,8 @@ typedef struct gdn_scan_desc {
     int32_t reserved[4];       /* must be zero */
 } gdn_scan_desc;
 
-/* Bytes of the workspaces (256-byte aligned) and of the kept states. The sizes depend on B*T, D
- * alone. */
+/* Bytes of the workspaces (256-byte aligned) and of the kept states. They do not depend on the
+ * types; a packed call never needs more than the unpacked one of its B, T and D. */
 gdn_status gdn_gated_scan_fwd_workspace_size(const gdn_scan_desc* desc, size_t* bytes);
 gdn_status gdn_gated_scan_bwd_workspace_size(const gdn_scan_desc* desc, size_t* bytes);
 gdn_status gdn_gated_scan_states_size(const gdn_scan_desc* desc, size_t* bytes);
@@ -370,8 +372,7 @@ gdn_status gdn_gated_scan_states_size(const gdn_scan_desc* desc, size_t* bytes);
  *   itself (updated in place, for decoding)
  *   states: NULL, or a buffer of gdn_gated_scan_states_size bytes (256-byte aligned) that receives
  *   the fp32 state entering every 64th token, for gdn_gated_scan_bwd
- * A call of a few tokens per sequence (decoding) is one launch and touches no workspace; the
- * workspace argument is checked all the same. */
+ * A call of a few tokens per sequence (decoding) is one launch and needs no workspace. */
 gdn_status gdn_gated_scan_fwd(const gdn_scan_desc* desc, const void* x, const void* g,
                               const float* initial_state, void* h, float* final_state, void* states,
                               void* workspace, size_t workspace_bytes, void* stream);

@@ -43,7 +43,7 @@ def packed(lens, head=0, tail=0):
 # belong to no sequence in front and behind, channels that fill vectors and ones that do not
 ROWS = [(1, 1, 1), (3, 1, 64), (2, 5, 256), (1, 16, 513), (1, 63, 64), (1, 64, 128), (1, 65, 260), (2, 129, 96),
         (3, 200, 77), (1, 700, 520)]
-PACKS = [([1], 0, 0, 8), ([0, 5, 0, 0, 70, 1, 1, 1, 64, 3, 0], 0, 0, 256), ([130, 200, 33], 7, 90, 72),
+PACKS = [([1], 0, 0, 8), ([0] * 200 + [20] + [0] * 300 + [90, 0] + [7] * 9, 3, 2, 132), ([2, 0, 3, 9, 1, 0, 0, 4] * 5, 0, 0, 131), ([0, 5, 0, 0, 70, 1, 1, 1, 64, 3, 0], 0, 0, 256), ([130, 200, 33], 7, 90, 72),
          ([0, 0], 0, 10, 16), ([1] * 70, 1, 1, 33), ([300, 2, 1, 90], 64, 64, 512)]
 SHAPES = [("rows", s) for s in ROWS] + [("pack", s) for s in PACKS]
 
@@ -184,6 +184,44 @@ def test_scan_in_place_state_of_long_rows(gpu_lib):
     assert torch.equal(state, fin)
 
 
+def test_scan_in_place_state_of_packed_sequences(gpu_lib):
+    """Sequences that start and end in one tile, in one wave and tiles apart."""
+    for lens in ([300, 2, 3, 0, 1, 100, 700, 5], [1, 0, 2, 3, 1]):
+        cu, T = packed(lens)
+        x, g, s0, _ = scan_inputs(1, T, 260, cu, F32, F32, True)
+        x, g, cd = x.cuda(), g.cuda(), cu_dev(cu)
+        h, fin = gdn.gdn_gated_scan_fwd(x, g, s0.cuda(), cu_seqlens=cd)
+        for _ in range(3):
+            state = s0.cuda()
+            h2, _ = gdn.gdn_gated_scan_fwd(x, g, state, cu_seqlens=cd, final_state=state)
+            assert torch.equal(state, fin) and torch.equal(h, h2)
+
+
+def test_scan_many_sequences(gpu_lib):
+    """Thousands of short sequences, most of them empty in one case, equal a plain loop over the longest."""
+    for lens in ([3] * 3000, ([0] * 9 + [41]) * 400, [5, 0, 8] * 700):
+        cu, T = packed(lens)
+        D, N = 128, len(lens)
+        x, g, s0, _ = scan_inputs(1, T, D, cu, F32, F32, True)
+        h, fin = gdn.gdn_gated_scan_fwd(x.cuda(), g.cuda(), s0.cuda(), cu_seqlens=cu_dev(cu))
+        y, cf = gdn.gdn_short_conv_fwd(x.cuda(), rnd(D, 2, seed=5).cuda(), None, s0[:, None].contiguous().cuda(), activation=None,
+                                       cu_seqlens=cu_dev(cu), output_final_state=True)
+        start, n = torch.tensor(cu[:-1]), torch.tensor(lens)
+        c, prev = s0.double(), s0.double()
+        w = rnd(D, 2, seed=5).double()
+        for t in range(max(lens)):
+            on = n > t
+            at = (start + t)[on]
+            c[on] = g[0, at].double().exp() * c[on] + x[0, at].double()
+            # 32 bits: 5 half steps a token of a state below 10, over at most 41 tokens
+            assert (h[0].cpu().double()[at] - c[on]).abs().max() < 41 * 5 * ref.U * 10
+            z = prev[on] * w[:, 0] + x[0, at].double() * w[:, 1]
+            assert (y[0].cpu().double()[at] - z).abs().max() < 3 * ref.U * 40
+            prev[on] = x[0, at].double()
+        assert (fin.cpu().double() - c).abs().max() < 41 * 5 * ref.U * 10
+        assert torch.equal(cf[:, 0].cpu().double(), prev)
+
+
 def test_scan_gates_at_the_edges(gpu_lib):
     """-inf forgets, +growth from a zero state stays finite, and what one sequence holds (NaN, infinity) does not
     reach the next."""
@@ -201,6 +239,12 @@ def test_scan_gates_at_the_edges(gpu_lib):
     gr = gdn.gdn_gated_scan_bwd(x.cuda(), g.cuda(), d_h.cuda(), cu_seqlens=cu_dev(cu))
     assert torch.isfinite(gr["dx"][0, :300]).all() and torch.isfinite(gr["dx"][0, 321:]).all()
     assert (gr["dg"][0, 100] == 0).all()
+    # gates above zero: a state that grows fourfold over a tile, against the sequential form
+    x, g, s0, _ = scan_inputs(1, 200, 64, None, F32, F32, True)
+    want_h, want_fin = ref.scan_fwd(x, -g * 0.1, s0)
+    h, fin = gdn.gdn_gated_scan_fwd(x.cuda(), (-g * 0.1).cuda(), s0.cuda())
+    close(h, want_h, "h")
+    close(fin, want_fin, "final_state")
     # growth: the product of 64 gates overflows, but there is no state for it to act on until the input comes
     x = torch.zeros(1, 600, 64)
     x[0, 599] = 1.0

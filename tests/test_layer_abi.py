@@ -72,6 +72,28 @@ def test_scan_refusals(lib, change, code):
     assert lib.gdn_gated_scan_states_size(ctypes.byref(d), ctypes.byref(n)) == code
 
 
+def test_grids_beyond_32_bits(lib):
+    """More threads than a launch can count: refused before anything is launched."""
+    n = ctypes.c_size_t(1 << 50)
+    out = ctypes.c_void_p(0x50000)
+    assert lib.gdn_rmsnorm_fwd(ctypes.byref(rms_desc(rows=5_000_000, D=4)), P, None, Q, R, None, None, None) == 2
+    assert lib.gdn_rmsnorm_fwd(ctypes.byref(rms_desc(rows=100_000_000, D=64)), P, None, Q, R, None, None, None) == 2
+    assert lib.gdn_rmsnorm_bwd(ctypes.byref(rms_desc(rows=5_000_000, D=4)), P, Q, R, None, S, None, S, n, None) == 2
+    assert lib.gdn_gated_scan_fwd(ctypes.byref(scan_desc(B=1, T=2_000_000_000, D=1024)), P, Q, None, R, None, None, S, n, None) == 2
+    assert lib.gdn_gated_scan_fwd(ctypes.byref(scan_desc(B=200_000_000, T=1, D=64)), P, Q, None, R, None, None, S, n, None) == 2
+    assert lib.gdn_gated_scan_bwd(ctypes.byref(scan_desc(B=1, T=2_000_000_000, D=1024)), P, Q, None, R, None, P, S, out, None, S, n, None) == 2
+    assert lib.gdn_short_conv_fwd(ctypes.byref(conv_desc(B=200_000_000, T=1, D=64)), P, Q, None, None, R, None, None) == 2
+    assert lib.gdn_short_conv_bwd(ctypes.byref(conv_desc(B=1, T=2_000_000_000, D=4096)), P, Q, None, None, R, None, S, out, None, None, S, n, None) == 2
+
+
+def test_scan_workspace_of_decoding(lib):
+    """Short rows need none; packed sequences never more than the unpacked call of their size."""
+    fn = lib.gdn_gated_scan_fwd_workspace_size
+    assert size(fn, scan_desc(B=1000, T=16)) == 0 and size(fn, scan_desc(B=1000, T=17)) > 0
+    for N in (1, 50, 300):
+        assert size(fn, scan_desc(B=1, T=1000, cu_seqlens=0x1000, num_seqs=N)) <= size(fn, scan_desc(B=1, T=1000))
+
+
 def test_scan_refused_buffers(lib):
     d = scan_desc()
     r = ctypes.byref(d)
