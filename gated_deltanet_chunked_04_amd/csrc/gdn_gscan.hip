@@ -188,9 +188,10 @@ __device__ __forceinline__ int take(const Chain& ch, bool chain, int* sh) {
     return __builtin_amdgcn_readfirstlane(*sh);
 }
 
+// `span`: tokens of a tile. A chain's tiles are full (kWaves kTokens); without a chain a tile is a whole row, or
+// the only one.
 template <bool kOdd, typename TX, typename TG, int VEC, int kTokens, bool kChain>
-__global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, int cblocks, Chain ch) {
-    constexpr int kTile = kWaves * kTokens;
+__global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, int span, int cblocks, Chain ch) {
     constexpr int kKeep = kScanTile / kTokens;  // waves between two kept states
     constexpr int CH = kWave * VEC;
     __shared__ __attribute__((aligned(16))) float2 agg[kWaves][CH];
@@ -206,9 +207,9 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
     const int lo = live ? lane * VEC - skip : 0;  // the lane's first channel, from the block's
     const int64_t c = cbase + lo;
     if (tile == tiles) return pass_empty<kOdd, VEC>(p, p.s0, p.sT, c, skip, live);
-    const int64_t w0l = (int64_t)tile * kTile + wave * kTokens;
-    const int32_t w0 = w0l < p.seq.total ? (int32_t)w0l : p.seq.total;
-    const int32_t w1 = p.seq.total - w0 < kTokens ? p.seq.total : w0 + kTokens;
+    const int32_t t0 = tile * span, t1 = p.seq.total - t0 < span ? p.seq.total : t0 + span;
+    const int32_t w0 = t1 - t0 < wave * kTokens ? t1 : t0 + wave * kTokens;
+    const int32_t w1 = t1 - w0 < kTokens ? t1 : w0 + kTokens;
     Raw<TX, VEC> x[kTokens];
     Raw<TG, VEC> g[kTokens];
 #pragma unroll
@@ -220,7 +221,7 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
     const SeqPos s0 = seq_find(p.seq, min(w0, p.seq.total - 1));
     // all of the wave's tokens inside one sequence, none of them its first
     const bool inside = w0 > s0.start && w0 + kTokens <= s0.end;
-    if (kChain && threadIdx.x == 0) sh_first = w0 >= s0.start && w0 < s0.end ? s0.start / kTile : tile;
+    if (kChain && threadIdx.x == 0) sh_first = w0 >= s0.start && w0 < s0.end ? s0.start / span : tile;
     float A[VEC], H[VEC], last[VEC] = {};  // last: the entering state of the last sequence that starts here
     int32_t last_n = -1;
 #pragma unroll
@@ -305,8 +306,8 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
 }
 
 template <bool kOdd, typename TX, typename TG, int VEC, bool kChain>
-__global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, int cblocks, Chain ch) {
-    constexpr int kTokens = kBwdTokens, kTile = kScanTile;
+__global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, int span, int cblocks, Chain ch) {
+    constexpr int kTokens = kBwdTokens;
     constexpr int CH = kWave * VEC;
     __shared__ __attribute__((aligned(16))) float2 agg[kWaves][CH];  // the forward's pairs, then the adjoint's
     __shared__ __attribute__((aligned(16))) float2 ragg[kWaves][CH];
@@ -323,9 +324,9 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
     const int lo = live ? lane * VEC - skip : 0;
     const int64_t c = cbase + lo;
     if (pos == tiles) return pass_empty<kOdd, VEC>(p, p.d_sT, p.ds0, c, skip, live);
-    const int64_t w0l = (int64_t)tile * kTile + wave * kTokens;
-    const int32_t w0 = w0l < p.seq.total ? (int32_t)w0l : p.seq.total;
-    const int32_t w1 = p.seq.total - w0 < kTokens ? p.seq.total : w0 + kTokens;
+    const int32_t t0 = tile * span, t1 = p.seq.total - t0 < span ? p.seq.total : t0 + span;
+    const int32_t w0 = t1 - t0 < wave * kTokens ? t1 : t0 + wave * kTokens;
+    const int32_t w1 = t1 - w0 < kTokens ? t1 : w0 + kTokens;
     Raw<TX, VEC> x[kTokens], d[kTokens];
     Raw<TG, VEC> g[kTokens];
 #pragma unroll
@@ -340,9 +341,8 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
     const bool inside = w0 > s0.start && w0 + kTokens < s0.end;
     if (kChain && threadIdx.x == kThreads - kWave) {
         // the chain comes from the sequence that goes on behind the tile
-        const int32_t t1 = min((int64_t)(tile + 1) * kTile, (int64_t)p.seq.total);
         const SeqPos e = seq_find(p.seq, t1 - 1);
-        sh_first = t1 > e.start && t1 < e.end ? tiles - 1 - (e.end - 1) / kTile : pos;
+        sh_first = t1 > e.start && t1 < e.end ? tiles - 1 - (e.end - 1) / span : pos;
     }
     float A[VEC], H[VEC], R[VEC], M[VEC];
 #pragma unroll
@@ -415,7 +415,8 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
     if (threadIdx.x >= kThreads - CH) {
         // the states that enter the waves, from the tile's kept one
         const int t = threadIdx.x - (kThreads - CH);
-        float h = cbase + t < p.D ? p.states[(int64_t)tile * p.D + cbase + t] : 0.f;
+        // (none where nothing enters a tile from outside)
+        float h = p.states && cbase + t < p.D ? p.states[(int64_t)tile * p.D + cbase + t] : 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
             cin[w][t] = h;
@@ -522,6 +523,10 @@ __global__ __launch_bounds__(kRowThreads) void k_gscan_rows(GScanArgs p, int cbl
 // Sequences of up to 16 tokens, or on average up to 4 where they are packed, get a wave each.
 bool by_rows(const SeqView& s) { return s.cu ? s.total / s.N <= 4 : s.T <= 16; }
 
+// Whether a tile of `span` tokens takes every row, or the whole of a packed batch: then no state passes from tile to
+// tile (256 rows of 64 x 2048: 52 us, as a chain of full tiles 61; 16 rows of 24: 5.5 and 10).
+bool one_tile(const SeqView& s, int span) { return (s.cu ? s.total : s.T) <= span; }
+
 // Tokens of a wave forward: 16 where x and g are both bf16 (as many registers as 8 with fp32 gates), for half as
 // many pairs to look back over (64K x 4096 packed: 309 -> 285 us).
 template <typename TX, typename TG>
@@ -545,7 +550,7 @@ constexpr int64_t kSlim = 128;
 constexpr int kMinGroup = 8;
 size_t chain_bytes(size_t tiles, int64_t D) {
     const size_t groups = (tiles + kMinGroup - 1) / kMinGroup;
-    return tiles < 2 ? 0 : 256 + align256(tiles * D * 8) + align256(groups * D * 4);
+    return 256 + align256(tiles * D * 8) + align256(groups * D * 4);
 }
 // A group hands its state on in about a microsecond, one group after the other, while a tile looks back over half
 // a group's pairs. With eight channel blocks or more to a tile the memory takes longer than the chain and small
@@ -569,13 +574,21 @@ hipError_t fwd_tiles(const GScanArgs& a, int cb, hipStream_t st) {
     const int extra = a.sT && a.seq.cu;
     Chain ch{};
     if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)(tiles + extra) * (unsigned)cb);
-    if (tiles > 1) {
-        if (hipError_t e = make_chain(a.ws, tiles, a.D, cb, ch, st)) return e;
-        hipLaunchKernelGGL((k_gscan_fwd<kOdd, TX, TG, VEC, TOK, true>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
-    } else {
-        hipLaunchKernelGGL((k_gscan_fwd<kOdd, TX, TG, VEC, TOK, false>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
-    }
+    if (hipError_t e = make_chain(a.ws, tiles, a.D, cb, ch, st)) return e;
+    hipLaunchKernelGGL((k_gscan_fwd<kOdd, TX, TG, VEC, TOK, true>), dim3((unsigned)(tiles + extra) * (unsigned)cb),
+                       dim3(kThreads), 0, st, a, tiles, kWaves * TOK, cb, ch);
+    return hipGetLastError();
+}
+
+// Without a chain, in one launch: rows that are a tile each, or a packed batch that is one.
+template <bool kOdd, typename TX, typename TG, int VEC, int TOK>
+hipError_t fwd_single(GScanArgs a, int cb, hipStream_t st) {
+    const int tiles = a.seq.cu ? (a.seq.total > 0) : a.seq.N, extra = a.sT && a.seq.cu;
+    if (tiles + extra == 0) return hipSuccess;
+    if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
+    a.states = nullptr;  // nothing enters a tile from outside: the gradient needs none
+    hipLaunchKernelGGL((k_gscan_fwd<kOdd, TX, TG, VEC, TOK, false>), dim3((unsigned)(tiles + extra) * (unsigned)cb),
+                       dim3(kThreads), 0, st, a, tiles, a.seq.cu ? kWaves * TOK : a.seq.T, cb, Chain{});
     return hipGetLastError();
 }
 
@@ -588,31 +601,38 @@ hipError_t fwd_v(const GScanArgs& a, hipStream_t st) {
         hipLaunchKernelGGL((k_gscan_rows<kOdd, TX, TG, VEC>), dim3((unsigned)((items + per - 1) / per)), dim3(kRowThreads), 0, st, a, cb);
         return hipGetLastError();
     }
+    // Kept states lie 64 tokens apart, so rows that need them and have more take the chain.
+    if (one_tile(a.seq, kScanTile)) return fwd_single<kOdd, TX, TG, VEC, 8>(a, cb, st);
+    if (!a.states && one_tile(a.seq, 2 * kScanTile)) return fwd_single<kOdd, TX, TG, VEC, 16>(a, cb, st);
     return fwd_tiles<kOdd, TX, TG, VEC, fwd_tokens<TX, TG>()>(a, cb, st);
 }
 
 template <bool kOdd, typename TX, typename TG, int VEC>
 hipError_t bwd_v(GScanArgs a, bool have, hipStream_t st) {
-    const int tiles = tiles_of(a.seq.total, kScanTile);
     const int cb = (int)((a.D + kWave * VEC - 1) / (kWave * VEC));
+    const bool single = one_tile(a.seq, kScanTile), rows = single && !a.seq.cu;  // (as forward)
+    const int tiles = rows ? (a.seq.T > 0 ? a.seq.N : 0) : tiles_of(a.seq.total, kScanTile);
     const int extra = a.ds0 && (a.seq.cu || a.seq.T == 0);
     if (tiles + extra == 0) return hipSuccess;
-    if (!have && tiles) {
+    if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
+    if (single) {
+        a.states = nullptr;  // nothing enters a tile from outside
+    } else if (!have && tiles) {
         a.states = reinterpret_cast<float*>(a.ws + chain_bytes(tiles, a.D));
         GScanArgs f = a;
         f.h = nullptr;
         f.sT = nullptr;
         if (hipError_t e = fwd_v<kOdd, TX, TG, VEC>(f, st)) return e;
     }
-    Chain ch{};
-    if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)(tiles + extra) * (unsigned)cb);
-    if (tiles > 1) {
-        if (hipError_t e = make_chain(a.ws, tiles, a.D, cb, ch, st)) return e;
-        hipLaunchKernelGGL((k_gscan_bwd<kOdd, TX, TG, VEC, true>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
-    } else {
-        hipLaunchKernelGGL((k_gscan_bwd<kOdd, TX, TG, VEC, false>), grid, dim3(kThreads), 0, st, a, tiles, cb, ch);
+    if (single) {
+        hipLaunchKernelGGL((k_gscan_bwd<kOdd, TX, TG, VEC, false>), grid, dim3(kThreads), 0, st, a, tiles,
+                           rows && a.seq.T ? a.seq.T : kScanTile, cb, Chain{});
+        return hipGetLastError();
     }
+    Chain ch{};
+    if (hipError_t e = make_chain(a.ws, tiles, a.D, cb, ch, st)) return e;
+    hipLaunchKernelGGL((k_gscan_bwd<kOdd, TX, TG, VEC, true>), grid, dim3(kThreads), 0, st, a, tiles, kScanTile, cb, ch);
     return hipGetLastError();
 }
 
@@ -631,10 +651,11 @@ hipError_t bwd_t(const GScanArgs& a, bool have, hipStream_t st) {
 
 // (sized for 64-token tiles, whatever the types)
 size_t gscan_fwd_ws(const SeqView& seq, int64_t D) {
-    return by_rows(seq) ? 0 : chain_bytes(tiles_of(seq.total, kScanTile), D);
+    return by_rows(seq) || one_tile(seq, kScanTile) ? 0 : chain_bytes(tiles_of(seq.total, kScanTile), D);
 }
-size_t gscan_bwd_ws(int64_t total, int64_t D) {
-    const size_t tiles = tiles_of(total, kScanTile);
+size_t gscan_bwd_ws(const SeqView& seq, int64_t D) {
+    if (one_tile(seq, kScanTile)) return 0;
+    const size_t tiles = tiles_of(seq.total, kScanTile);
     return chain_bytes(tiles, D) + tiles * D * 4;
 }
 

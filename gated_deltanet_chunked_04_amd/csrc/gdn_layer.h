@@ -96,7 +96,7 @@ struct GScanArgs {
     unsigned char* ws;
 };
 size_t gscan_fwd_ws(const SeqView& seq, int64_t D);
-size_t gscan_bwd_ws(int64_t total, int64_t D);
+size_t gscan_bwd_ws(const SeqView& seq, int64_t D);
 hipError_t launch_gscan_fwd(const GScanArgs& a, int dtype, int g_dtype, hipStream_t st);
 hipError_t launch_gscan_bwd(const GScanArgs& a, int dtype, int g_dtype, bool have_states, hipStream_t st);
 

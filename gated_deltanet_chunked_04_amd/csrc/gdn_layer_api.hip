@@ -83,7 +83,7 @@ gdn_status gdn_gated_scan_bwd_workspace_size(const gdn_scan_desc* desc, size_t* 
     SeqView seq;
     if (!bytes) return GDN_ERR_INVALID_ARG;
     if (gdn_status s = check_scan(desc, seq)) return s;
-    *bytes = gscan_bwd_ws(seq.total, desc->D);
+    *bytes = gscan_bwd_ws(seq, desc->D);
     return GDN_OK;
 }
 
@@ -126,7 +126,7 @@ gdn_status gdn_gated_scan_bwd(const gdn_scan_desc* desc, const void* x, const vo
     if (a.seq.total && (!x || !g || !d_h || !dx || !dg)) return GDN_ERR_INVALID_ARG;
     if (a.seq.total && (dx == x || dx == g || dx == d_h || dg == x || dg == g || dg == d_h || dx == dg)) return GDN_ERR_INVALID_ARG;
     if (d_initial_state && (d_initial_state == initial_state || d_initial_state == d_final_state)) return GDN_ERR_INVALID_ARG;
-    const size_t need = gscan_bwd_ws(a.seq.total, desc->D);
+    const size_t need = gscan_bwd_ws(a.seq, desc->D);
     if (need)
         if (gdn_status s = check_buf(workspace, need, workspace_bytes)) return s;
     if (states && reinterpret_cast<uintptr_t>(states) % 256) return GDN_ERR_WORKSPACE;

@@ -181,7 +181,9 @@ def gdn_gated_scan_fwd(x, g, initial_state=None, *, cu_seqlens=None, output_fina
     pg = _like("g", g, shape, g.dtype, dev)
     p0 = _like("initial_state", initial_state, (N, shape[2]), torch.float32, dev)
     h, ph = _out("h", h, x, shape, x.dtype, dev)
-    if output_final_state:
+    if output_final_state and final_state is not None and final_state is initial_state:
+        pT = p0
+    elif output_final_state:
         final_state, pT = _out("final_state", final_state, x, (N, shape[2]), torch.float32, dev)
     else:
         final_state = pT = None
@@ -256,7 +258,9 @@ def gdn_short_conv_fwd(x, weight, bias=None, initial_state=None, *, activation="
     p0 = _like("initial_state", initial_state, sshape, x.dtype, dev)
     y, py = _out("y", y, x, shape, x.dtype, dev)
     pT = None
-    if final_state is not None or output_final_state:
+    if final_state is not None and final_state is initial_state:
+        pT = p0
+    elif final_state is not None or output_final_state:
         final_state, pT = _out("final_state", final_state, x, sshape, x.dtype, dev)
     _run(load_library().gdn_short_conv_fwd, dev, ref, x.data_ptr(), pw, pb, p0, py, pT)
     return y, final_state

@@ -371,7 +371,8 @@ gdn_status gdn_gated_scan_states_size(const gdn_scan_desc* desc, size_t* bytes);
  *   initial_state may be NULL (zeros); final_state may be NULL (not written) or initial_state
  *   itself (updated in place, for decoding)
  *   states: NULL, or a buffer of gdn_gated_scan_states_size bytes (256-byte aligned) that receives
- *   the fp32 state entering every 64th token, for gdn_gated_scan_bwd
+ *   what gdn_gated_scan_bwd needs of the forward: the fp32 state entering every 64th token (nothing
+ *   is written where a call is one tile of tokens and needs none)
  * A call of a few tokens per sequence (decoding) is one launch and needs no workspace. */
 gdn_status gdn_gated_scan_fwd(const gdn_scan_desc* desc, const void* x, const void* g,
                               const float* initial_state, void* h, float* final_state, void* states,

@@ -41,7 +41,7 @@ def packed(lens, head=0, tail=0):
 
 # (B, T, D) and packed batches: one token, tiles met and passed by one, ragged and empty sequences, tokens that
 # belong to no sequence in front and behind, channels that fill vectors and ones that do not
-ROWS = [(1, 1, 1), (3, 1, 64), (2, 5, 256), (1, 16, 513), (1, 63, 64), (1, 64, 128), (1, 65, 260), (2, 129, 96),
+ROWS = [(1, 128, 136), (5, 64, 130), (70, 17, 128), (130, 64, 3), (3, 128, 260), (2, 17, 64), (1, 1, 1), (3, 1, 64), (2, 5, 256), (1, 16, 513), (1, 63, 64), (1, 64, 128), (1, 65, 260), (2, 129, 96),
         (3, 200, 77), (1, 700, 520)]
 PACKS = [([1], 0, 0, 8), ([0] * 200 + [20] + [0] * 300 + [90, 0] + [7] * 9, 3, 2, 132), ([2, 0, 3, 9, 1, 0, 0, 4] * 5, 0, 0, 131), ([0, 5, 0, 0, 70, 1, 1, 1, 64, 3, 0], 0, 0, 256), ([130, 200, 33], 7, 90, 72),
          ([0, 0], 0, 10, 16), ([1] * 70, 1, 1, 33), ([300, 2, 1, 90], 64, 64, 512)]

@@ -89,7 +89,9 @@ def test_grids_beyond_32_bits(lib):
 def test_scan_workspace_of_decoding(lib):
     """Short rows need none; packed sequences never more than the unpacked call of their size."""
     fn = lib.gdn_gated_scan_fwd_workspace_size
-    assert size(fn, scan_desc(B=1000, T=16)) == 0 and size(fn, scan_desc(B=1000, T=17)) > 0
+    for B, T in ((1000, 1), (1000, 16), (10, 64)):
+        assert size(fn, scan_desc(B=B, T=T)) == size(lib.gdn_gated_scan_bwd_workspace_size, scan_desc(B=B, T=T)) == 0
+    assert size(fn, scan_desc(B=10, T=65)) > 0
     for N in (1, 50, 300):
         assert size(fn, scan_desc(B=1, T=1000, cu_seqlens=0x1000, num_seqs=N)) <= size(fn, scan_desc(B=1, T=1000))
 
