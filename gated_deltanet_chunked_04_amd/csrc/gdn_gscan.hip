@@ -27,8 +27,6 @@ namespace {
 
 constexpr int kWaves = 8;              // waves of a tile
 constexpr int kThreads = kWaves * kWave;
-constexpr int kBwdTokens = 8;          // tokens of a wave in the gradient
-static_assert(kWaves * kBwdTokens == kScanTile, "a kept state per tile of the gradient");
 constexpr int kMaxSpins = 1 << 20;     // (about a second) a wait gives up with NaN rather than hang
 
 struct Chain {
@@ -305,9 +303,9 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
     }
 }
 
-template <bool kOdd, typename TX, typename TG, int VEC, bool kChain>
+template <bool kOdd, typename TX, typename TG, int VEC, int kTokens, bool kChain>
 __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, int span, int cblocks, Chain ch) {
-    constexpr int kTokens = kBwdTokens;
+    static_assert(kWaves * kTokens % kScanTile == 0, "a tile starts at a kept state");
     constexpr int CH = kWave * VEC;
     __shared__ __attribute__((aligned(16))) float2 agg[kWaves][CH];  // the forward's pairs, then the adjoint's
     __shared__ __attribute__((aligned(16))) float2 ragg[kWaves][CH];
@@ -416,7 +414,7 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
         // the states that enter the waves, from the tile's kept one
         const int t = threadIdx.x - (kThreads - CH);
         // (none where nothing enters a tile from outside)
-        float h = p.states && cbase + t < p.D ? p.states[(int64_t)tile * p.D + cbase + t] : 0.f;
+        float h = p.states && cbase + t < p.D ? p.states[(int64_t)(t0 / kScanTile) * p.D + cbase + t] : 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
             cin[w][t] = h;
@@ -528,9 +526,12 @@ bool by_rows(const SeqView& s) { return s.cu ? s.total / s.N <= 4 : s.T <= 16; }
 bool one_tile(const SeqView& s, int span) { return (s.cu ? s.total : s.T) <= span; }
 
 // Tokens of a wave forward: 16 where x and g are both bf16 (as many registers as 8 with fp32 gates), for half as
-// many pairs to look back over (64K x 4096 packed: 309 -> 285 us).
-template <typename TX, typename TG>
-constexpr int fwd_tokens() { return sizeof(TX) + sizeof(TG) == 4 ? 16 : 8; }
+// many pairs to look back over (64K x 4096 packed: 309 -> 285 us). With one channel per lane 16 too, in both
+// directions (64K x 64: 8 tokens 35 us, 16 23, 32 17, but 2,000 x 64: 7.5, 8.6, 13; training 60,000 x 16: 62, 44, 50).
+template <typename TX, typename TG, int VEC>
+constexpr int fwd_tokens() { return VEC == 1 || sizeof(TX) + sizeof(TG) == 4 ? 16 : 8; }
+template <int VEC>
+constexpr int bwd_tokens() { return VEC == 1 ? 16 : 8; }
 
 // Clears a chain: the ticket to zero, every word behind it to "not there yet".
 __global__ __launch_bounds__(256) void k_clear(u32x4* p, int64_t n) {
@@ -604,21 +605,22 @@ hipError_t fwd_v(const GScanArgs& a, hipStream_t st) {
     // Kept states lie 64 tokens apart, so rows that need them and have more take the chain.
     if (one_tile(a.seq, kScanTile)) return fwd_single<kOdd, TX, TG, VEC, 8>(a, cb, st);
     if (!a.states && one_tile(a.seq, 2 * kScanTile)) return fwd_single<kOdd, TX, TG, VEC, 16>(a, cb, st);
-    return fwd_tiles<kOdd, TX, TG, VEC, fwd_tokens<TX, TG>()>(a, cb, st);
+    return fwd_tiles<kOdd, TX, TG, VEC, fwd_tokens<TX, TG, VEC>()>(a, cb, st);
 }
 
 template <bool kOdd, typename TX, typename TG, int VEC>
 hipError_t bwd_v(GScanArgs a, bool have, hipStream_t st) {
     const int cb = (int)((a.D + kWave * VEC - 1) / (kWave * VEC));
+    constexpr int kTok = bwd_tokens<VEC>();
     const bool single = one_tile(a.seq, kScanTile), rows = single && !a.seq.cu;  // (as forward)
-    const int tiles = rows ? (a.seq.T > 0 ? a.seq.N : 0) : tiles_of(a.seq.total, kScanTile);
+    const int tiles = rows ? (a.seq.T > 0 ? a.seq.N : 0) : tiles_of(a.seq.total, single ? kScanTile : kWaves * kTok);
     const int extra = a.ds0 && (a.seq.cu || a.seq.T == 0);
     if (tiles + extra == 0) return hipSuccess;
     if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
     if (single) {
         a.states = nullptr;  // nothing enters a tile from outside
     } else if (!have && tiles) {
-        a.states = reinterpret_cast<float*>(a.ws + chain_bytes(tiles, a.D));
+        a.states = reinterpret_cast<float*>(a.ws + chain_bytes(tiles_of(a.seq.total, kScanTile), a.D));
         GScanArgs f = a;
         f.h = nullptr;
         f.sT = nullptr;
@@ -626,13 +628,13 @@ hipError_t bwd_v(GScanArgs a, bool have, hipStream_t st) {
     }
     const dim3 grid((unsigned)(tiles + extra) * (unsigned)cb);
     if (single) {
-        hipLaunchKernelGGL((k_gscan_bwd<kOdd, TX, TG, VEC, false>), grid, dim3(kThreads), 0, st, a, tiles,
+        hipLaunchKernelGGL((k_gscan_bwd<kOdd, TX, TG, VEC, 8, false>), grid, dim3(kThreads), 0, st, a, tiles,
                            rows && a.seq.T ? a.seq.T : kScanTile, cb, Chain{});
         return hipGetLastError();
     }
     Chain ch{};
     if (hipError_t e = make_chain(a.ws, tiles, a.D, cb, ch, st)) return e;
-    hipLaunchKernelGGL((k_gscan_bwd<kOdd, TX, TG, VEC, true>), grid, dim3(kThreads), 0, st, a, tiles, kScanTile, cb, ch);
+    hipLaunchKernelGGL((k_gscan_bwd<kOdd, TX, TG, VEC, kTok, true>), grid, dim3(kThreads), 0, st, a, tiles, kWaves * kTok, cb, ch);
     return hipGetLastError();
 }
 

@@ -21,6 +21,7 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxWaves = 16;
 constexpr float kE4m3Max = 448.f;
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
@@ -38,32 +39,48 @@ __device__ __forceinline__ uint32_t umax_ln(uint32_t x) {
     return max(x, dpp_u<0x140>(x));
 }
 
-// Sum (or largest) over the lanes of a row: a wave, or the workgroup's LANES / 64 waves through LDS. The
-// same bits in every lane. `slot`: which of the kernel's LDS words this call uses (two calls in a row use
-// different ones, so one barrier per call is enough).
+// Sum (or largest) over the LANES threads of a row: 4, 16 or 32 lanes, a wave, or LANES / 64 waves through LDS. The
+// same bits in every one. `slot`: which of the kernel's LDS words this call uses (two calls in a row use different
+// ones, so one barrier per call is enough). All threads call it.
+template <int LANES> constexpr int waves_of() { return LANES > 64 ? LANES / 64 : 1; }
 template <int LANES>
-__device__ __forceinline__ float row_sum(float v, float (*sh)[LANES / 64], int slot) {
-    v = sum_rows(sum_ln(v));
+__device__ __forceinline__ float row_sum(float v, float (*sh)[kMaxWaves], int slot) {
+    if constexpr (LANES == 4) {
+        v += dpp_f<0xB1>(v);
+        return v + dpp_f<0x4E>(v);
+    }
+    v = sum_ln(v);
+    if constexpr (LANES == 16) return v;
+    if constexpr (LANES == 32) return v + __shfl_xor(v, 16);
+    v = sum_rows(v);
     if constexpr (LANES > 64) {
+        const int first = (threadIdx.x / LANES) * waves_of<LANES>();
         if ((threadIdx.x & 63) == 0) sh[slot][threadIdx.x >> 6] = v;
         __syncthreads();
         v = 0.f;
 #pragma unroll
-        for (int i = 0; i < LANES / 64; ++i) v += sh[slot][i];
+        for (int i = 0; i < waves_of<LANES>(); ++i) v += sh[slot][first + i];
     }
     return v;
 }
 template <int LANES>
-__device__ __forceinline__ uint32_t row_umax(uint32_t v, float (*sh)[LANES / 64], int slot) {
+__device__ __forceinline__ uint32_t row_umax(uint32_t v, float (*sh)[kMaxWaves], int slot) {
+    if constexpr (LANES == 4) {
+        v = max(v, dpp_u<0xB1>(v));
+        return max(v, dpp_u<0x4E>(v));
+    }
     v = umax_ln(v);
+    if constexpr (LANES == 16) return v;
     v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+    if constexpr (LANES == 32) return v;
     v = max(v, (uint32_t)__shfl_xor((int)v, 32));
     if constexpr (LANES > 64) {
+        const int first = (threadIdx.x / LANES) * waves_of<LANES>();
         if ((threadIdx.x & 63) == 0) sh[slot][threadIdx.x >> 6] = __uint_as_float(v);
         __syncthreads();
         v = 0;
 #pragma unroll
-        for (int i = 0; i < LANES / 64; ++i) v = max(v, __float_as_uint(sh[slot][i]));
+        for (int i = 0; i < waves_of<LANES>(); ++i) v = max(v, __float_as_uint(sh[slot][first + i]));
     }
     return v;
 }
@@ -102,15 +119,17 @@ __device__ __forceinline__ float own(float x, int i, int skip) { return kOdd && 
 
 enum { kPlain = 0, kRowScale = 1, kGroupScale = 2 };
 
-// One row per LANES threads; LANES = 64 puts four rows in a workgroup of 256, else a row has the workgroup.
+// A row per LANES threads, in workgroups of 256 or one row.
+template <int LANES> constexpr int threads_of() { return LANES > kThreads ? LANES : kThreads; }
+template <int LANES> constexpr int rows_of() { return threads_of<LANES>() / LANES; }
+
 template <bool kOdd, typename T, typename TW, int LANES, int NV, int OUT>
-__global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_fwd(RmsArgs p) {
-    __shared__ float sh[2][LANES / 64];
-    constexpr int kRows = LANES == 64 ? kThreads / 64 : 1;
+__global__ __launch_bounds__(threads_of<LANES>()) void k_rms_fwd(RmsArgs p) {
+    __shared__ float sh[2][kMaxWaves];
     const int lane = threadIdx.x % LANES;
-    const int64_t row = LANES == 64 ? (int64_t)blockIdx.x * kRows + wave_id() : (int64_t)blockIdx.x;
-    if (row >= p.rows) return;  // whole waves, and with LANES > 64 never
-    const int64_t base = row * p.D;
+    const int64_t row = (int64_t)blockIdx.x * rows_of<LANES>() + threadIdx.x / LANES;
+    const bool active = rows_of<LANES>() == 1 || row < p.rows;  // (threads without a row take part in the sums)
+    const int64_t base = active ? row * p.D : 0;
     Raw<T, 8> r[NV], s[NV];
     Raw<TW, 8> w[NV];
     int skip[NV];
@@ -120,7 +139,7 @@ __global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_fwd
     for (int v = 0; v < NV; ++v) {
         const int64_t c0 = 8 * ((int64_t)v * LANES + lane);
         const Lane ln(c0, p.D, 8);
-        live[v] = c0 < p.D;
+        live[v] = active && c0 < p.D;
         at[v] = ln.at;
         skip[v] = ln.skip;
         r[v].clear();
@@ -169,8 +188,8 @@ __global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_fwd
 #pragma unroll
                 for (int i = 0; i < 8; ++i) m = max(m, abs_bits(own<kOdd>(r[v].get(i) * rstd * w[v].get(i), i, skip[v])));
             if constexpr (OUT == kGroupScale) {
-                scale[v] = scale_of(umax_ln(m));
-                if (live[v] && (lane & 15) == 0)
+                scale[v] = scale_of(row_umax<(LANES < 16 ? LANES : 16)>(m, sh, 1));
+                if (live[v] && lane % 16 == 0)
                     p.scale[row * ((p.D + 127) / 128) + (v * LANES + lane) / 16] = scale[v];
             } else {
                 top = max(top, m);
@@ -180,7 +199,7 @@ __global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_fwd
             const float sc = scale_of(row_umax<LANES>(top, sh, 1));
 #pragma unroll
             for (int v = 0; v < NV; ++v) scale[v] = sc;
-            if (lane == 0) p.scale[row] = sc;
+            if (active && lane == 0) p.scale[row] = sc;
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -201,11 +220,12 @@ __global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_fwd
 // columns' dy rh in registers; at the end the workgroup's waves add theirs in LDS where they hold the same
 // columns, and part[blockIdx.x] gets them.
 template <bool kOdd, typename T, typename TW, int LANES, int NV>
-__global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_bwd(RmsArgs p, float* part) {
-    constexpr int kRows = LANES == 64 ? kThreads / 64 : 1;
-    __shared__ float sh[4][LANES / 64];
-    __shared__ float shw[LANES == 64 ? (kRows - 1) * 64 * 8 * NV : 1];
-    const int lane = threadIdx.x % LANES;
+__global__ __launch_bounds__(threads_of<LANES>()) void k_rms_bwd(RmsArgs p, float* part) {
+    constexpr int kRows = rows_of<LANES>();
+    static_assert(kRows == 1 || NV == 1, "rows that share a workgroup have one vector a lane");
+    __shared__ float sh[4][kMaxWaves];
+    __shared__ float shw[kRows > 1 ? kRows : 1][8][LANES];
+    const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     int skip[NV];
     int64_t at[NV];
     bool live[NV];
@@ -222,29 +242,29 @@ __global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_bwd
     }
     float dw[NV][8] = {};
     int slot = 0;
-    const int64_t first = LANES == 64 ? (int64_t)blockIdx.x * kRows + wave_id() : (int64_t)blockIdx.x;
     // the next row is loaded while the present one is worked on, where both fit the registers of two waves a SIMD
     constexpr bool kAhead = NV < 4;
     Raw<T, 8> nr[NV], nd[NV], ns[NV];
-    auto fetch = [&](int64_t row) {
-        const int64_t base = row * p.D;
+    auto fetch = [&](int64_t first) {
+        const int64_t row = first + sub, base = row * p.D;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             nr[v].clear();
             nd[v].clear();
             ns[v].clear();
-            if (live[v]) {
+            if (live[v] && (kRows == 1 || row < p.rows)) {
                 nr[v] = load_raw<T, 8>(static_cast<const T*>(p.x) + base + at[v]);
                 nd[v] = load_raw<T, 8>(static_cast<const T*>(p.d_y) + base + at[v]);
                 if (p.d_res) ns[v] = load_raw<T, 8>(static_cast<const T*>(p.d_res) + base + at[v]);
             }
         }
     };
-    const int64_t step = (int64_t)gridDim.x * kRows;
-    if (first < p.rows) fetch(first);
-    for (int64_t row = first; row < p.rows; row += step) {
-        const int64_t base = row * p.D;
-        if (!kAhead && row != first) fetch(row);
+    const int64_t step = (int64_t)gridDim.x * kRows, begin = (int64_t)blockIdx.x * kRows;
+    if (begin < p.rows) fetch(begin);
+    for (int64_t first = begin; first < p.rows; first += step) {
+        const int64_t row = first + sub, base = row * p.D;
+        const bool active = kRows == 1 || row < p.rows;
+        if (!kAhead && first != begin) fetch(first);
         Raw<T, 8> r[NV], d[NV], s[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -252,7 +272,7 @@ __global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_bwd
             d[v] = nd[v];
             s[v] = ns[v];
         }
-        if (kAhead && row + step < p.rows) fetch(row + step);
+        if (kAhead && first + step < p.rows) fetch(first + step);
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
@@ -265,7 +285,7 @@ __global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_bwd
         ss = row_sum<LANES>(ss, sh, slot);
         dot = row_sum<LANES>(dot, sh, slot + 1);
         slot ^= 2;
-        const float rstd = 1.f / sqrtf(ss / (float)p.D + p.eps);
+        const float rstd = active ? 1.f / sqrtf(ss / (float)p.D + p.eps) : 0.f;
         const float m = dot * rstd / (float)p.D;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -279,25 +299,18 @@ __global__ __launch_bounds__(LANES > kThreads ? LANES : kThreads) void k_rms_bwd
             if (p.d_res)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i] += s[v].get(i);
-            if (live[v]) store_own<kOdd, T, 8>(static_cast<T*>(p.dx) + base + at[v], o, skip[v]);
+            if (live[v] && active) store_own<kOdd, T, 8>(static_cast<T*>(p.dx) + base + at[v], o, skip[v]);
         }
     }
     if (!p.dw) return;
-    if constexpr (LANES == 64) {
-        const int wave = wave_id();
-        if (wave > 0)
+    if constexpr (kRows > 1) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) shw[(((wave - 1) * NV + v) * 8 + i) * 64 + lane] = dw[v][i];
+        for (int i = 0; i < 8; ++i) shw[sub][i][lane] = dw[0][i];
         __syncthreads();
-        if (wave > 0) return;
+        if (sub > 0) return;
+        for (int k = 1; k < kRows; ++k)
 #pragma unroll
-        for (int k = 0; k < kRows - 1; ++k)
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dw[v][i] += shw[((k * NV + v) * 8 + i) * 64 + lane];
+            for (int i = 0; i < 8; ++i) dw[0][i] += shw[k][i][lane];
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -316,7 +329,7 @@ __global__ __launch_bounds__(kSumThreads) void k_rms_dw_sum(const float* part, i
 constexpr int kLoopThreads = 1024;
 constexpr int kSlots = kLoopThreads / 64;
 
-__device__ __forceinline__ float loop_sum(float v, float (*sh)[kSlots]) {
+__device__ __forceinline__ float loop_sum(float v, float (*sh)[kMaxWaves]) {
     const float s = row_sum<kLoopThreads>(v, sh, 0);
     __syncthreads();
     return s;
@@ -324,7 +337,7 @@ __device__ __forceinline__ float loop_sum(float v, float (*sh)[kSlots]) {
 
 template <typename T, typename TW, bool kQuant>
 __global__ __launch_bounds__(kLoopThreads) void k_rms_fwd_loop(RmsArgs p) {
-    __shared__ float sh[1][kSlots];
+    __shared__ float sh[1][kMaxWaves];
     const int64_t base = (int64_t)blockIdx.x * p.D;
     const T* x = static_cast<const T*>(p.x) + base;
     const T* res = p.res ? static_cast<const T*>(p.res) + base : nullptr;
@@ -369,7 +382,7 @@ __global__ __launch_bounds__(kLoopThreads) void k_rms_fwd_loop(RmsArgs p) {
 
 template <typename T, typename TW>
 __global__ __launch_bounds__(kLoopThreads) void k_rms_dx_loop(RmsArgs p, float* rstds) {
-    __shared__ float sh[1][kSlots];
+    __shared__ float sh[1][kMaxWaves];
     const int64_t base = (int64_t)blockIdx.x * p.D;
     const T* r = static_cast<const T*>(p.x) + base;
     const T* dy = static_cast<const T*>(p.d_y) + base;
@@ -411,18 +424,19 @@ __global__ __launch_bounds__(kThreads) void k_rms_dw_loop(RmsArgs p, const float
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Lanes and vectors of a row: a wave up to 512 columns, a workgroup of 256 up to 8,192, one of 1,024 up to
-// 32,768 columns; 0: by elements. (A wave for 2,048 columns, four vectors a lane, was slower: 32,768 rows of
-// them to e4m3 took 85 us against 80, and 5,003 fp32 rows of 1,001 columns 19 against 15.5.)
+// Threads and vectors of a row: as many threads as it has vectors, in steps of 4 (32 columns), 16 (128), 32, 64, 128
+// and 256, then up to four vectors a thread, of 256 threads to 8,192 columns and of 1,024 to 32,768; 0: by
+// elements. (A wave for 2,048 columns, four vectors a lane, was slower: 32,768 rows of them to e4m3 took 85 us
+// against 80, and 5,003 fp32 rows of 1,001 columns 19 against 15.5.)
 struct Shape {
     int lanes, nv;
 };
 Shape shape_of(int64_t D) {
     if (D < 8 || D > 32768) return {0, 0};
-    auto nv = [&](int lanes) { const int64_t n = (D + 8 * lanes - 1) / (8 * lanes); return (int)(n <= 1 ? 1 : (n <= 2 ? 2 : 4)); };
-    if (D <= 512) return {64, nv(64)};
-    if (D <= 8192) return {256, nv(256)};
-    return {1024, nv(1024)};
+    if (D <= 1024) return {D <= 32 ? 4 : (D <= 128 ? 16 : (D <= 256 ? 32 : (D <= 512 ? 64 : 128))), 1};
+    const int lanes = D <= 8192 ? 256 : 1024;
+    const int64_t n = (D + 8 * lanes - 1) / (8 * lanes);
+    return {lanes, (int)(n <= 1 ? 1 : (n <= 2 ? 2 : 4))};
 }
 // The gradient's: its sums of dw double the registers a column takes, so 512 lanes and four vectors are the most.
 Shape bwd_shape_of(int64_t D) {
@@ -435,14 +449,17 @@ hipError_t fwd_o(const RmsArgs& a, hipStream_t st) {
     const Shape s = shape_of(a.D);
 #define GDN_RMS_FWD(LANES, NV)                                                                              \
     if (s.lanes == LANES && s.nv == NV) {                                                                   \
-        constexpr int kRows = LANES == 64 ? kThreads / 64 : 1;                                              \
-        if (!grid_fits((a.rows + kRows - 1) / kRows, LANES > kThreads ? LANES : kThreads))                  \
-            return hipErrorInvalidConfiguration;                                                            \
-        hipLaunchKernelGGL((k_rms_fwd<kOdd, T, TW, LANES, NV, OUT>), dim3((unsigned)((a.rows + kRows - 1) / kRows)), \
-                           dim3(LANES > kThreads ? LANES : kThreads), 0, st, a);                            \
+        const int64_t groups = (a.rows + rows_of<LANES>() - 1) / rows_of<LANES>();                          \
+        if (!grid_fits(groups, threads_of<LANES>())) return hipErrorInvalidConfiguration;                   \
+        hipLaunchKernelGGL((k_rms_fwd<kOdd, T, TW, LANES, NV, OUT>), dim3((unsigned)groups),                \
+                           dim3(threads_of<LANES>()), 0, st, a);                                            \
         return hipGetLastError();                                                                           \
     }
+    GDN_RMS_FWD(4, 1)
+    GDN_RMS_FWD(16, 1)
+    GDN_RMS_FWD(32, 1)
     GDN_RMS_FWD(64, 1)
+    GDN_RMS_FWD(128, 1)
     GDN_RMS_FWD(256, 1)
     GDN_RMS_FWD(256, 2)
     GDN_RMS_FWD(256, 4)
@@ -462,13 +479,13 @@ hipError_t fwd_t(const RmsArgs& a, int out, hipStream_t st) {
     return odd ? fwd_o<true, T, TW, kRowScale>(a, st) : fwd_o<false, T, TW, kRowScale>(a, st);
 }
 
-// Workgroups of the gradient, each with its own partial sums of dw: two to each of the 256 compute units, or
-// fewer where there are fewer rows (32,768 rows of 2,048: 98 us; four to each 106, eight 116, for the partial
-// sums grow with them).
+// Workgroups of the gradient, each with its own partial sums of dw: as many as the 256 compute units hold at a time
+// (two each, one where a thread has four vectors), or fewer where there are fewer rows. 32,768 rows of 2,048: 256
+// 124 us, 512 98, 1,024 106, 2,048 116; 8,000 rows of 8,192: 256 111, 512 117.
 int64_t bwd_groups(int64_t rows, const Shape& s) {
-    const int64_t per = s.lanes == 64 ? kThreads / 64 : 1;
+    const int64_t per = s.lanes < kThreads ? kThreads / s.lanes : 1, most = s.nv == 4 ? 256 : 512;
     const int64_t n = (rows + per - 1) / per;
-    return n < 512 ? n : 512;
+    return n < most ? n : most;
 }
 int64_t loop_parts(int64_t rows) { return (rows + kLoopSumRows - 1) / kLoopSumRows; }
 
@@ -483,10 +500,14 @@ hipError_t bwd_o(const RmsArgs& a, hipStream_t st) {
 #define GDN_RMS_BWD(LANES, NV)                                                                              \
         if (s.lanes == LANES && s.nv == NV) {                                                               \
             hipLaunchKernelGGL((k_rms_bwd<kOdd, T, TW, LANES, NV>), dim3((unsigned)parts),                  \
-                               dim3(LANES > kThreads ? LANES : kThreads), 0, st, a, part);                  \
+                               dim3(threads_of<LANES>()), 0, st, a, part);                                  \
             done = true;                                                                                    \
         }
+        GDN_RMS_BWD(4, 1)
+        GDN_RMS_BWD(16, 1)
+        GDN_RMS_BWD(32, 1)
         GDN_RMS_BWD(64, 1)
+        GDN_RMS_BWD(128, 1)
         GDN_RMS_BWD(256, 1)
         GDN_RMS_BWD(256, 2)
         GDN_RMS_BWD(256, 4)

@@ -346,7 +346,7 @@ def test_conv_nan_stays_in_its_sequence(gpu_lib):
 
 # ---- RMS norm -----------------------------------------------------------------------------------
 
-RMS_SHAPES = [(1, 1), (3, 8), (2, 100), (5, 128), (7, 129), (4, 512), (3, 513), (2, 1000), (9, 1024), (3, 2047), (2, 2048),
+RMS_SHAPES = [(1, 1), (70, 8), (35, 255), (9, 256), (9, 257), (700, 136), (131, 31), (65, 32), (66, 33), (19, 127), (17, 128), (3, 1023), (5, 520), (3, 8), (2, 100), (5, 128), (7, 129), (4, 512), (3, 513), (2, 1000), (9, 1024), (3, 2047), (2, 2048),
               (300, 2056), (2, 4096), (2, 5120), (3, 8192), (2, 8200), (1, 16384), (70, 264)]
 
 
