@@ -392,11 +392,11 @@ template <typename T> int bwd_vec(int64_t D) {
 }
 
 // Tokens per wave: rows of at most 16 tokens go to one wave each (which makes their state's update in
-// place safe: one wave reads it before it writes it). Longer axes take 32, or 8 where 32 would leave
-// the chip's 1,024 SIMDs without two waves each: fewer tokens re-read against more waves in flight.
+// place safe: one wave reads it before it writes it). Longer axes take 16, or 8 where there are too few for 4,096
+// waves of 16 (32K x 6144 bf16: 8 tokens 145 us, 16 139, 32 153, 64 164; 8192 x 2048: 15.0, 18.6).
 int fwd_run(const SeqView& s, unsigned cblocks) {
     if (!s.cu && s.T <= 16) return s.T > 0 ? s.T : 1;
-    return (int64_t)s.total * cblocks >= 2048 * 16 ? 16 : 8;
+    return (int64_t)s.total * cblocks >= 4096 * 16 ? 16 : 8;
 }
 
 template <typename T, typename TW, int W, int VEC>
@@ -423,11 +423,15 @@ hipError_t fwd_t(const ConvArgs& a, hipStream_t st) {
     return v == wide ? fwd_v<T, TW, W, wide>(a, st) : (v == slim ? fwd_v<T, TW, W, slim>(a, st) : fwd_v<T, TW, W, 1>(a, st));
 }
 
-// Tokens per wave in the gradient: 24, or 8 where 24 would leave fewer than 4,096 waves. Longer runs re-read less
-// and leave fewer partial sums, shorter ones put more waves in flight and lose less where sequences end inside
-// them (2 x 16384 x 6144 bf16, W = 4: 24 tokens 239 us, 32 253, 48 256, 64 271, 136 292; 30,000 tokens in 50
-// sequences: 234, 238, 247, 259, 320; 4,099 x 768 fp32, W = 3: 8 tokens 15.7 us, 16 19.9).
-int bwd_run(int64_t total, unsigned cblocks) { return total * cblocks >= 24 * 4096 ? 24 : 8; }
+// Tokens per wave in the gradient: 24, or 16 or 8 where there are too few for 2,304 waves of 24, 2,048 of 16. Longer
+// runs re-read less and leave fewer partial sums, shorter ones put more waves in flight and lose less where
+// sequences end inside them (2 x 16384 x 6144 bf16, W = 4: 24 tokens 239 us, 32 253, 48 256, 64 271, 136 292; 30,000
+// tokens in 50 sequences: 234, 238, 247, 259, 320; 30,000 x 512: 8 tokens 34 us, 16 33, 24 31; 2,048 x 6144: 26, 25,
+// 28; 4,099 x 768 fp32, W = 3: 8 tokens 15.7 us, 16 19.9).
+int bwd_run(int64_t total, unsigned cblocks) {
+    const int64_t n = total * cblocks;
+    return n >= 24 * 2304 ? 24 : (n >= 16 * 2048 ? 16 : 8);
+}
 int bwd_parts(int64_t total, int run) { return (int)((total + (int64_t)run * kWaves - 1) / ((int64_t)run * kWaves)); }
 
 template <typename T, typename TW, int W, int VEC>
