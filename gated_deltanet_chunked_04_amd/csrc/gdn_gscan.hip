@@ -5,9 +5,9 @@
 //
 // Bound by memory: 3 operations per element forward and 8 backward, against 8 and 14 bytes (bf16
 // with fp32 gates). So every input is read once, in a single pass over the token axis:
-//   * A workgroup of eight waves holds a tile of tokens by 64 VEC channels in registers, eight tokens
-//     to a wave. A run of tokens acts on the state that enters it as c -> A c + H; the waves' pairs
-//     (A, H) meet in LDS and make the tile's pair.
+//   * A workgroup of eight waves holds a tile of tokens by 64 VEC channels in registers, 8 or 16 tokens to a
+//     wave. A run of tokens acts on the state that enters it as c -> A c + H; the waves' pairs (A, H) meet in
+//     LDS and make the tile's pair.
 //   * The tile publishes its pair, gathers the state that enters it from the tiles before it (enter_tile),
 //     and each wave runs its tokens again from its own entering state, now with their outputs.
 //   * Tiles are handed out in the order of the token axis by a counter, so a tile only ever waits for
@@ -525,11 +525,12 @@ bool by_rows(const SeqView& s) { return s.cu ? s.total / s.N <= 4 : s.T <= 16; }
 // tile (256 rows of 64 x 2048: 52 us, as a chain of full tiles 61; 16 rows of 24: 5.5 and 10).
 bool one_tile(const SeqView& s, int span) { return (s.cu ? s.total : s.T) <= span; }
 
-// Tokens of a wave forward: 16 where x and g are both bf16 (as many registers as 8 with fp32 gates), for half as
-// many pairs to look back over (64K x 4096 packed: 309 -> 285 us). With one channel per lane 16 too, in both
-// directions (64K x 64: 8 tokens 35 us, 16 23, 32 17, but 2,000 x 64: 7.5, 8.6, 13; training 60,000 x 16: 62, 44, 50).
-template <typename TX, typename TG, int VEC>
-constexpr int fwd_tokens() { return VEC == 1 || sizeof(TX) + sizeof(TG) == 4 ? 16 : 8; }
+// Channels per lane and tokens per wave (with a chain). Forward 2 channels by 16 tokens: as many registers as 4 by 8,
+// for tiles of half the channels and twice the tokens, which look back over half as many pairs and hand half as many
+// states on (32K x 2048 fp32 gates 104 us, 4 by 8 111, 4 by 16 112, 2 by 32 111; 256K x 1024 376 and 429). The gradient
+// 4 by 8, with more bytes a tile to each pair (2 by 16 was 4% slower). One channel in rows that would not fill a wave
+// otherwise, 16 tokens (64K x 64: 8 tokens 35 us, 16 23, 32 17, but 2,000 x 64: 7.5, 8.6, 13).
+constexpr int kFwdTokens = 16;
 template <int VEC>
 constexpr int bwd_tokens() { return VEC == 1 ? 16 : 8; }
 
@@ -544,7 +545,7 @@ __global__ __launch_bounds__(256) void k_clear(u32x4* p, int64_t n) {
 int tiles_of(int64_t total, int tile) { return (int)((total + tile - 1) / tile); }
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Four channels per lane, or one in rows so short that a wave would not be filled.
+// Rows of fewer channels have one channel per lane.
 constexpr int64_t kSlim = 128;
 
 // A chain in the workspace: 256 bytes for the ticket, the pairs, the groups' states.
@@ -554,13 +555,13 @@ size_t chain_bytes(size_t tiles, int64_t D) {
     return 256 + align256(tiles * D * 8) + align256(groups * D * 4);
 }
 // A group hands its state on in about a microsecond, one group after the other, while a tile looks back over half
-// a group's pairs. With eight channel blocks or more to a tile the memory takes longer than the chain and small
-// groups read less (32K x 2048 fp32 gates: groups of 8 110 us, 16 109, 32 119; 64K x 4096 bf16 gates: 285, 288, -).
-// With fewer, longer groups keep the chain short (64K tokens of 1024 channels: 8 138 us, 16 115; of 256: 8 101,
-// 32 51, 64 49; of 64: 8 116, 32 46, 64 35).
-hipError_t make_chain(unsigned char* ws, size_t tiles, int64_t D, int cblocks, Chain& ch, hipStream_t st) {
+// a group's pairs. From `wide` channels on the memory takes longer than the chain, and small groups read less (64K x
+// 4096: groups of 8 285 us, 16 288; training 2 x 16K x 2048: 279, 282). In fewer, longer groups keep the chain short
+// (64K tokens of 1024 channels: 8 138 us, 16 115; of 256: 8 101, 32 51, 64 49; of 64: 8 116, 32 46, 64 35; all these with
+// 64-token tiles).
+hipError_t make_chain(unsigned char* ws, size_t tiles, int64_t D, int64_t wide, Chain& ch, hipStream_t st) {
     const size_t bytes = chain_bytes(tiles, D);
-    ch.group = cblocks >= 8 ? kMinGroup : (cblocks >= 4 ? 16 : (D >= kSlim ? 32 : 64));
+    ch.group = D >= wide ? kMinGroup : (D >= 512 ? 16 : (D >= kSlim ? 32 : 64));
     ch.ticket = reinterpret_cast<uint32_t*>(ws);
     ch.pairs = reinterpret_cast<uint64_t*>(ws + 256);
     ch.carry = reinterpret_cast<uint32_t*>(ws + 256 + align256(tiles * D * 8));
@@ -575,7 +576,7 @@ hipError_t fwd_tiles(const GScanArgs& a, int cb, hipStream_t st) {
     const int extra = a.sT && a.seq.cu;
     Chain ch{};
     if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
-    if (hipError_t e = make_chain(a.ws, tiles, a.D, cb, ch, st)) return e;
+    if (hipError_t e = make_chain(a.ws, tiles, a.D, 4096, ch, st)) return e;
     hipLaunchKernelGGL((k_gscan_fwd<kOdd, TX, TG, VEC, TOK, true>), dim3((unsigned)(tiles + extra) * (unsigned)cb),
                        dim3(kThreads), 0, st, a, tiles, kWaves * TOK, cb, ch);
     return hipGetLastError();
@@ -605,9 +606,14 @@ hipError_t fwd_v(const GScanArgs& a, hipStream_t st) {
     // Kept states lie 64 tokens apart, so rows that need them and have more take the chain.
     if (one_tile(a.seq, kScanTile)) return fwd_single<kOdd, TX, TG, VEC, 8>(a, cb, st);
     if (!a.states && one_tile(a.seq, 2 * kScanTile)) return fwd_single<kOdd, TX, TG, VEC, 16>(a, cb, st);
-    return fwd_tiles<kOdd, TX, TG, VEC, fwd_tokens<TX, TG, VEC>()>(a, cb, st);
+    return fwd_tiles<kOdd, TX, TG, VEC, kFwdTokens>(a, cb, st);
 }
 
+template <typename TX, typename TG>
+hipError_t fwd_t(const GScanArgs& a, hipStream_t st) {
+    if (a.D < kSlim) return fwd_v<false, TX, TG, 1>(a, st);
+    return a.D % 2 ? fwd_v<true, TX, TG, 2>(a, st) : fwd_v<false, TX, TG, 2>(a, st);
+}
 template <bool kOdd, typename TX, typename TG, int VEC>
 hipError_t bwd_v(GScanArgs a, bool have, hipStream_t st) {
     const int cb = (int)((a.D + kWave * VEC - 1) / (kWave * VEC));
@@ -624,7 +630,7 @@ hipError_t bwd_v(GScanArgs a, bool have, hipStream_t st) {
         GScanArgs f = a;
         f.h = nullptr;
         f.sT = nullptr;
-        if (hipError_t e = fwd_v<kOdd, TX, TG, VEC>(f, st)) return e;
+        if (hipError_t e = fwd_t<TX, TG>(f, st)) return e;
     }
     const dim3 grid((unsigned)(tiles + extra) * (unsigned)cb);
     if (single) {
@@ -633,16 +639,11 @@ hipError_t bwd_v(GScanArgs a, bool have, hipStream_t st) {
         return hipGetLastError();
     }
     Chain ch{};
-    if (hipError_t e = make_chain(a.ws, tiles, a.D, cb, ch, st)) return e;
+    if (hipError_t e = make_chain(a.ws, tiles, a.D, 2048, ch, st)) return e;
     hipLaunchKernelGGL((k_gscan_bwd<kOdd, TX, TG, VEC, kTok, true>), grid, dim3(kThreads), 0, st, a, tiles, kWaves * kTok, cb, ch);
     return hipGetLastError();
 }
 
-template <typename TX, typename TG>
-hipError_t fwd_t(const GScanArgs& a, hipStream_t st) {
-    if (a.D < kSlim) return fwd_v<false, TX, TG, 1>(a, st);
-    return a.D % 4 ? fwd_v<true, TX, TG, 4>(a, st) : fwd_v<false, TX, TG, 4>(a, st);
-}
 template <typename TX, typename TG>
 hipError_t bwd_t(const GScanArgs& a, bool have, hipStream_t st) {
     if (a.D < kSlim) return bwd_v<false, TX, TG, 1>(a, have, st);
