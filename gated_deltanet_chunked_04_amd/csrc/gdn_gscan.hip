@@ -186,6 +186,14 @@ __device__ __forceinline__ int take(const Chain& ch, bool chain, int* sh) {
     return __builtin_amdgcn_readfirstlane(*sh);
 }
 
+// A lane's first channel, counted from the block's (below zero where the vector is moved back, Lane). Lanes behind
+// the row load a vector inside it too.
+template <bool kOdd, int VEC>
+__device__ __forceinline__ int first_channel(int64_t D, int64_t cbase, bool live, int lane, int skip) {
+    if (live) return lane * VEC - skip;
+    return kOdd && cbase + VEC > D ? (int)(D - VEC - cbase) : 0;
+}
+
 // `span`: tokens of a tile. A chain's tiles are full (kWaves kTokens); without a chain a tile is a whole row, or
 // the only one.
 template <bool kOdd, typename TX, typename TG, int VEC, int kTokens, bool kChain>
@@ -202,7 +210,7 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
     const bool live = cbase + lane * VEC < p.D;
     const Lane ln(cbase + lane * VEC, p.D, VEC);
     const int skip = kOdd ? ln.skip : 0;
-    const int lo = live ? lane * VEC - skip : 0;  // the lane's first channel, from the block's
+    const int lo = first_channel<kOdd, VEC>(p.D, cbase, live, lane, skip);
     const int64_t c = cbase + lo;
     if (tile == tiles) return pass_empty<kOdd, VEC>(p, p.s0, p.sT, c, skip, live);
     const int32_t t0 = tile * span, t1 = p.seq.total - t0 < span ? p.seq.total : t0 + span;
@@ -319,7 +327,7 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
     const bool live = cbase + lane * VEC < p.D;
     const Lane ln(cbase + lane * VEC, p.D, VEC);
     const int skip = kOdd ? ln.skip : 0;
-    const int lo = live ? lane * VEC - skip : 0;
+    const int lo = first_channel<kOdd, VEC>(p.D, cbase, live, lane, skip);
     const int64_t c = cbase + lo;
     if (pos == tiles) return pass_empty<kOdd, VEC>(p, p.d_sT, p.ds0, c, skip, live);
     const int32_t t0 = tile * span, t1 = p.seq.total - t0 < span ? p.seq.total : t0 + span;
@@ -383,11 +391,13 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
                 A[v] *= a;
             }
         }
+        SeqPos e = s;
+        if (w0 < w1) e = seq_find(p.seq, w1 - 1);
 #pragma unroll
         for (int i = kTokens - 1; i >= 0; --i) {
             const int32_t t = w0 + i;
             if (t >= w1) continue;
-            const SeqPos e = seq_find(p.seq, t);
+            seq_retreat(p.seq, e, t);
             if (t < e.start || t >= e.end) continue;
             if (t + 1 == e.end) {
                 state_of<VEC>(p.d_sT, e.n, p.D, c, M);
@@ -467,11 +477,12 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
         if (t == s.start) state_of<VEC>(p.s0, s.n, p.D, c, h);
         ahead(i);
     }
+    SeqPos e = seq_find(p.seq, w1 - 1);
 #pragma unroll
     for (int i = kTokens - 1; i >= 0; --i) {
         const int32_t t = w0 + i;
         if (t >= w1) continue;
-        const SeqPos e = seq_find(p.seq, t);
+        seq_retreat(p.seq, e, t);
         if (t < e.start || t >= e.end) continue;
         if (t + 1 == e.end) state_of<VEC>(p.d_sT, e.n, p.D, c, mu);
         back(i);

@@ -53,6 +53,12 @@ __device__ __forceinline__ void seq_advance(const SeqView& s, SeqPos& p, int32_t
     p = seq_at(s, p.n + 1);
     if (t >= p.end) p = seq_find(s, t);
 }
+// The same backwards, t before p's end.
+__device__ __forceinline__ void seq_retreat(const SeqView& s, SeqPos& p, int32_t t) {
+    if (t >= p.start || p.n == 0) return;
+    p = seq_at(s, p.n - 1);
+    if (t < p.start || t >= p.end) p = seq_find(s, t);
+}
 // Calls f(n) (uniform) for every sequence without tokens, 64 sequences looked at together by each of `waves` waves.
 // Whole waves call it.
 template <typename F>

@@ -222,6 +222,19 @@ def test_scan_many_sequences(gpu_lib):
         assert torch.equal(cf[:, 0].cpu().double(), prev)
 
 
+def test_scan_gradient_of_many_sequences(gpu_lib):
+    lens = [3, 0, 1, 9, 0, 0, 17, 2] * 20 + [0] * 50 + [70, 1]
+    cu, T = packed(lens, 2, 5)
+    x, g, s0, N = scan_inputs(1, T, 129, cu, BF, F32, True)
+    d_h, d_fin = rnd(1, T, 129, seed=7, dtype=BF), rnd(N, 129, seed=8)
+    want = ref.scan_bwd(x, g, s0, d_h, d_fin, cu)
+    keep = owned(1, T, cu)
+    got = gdn.gdn_gated_scan_bwd(x.cuda(), g.cuda(), d_h.cuda(), s0.cuda(), d_fin.cuda(), cu_seqlens=cu_dev(cu))
+    for k in ("dx", "dg"):
+        close(got[k][keep.cuda()], (want[k][0][keep], want[k][1][keep]), k)
+    close(got["d_initial_state"], want["d_initial_state"], "d_initial_state")
+
+
 def test_scan_gates_at_the_edges(gpu_lib):
     """-inf forgets, +growth from a zero state stays finite, and what one sequence holds (NaN, infinity) does not
     reach the next."""
