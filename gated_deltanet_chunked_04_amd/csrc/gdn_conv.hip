@@ -9,7 +9,8 @@
 // in bf16. So every input is read once: a wave walks a run of tokens down its block of channels (a
 // lane holds a few neighbouring ones, so a wave reads whole cache lines of a token's row) with the
 // last W-1 inputs, and in the gradient the last W-1 dz, in registers; only the W-1 tokens around the
-// ends of a run are read by two waves. The next tokens' loads are issued before the present ones
+// ends of a run are read by two waves, and what the gradient needs behind a run comes through LDS from
+// the wave that starts there (240 -> 233 us). The next tokens' loads are issued before the present ones
 // are used. Runs that lie inside one sequence take a path without any test per token.
 #include <type_traits>
 
@@ -184,24 +185,32 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
     const int64_t c0 = ln.at;
     if (block == token_blocks) return pass_empty<kOdd, T, VEC>(p, p.d_sT, p.ds0, c0, ln.skip, live);
     float dw[W][VEC] = {}, db[VEC] = {};
+    struct Pair {
+        Raw<T, VEC> x, d;
+    };
+    // The first W-1 tokens of each wave's run, for the wave before it, whose last results need them: read once.
+    __shared__ Pair head[kWaves][W - 1][kWave];
     const int64_t w0l = ((int64_t)block * kWaves + wave) * run;
-    if (live && w0l < p.seq.total) {
-        const int32_t w0 = (int32_t)w0l;
-        const int32_t w1 = w0l + run < p.seq.total ? w0 + run : p.seq.total;
-        const int32_t w2 = min(w1 + W - 1, p.seq.total);  // dx of the run's last tokens needs dz up to here
-        struct Pair {
-            Raw<T, VEC> x, d;
-        };
-        auto fetch = [&](int32_t t, Pair (&q)[U]) {
+    const bool busy = live && w0l < p.seq.total;
+    const int32_t w0 = w0l < p.seq.total ? (int32_t)w0l : 0;  // (uniform)
+    const int32_t w1 = w0 + run < p.seq.total ? w0 + run : p.seq.total;
+    const int32_t w2 = min(w1 + W - 1, p.seq.total);  // dx of the run's last tokens needs dz up to here
+    auto fetch = [&](int32_t t, Pair (&q)[U]) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int32_t at = min(t + u, w2 - 1);
-                q[u].x = row<T, VEC>(p.x, at, p, c0);
-                q[u].d = row<T, VEC>(p.d_y, at, p, c0);
-            }
-        };
-        Pair qa[U];
+        for (int u = 0; u < U; ++u) {
+            const int32_t at = min(t + u, w2 - 1);
+            q[u].x = row<T, VEC>(p.x, at, p, c0);
+            q[u].d = row<T, VEC>(p.d_y, at, p, c0);
+        }
+    };
+    Pair qa[U];
+    if (busy) {
         fetch(w0, qa);
+#pragma unroll
+        for (int r = 0; r < W - 1; ++r) head[wave][r][lane] = qa[r];
+    }
+    __syncthreads();
+    if (busy) {
         Filter<TW, W, VEC> f;
         f.load(p, c0);
         SeqPos s = seq_find(p.seq, w0);
@@ -258,29 +267,52 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
         // Inside one sequence: blocks of U tokens, the next two in flight, in two buffers that take turns. The
         // first W-1 results belong to the wave before; W-1 tokens behind the run complete its last ones.
         auto inside = [&](auto silu) {
-            static_assert(U >= W - 1, "the tokens behind the run fit one block");
-            auto block = [&](const Pair (&q)[U], int32_t t, int from, int to, bool own) {
+            static_assert(U >= W - 1, "the first block holds the tokens that the wave before needs");
+            auto block = [&](const Pair (&q)[U], int32_t t, int from) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    if (u >= to) break;
                     float back[VEC];
-                    token(q[u], silu, own, back);
+                    token(q[u], silu, true, back);
                     if (u >= from) store_own<kOdd, T, VEC>(dx + (int64_t)(t + u - (W - 1)) * p.D + c0, back, ln.skip);
                 }
             };
-            Pair qb[U];
-            fetch(w0 + U, qb);
-            block(qa, w0, W - 1, U, true);
-            fetch(w0 + 2 * U, qa);
+            Pair qb[U], tail[W - 1];
+            // (behind the run the loads stay on its last token, which the cache has)
+            auto ahead = [&](int32_t t, Pair (&q)[U]) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int32_t at = min(t + u, w1 - 1);
+                    q[u].x = row<T, VEC>(p.x, at, p, c0);
+                    q[u].d = row<T, VEC>(p.d_y, at, p, c0);
+                }
+            };
+            ahead(w0 + U, qb);
+            block(qa, w0, W - 1);
+            ahead(w0 + 2 * U, qa);
             int32_t t = w0 + U;
             for (; t + U < w1; t += 2 * U) {
-                block(qb, t, 0, U, true);
-                fetch(t + 2 * U, qb);
-                block(qa, t + U, 0, U, true);
-                fetch(t + 3 * U, qa);
+                block(qb, t, 0);
+                ahead(t + 2 * U, qb);
+                block(qa, t + U, 0);
+                ahead(t + 3 * U, qa);
             }
-            block(qb, t, 0, U, true);
-            block(qa, w1, 0, W - 1, false);
+            // the tokens behind the run: the next wave's first, or from memory for the workgroup's last wave
+#pragma unroll
+            for (int r = 0; r < W - 1; ++r) {
+                if (wave < kWaves - 1) {
+                    tail[r] = head[wave + 1][r][lane];
+                } else {
+                    tail[r].x = row<T, VEC>(p.x, w1 + r, p, c0);
+                    tail[r].d = row<T, VEC>(p.d_y, w1 + r, p, c0);
+                }
+            }
+            block(qb, t, 0);
+#pragma unroll
+            for (int r = 0; r < W - 1; ++r) {
+                float back[VEC];
+                token(tail[r], silu, false, back);
+                store_own<kOdd, T, VEC>(dx + (int64_t)(w1 + r - (W - 1)) * p.D + c0, back, ln.skip);
+            }
         };
         // where the gradient of position t of sequence s goes: the token's owner stores it, positions before
         // the first token (rows of the entering state) go by the first token's owner
@@ -425,9 +457,9 @@ hipError_t fwd_t(const ConvArgs& a, hipStream_t st) {
 
 // Tokens per wave in the gradient: 24, or 16 or 8 where there are too few for 2,304 waves of 24, 2,048 of 16. Longer
 // runs re-read less and leave fewer partial sums, shorter ones put more waves in flight and lose less where
-// sequences end inside them (2 x 16384 x 6144 bf16, W = 4: 24 tokens 239 us, 32 253, 48 256, 64 271, 136 292; 30,000
-// tokens in 50 sequences: 234, 238, 247, 259, 320; 30,000 x 512: 8 tokens 34 us, 16 33, 24 31; 2,048 x 6144: 26, 25,
-// 28; 4,099 x 768 fp32, W = 3: 8 tokens 15.7 us, 16 19.9).
+// sequences end inside them (2 x 16384 x 6144 bf16, W = 4: 16 tokens 239 us, 24 233, 32 242, 40 232; 30,000 tokens in
+// 50 sequences: 234, 232, 236, 240; 30,000 x 512: 8 tokens 34 us, 16 33, 24 31, 40 38; 2,048 x 6144: 8 tokens 26, 16 24,
+// 24 28; 4,099 x 768 fp32, W = 3: 8 tokens 15.7 us, 16 19.9).
 int bwd_run(int64_t total, unsigned cblocks) {
     const int64_t n = total * cblocks;
     return n >= 24 * 2304 ? 24 : (n >= 16 * 2048 ? 16 : 8);

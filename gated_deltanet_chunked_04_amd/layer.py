@@ -49,9 +49,9 @@ def _like(name, t, shape, dtype, device):
 
 
 def _out(name, t, x, shape, dtype, device):
-    """(tensor, pointer) of a caller's output, or of a new one."""
+    """(tensor, pointer) of a caller's output, or of a new one (empty_like is the quicker call where it serves)."""
     if t is None:
-        t = x.new_empty(shape, dtype=dtype)
+        t = torch.empty_like(x) if dtype == x.dtype and shape == x.shape else x.new_empty(shape, dtype=dtype)
         return t, t.data_ptr()
     return t, _like(name, t, shape, dtype, device)
 
@@ -60,7 +60,7 @@ def _outs(out, x, device, **want):
     """(dict, its pointers in order) of a backward's outputs, name=(shape, dtype, whether a new dict has it): new
     ones, or the caller's, which must hold all but the ones that may be left out (a state's or a bias's)."""
     if out is None:
-        out = {k: x.new_empty(shape, dtype=dtype) if need else None for k, (shape, dtype, need) in want.items()}
+        out = {k: _out(k, None, x, shape, dtype, device)[0] if need else None for k, (shape, dtype, need) in want.items()}
         return (out, *(None if t is None else t.data_ptr() for t in out.values()))
     for k in ("dx", "dg", "dweight"):
         if k in want and want[k][2] and out.get(k) is None:

@@ -77,7 +77,7 @@ def test_grids_beyond_32_bits(lib):
     n = ctypes.c_size_t(1 << 50)
     out = ctypes.c_void_p(0x50000)
     assert lib.gdn_rmsnorm_fwd(ctypes.byref(rms_desc(rows=5_000_000, D=4)), P, None, Q, R, None, None, None) == 2
-    assert lib.gdn_rmsnorm_fwd(ctypes.byref(rms_desc(rows=100_000_000, D=64)), P, None, Q, R, None, None, None) == 2
+    assert lib.gdn_rmsnorm_fwd(ctypes.byref(rms_desc(rows=2_000_000_000, D=512)), P, None, Q, R, None, None, None) == 2
     assert lib.gdn_rmsnorm_bwd(ctypes.byref(rms_desc(rows=5_000_000, D=4)), P, Q, R, None, S, None, S, n, None) == 2
     assert lib.gdn_gated_scan_fwd(ctypes.byref(scan_desc(B=1, T=2_000_000_000, D=1024)), P, Q, None, R, None, None, S, n, None) == 2
     assert lib.gdn_gated_scan_fwd(ctypes.byref(scan_desc(B=200_000_000, T=1, D=64)), P, Q, None, R, None, None, S, n, None) == 2
