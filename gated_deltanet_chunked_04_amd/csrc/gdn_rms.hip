@@ -280,7 +280,8 @@ __global__ __launch_bounds__(threads_of<LANES>()) void k_rms_bwd(RmsArgs p, floa
             for (int i = 0; i < 8; ++i) {
                 const float x = own<kOdd>(r[v].get(i), i, skip[v]);
                 ss = fmaf(x, x, ss);
-                dot = fmaf(d[v].get(i) * w[v].get(i), x, dot);
+                // (both factors masked: zero times an infinity would not count for nothing)
+                dot = fmaf(own<kOdd>(d[v].get(i) * w[v].get(i), i, skip[v]), x, dot);
             }
         ss = row_sum<LANES>(ss, sh, slot);
         dot = row_sum<LANES>(dot, sh, slot + 1);

@@ -428,6 +428,21 @@ def test_rms_zero_rows_and_bad_values(gpu_lib):
         assert torch.isfinite(gr["dx"][[0, 1, 4, 5]]).all()
 
 
+def test_rms_infinite_gradient(gpu_lib):
+    """An infinity in d_y reaches its row as the formula says (mean(w d_y rh) infinite), also where the row's last
+    columns are read along with their neighbours'."""
+    for D in (12, 100, 300, 2044, 9001):
+        r, w, d_y = rnd(2, D).abs() + 0.1, rnd(D, seed=1).abs() + 0.1, rnd(2, D, seed=2)
+        r[:, ::3] *= -1
+        at = D - 6  # before the columns that the last vector owns (8 ceil(D / 8) - 8 on), inside what it reads
+        d_y[0, at] = float("inf")
+        got = gdn.gdn_rmsnorm_bwd(r.cuda(), w.cuda(), d_y.cuda())
+        rest = torch.arange(D) != at
+        want = -torch.sign(r[0]) * torch.sign(r[0, at]) * float("inf")
+        assert torch.equal(got["dx"][0].cpu()[rest], want[rest]), D
+        close(got["dx"][1:], [v[1:] for v in ref.rms_bwd(r, w, torch.nan_to_num(d_y, posinf=0.0), None, 1e-6)["dx"]], "dx")
+
+
 def test_rms_in_place_residual(gpu_lib):
     for D in (2048, 300, 20000):
         x, res, w = rnd(9, D, dtype=BF).cuda(), rnd(9, D, seed=1, dtype=BF).cuda(), torch.ones(D).cuda()
