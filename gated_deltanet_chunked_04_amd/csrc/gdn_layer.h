@@ -41,7 +41,7 @@ __device__ __forceinline__ SeqPos seq_find(const SeqView& s, int32_t t) {
     if (!s.cu) return seq_at(s, t / s.T);
     int32_t lo = 0, hi = s.N - 1;
     while (lo < hi) {
-        const int32_t mid = (lo + hi + 1) >> 1;
+        const int32_t mid = hi - ((hi - lo) >> 1);  // (no sum of the two: N may be near 2^31)
         if (seq_off(s, mid) <= t) lo = mid; else hi = mid - 1;
     }
     return seq_at(s, lo);

@@ -222,6 +222,20 @@ def test_scan_many_sequences(gpu_lib):
         assert torch.equal(cf[:, 0].cpu().double(), prev)
 
 
+def test_nearly_all_sequences_empty(gpu_lib):
+    """More sequences than 2^30: their numbers' sum passes 32 bits."""
+    N, T, D = 1_200_000_000, 100, 8
+    cu = torch.zeros(N + 1, dtype=torch.int32, device="cuda")
+    cu[-1] = T
+    x, w = rnd(1, T, D).cuda(), rnd(D, 4, seed=1).cuda()
+    y, _ = gdn.gdn_short_conv_fwd(x, w, cu_seqlens=cu)
+    assert torch.equal(y, gdn.gdn_short_conv_fwd(x, w)[0])
+    g = -torch.ones(1, T, D).cuda()
+    h, _ = gdn.gdn_gated_scan_fwd(torch.cat([x] * 6, 1), torch.cat([g] * 6, 1), cu_seqlens=cu * 6, output_final_state=False)
+    want, _ = gdn.gdn_gated_scan_fwd(torch.cat([x] * 6, 1), torch.cat([g] * 6, 1))
+    assert torch.equal(h, want)
+
+
 def test_scan_gradient_of_many_sequences(gpu_lib):
     lens = [3, 0, 1, 9, 0, 0, 17, 2] * 20 + [0] * 50 + [70, 1]
     cu, T = packed(lens, 2, 5)
