@@ -492,6 +492,7 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
 
 // Short sequences (decoding): a wave per sequence and block of channels walks the tokens; one launch, no workspace.
 constexpr int kRowThreads = 256;
+constexpr int kRowAhead = 8;  // tokens loaded ahead in a sequence of two such blocks or more (0.21 -> 0.11 us a token)
 template <bool kOdd, typename TX, typename TG, int VEC>
 __global__ __launch_bounds__(kRowThreads) void k_gscan_rows(GScanArgs p, int cblocks) {
     const int64_t item = (int64_t)blockIdx.x * (kRowThreads / kWave) + wave_id();
@@ -508,29 +509,63 @@ __global__ __launch_bounds__(kRowThreads) void k_gscan_rows(GScanArgs p, int cbl
     const TX* x = static_cast<const TX*>(p.x) + c;
     const TG* g = static_cast<const TG*>(p.g) + c;
     TX* out = static_cast<TX*>(p.h);
+    auto step = [&](int32_t t, const Raw<TX, VEC>& xt, const Raw<TG, VEC>& gt) {
+        if (p.states && t % kScanTile == 0) store_own<kOdd, float, VEC>(p.states + (int64_t)(t / kScanTile) * p.D + c, h, skip);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) h[v] = fmaf(fast_exp(gt.get(v)), h[v], xt.get(v));
+        if (out) store_own<kOdd, TX, VEC>(out + (int64_t)t * p.D + c, h, skip);
+    };
+    int32_t t = s.start;
+    if (s.end - t >= 2 * kRowAhead) {
+        Raw<TX, VEC> nx[kRowAhead];
+        Raw<TG, VEC> ng[kRowAhead];
+        auto fetch = [&](int32_t from) {
+#pragma unroll
+            for (int u = 0; u < kRowAhead; ++u) {
+                const int64_t at = (int64_t)min(from + u, s.end - 1) * p.D;
+                nx[u] = load_raw<TX, VEC>(x + at);
+                ng[u] = load_raw<TG, VEC>(g + at);
+            }
+        };
+        fetch(t);
+        for (; s.end - t >= kRowAhead; t += kRowAhead) {
+            Raw<TX, VEC> xt[kRowAhead];
+            Raw<TG, VEC> gt[kRowAhead];
+#pragma unroll
+            for (int u = 0; u < kRowAhead; ++u) {
+                xt[u] = nx[u];
+                gt[u] = ng[u];
+            }
+            fetch(t + kRowAhead);
+#pragma unroll
+            for (int u = 0; u < kRowAhead; ++u) step(t + u, xt[u], gt[u]);
+        }
+    }
     Raw<TX, VEC> nx;
     Raw<TG, VEC> ng;
-    if (s.start < s.end) {
-        nx = load_raw<TX, VEC>(x + (int64_t)s.start * p.D);
-        ng = load_raw<TG, VEC>(g + (int64_t)s.start * p.D);
+    if (t < s.end) {
+        nx = load_raw<TX, VEC>(x + (int64_t)t * p.D);
+        ng = load_raw<TG, VEC>(g + (int64_t)t * p.D);
     }
-    for (int32_t t = s.start; t < s.end; ++t) {
+    for (; t < s.end; ++t) {
         const Raw<TX, VEC> xt = nx;
         const Raw<TG, VEC> gt = ng;
         if (t + 1 < s.end) {
             nx = load_raw<TX, VEC>(x + (int64_t)(t + 1) * p.D);
             ng = load_raw<TG, VEC>(g + (int64_t)(t + 1) * p.D);
         }
-        if (p.states && t % kScanTile == 0) store_own<kOdd, float, VEC>(p.states + (int64_t)(t / kScanTile) * p.D + c, h, skip);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) h[v] = fmaf(fast_exp(gt.get(v)), h[v], xt.get(v));
-        if (out) store_own<kOdd, TX, VEC>(out + (int64_t)t * p.D + c, h, skip);
+        step(t, xt, gt);
     }
     if (p.sT) store_own<kOdd, float, VEC>(p.sT + (int64_t)s.n * p.D + c, h, skip);
 }
 
-// Sequences of up to 16 tokens, or on average up to 4 where they are packed, get a wave each.
-bool by_rows(const SeqView& s) { return s.cu ? s.total / s.N <= 4 : s.T <= 16; }
+// A wave for every sequence: rows of up to 16 tokens, and packed batches that hold no more tokens than sequences
+// (one each, as decoding has them) and at most 512 tokens. The lengths are on the device, so what bounds the loss is the longest
+// walk that may be among them: a token costs 0.11 us there, and tiles take 13 to 20 us (x 2048 channels: 256
+// sequences of a token 3.7 us by rows, 20 by tiles; 128 of one and one of 400 50 and 21; 1,024 of one and one of 2,048
+// 285 and 33).
+constexpr int kRowTokens = 512;
+bool by_rows(const SeqView& s) { return s.cu ? s.total <= s.N && s.total <= kRowTokens : s.T <= 16; }
 
 // Whether a tile of `span` tokens takes every row, or the whole of a packed batch: then no state passes from tile to
 // tile (256 rows of 64 x 2048: 52 us, as a chain of full tiles 61; 16 rows of 24: 5.5 and 10).

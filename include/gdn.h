@@ -373,7 +373,8 @@ gdn_status gdn_gated_scan_states_size(const gdn_scan_desc* desc, size_t* bytes);
  *   states: NULL, or a buffer of gdn_gated_scan_states_size bytes (256-byte aligned) that receives
  *   what gdn_gated_scan_bwd needs of the forward: the fp32 state entering every 64th token (nothing
  *   is written where a call is one tile of tokens and needs none)
- * A call of a few tokens per sequence (decoding) is one launch and needs no workspace. */
+ * A call of up to 16 tokens per row (decoding), or of a packed batch of up to 512 tokens and no more of
+ * them than sequences, is one launch and needs no workspace. */
 gdn_status gdn_gated_scan_fwd(const gdn_scan_desc* desc, const void* x, const void* g,
                               const float* initial_state, void* h, float* final_state, void* states,
                               void* workspace, size_t workspace_bytes, void* stream);

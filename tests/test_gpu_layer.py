@@ -222,6 +222,15 @@ def test_scan_many_sequences(gpu_lib):
         assert torch.equal(cf[:, 0].cpu().double(), prev)
 
 
+@pytest.mark.parametrize("dt,gdt", [(BF, F32), (F32, F32)])
+@pytest.mark.parametrize("s", [([1] * 90, 0, 0, 260), ([0] * 300 + [40, 1, 0, 16, 1, 17, 1, 1], 5, 3, 131),
+                               ([1] * 300, 2, 0, 64), ([0] * 400 + [300], 0, 1, 130), ([1] * 128 + [400], 0, 0, 256),
+                               ([1] * 600, 0, 0, 128)])
+def test_scan_decoding_batches(s, dt, gdt, gpu_lib):
+    """Packed batches of single tokens, among them long sequences between empty ones, and a long prefill."""
+    test_scan("pack", s, dt, gdt, gpu_lib)
+
+
 def test_nearly_all_sequences_empty(gpu_lib):
     """More sequences than 2^30: their numbers' sum passes 32 bits."""
     N, T, D = 1_200_000_000, 100, 8
