@@ -81,11 +81,11 @@ __device__ __forceinline__ void pre_act(const Filter<TW, W, VEC>& f, const float
 // 1 / (1 + exp(-z)); 0 where exp(-z) is infinite
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + fast_exp(-z)); }
 
-// Sequences without tokens: their state (or its gradient) passes through, by the workgroups of the
-// grid's last row.
+// Sequences without tokens: their state (or its gradient) passes through, by the workgroups behind
+// the tokens': number `block` of `blocks`.
 template <bool kOdd, typename T, int VEC>
-__device__ void pass_empty(const ConvArgs& p, const void* in, void* out, int64_t c0, int skip, bool live) {
-    for_each_empty(p.seq, wave_id(), kWaves, [&](int32_t s) {
+__device__ void pass_empty(const ConvArgs& p, int block, int blocks, const void* in, void* out, int64_t c0, int skip, bool live) {
+    for_each_empty(p.seq, block * kWaves + wave_id(), blocks * kWaves, [&](int32_t s) {
         if (!live) return;
         for (int r = 0; r < p.W - 1; ++r)
             store_own<kOdd, T, VEC>(static_cast<T*>(out) + ((int64_t)s * (p.W - 1) + r) * p.D + c0,
@@ -100,7 +100,8 @@ __global__ __launch_bounds__(kThreads) void k_conv_fwd(ConvArgs p, int run, int 
     const int64_t ch = ((int64_t)(blockIdx.x % cblocks) * kWave + (threadIdx.x & 63)) * VEC;
     const Lane ln(ch, p.D, VEC);
     const int64_t c0 = ln.at;
-    if (block == token_blocks) return pass_empty<kOdd, T, VEC>(p, p.s0, p.sT, c0, ln.skip, ch < p.D);
+    if (block >= token_blocks)
+        return pass_empty<kOdd, T, VEC>(p, block - token_blocks, gridDim.x / cblocks - token_blocks, p.s0, p.sT, c0, ln.skip, ch < p.D);
     if (ch >= p.D) return;
     const int64_t w0l = ((int64_t)block * kWaves + wave_id()) * run;
     if (w0l >= p.seq.total) return;
@@ -183,7 +184,8 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
     const bool live = ch < p.D;
     const Lane ln(ch, p.D, VEC);
     const int64_t c0 = ln.at;
-    if (block == token_blocks) return pass_empty<kOdd, T, VEC>(p, p.d_sT, p.ds0, c0, ln.skip, live);
+    if (block >= token_blocks)
+        return pass_empty<kOdd, T, VEC>(p, block - token_blocks, gridDim.x / cblocks - token_blocks, p.d_sT, p.ds0, c0, ln.skip, live);
     float dw[W][VEC] = {}, db[VEC] = {};
     struct Pair {
         Raw<T, VEC> x, d;
@@ -436,7 +438,7 @@ hipError_t fwd_v(const ConvArgs& a, hipStream_t st) {
     const unsigned cb = blocks_of(a.D, VEC);
     const int run = fwd_run(a.seq, cb);
     const int tb = (int)(((int64_t)a.seq.total + (int64_t)run * kWaves - 1) / ((int64_t)run * kWaves));
-    const int extra = a.sT && (a.seq.cu || a.seq.T == 0);
+    const int extra = a.sT && (a.seq.cu || a.seq.T == 0) ? empty_blocks(a.seq, kWaves) : 0;
     if (tb + extra == 0) return hipSuccess;
     if (!grid_fits((int64_t)cb * (tb + extra), kThreads)) return hipErrorInvalidConfiguration;
     const dim3 grid(cb * (unsigned)(tb + extra));
@@ -471,7 +473,7 @@ hipError_t bwd_v(const ConvArgs& a, hipStream_t st) {
     const unsigned cb = blocks_of(a.D, VEC);
     const int run = bwd_run(a.seq.total, cb);
     const int parts = bwd_parts(a.seq.total, run);
-    const int extra = a.ds0 && (a.seq.cu || a.seq.T == 0);
+    const int extra = a.ds0 && (a.seq.cu || a.seq.T == 0) ? empty_blocks(a.seq, kWaves) : 0;
     float* part = reinterpret_cast<float*>(a.ws);
     if (!grid_fits((int64_t)cb * (parts + extra), kThreads)) return hipErrorInvalidConfiguration;
     const dim3 grid(cb * (unsigned)(parts + extra));

@@ -167,10 +167,11 @@ __device__ __forceinline__ void state_of(const float* s, int32_t n, int64_t D, i
     }
 }
 
-// Sequences without tokens: their state (or its gradient) passes through, by the workgroups behind the tiles.
+// Sequences without tokens: their state (or its gradient) passes through, by the workgroups behind the tiles: number
+// `block` of `blocks`.
 template <bool kOdd, int VEC>
-__device__ void pass_empty(const GScanArgs& p, const float* in, float* out, int64_t c, int skip, bool live) {
-    for_each_empty(p.seq, wave_id(), kWaves, [&](int32_t n) {
+__device__ void pass_empty(const GScanArgs& p, int block, int blocks, const float* in, float* out, int64_t c, int skip, bool live) {
+    for_each_empty(p.seq, block * kWaves + wave_id(), blocks * kWaves, [&](int32_t n) {
         if (!live) return;
         float x[VEC];
         state_of<VEC>(in, n, p.D, c, x);
@@ -212,7 +213,7 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
     const int skip = kOdd ? ln.skip : 0;
     const int lo = first_channel<kOdd, VEC>(p.D, cbase, live, lane, skip);
     const int64_t c = cbase + lo;
-    if (tile == tiles) return pass_empty<kOdd, VEC>(p, p.s0, p.sT, c, skip, live);
+    if (tile >= tiles) return pass_empty<kOdd, VEC>(p, tile - tiles, gridDim.x / cblocks - tiles, p.s0, p.sT, c, skip, live);
     const int32_t t0 = tile * span, t1 = p.seq.total - t0 < span ? p.seq.total : t0 + span;
     const int32_t w0 = t1 - t0 < wave * kTokens ? t1 : t0 + wave * kTokens;
     const int32_t w1 = t1 - w0 < kTokens ? t1 : w0 + kTokens;
@@ -329,7 +330,7 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
     const int skip = kOdd ? ln.skip : 0;
     const int lo = first_channel<kOdd, VEC>(p.D, cbase, live, lane, skip);
     const int64_t c = cbase + lo;
-    if (pos == tiles) return pass_empty<kOdd, VEC>(p, p.d_sT, p.ds0, c, skip, live);
+    if (pos >= tiles) return pass_empty<kOdd, VEC>(p, pos - tiles, gridDim.x / cblocks - tiles, p.d_sT, p.ds0, c, skip, live);
     const int32_t t0 = tile * span, t1 = p.seq.total - t0 < span ? p.seq.total : t0 + span;
     const int32_t w0 = t1 - t0 < wave * kTokens ? t1 : t0 + wave * kTokens;
     const int32_t w1 = t1 - w0 < kTokens ? t1 : w0 + kTokens;
@@ -619,7 +620,7 @@ hipError_t make_chain(unsigned char* ws, size_t tiles, int64_t D, int64_t wide, 
 template <bool kOdd, typename TX, typename TG, int VEC, int TOK>
 hipError_t fwd_tiles(const GScanArgs& a, int cb, hipStream_t st) {
     const int tiles = tiles_of(a.seq.total, kWaves * TOK);
-    const int extra = a.sT && a.seq.cu;
+    const int extra = a.sT && a.seq.cu ? empty_blocks(a.seq, kWaves) : 0;
     Chain ch{};
     if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
     if (hipError_t e = make_chain(a.ws, tiles, a.D, 4096, ch, st)) return e;
@@ -631,7 +632,8 @@ hipError_t fwd_tiles(const GScanArgs& a, int cb, hipStream_t st) {
 // Without a chain, in one launch: rows that are a tile each, or a packed batch that is one.
 template <bool kOdd, typename TX, typename TG, int VEC, int TOK>
 hipError_t fwd_single(GScanArgs a, int cb, hipStream_t st) {
-    const int tiles = a.seq.cu ? (a.seq.total > 0) : a.seq.N, extra = a.sT && a.seq.cu;
+    const int tiles = a.seq.cu ? (a.seq.total > 0) : a.seq.N;
+    const int extra = a.sT && a.seq.cu ? empty_blocks(a.seq, kWaves) : 0;
     if (tiles + extra == 0) return hipSuccess;
     if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
     a.states = nullptr;  // nothing enters a tile from outside: the gradient needs none
@@ -666,7 +668,7 @@ hipError_t bwd_v(GScanArgs a, bool have, hipStream_t st) {
     constexpr int kTok = bwd_tokens<VEC>();
     const bool single = one_tile(a.seq, kScanTile), rows = single && !a.seq.cu;  // (as forward)
     const int tiles = rows ? (a.seq.T > 0 ? a.seq.N : 0) : tiles_of(a.seq.total, single ? kScanTile : kWaves * kTok);
-    const int extra = a.ds0 && (a.seq.cu || a.seq.T == 0);
+    const int extra = a.ds0 && (a.seq.cu || a.seq.T == 0) ? empty_blocks(a.seq, kWaves) : 0;
     if (tiles + extra == 0) return hipSuccess;
     if (!grid_fits((int64_t)(tiles + extra) * cb, kThreads)) return hipErrorInvalidConfiguration;
     if (single) {

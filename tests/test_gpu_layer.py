@@ -231,6 +231,24 @@ def test_scan_decoding_batches(s, dt, gdt, gpu_lib):
     test_scan("pack", s, dt, gdt, gpu_lib)
 
 
+def test_states_of_many_empty_sequences(gpu_lib):
+    """States (and their gradients) of 10,000 sequences without tokens pass through, those of the others do not."""
+    lens = [0] * 5000 + [33, 0, 600] + [0] * 5000
+    cu, T = packed(lens)
+    for D in (64, 131):
+        x, g, s0, N = scan_inputs(1, T, D, cu, F32, F32, True)
+        some = torch.tensor(lens) == 0
+        h, fin = gdn.gdn_gated_scan_fwd(x.cuda(), g.cuda(), s0.cuda(), cu_seqlens=cu_dev(cu))
+        gr = gdn.gdn_gated_scan_bwd(x.cuda(), g.cuda(), h, s0.cuda(), s0.cuda() * 2, cu_seqlens=cu_dev(cu))
+        assert torch.equal(fin.cpu()[some], s0[some]) and torch.equal(gr["d_initial_state"].cpu()[some], 2 * s0[some])
+        assert (fin.cpu()[~some] != s0[~some]).all() and torch.isfinite(fin).all()
+        w, c0 = rnd(D, 4, seed=9), rnd(N, 3, D, seed=10)
+        y, cf = gdn.gdn_short_conv_fwd(x.cuda(), w.cuda(), None, c0.cuda(), cu_seqlens=cu_dev(cu), output_final_state=True)
+        gc = gdn.gdn_short_conv_bwd(x.cuda(), w.cuda(), y, None, c0.cuda(), c0.cuda() * 2, cu_seqlens=cu_dev(cu))
+        assert torch.equal(cf.cpu()[some], c0[some]) and torch.equal(gc["d_initial_state"].cpu()[some], 2 * c0[some])
+        assert torch.equal(cf[5000].cpu(), x[0, 30:33]) and torch.equal(cf[5002].cpu(), x[0, -3:])
+
+
 def test_nearly_all_sequences_empty(gpu_lib):
     """More sequences than 2^30: their numbers' sum passes 32 bits."""
     N, T, D = 1_200_000_000, 100, 8
