@@ -98,6 +98,18 @@ __device__ __forceinline__ float scale_of(uint32_t amax_bits) {
     const float s = __uint_as_float(amax_bits) / kE4m3Max;
     return s < 0x1p-126f ? 0x1p-126f : s;  // its reciprocal stays finite (NaN stays NaN)
 }
+// y / scale to nearest, from the scale's reciprocal: y inv is off by up to 1.5 fp32 steps, which put values that lie on
+// an 8-bit tie to either side (0.2% of the values of rows of small whole numbers); what it leaves of y, times inv
+// again, makes it the nearest in three operations (32,768 x 2,048 80.8 us, one product alone 80.1). An infinite scale
+// has inv = 0, and its finite values are 0 / inf = 0: with 0 in place of the scale nothing is added to them.
+struct Divisor {
+    float scale, inv;
+    __device__ __forceinline__ explicit Divisor(float s) : inv(1.f / s) { scale = inv == 0.f ? 0.f : s; }
+    __device__ __forceinline__ float quotient(float y) const {
+        const float q = y * inv;
+        return fmaf(fmaf(-q, scale, y), inv, q);
+    }
+};
 
 // 8 bytes of 8-bit values, of which the lane owns those from `skip` on.
 template <bool kOdd>
@@ -203,12 +215,10 @@ __global__ __launch_bounds__(threads_of<LANES>()) void k_rms_fwd(RmsArgs p) {
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            // one quotient and eight products: off from eight quotients by half a step of the fp32 y, far
-            // below the 8-bit values' steps
-            const float inv = 1.f / scale[v];
+            const Divisor by(scale[v]);
             float q[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = r[v].get(i) * rstd * w[v].get(i) * inv;
+            for (int i = 0; i < 8; ++i) q[i] = by.quotient(r[v].get(i) * rstd * w[v].get(i));
             if (live[v])
                 store_e4m3<kOdd>(static_cast<uint8_t*>(p.y) + base + at[v], pack_e4m3(q[0], q[1], q[2], q[3]),
                                  pack_e4m3(q[4], q[5], q[6], q[7]), skip[v]);
@@ -371,9 +381,10 @@ __global__ __launch_bounds__(kLoopThreads) void k_rms_fwd_loop(RmsArgs p) {
             uint32_t m = 0;
             for (int64_t c = g * G + id; c < c1; c += n) m = max(m, abs_bits(norm(c)));
             m = by_wave ? row_umax<64>(m, nullptr, 0) : row_umax<kLoopThreads>(m, sh, 0);
-            const float scale = scale_of(m), inv = 1.f / scale;
+            const float scale = scale_of(m);
+            const Divisor by(scale);
             for (int64_t c = g * G + id; c < c1; c += n) {
-                const float q = norm(c) * inv;
+                const float q = by.quotient(norm(c));
                 y[c] = (uint8_t)pack_e4m3(q, q, q, q);
             }
             if (id == 0) p.scale[(int64_t)blockIdx.x * groups + g] = scale;
