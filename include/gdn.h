@@ -349,7 +349,8 @@ gdn_status gdn_cp_windows(const gdn_desc* desc, const void* k, const void* v,
  *     h_t = exp(g_t) h_{t-1} + x_t,    h_0 = initial_state (zeros when NULL),
  * per sequence and channel; g is a natural-log decay (usually <= 0; -inf forgets). Gates above zero
  * are taken too, but the tokens are worked on in runs of up to 128, whose gates' products must stay
- * within fp32's range where a state other than zero enters the run. */
+ * within fp32's range where a state other than zero enters the run (in the gradient: where a gradient
+ * other than zero does, from behind). A product below the range counts as zero. */
 typedef struct gdn_scan_desc {
     int64_t B, T, D;
     int32_t dtype;             /* gdn_dtype of x, h and their gradients */

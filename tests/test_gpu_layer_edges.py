@@ -43,3 +43,91 @@ def test_8_bit_values_beside_an_infinity(gpu_lib):
             q = q.float().cpu()
             assert torch.isinf(scale[:, 0]).all() and torch.isnan(q[:, 3]).all()
             assert (q[:, :3] == 0).all() and (q[:, 4] == 0).all()
+
+
+# ---- gated scan: gates whose product over many tiles leaves fp32's range ------------------------
+
+
+def check_scan(x, g, s0, cu=None, d_h=None, d_fin=None):
+    """Forward and gradient (states kept and recomputed) against the 64-bit form."""
+    B, T, D = x.shape
+    cd, keep = cu_dev(cu), owned(B, T, cu)
+    rows = lambda got, want, what: close(got[keep.cuda()], (want[0][keep], want[1][keep]), what)  # noqa: E731
+    want_h, want_fin = ref.scan_fwd(x, g, s0, cu)
+    states = gdn.gdn_gated_scan_states(x.cuda())
+    h, fin = gdn.gdn_gated_scan_fwd(x.cuda(), g.cuda(), cuda(s0), cu_seqlens=cd, states=states)
+    rows(h, want_h, "h")
+    close(fin, want_fin, "final_state")
+    d_h = torch.zeros_like(x) if d_h is None else d_h
+    want = ref.scan_bwd(x, g, s0, d_h, d_fin, cu)
+    for st in (states, None):
+        gr = gdn.gdn_gated_scan_bwd(x.cuda(), g.cuda(), d_h.cuda(), cuda(s0), cuda(d_fin), cu_seqlens=cd, states=st)
+        for k in ("dx", "dg"):
+            rows(gr[k], want[k], k)
+        close(gr["d_initial_state"], want["d_initial_state"], "d_initial_state")
+
+
+def steps(T, D, *parts):
+    """g [1, T, D], zero but for the parts (first token, one behind the last, gate)."""
+    g = torch.zeros(1, T, D)
+    for a, b, v in parts:
+        g[:, a:b] = v
+    return g
+
+
+@pytest.mark.parametrize("D", [64, 130, 256, 2048])
+def test_scan_growth_over_many_tiles(D, gpu_lib):
+    """A tiny state grows by e^102 over 512 tokens, 128 of which grow by 1.3e11 at most."""
+    T = 2048
+    tiny = torch.full((1, D), 1e-36)
+    check_scan(torch.zeros(1, T, D), steps(T, D, (512, 1024, 0.2)), tiny, d_fin=tiny)
+    check_scan(torch.zeros(1, T, D), steps(T, D, (1024, 1536, 0.2)), tiny, d_fin=tiny)
+
+
+@pytest.mark.parametrize("D", [64, 131, 256, 2048])
+def test_scan_growth_then_decay_and_forgetting(D, gpu_lib):
+    """Growth to 3e34 from a state and inputs, then decay, and a gate of -inf in half of the channels."""
+    T = 4096
+    g = steps(T, D, (1024, 2048, 0.1), (2048, 4096, -0.05))
+    g[0, 3000, ::2] = float("-inf")
+    x = rnd(1, T, D, scale=1e-12)
+    x[:, 1500:] = 0
+    x[:, 3000:] = rnd(1, T - 3000, D, seed=1)
+    check_scan(x, g, torch.full((1, D), 1e-10), d_h=rnd(1, T, D, seed=2, scale=1e-12), d_fin=rnd(1, D, seed=3, scale=1e-10))
+
+
+@pytest.mark.parametrize("D", [64, 131, 256, 2048])
+def test_scan_decay_and_growth_that_undo_each_other(D, gpu_lib):
+    """The product falls to e^-102 (or rises to e^102) over 1,024 tokens and comes back to 1."""
+    T = 2048
+    up, down = torch.full((1, D), 1e30), torch.full((1, D), 1e-30)
+    check_scan(torch.zeros(1, T, D), steps(T, D, (0, 1024, -0.1), (1024, 2048, 0.1)), up, d_fin=down)
+    check_scan(torch.zeros(1, T, D), steps(T, D, (0, 1024, 0.1), (1024, 2048, -0.1)), down, d_fin=up)
+
+
+@pytest.mark.parametrize("D", [64, 256, 2048])
+def test_scan_growth_behind_a_cancelled_state(D, gpu_lib):
+    """An input cancels the state, and what it would have left from a zero state grows beyond the range (e^99 over 330
+    tokens, which every part of the chain that holds them sees; 128 of them grow by e^38)."""
+    T = 3000
+    x, s0 = torch.zeros(1, T, D), torch.full((1, D), -1.0)
+    for at in (0, 300, 1100):
+        x.zero_()
+        x[0, at] = 1.0
+        check_scan(x, steps(T, D, (at + 1, at + 331, 0.3)), s0)
+    d_h = torch.zeros(1, T, D)
+    for at in (T - 1, 2500, 1700):
+        d_h.zero_()
+        d_h[0, at] = 1.0
+        check_scan(torch.zeros(1, T, D), steps(T, D, (at - 330, at, 0.3)), None, d_h=d_h, d_fin=s0)
+
+
+def test_scan_infinite_state_stays_infinite(gpu_lib):
+    """Behind decay over many tiles (each product in range) an infinite state is infinite, not NaN."""
+    T, D = 2048, 256
+    s0 = torch.full((1, D), float("inf"))
+    g = torch.full((1, T, D), -0.1)
+    h, fin = gdn.gdn_gated_scan_fwd(torch.zeros(1, T, D).cuda(), g.cuda(), s0.cuda())
+    assert torch.isposinf(h).all() and torch.isposinf(fin).all()
+    gr = gdn.gdn_gated_scan_bwd(torch.zeros(1, T, D).cuda(), g.cuda(), torch.zeros(1, T, D).cuda(), torch.ones(1, D).cuda(), s0.cuda())
+    assert torch.isposinf(gr["dx"]).all() and torch.isposinf(gr["d_initial_state"]).all()
