@@ -17,6 +17,7 @@ GDN_DTYPE_BF16, GDN_DTYPE_FP32 = 0, 1
 CP_MODES = {"auto": 0, "off": 1, "on": 2, "exact": 3, "warmup": 4, "pages": 5}
 GDN_FLAG_KEEP_FORWARD, GDN_FLAG_REUSE_FORWARD, GDN_FLAG_QK_L2NORM, GDN_FLAG_BWD_ADJOINT_PASS = 1, 2, 4, 8
 GDN_FLAG_FWD_FUSED, GDN_FLAG_FWD_SPLIT, GDN_FLAG_REUSE_CP = 16, 32, 64
+GDN_FLAG_ZERO_OUTSIDE = 128
 GDN_ABI_VERSION = 10
 GDN_NOALLOC_SCRATCH_BYTES = 128 << 20
 

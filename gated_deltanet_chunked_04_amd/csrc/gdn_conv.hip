@@ -154,7 +154,10 @@ __global__ __launch_bounds__(kThreads) void k_conv_fwd(ConvArgs p, int run, int 
             const int32_t t = t0 + u;
             if (t >= w1) break;
             seq_advance(p.seq, s, t);
-            if (t < s.start || t >= s.end) continue;
+            if (t < s.start || t >= s.end) {
+                if (p.zero) zero_own<kOdd, T, VEC>(y + (int64_t)t * p.D + c0, ln.skip);
+                continue;
+            }
             if (t == s.start && t > w0)
 #pragma unroll
                 for (int r = 0; r < W - 1; ++r) {
@@ -337,7 +340,10 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(ConvArgs p, int run, int 
                 qa[U - 1].d = row<T, VEC>(p.d_y, at, p, c0);
                 // behind the run only the sequence that its last token is in matters
                 if (t < w1) seq_advance(p.seq, s, t);
-                if (t < s.start || t >= s.end) continue;
+                if (t < s.start || t >= s.end) {
+                    if (p.zero && t < w1) zero_own<kOdd, T, VEC>(dx + (int64_t)t * p.D + c0, ln.skip);
+                    continue;
+                }
                 if (t == s.start && t > w0)
 #pragma unroll
                     for (int r = 0; r < W - 1; ++r) {

@@ -342,7 +342,10 @@ __global__ __launch_bounds__(kThreads) void k_gscan_fwd(GScanArgs p, int tiles, 
         const int32_t t = w0 + i;
         if (t >= w1) break;
         seq_advance(p.seq, s, t);
-        if (t < s.start || t >= s.end) continue;
+        if (t < s.start || t >= s.end) {
+            if (p.zero && out) zero_own<kOdd, TX, VEC>(out + ((int64_t)t * p.D + cbase) + lo, skip);
+            continue;
+        }
         if (t == s.start) {
             // final_state may be initial_state: the last sequence's end may lie in another workgroup, which may
             // have written it by now, so its start was kept; the others end in this wave, behind this read
@@ -531,7 +534,14 @@ __global__ __launch_bounds__(kThreads) void k_gscan_bwd(GScanArgs p, int tiles, 
         const int32_t t = w0 + i;
         if (t >= w1) continue;
         seq_retreat(p.seq, e, t);
-        if (t < e.start || t >= e.end) continue;
+        if (t < e.start || t >= e.end) {
+            const int64_t at = (int64_t)t * p.D + cbase;
+            if (p.zero) {
+                zero_own<kOdd, TX, VEC>(dx + at + lo, skip);
+                zero_own<kOdd, TG, VEC>(dg + at + lo, skip);
+            }
+            continue;
+        }
         if (t + 1 == e.end) state_of<VEC>(p.d_sT, e.n, p.D, c, mu);
         back(i);
         if (p.ds0 && t == e.start) store_own<kOdd, float, VEC>(p.ds0 + (int64_t)e.n * p.D + c, mu, skip);
@@ -605,6 +615,10 @@ __global__ __launch_bounds__(kRowThreads) void k_gscan_rows(GScanArgs p, int cbl
         step(t, xt, gt);
     }
     if (p.sT) store_own<kOdd, float, VEC>(p.sT + (int64_t)s.n * p.D + c, h, skip);
+    if (p.zero && out) {  // in front of the first sequence and behind the last one
+        for (int32_t t0 = 0; nl == 0 && t0 < s.start; ++t0) zero_own<kOdd, TX, VEC>(out + (int64_t)t0 * p.D + c, skip);
+        for (int32_t t0 = s.end; nl == p.seq.N - 1 && t0 < p.seq.total; ++t0) zero_own<kOdd, TX, VEC>(out + (int64_t)t0 * p.D + c, skip);
+    }
 }
 
 // A wave for every sequence: rows of up to 16 tokens, and packed batches that hold no more tokens than sequences

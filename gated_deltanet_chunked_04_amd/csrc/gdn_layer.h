@@ -108,6 +108,7 @@ struct GScanArgs {
     void* dg;
     float* ds0;
     unsigned char* ws;
+    bool zero;     // rows of no sequence get zeros
 };
 size_t gscan_fwd_ws(const SeqView& seq, int64_t D);
 size_t gscan_bwd_ws(const SeqView& seq, int64_t D);
@@ -132,6 +133,7 @@ struct ConvArgs {
     float* db;
     void* ds0;
     unsigned char* ws;
+    bool zero;  // as above
 };
 size_t conv_bwd_ws(int64_t total, int64_t D, int W, int dtype);
 hipError_t launch_conv_fwd(const ConvArgs& a, int dtype, int w_dtype, hipStream_t st);

@@ -43,12 +43,12 @@ gdn_status check_buf(const void* p, size_t need, size_t bytes) {
 }
 
 gdn_status check_scan(const gdn_scan_desc* d, SeqView& seq) {
-    if (!d || d->flags || !zeros(d->reserved, 4) || !types_ok(d->dtype, d->g_dtype)) return GDN_ERR_INVALID_ARG;
+    if (!d || (d->flags & ~GDN_FLAG_ZERO_OUTSIDE) || !zeros(d->reserved, 4) || !types_ok(d->dtype, d->g_dtype)) return GDN_ERR_INVALID_ARG;
     return check_sizes(d->B, d->T, d->D, d->cu_seqlens, d->num_seqs, seq);
 }
 
 gdn_status check_conv(const gdn_conv_desc* d, SeqView& seq) {
-    if (!d || d->flags || !zeros(d->reserved, 4) || !types_ok(d->dtype, d->w_dtype)) return GDN_ERR_INVALID_ARG;
+    if (!d || (d->flags & ~GDN_FLAG_ZERO_OUTSIDE) || !zeros(d->reserved, 4) || !types_ok(d->dtype, d->w_dtype)) return GDN_ERR_INVALID_ARG;
     if (d->activation != GDN_ACT_NONE && d->activation != GDN_ACT_SILU) return GDN_ERR_INVALID_ARG;
     if (d->width < 2 || d->width > 4) return GDN_ERR_UNSUPPORTED;
     return check_sizes(d->B, d->T, d->D, d->cu_seqlens, d->num_seqs, seq);
@@ -114,6 +114,7 @@ gdn_status gdn_gated_scan_fwd(const gdn_scan_desc* desc, const void* x, const vo
     a.sT = final_state;
     a.states = static_cast<float*>(states);
     a.ws = static_cast<unsigned char*>(workspace);
+    a.zero = desc->flags & GDN_FLAG_ZERO_OUTSIDE;
     ProfScope ps(kKGScanFwd, (hipStream_t)stream);
     return launched(launch_gscan_fwd(a, desc->dtype, desc->g_dtype, (hipStream_t)stream));
 }
@@ -141,6 +142,7 @@ gdn_status gdn_gated_scan_bwd(const gdn_scan_desc* desc, const void* x, const vo
     a.dg = dg;
     a.ds0 = d_initial_state;
     a.ws = static_cast<unsigned char*>(workspace);
+    a.zero = desc->flags & GDN_FLAG_ZERO_OUTSIDE;
     ProfScope ps(kKGScanBwd, (hipStream_t)stream);
     return launched(launch_gscan_bwd(a, desc->dtype, desc->g_dtype, states != nullptr, (hipStream_t)stream));
 }
@@ -169,6 +171,7 @@ gdn_status gdn_short_conv_fwd(const gdn_conv_desc* desc, const void* x, const vo
     a.s0 = initial_state;
     a.sT = final_state;
     a.y = y;
+    a.zero = desc->flags & GDN_FLAG_ZERO_OUTSIDE;
     ProfScope ps(kKConvFwd, (hipStream_t)stream);
     return launched(launch_conv_fwd(a, desc->dtype, desc->w_dtype, (hipStream_t)stream));
 }
@@ -198,6 +201,7 @@ gdn_status gdn_short_conv_bwd(const gdn_conv_desc* desc, const void* x, const vo
     a.db = dbias;
     a.ds0 = d_initial_state;
     a.ws = static_cast<unsigned char*>(workspace);
+    a.zero = desc->flags & GDN_FLAG_ZERO_OUTSIDE;
     ProfScope ps(kKConvBwd, (hipStream_t)stream);
     return launched(launch_conv_bwd(a, desc->dtype, desc->w_dtype, (hipStream_t)stream));
 }

@@ -82,6 +82,15 @@ __device__ __forceinline__ void store_own(T* p, const float (&x)[N], int skip) {
     store_own<kOdd, T, N>(p, r, skip);
 }
 
+// For tokens of no sequence, by the waves that meet them (no launch of its own; calls without such tokens take what
+// they took within 1%).
+template <bool kOdd, typename T, int N>
+__device__ __forceinline__ void zero_own(T* p, int skip) {
+    Raw<T, N> r;
+    r.clear();
+    store_own<kOdd, T, N>(p, r, skip);
+}
+
 // Sum over `parts` rows of partial sums [parts, n] for COLS columns from c0 on, by a workgroup of
 // kSumThreads: COLS lanes side by side on the columns of a row, eight loads in flight per lane, then a tree
 // over the rows in LDS (`sh`: kSumThreads words). The order of the additions depends on `parts` and COLS

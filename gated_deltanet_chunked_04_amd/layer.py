@@ -2,7 +2,9 @@
 
 Like the rest of the package these functions carry the C ABI's names (include/gdn.h) and only marshal
 tensors into it; every step of the computation runs in the HIP library. Tensors are contiguous, on one
-device; work runs on that device's current stream.
+device; work runs on that device's current stream. Tokens in front of a packed batch's first sequence and
+behind its last one get zeros in outputs and gradients that these functions allocate, and leave a caller's
+own as they were.
 
   gdn_gated_scan_fwd / _bwd     h_t = exp(g_t) h_{t-1} + x_t per channel, and its gradients
   gdn_gated_scan_states(x)      the buffer that carries the forward's states to the backward
@@ -19,8 +21,8 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._abi import (GDN_ACT_NONE, GDN_ACT_SILU, GDN_DTYPE_BF16, GDN_DTYPE_FP32, GDN_OUT_E4M3, GDN_OUT_SAME,
-                   GdnConvDesc, GdnRmsnormDesc, GdnScanDesc, check, load_library)
+from ._abi import (GDN_ACT_NONE, GDN_ACT_SILU, GDN_DTYPE_BF16, GDN_DTYPE_FP32, GDN_FLAG_ZERO_OUTSIDE, GDN_OUT_E4M3,
+                   GDN_OUT_SAME, GdnConvDesc, GdnRmsnormDesc, GdnScanDesc, check, load_library)
 
 _DTYPES = {torch.bfloat16: GDN_DTYPE_BF16, torch.float32: GDN_DTYPE_FP32}
 _ACTIVATIONS = {None: GDN_ACT_NONE, "silu": GDN_ACT_SILU}
@@ -74,14 +76,14 @@ def _second_type(name, t, x) -> int:
     return _DTYPES[t.dtype]
 
 
-def _packing(x, cu_seqlens) -> int:
-    """N of a packed batch."""
+def _packing(x, cu_seqlens, new):
+    """(N, flags) of a packed batch; new: the outputs are, and get zeros in rows of no sequence."""
     if (not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype != torch.int32 or cu_seqlens.device != x.device
             or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or cu_seqlens.numel() < 2):
         raise TypeError(f"cu_seqlens must be a contiguous int32 tensor [N+1], N >= 1, on {x.device}")
     if x.shape[0] != 1:
         raise ValueError("cu_seqlens needs B = 1")
-    return cu_seqlens.numel() - 1
+    return cu_seqlens.numel() - 1, GDN_FLAG_ZERO_OUTSIDE if new else 0
 
 
 # The current stream's handle. The first form gives it without building a Stream object (0.1 against 1.9 us of a
@@ -138,7 +140,7 @@ def _scan_plan(B, T, D, dtype, g_dtype):
             _bytes("gdn_gated_scan_bwd_workspace_size", desc))
 
 
-def _scan_call(x, g, cu_seqlens):
+def _scan_call(x, g, cu_seqlens, new):
     """(descriptor, forward and backward workspace bytes, N)."""
     _lead("x", x, 3)
     dtype, g_dtype = _dtype(x), _second_type("g", g, x)
@@ -146,8 +148,8 @@ def _scan_call(x, g, cu_seqlens):
     ref, fwd, bwd = _scan_plan(B, T, D, dtype, g_dtype)
     if cu_seqlens is None:
         return ref, fwd, bwd, B
-    N = _packing(x, cu_seqlens)
-    return ctypes.byref(GdnScanDesc(B, T, D, dtype, g_dtype, N, 0, cu_seqlens.data_ptr())), fwd, bwd, N
+    N, flags = _packing(x, cu_seqlens, new)
+    return ctypes.byref(GdnScanDesc(B, T, D, dtype, g_dtype, N, flags, cu_seqlens.data_ptr())), fwd, bwd, N
 
 
 def gdn_gated_scan_states(x):
@@ -176,7 +178,7 @@ def gdn_gated_scan_fwd(x, g, initial_state=None, *, cu_seqlens=None, output_fina
     or None (zeros); cu_seqlens int32 device tensor [N+1] (B = 1), no host copy needed. final_state may be
     initial_state itself (updated in place). states (see gdn_gated_scan_states) receives what
     gdn_gated_scan_bwd needs of the forward."""
-    ref, need, _, N = _scan_call(x, g, cu_seqlens)
+    ref, need, _, N = _scan_call(x, g, cu_seqlens, h is None)
     shape, dev = x.shape, x.device
     pg = _like("g", g, shape, g.dtype, dev)
     p0 = _like("initial_state", initial_state, (N, shape[2]), torch.float32, dev)
@@ -198,7 +200,7 @@ def gdn_gated_scan_bwd(x, g, d_h, initial_state=None, d_final_state=None, *, cu_
     """Gradients of <d_h, h> + <d_final_state, final_state>: dict(dx, dg, d_initial_state); `out` may hold
     them preallocated. states: what gdn_gated_scan_fwd(states=...) wrote for these inputs, or None (the
     states are recomputed)."""
-    ref, _, need, N = _scan_call(x, g, cu_seqlens)
+    ref, _, need, N = _scan_call(x, g, cu_seqlens, out is None)
     shape, dev = x.shape, x.device
     if d_h is None:
         raise ValueError("d_h is required")
@@ -224,7 +226,7 @@ def _conv_plan(B, T, D, W, dtype, w_dtype, activation):
     return ctypes.byref(desc), _bytes("gdn_short_conv_bwd_workspace_size", desc)
 
 
-def _conv_call(x, weight, bias, activation, cu_seqlens):
+def _conv_call(x, weight, bias, activation, cu_seqlens, new):
     """(descriptor, backward workspace bytes, N, W, pointers of weight and bias)."""
     _lead("x", x, 3)
     dtype, w_dtype = _dtype(x), _second_type("weight", weight, x)
@@ -240,8 +242,8 @@ def _conv_call(x, weight, bias, activation, cu_seqlens):
     ref, bwd = _conv_plan(B, T, D, W, dtype, w_dtype, act)
     if cu_seqlens is None:
         return ref, bwd, B, W, pw, pb
-    N = _packing(x, cu_seqlens)
-    return ctypes.byref(GdnConvDesc(B, T, D, W, dtype, w_dtype, act, N, 0, cu_seqlens.data_ptr())), bwd, N, W, pw, pb
+    N, flags = _packing(x, cu_seqlens, new)
+    return ctypes.byref(GdnConvDesc(B, T, D, W, dtype, w_dtype, act, N, flags, cu_seqlens.data_ptr())), bwd, N, W, pw, pb
 
 
 def gdn_short_conv_fwd(x, weight, bias=None, initial_state=None, *, activation="silu", cu_seqlens=None,
@@ -252,7 +254,7 @@ def gdn_short_conv_fwd(x, weight, bias=None, initial_state=None, *, activation="
     'silu' or None; initial_state [N,W-1,D] in x's type: the inputs before each sequence's first token,
     oldest first (zeros if None). The final state is a sequence's last W-1 inputs; a final_state tensor
     asks for it, and may be initial_state itself for up to 16 tokens per row (decoding)."""
-    ref, _, N, W, pw, pb = _conv_call(x, weight, bias, activation, cu_seqlens)
+    ref, _, N, W, pw, pb = _conv_call(x, weight, bias, activation, cu_seqlens, y is None)
     shape, dev = x.shape, x.device
     sshape = (N, W - 1, shape[2])
     p0 = _like("initial_state", initial_state, sshape, x.dtype, dev)
@@ -270,7 +272,7 @@ def gdn_short_conv_bwd(x, weight, d_y, bias=None, initial_state=None, d_final_st
                        cu_seqlens=None, need_d_initial_state=True, workspace=None, out=None):
     """Gradients of <d_y, y> + <d_final_state, final_state>: dict(dx, dweight, dbias, d_initial_state), dweight
     and dbias in fp32, dbias None without a bias; `out` may hold them preallocated."""
-    ref, need, N, W, pw, pb = _conv_call(x, weight, bias, activation, cu_seqlens)
+    ref, need, N, W, pw, pb = _conv_call(x, weight, bias, activation, cu_seqlens, out is None)
     shape, dev = x.shape, x.device
     D = shape[2]
     sshape = (N, W - 1, D)

@@ -339,11 +339,13 @@ gdn_status gdn_cp_windows(const gdn_desc* desc, const void* k, const void* v,
  *
  * Sequences: without cu_seqlens, row b of [B, T, D] is sequence b (N = B). With cu_seqlens (device
  * int32 [N+1], not decreasing), B is 1 and sequence n owns tokens [cu_seqlens[n], cu_seqlens[n+1]);
- * tokens before cu_seqlens[0] and from cu_seqlens[N] on belong to no sequence and their outputs are
- * left as they were. No host copy is needed. Offsets are read clamped into [0, T]: an array that
+ * tokens before cu_seqlens[0] and from cu_seqlens[N] on belong to no sequence: their inputs reach no
+ * result, and their rows of the outputs (and of dx and dg) are left as they were, or receive zeros
+ * with GDN_FLAG_ZERO_OUTSIDE. No host copy is needed. Offsets are read clamped into [0, T]: an array that
  * decreases gives unspecified values, never an access out of range.
  * An empty sequence passes its entering state on as its final state (and the final state's
  * gradient on as the entering state's). */
+#define GDN_FLAG_ZERO_OUTSIDE 128
 
 /* Gated scan: the recurrence with a gate per channel,
  *     h_t = exp(g_t) h_{t-1} + x_t,    h_0 = initial_state (zeros when NULL),
@@ -356,7 +358,7 @@ typedef struct gdn_scan_desc {
     int32_t dtype;             /* gdn_dtype of x, h and their gradients */
     int32_t g_dtype;           /* gdn_dtype of g and dg: dtype's, or GDN_DTYPE_FP32 */
     int32_t num_seqs;          /* with cu_seqlens: N (>= 1); ignored otherwise */
-    int32_t flags;             /* must be zero */
+    int32_t flags;             /* 0 or GDN_FLAG_ZERO_OUTSIDE */
     const int32_t* cu_seqlens; /* device [N+1], or NULL */
     int32_t reserved[4];       /* must be zero */
 } gdn_scan_desc;
@@ -401,7 +403,7 @@ typedef struct gdn_conv_desc {
     int32_t w_dtype;           /* gdn_dtype of weight and bias: dtype's, or GDN_DTYPE_FP32 */
     int32_t activation;        /* gdn_activation */
     int32_t num_seqs;          /* with cu_seqlens: N (>= 1); ignored otherwise */
-    int32_t flags;             /* must be zero */
+    int32_t flags;             /* 0 or GDN_FLAG_ZERO_OUTSIDE */
     const int32_t* cu_seqlens; /* device [N+1], or NULL */
     int32_t reserved[4];       /* must be zero */
 } gdn_conv_desc;

@@ -131,3 +131,78 @@ def test_scan_infinite_state_stays_infinite(gpu_lib):
     assert torch.isposinf(h).all() and torch.isposinf(fin).all()
     gr = gdn.gdn_gated_scan_bwd(torch.zeros(1, T, D).cuda(), g.cuda(), torch.zeros(1, T, D).cuda(), torch.ones(1, D).cuda(), s0.cuda())
     assert torch.isposinf(gr["dx"]).all() and torch.isposinf(gr["d_initial_state"]).all()
+
+
+# ---- packed batches with tokens of no sequence --------------------------------------------------
+
+
+def litter():
+    """Memory that the allocator hands out next holds NaN."""
+    junk = [torch.full((1 << k,), float("nan"), device="cuda") for k in range(10, 21) for _ in range(4)]
+    del junk
+
+
+# the batch is padded behind (and in front): in one tile, several, as decoding takes it, and with nothing but padding
+PADDED = [([5, 0, 30], 0, 29, 64), ([5, 0, 30], 3, 9, 131), ([300, 2, 400], 0, 322, 256), ([300, 2, 400], 70, 200, 130),
+          ([1] * 40, 0, 24, 64), ([1] * 30 + [0] * 60, 2, 40, 130), ([0] * 700 + [50, 0], 9, 450, 256), ([0, 0], 0, 300, 64), ([0], 4, 0, 8)]
+
+
+@pytest.mark.parametrize("lens,head,tail,D", PADDED)
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_padding_gets_zeros(lens, head, tail, D, dt, gpu_lib):
+    """Outputs and gradients that the package allocates hold zeros in rows of no sequence, whatever the inputs hold
+    there; the other rows are what they are without the padding's values."""
+    cu, T = packed(lens, head, tail)
+    x, g, s0, N = scan_inputs(1, T, D, cu, dt, F32, True)
+    keep, cd = owned(1, T, cu), cu_dev(cu)
+    w, c0 = rnd(D, 4, seed=3).cuda(), rnd(N, 3, D, seed=4, dtype=dt).cuda()
+    d = rnd(1, T, D, seed=5, dtype=dt)
+    want = ref.scan_fwd(x, g, s0, cu)[0], ref.conv_fwd(x, w.cpu(), None, c0.cpu(), True, cu)[0]
+    wantg = ref.scan_bwd(x, g, s0, d, None, cu), ref.conv_bwd(x, w.cpu(), None, c0.cpu(), d, None, True, cu)
+    for t in (x, g, d):
+        t[~keep] = float("nan")
+    x, g, s0, d = x.cuda(), g.cuda(), s0.cuda(), d.cuda()
+
+    def check(got, want, what):
+        assert (got[~keep.cuda()] == 0).all(), what + ": padding"
+        close(got[keep.cuda()], (want[0][keep], want[1][keep]), what)
+
+    litter()
+    check(gdn.gdn_gated_scan_fwd(x, g, s0, cu_seqlens=cd)[0], want[0], "h")
+    litter()
+    check(gdn.gdn_short_conv_fwd(x, w, None, c0, cu_seqlens=cd)[0], want[1], "y")
+    states = gdn.gdn_gated_scan_states(x)
+    gdn.gdn_gated_scan_fwd(x, g, s0, cu_seqlens=cd, states=states)
+    for st in (states, None):
+        litter()
+        gr = gdn.gdn_gated_scan_bwd(x, g, d, s0, cu_seqlens=cd, states=st)
+        for k in ("dx", "dg"):
+            check(gr[k], wantg[0][k], k)
+    litter()
+    gr = gdn.gdn_short_conv_bwd(x, w, d, None, c0, cu_seqlens=cd)
+    check(gr["dx"], wantg[1]["dx"], "dx")
+    for k in ("dweight", "d_initial_state"):
+        close(gr[k], wantg[1][k], k)
+
+
+def test_padding_reaches_no_weight(gpu_lib):
+    """A projection in front of and behind a convolution and a scan of a padded batch, whose loss takes the tokens
+    alone: its weights' gradients are finite and those of the batch without padding."""
+    cu, T = packed([70, 1, 130], 0, 55)
+    real, cd = cu[-1], cu_dev(cu)
+    u, gates = rnd(1, T, 32).cuda(), (-rnd(1, T, 64, seed=1).abs() * 0.1).cuda()
+    up = rnd(1, real, 32, seed=2).cuda()
+    grads = []
+    for n in (T, real):
+        litter()
+        a, b = (rnd(64, 32, seed=3).cuda().requires_grad_(), rnd(32, 64, seed=4).cuda().requires_grad_())
+        wc = rnd(64, 4, seed=5).cuda().requires_grad_()
+        m, _ = gdn.short_conv(u[:, :n] @ a.t(), wc, cu_seqlens=cd)
+        h, _ = gdn.gated_scan(m, gates[:, :n].contiguous(), cu_seqlens=cd)
+        ((h @ b.t())[:, :real] * up).sum().backward()
+        grads.append([a.grad, b.grad, wc.grad])
+    for p, q in zip(*grads):
+        assert torch.isfinite(p).all()
+        # the same sums of at most 256 terms in another grouping: 256 half steps of the sum of absolute values, which is
+        # about 16 times the sum where signs are random, taken of the largest weight
+        assert (p - q).abs().max() <= 256 * ref.U * q.abs().max() * 16

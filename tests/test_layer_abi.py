@@ -190,3 +190,13 @@ def test_python_refuses_host_tensors():
         gdn.gdn_rmsnorm_fwd(x, torch.zeros(8))
     with pytest.raises(ValueError):
         gdn.rms_norm(x, torch.zeros(8))
+
+
+def test_zero_outside_flag(lib):
+    """Taken by the operators that know sequences, alone; other bits beside it are refused."""
+    n = ctypes.c_size_t(BIG)
+    assert _abi.GDN_FLAG_ZERO_OUTSIDE == 128
+    for flags, code in ((128, 0), (129, 1), (256, 1), (-1, 1)):
+        assert lib.gdn_gated_scan_fwd_workspace_size(ctypes.byref(scan_desc(flags=flags)), ctypes.byref(n)) == code
+        assert lib.gdn_short_conv_bwd_workspace_size(ctypes.byref(conv_desc(flags=flags)), ctypes.byref(n)) == code
+        assert lib.gdn_rmsnorm_bwd_workspace_size(ctypes.byref(rms_desc(flags=flags)), ctypes.byref(n)) == 1
