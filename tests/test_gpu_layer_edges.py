@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import gated_deltanet_chunked_04_amd as gdn
+import test_gpu_layer as base
 from oracle import layer as ref
 from test_gpu_layer import close, cu_dev, cuda, owned, packed, rnd, scan_inputs
 
@@ -206,3 +207,38 @@ def test_padding_reaches_no_weight(gpu_lib):
         # the same sums of at most 256 terms in another grouping: 256 half steps of the sum of absolute values, which is
         # about 16 times the sum where signs are random, taken of the largest weight
         assert (p - q).abs().max() <= 256 * ref.U * q.abs().max() * 16
+
+
+# ---- chains over several groups of tiles --------------------------------------------------------
+
+# A tile is 64 or 128 tokens; a group 8 to 64 tiles by the number of channels and the direction (512 to 8,192 tokens).
+# Slow gates, so that what enters a group is much of its states.
+LONG = [(2500, 2048), (5000, 512), (5000, 130), (5000, 259), (2600, 4096), (2600, 4099), (9001, 100)]
+# sequences that start before a group's first token (from either end), at it and behind it, and that span groups
+CUTS = [(4608, 2048, [512, 512, 1000, 24, 1, 511, 1536, 512]), (5300, 512, [1024, 1023, 2, 2047, 1204]), (5300, 131, [2047, 1, 2049, 1203]),
+        (5300, 256, [4096, 0, 1204]), (3100, 4096, [1023, 2, 1023, 1052])]
+
+
+@pytest.mark.parametrize("dt,gdt", [(BF, F32), (BF, BF), (F32, F32)])
+@pytest.mark.parametrize("T,D", LONG)
+def test_scan_chain(T, D, dt, gdt, gpu_lib):
+    x, g, s0, _ = scan_inputs(1, T, D, None, dt, gdt, True, decay=0.002)
+    check_scan(x, g, s0, d_h=rnd(1, T, D, seed=7, dtype=dt), d_fin=rnd(1, D, seed=8, scale=30.0))
+
+
+@pytest.mark.parametrize("T,D,lens", CUTS)
+def test_scan_chain_of_packed_sequences(T, D, lens, gpu_lib):
+    cu, _ = packed(lens)
+    assert cu[-1] <= T
+    x, g, s0, N = scan_inputs(1, T, D, cu, F32, F32, True, decay=0.002)
+    check_scan(x, g, s0, cu, d_h=rnd(1, T, D, seed=7), d_fin=rnd(N, D, seed=8, scale=30.0))
+
+
+# ---- norm: rows of a few columns and of more than registers hold --------------------------------
+
+
+@pytest.mark.parametrize("dt,wdt", [(BF, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("rows,D", [(9, 2), (3, 5), (70, 7), (2, 16392), (2, 20001), (3, 32768), (2, 33001), (2, 65536)])
+def test_rms_narrow_and_wide_rows(rows, D, dt, wdt, gpu_lib):
+    """(The bounds' 64 terms a thread hold for 1,024 threads up to 65,536 columns.)"""
+    base.test_rms(rows, D, dt, wdt, gpu_lib)
