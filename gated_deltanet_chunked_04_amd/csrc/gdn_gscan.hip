@@ -663,10 +663,15 @@ size_t chain_bytes(size_t tiles, int64_t D) {
     return 256 + align256(tiles * D * 8) + align256(groups * D * 4);
 }
 // A group hands its state on in about a microsecond, one group after the other, while a tile looks back over half
-// a group's pairs. From `wide` channels on the memory takes longer than the chain, and small groups read less (64K x
-// 4096: groups of 8 285 us, 16 288; training 2 x 16K x 2048: 279, 282). In fewer, longer groups keep the chain short
-// (64K tokens of 1024 channels: 8 138 us, 16 115; of 256: 8 101, 32 51, 64 49; of 64: 8 116, 32 46, 64 35; all these with
-// 64-token tiles).
+// a group's pairs. From `wide` channels on the memory takes longer than the chain, and small groups read less; with
+// fewer, longer groups keep the chain short. us forward / backward in groups of 8, 16, 32 and 64 tiles:
+//   64K x 4096   371 / 640   373 / 643   377 / 686   396 / 709
+//   32K x 2048   106 / 173   106 / 176   108 / 179   114 / 199
+//   64K x 1024   112 / 182   108 / 177   109 / 184   118 / 198
+//   64K x  512    71 / 128    57 / 103    58 / 103    61 / 110
+//   64K x  256    64 / 111    45 /  73    38 /  58    39 /  61
+//   64K x   64    62 /  67    39 /  44    28 /  33    23 /  29
+// Rows of fewer tiles have a shorter chain and care less (16 rows of 4096 x 256: 36 / 54, 35 / 54, 36 / 56, 36 / 57).
 hipError_t make_chain(unsigned char* ws, size_t tiles, int64_t D, int64_t wide, Chain& ch, hipStream_t st) {
     const size_t bytes = chain_bytes(tiles, D);
     ch.group = D >= wide ? kMinGroup : (D >= 512 ? 16 : (D >= kSlim ? 32 : 64));

@@ -103,7 +103,7 @@ struct GScanArgs {
     const float* d_sT;
     void* h;       // null: only the states are wanted
     float* sT;
-    float* states;  // [tiles, D] entering state of every tile
+    float* states;  // [ceil(total / 64), D]: the state entering every 64th token
     void* dx;
     void* dg;
     float* ds0;

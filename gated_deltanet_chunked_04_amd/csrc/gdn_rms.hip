@@ -10,9 +10,10 @@
 //
 // Bound by memory (about 6 operations per element forward and 10 backward against 7 or 8 bytes in
 // bf16), so a row is read once and stays in registers between its sum and its output: a lane owns
-// vectors of 8 neighbouring columns, a row belongs to one wave (up to 2,048 columns) or to one
-// workgroup. 16 lanes that sit side by side own 128 columns, so the maximum behind a scale of 128 columns is
-// taken inside a row of 16 lanes. Rows too long for a workgroup's registers are read again.
+// vectors of 8 neighbouring columns, a row belongs to 4 to 1,024 threads: up to 256 columns several rows share a
+// wave, up to 512 a wave takes one and up to 1,024 two waves, above that a workgroup (shape_of). 16 lanes that sit
+// side by side own 128 columns, so the maximum behind a scale of 128 columns is taken inside a row of 16 lanes.
+// Rows too long for a workgroup's registers are read again.
 #include "gdn_layer.h"
 #include "gdn_vec.h"
 
@@ -226,8 +227,8 @@ __global__ __launch_bounds__(threads_of<LANES>()) void k_rms_fwd(RmsArgs p) {
     }
 }
 
-// Gradient: the workgroup's rows one after the other (a row per wave, or per workgroup), each lane adding its
-// columns' dy rh in registers; at the end the workgroup's waves add theirs in LDS where they hold the same
+// Gradient: the workgroup's rows one after the other (256 / LANES at a time where a row has fewer threads), each lane
+// adding its columns' dy rh in registers; at the end the workgroup's waves add theirs in LDS where they hold the same
 // columns, and part[blockIdx.x] gets them.
 template <bool kOdd, typename T, typename TW, int LANES, int NV>
 __global__ __launch_bounds__(threads_of<LANES>()) void k_rms_bwd(RmsArgs p, float* part) {
@@ -336,7 +337,8 @@ __global__ __launch_bounds__(kSumThreads) void k_rms_dw_sum(const float* part, i
     if (threadIdx.x < COLS && c0 + threadIdx.x < D) dw[c0 + threadIdx.x] = s;
 }
 
-// ---- rows of any length, element by element: fewer than 8 columns, or more than a workgroup's registers hold.
+// ---- rows of any length, element by element: fewer than 8 columns, or more than a workgroup's registers hold (4,000 x
+// 32,776 bf16 454 us, x 32,768 190). A workgroup of 1,024 threads each, whatever the length, so 4,194,303 rows at most.
 constexpr int kLoopThreads = 1024;
 constexpr int kSlots = kLoopThreads / 64;
 
@@ -450,7 +452,9 @@ Shape shape_of(int64_t D) {
     const int64_t n = (D + 8 * lanes - 1) / (8 * lanes);
     return {lanes, (int)(n <= 1 ? 1 : (n <= 2 ? 2 : 4))};
 }
-// The gradient's: its sums of dw double the registers a column takes, so 512 lanes and four vectors are the most.
+// The gradient's: its sums of dw double the registers a column takes, so 512 lanes and four vectors are the most. Those
+// take all 256 registers, and 4 (fp32, rows that are not whole vectors) to 19 (bf16) of them spill, 80 bytes a lane at
+// most: 8,000 x 16,384 bf16 201 us of a floor of 169, 4,000 x 16,384 fp32, which does not spill, 229.
 Shape bwd_shape_of(int64_t D) {
     if (D > 16384) return {0, 0};
     return D > 8192 ? Shape{512, 4} : shape_of(D);

@@ -377,7 +377,9 @@ gdn_status gdn_gated_scan_states_size(const gdn_scan_desc* desc, size_t* bytes);
  *   what gdn_gated_scan_bwd needs of the forward: the fp32 state entering every 64th token (nothing
  *   is written where a call is one tile of tokens and needs none)
  * A call of up to 16 tokens per row (decoding), or of a packed batch of up to 512 tokens and no more of
- * them than sequences, is one launch and needs no workspace. */
+ * them than sequences, is one launch and needs no workspace. In the others a run of tokens waits on the
+ * device for the state of the run before it; a wait that lasts about a second (which no call in working
+ * order comes near) gives up, and leaves NaN from there to the sequence's end. */
 gdn_status gdn_gated_scan_fwd(const gdn_scan_desc* desc, const void* x, const void* g,
                               const float* initial_state, void* h, float* final_state, void* states,
                               void* workspace, size_t workspace_bytes, void* stream);
@@ -451,7 +453,8 @@ typedef struct gdn_rmsnorm_desc {
 } gdn_rmsnorm_desc;
 
 /* Forward. residual and residual_out are both given or both NULL; residual_out may be x or residual
- * itself (in place). scale only with GDN_OUT_E4M3. */
+ * itself (in place). scale only with GDN_OUT_E4M3. Rows of fewer than 8 columns or more than 32,768
+ * (in the gradient 16,384): at most 4,194,303 of them (GDN_ERR_UNSUPPORTED). */
 gdn_status gdn_rmsnorm_fwd(const gdn_rmsnorm_desc* desc, const void* x, const void* residual,
                            const void* weight, void* y, float* scale, void* residual_out,
                            void* stream);
