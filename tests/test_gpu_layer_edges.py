@@ -242,3 +242,42 @@ def test_scan_chain_of_packed_sequences(T, D, lens, gpu_lib):
 def test_rms_narrow_and_wide_rows(rows, D, dt, wdt, gpu_lib):
     """(The bounds' 64 terms a thread hold for 1,024 threads up to 65,536 columns.)"""
     base.test_rms(rows, D, dt, wdt, gpu_lib)
+
+
+# ---- captured calls whose offsets change --------------------------------------------------------
+
+
+@pytest.mark.parametrize("T,N,D", [(700, 5, 256), (60, 3, 131), (300, 400, 64)])
+def test_graph_of_a_padded_batch(T, N, D, gpu_lib):
+    """A captured forward and gradient, replayed with other inputs and other sequences (and other padding: rows that
+    held results at the last replay), agrees with eager calls in every bit."""
+    x, g, s0, _ = scan_inputs(1, T, D, [0] * (N + 1), BF, F32, True)
+    bufs = [t.cuda() for t in (x, g, s0, rnd(D, 4, dtype=BF), rnd(N, 3, D, dtype=BF))] + [cu_dev([0] * N + [T])]
+
+    def call(x, g, s0, w, c0, cu):
+        m, cf = gdn.gdn_short_conv_fwd(x, w, None, c0, cu_seqlens=cu, output_final_state=True)
+        states = gdn.gdn_gated_scan_states(m)
+        h, f = gdn.gdn_gated_scan_fwd(m, g, s0, cu_seqlens=cu, states=states)
+        gs = gdn.gdn_gated_scan_bwd(m, g, h, s0, f, cu_seqlens=cu, states=states)
+        gc = gdn.gdn_short_conv_bwd(x, w, gs["dx"], None, c0, cf, cu_seqlens=cu)
+        return [m, cf, h, f, *gs.values(), gc["dx"], gc["dweight"], gc["d_initial_state"]]
+
+    call(*bufs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = call(*bufs)
+    gen = torch.Generator().manual_seed(1)
+    for it in range(5):
+        cuts = sorted(torch.randint(0, T + 1, (N + 1,), generator=gen).tolist())
+        fresh = scan_inputs(1, T, D, cuts, BF, F32, True, seed=10 * it + 1)[:3]
+        for b, t in zip(bufs, (*fresh, rnd(D, 4, seed=it, dtype=BF), rnd(N, 3, D, seed=it, dtype=BF), torch.tensor(cuts, dtype=torch.int32))):
+            b.copy_(t)
+        graph.replay()
+        want = call(*bufs)
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(outs, want)):
+            assert torch.equal(a, b), (it, i)
+        pad = ~owned(1, T, cuts).cuda()
+        for i in (0, 2, 4, 5, 7):
+            assert outs[i].shape == (1, T, D) and (outs[i][pad] == 0).all(), (it, i)
