@@ -20,7 +20,8 @@ missing they raise instead of computing anything elsewhere.
   chunk_gated_delta_rule(...) autograd wrapper over gdn_chunk_fwd / gdn_chunk_bwd
 
 The operators around the rule in a layer (layer.py): gated scan, short convolution, RMS norm with
-residual addition and 8-bit output, each with its gradient and an autograd wrapper.
+residual addition and 8-bit output, each with its gradient and an autograd wrapper. The layer's products
+(products.py): quantisation to e4m3, the product of e4m3 matrices, the gated feed-forward block.
 """
 from __future__ import annotations
 
@@ -35,13 +36,17 @@ from ._abi import (CP_MODES, EXPORTS, GDN_DTYPE_BF16, GDN_DTYPE_FP32, GDN_FLAG_B
                    load_library, status_string)
 from .layer import (gated_scan, gdn_gated_scan_bwd, gdn_gated_scan_fwd, gdn_gated_scan_states,  # noqa: F401
                     gdn_rmsnorm_bwd, gdn_rmsnorm_fwd, gdn_short_conv_bwd, gdn_short_conv_fwd, rms_norm, short_conv)
+from .products import (gated_ffn, gdn_gated_ffn_bwd, gdn_gated_ffn_e4m3, gdn_gated_ffn_fwd, gdn_gated_ffn_pre,  # noqa: F401
+                       gdn_matmul_e4m3, gdn_quant_e4m3, linear_e4m3)
 
 __all__ = ["gdn_plan", "gdn_chunk_fwd", "gdn_chunk_fwd_noalloc", "gdn_chunk_bwd", "gdn_workspace", "gdn_cp_states", "gdn_intra_chunk", "gdn_cp_modes",
            "gdn_cp_windows", "gdn_recurrent_fwd", "gdn_profile_enable", "gdn_profile_read", "chunk_gated_delta_rule", "load_library",
            "make_desc", "GdnError",
            "gdn_gated_scan_fwd", "gdn_gated_scan_bwd", "gdn_gated_scan_states", "gated_scan",
            "gdn_short_conv_fwd", "gdn_short_conv_bwd", "short_conv",
-           "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd", "rms_norm"]
+           "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd", "rms_norm",
+           "gdn_quant_e4m3", "gdn_matmul_e4m3", "linear_e4m3",
+           "gdn_gated_ffn_fwd", "gdn_gated_ffn_pre", "gdn_gated_ffn_bwd", "gdn_gated_ffn_e4m3", "gated_ffn"]
 
 
 def _ptr(t: Optional[torch.Tensor]):

@@ -27,8 +27,12 @@ EXPORTS = ("gdn_abi_version", "gdn_status_string", "gdn_plan", "gdn_chunk_fwd_wo
            "gdn_cp_modes", "gdn_cp_windows", "gdn_recurrent_fwd", "gdn_profile_enable", "gdn_profile_read",
            "gdn_gated_scan_fwd_workspace_size", "gdn_gated_scan_bwd_workspace_size", "gdn_gated_scan_states_size",
            "gdn_gated_scan_fwd", "gdn_gated_scan_bwd", "gdn_short_conv_bwd_workspace_size", "gdn_short_conv_fwd",
-           "gdn_short_conv_bwd", "gdn_rmsnorm_bwd_workspace_size", "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd")
-GDN_ACT_NONE, GDN_ACT_SILU = 0, 1
+           "gdn_short_conv_bwd", "gdn_rmsnorm_bwd_workspace_size", "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd",
+           "gdn_quant_e4m3", "gdn_matmul_e4m3_workspace_size", "gdn_matmul_e4m3", "gdn_gated_ffn_fwd_workspace_size",
+           "gdn_gated_ffn_bwd_workspace_size", "gdn_gated_ffn_fwd", "gdn_gated_ffn_bwd",
+           "gdn_gated_ffn_e4m3_workspace_size", "gdn_gated_ffn_e4m3")
+GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU_TANH = 0, 1, 2
+GDN_SCALE_ROW, GDN_SCALE_GROUP, GDN_SCALE_BLOCK = 0, 1, 2
 GDN_OUT_SAME, GDN_OUT_E4M3 = 0, 1
 GDN_CONV_INPLACE_T = 16
 
@@ -81,6 +85,23 @@ class GdnRmsnormDesc(ctypes.Structure):
                 ("eps", ctypes.c_float), ("flags", ctypes.c_int32), ("reserved", ctypes.c_int32 * 4)]
 
 
+class GdnQuantDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("scales", ctypes.c_int32), ("transpose", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("reserved", ctypes.c_int32 * 4)]
+
+
+class GdnMatmulDesc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("out_dtype", ctypes.c_int32),
+                ("scales", ctypes.c_int32), ("flags", ctypes.c_int32), ("reserved", ctypes.c_int32 * 5)]
+
+
+class GdnFfnDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("K", ctypes.c_int64), ("F", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("out_type", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("reserved", ctypes.c_int32 * 4)]
+
+
 class GdnKernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int64), ("total_ms", ctypes.c_double)]
 
@@ -129,6 +150,7 @@ def load_library(path: str = LIB_PATH):
     lib.gdn_recurrent_fwd.restype = i32
     lib.gdn_recurrent_fwd.argtypes = [dp] + [vp] * 8 + [vp]
     sp, cp, rp = ctypes.POINTER(GdnScanDesc), ctypes.POINTER(GdnConvDesc), ctypes.POINTER(GdnRmsnormDesc)
+    mp, fp = ctypes.POINTER(GdnMatmulDesc), ctypes.POINTER(GdnFfnDesc)
     for name, args in (("gdn_gated_scan_fwd_workspace_size", [sp, ctypes.POINTER(sz)]),
                        ("gdn_gated_scan_bwd_workspace_size", [sp, ctypes.POINTER(sz)]),
                        ("gdn_gated_scan_states_size", [sp, ctypes.POINTER(sz)]),
@@ -139,7 +161,16 @@ def load_library(path: str = LIB_PATH):
                        ("gdn_short_conv_bwd", [cp] + [vp] * 11 + [sz, vp]),
                        ("gdn_rmsnorm_bwd_workspace_size", [rp, ctypes.POINTER(sz)]),
                        ("gdn_rmsnorm_fwd", [rp] + [vp] * 7),
-                       ("gdn_rmsnorm_bwd", [rp] + [vp] * 7 + [sz, vp])):
+                       ("gdn_rmsnorm_bwd", [rp] + [vp] * 7 + [sz, vp]),
+                       ("gdn_quant_e4m3", [ctypes.POINTER(GdnQuantDesc)] + [vp] * 4),
+                       ("gdn_matmul_e4m3_workspace_size", [mp, ctypes.POINTER(sz)]),
+                       ("gdn_matmul_e4m3", [mp] + [vp] * 6 + [sz, vp]),
+                       ("gdn_gated_ffn_fwd_workspace_size", [fp, ctypes.POINTER(sz)]),
+                       ("gdn_gated_ffn_bwd_workspace_size", [fp, ctypes.POINTER(sz)]),
+                       ("gdn_gated_ffn_fwd", [fp] + [vp] * 6 + [sz, vp]),
+                       ("gdn_gated_ffn_bwd", [fp] + [vp] * 9 + [sz, vp]),
+                       ("gdn_gated_ffn_e4m3_workspace_size", [fp, ctypes.POINTER(sz)]),
+                       ("gdn_gated_ffn_e4m3", [fp] + [vp] * 9 + [sz, vp])):
         getattr(lib, name).restype = i32
         getattr(lib, name).argtypes = args
     lib.gdn_profile_enable.restype = i32

@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build", "gdn")
 LIB = os.path.join(HERE, "libgdn.so")
 SOURCES = ["gdn_api.hip", "gdn_intra.hip", "gdn_recur.hip", "gdn_bwd.hip", "gdn_decode.hip", "gdn_norm.hip",
-           "gdn_layer_api.hip", "gdn_gscan.hip", "gdn_conv.hip", "gdn_rms.hip"]
+           "gdn_layer_api.hip", "gdn_gscan.hip", "gdn_conv.hip", "gdn_rms.hip",
+           "gdn_product_api.hip", "gdn_quant.hip", "gdn_mm8.hip", "gdn_ffn.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

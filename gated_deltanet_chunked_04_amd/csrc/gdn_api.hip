@@ -302,7 +302,8 @@ const char* const kKernelNames[kKCount] = {"tables", "intra", "cp_decide", "cp_p
                                            "recur_out", "recur_states", "bwd_cp_prepass", "bwd_cp_scan",
                                            "bwd_reverse", "bwd_chunk", "recurrent", "qk_l2norm_bwd", "fused_fwd",
                                            "gated_scan_fwd", "gated_scan_bwd", "short_conv_fwd", "short_conv_bwd",
-                                           "rmsnorm_fwd", "rmsnorm_bwd"};
+                                           "rmsnorm_fwd", "rmsnorm_bwd",
+                                           "quant_e4m3", "matmul_e4m3", "gated_ffn_fwd", "gated_ffn_bwd", "gated_ffn_e4m3"};
 struct Pending {
     int kid;
     hipEvent_t start, stop;

@@ -1,0 +1,146 @@
+// gdn_ffn.hip -- the gated feed-forward block:  g = x Wg^T, u = x Wu^T, h = act(g) u,  and its gradients
+//   dg = d_h u act'(g), du = d_h act(g),  dx = dg Wg + du Wu,  dWg = dg^T x, dWu = du^T x.
+// Gate and up are computed side by side by the same waves, so h is made where both sums are and neither is written
+// (`pre` keeps them in fp32 for the backward, which otherwise computes them again).
+#include "gdn_layer.h"
+#include "gdn_mm.h"
+#include "gdn_products.h"
+
+namespace gdn {
+
+namespace {
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+const uint8_t* u8(const void* p) { return static_cast<const uint8_t*>(p); }
+
+MmArgs block_args(const FfnArgs& a, int64_t size) {
+    MmArgs p{};
+    p.x[0] = u8(a.x);
+    p.w[0] = u8(a.wg);
+    p.w[1] = u8(a.wu);
+    p.ldx = p.ldw = a.K * size;
+    p.M = a.M;
+    p.N = a.F;
+    p.K = a.K;
+    p.segs = p.outs = 1;
+    p.out[0] = a.h;
+    p.ldo = a.F;
+    p.pre = a.pre;
+    p.act = a.act;
+    return p;
+}
+
+template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
+hipError_t run(const MmArgs& p, hipStream_t st) {
+    const int64_t blocks = mm_any_blocks(p.M, p.N, DUAL);
+    if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((k_mm_any<KIND, SC, XT, WT, DUAL, EPI, T>), dim3((unsigned)blocks, (unsigned)p.outs), dim3(256), 0, st, p);
+    return hipGetLastError();
+}
+
+// gradients of gate and up from the forward's values, 8 at a time
+template <typename T>
+__global__ __launch_bounds__(256) void k_ffn_act_bwd(MmArgs p) {
+    const int64_t per = (p.N + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= per * p.M) return;
+    const int64_t m = i / per, n = i % per * 8;
+    float a[8], u[8];
+    mm_load<float, 8>(p.pre + m * p.N + n, a, p.N - n);
+    mm_load<float, 8>(p.pre + (p.M + m) * p.N + n, u, p.N - n);
+    mm_gate<kMmFfnBwd, T>(p, m, n, a, u);
+}
+
+// memory rows of the gradients of gate and up in the workspace: whole vectors
+int64_t grad_ld(int64_t F, int64_t size) { return (F * size + 15) / 16 * 16 / size; }
+
+template <int KIND, typename T>
+hipError_t bwd(const FfnArgs& a, hipStream_t st) {
+    const int64_t size = sizeof(T), ldd = grad_ld(a.F, size);
+    void* d[2] = {a.ws, a.ws + align256((size_t)(a.M * ldd * size))};
+    if (a.M) {
+        MmArgs p = block_args(a, size);
+        p.out[0] = d[0];
+        p.out[1] = d[1];
+        p.ldo = ldd;
+        p.d_h = a.d_h;
+        if (a.pre) {
+            const int64_t blocks = ((a.F + 7) / 8 * a.M + 255) / 256;
+            if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
+            hipLaunchKernelGGL(k_ffn_act_bwd<T>, dim3((unsigned)blocks), dim3(256), 0, st, p);
+        } else if (hipError_t e = run<KIND, kMmPlain, false, false, true, kMmFfnBwd, T>(p, st)) {
+            return e;
+        }
+    }
+    if (a.dx && a.M) {
+        MmArgs p{};
+        for (int i = 0; i < 2; ++i) p.x[i] = u8(d[i]);
+        p.w[0] = u8(a.wg);
+        p.w[1] = u8(a.wu);
+        p.ldx = ldd * size;
+        p.ldw = a.K * size;
+        p.M = a.M;
+        p.N = a.K;
+        p.K = a.F;
+        p.segs = 2;
+        p.outs = 1;
+        p.out[0] = a.dx;
+        p.ldo = a.K;
+        if (hipError_t e = run<KIND, kMmPlain, false, true, false, kMmOut, T>(p, st)) return e;
+    }
+    if (a.dwg) {
+        MmArgs p{};
+        for (int i = 0; i < 2; ++i) p.x[i] = u8(d[i]);
+        p.w[0] = u8(a.x);
+        p.ldx = ldd * size;
+        p.ldw = a.K * size;
+        p.M = a.F;
+        p.N = a.K;
+        p.K = a.M;
+        p.segs = 1;
+        p.outs = 2;
+        p.out[0] = a.dwg;
+        p.out[1] = a.dwu;
+        p.ldo = a.K;
+        if (hipError_t e = run<KIND, kMmPlain, true, true, false, kMmOut, T>(p, st)) return e;
+    }
+    return hipGetLastError();
+}
+
+template <int KIND, typename T>
+hipError_t ffn8(const FfnArgs& a, void* h, hipStream_t st) {
+    MmArgs p = block_args(a, 1);
+    p.xs = a.xs;
+    p.ws[0] = a.gs;
+    p.ws[1] = a.us;
+    p.kb = (a.K + 127) / 128;
+    p.out[0] = h;
+    return run<KIND, kMmBlock, false, false, true, kMmFfn, T>(p, st);
+}
+
+}  // namespace
+
+size_t ffn_fwd_ws(int64_t M, int64_t K, int64_t F, int dtype) { return 0; }
+size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
+    const int64_t size = dtype == 1 ? 4 : 2;
+    return 2 * align256((size_t)(M * grad_ld(F, size) * size));
+}
+size_t ffn8_ws(int64_t M, int64_t K, int64_t F, int dtype, bool quant) { return quant ? (size_t)(M * F * 4) : 0; }
+
+hipError_t launch_ffn_fwd(const FfnArgs& a, int dtype, hipStream_t st) {
+    if (a.M == 0) return hipSuccess;
+    if (dtype == 1) return run<kMmF32, kMmPlain, false, false, true, kMmFfn, float>(block_args(a, 4), st);
+    return run<kMmBf16, kMmPlain, false, false, true, kMmFfn, bf16_t>(block_args(a, 2), st);
+}
+hipError_t launch_ffn_bwd(const FfnArgs& a, int dtype, hipStream_t st) {
+    return dtype == 1 ? bwd<kMmF32, float>(a, st) : bwd<kMmBf16, bf16_t>(a, st);
+}
+hipError_t launch_ffn8(const FfnArgs& a, int dtype, hipStream_t st) {
+    if (a.M == 0) return hipSuccess;
+    if (!a.hs) return dtype == 1 ? ffn8<kMmF8x, float>(a, a.h, st) : ffn8<kMmF8, bf16_t>(a, a.h, st);
+    if (hipError_t e = ffn8<kMmF8x, float>(a, a.ws, st)) return e;
+    const QuantArgs q{a.M, a.F, a.ws, static_cast<uint8_t*>(a.h), a.hs};
+    return launch_quant(q, 1, 1, false, st);
+}
+
+}  // namespace gdn

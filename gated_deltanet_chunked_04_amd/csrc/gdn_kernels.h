@@ -390,7 +390,8 @@ hipError_t launch_decode(const DecodeArgs& a, int dtype, int K, int V, hipStream
 // launches of one operator, count under.
 enum KernelId { kKTables = 0, kKIntra, kKDecide, kKPrepass, kKScan, kKRecurOut, kKRecurStates,
                 kKBwdPrepass, kKBwdScan, kKBwdReverse, kKBwdChunk, kKDecode, kKL2NormBwd, kKFused,
-                kKGScanFwd, kKGScanBwd, kKConvFwd, kKConvBwd, kKRmsFwd, kKRmsBwd, kKCount };
+                kKGScanFwd, kKGScanBwd, kKConvFwd, kKConvBwd, kKRmsFwd, kKRmsBwd,
+                kKQuant, kKMatmul8, kKFfnFwd, kKFfnBwd, kKFfn8, kKCount };
 // Brackets the launches in its scope with two events on `st` while profiling is on.
 struct ProfScope {
     int kid;

@@ -1,0 +1,389 @@
+// gdn_mm.h -- matrix products on the matrix cores, shared by the e4m3 product (gdn_mm8.hip) and the gated
+// feed-forward block (gdn_ffn.hip): operands, tiles in LDS, fragments, the loop over the contraction.
+//
+// Everything is  Y[m, n] = sum_k X[m, k] W[n, k]  with X on the lanes and W on the registers of a 16x16 accumulator
+// tile (gdn_common.h: lane l holds rows 4 gq .. 4 gq + 3 of column ln; W's rows are the tile's rows and X's its
+// columns), so a lane holds outputs of one m and, by the choice of which W rows make up a tile, runs of neighbouring n.
+//
+// A step of the contraction is 128 bytes of a row (64 bf16, 32 fp32, 128 e4m3 values: one scale of the e4m3 product),
+// eight 16-byte chunks. Lane group gq takes chunks gq and gq + 4 of its row: which values of the contraction a matrix
+// instruction sees in which slot does not matter as long as both operands agree.
+//
+// An operand lies in memory either by its rows (the contraction is contiguous) or turned (the contraction walks over
+// memory rows: the gradients' products). Tiles keep that order in LDS; a turned bf16 tile is read by transposing reads.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdn_common.h"
+#include "gdn_e4m3.h"
+#include "gdn_vec.h"
+
+namespace gdn {
+
+// kMmF8 multiplies e4m3 by the 8-bit matrix instruction, kMmF8x widens e4m3 to bf16 (exact) first. The 8-bit
+// instruction adds products in groups of eight that it aligns to the largest of them and cuts about 13 bits below it
+// (measured: a product of 1 beside one of 448^2 in its group is lost; on quantised normal data its sums of 128 are off
+// by 1.5e-5 in the 2-norm, the widened ones by 1e-8). That is a hundredth of a bf16 output's own rounding, so kMmF8 is
+// for outputs in bf16 and kMmF8x for what is kept in 32 bits: fp32 outputs and the scales of an e4m3 output.
+enum MmKind { kMmBf16 = 0, kMmF32 = 1, kMmF8 = 2, kMmF8x = 3 };
+template <int KIND> constexpr int mm_size() { return KIND == kMmBf16 ? 2 : (KIND == kMmF32 ? 4 : 1); }
+constexpr int kMmStep = 128;  // bytes of a row per step
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// What a lane feeds for a step: its two chunks, in the form that the matrix instruction takes.
+template <int KIND> struct MmFrag;
+template <> struct MmFrag<kMmBf16> {
+    bf16x8_t v[2];
+    __device__ __forceinline__ void set(u32x4 a, u32x4 b) { v[0] = __builtin_bit_cast(bf16x8_t, a), v[1] = __builtin_bit_cast(bf16x8_t, b); }
+};
+template <> struct MmFrag<kMmF32> {
+    f32x4 v[2];
+    __device__ __forceinline__ void set(u32x4 a, u32x4 b) { v[0] = __builtin_bit_cast(f32x4, a), v[1] = __builtin_bit_cast(f32x4, b); }
+};
+template <> struct MmFrag<kMmF8> {
+    i32x8 v;
+    __device__ __forceinline__ void set(u32x4 a, u32x4 b) { v = i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w}; }
+};
+template <> struct MmFrag<kMmF8x> {
+    bf16x8_t v[4];
+    __device__ __forceinline__ void widen(int at, uint32_t lo, uint32_t hi) {
+        const bf16x2_t p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false), q = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
+        const bf16x2_t r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false), s = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+        v[at] = bf16x8_t{p.x, p.y, q.x, q.y, r.x, r.y, s.x, s.y};
+    }
+    __device__ __forceinline__ void set(u32x4 a, u32x4 b) { widen(0, a.x, a.y), widen(1, a.z, a.w), widen(2, b.x, b.y), widen(3, b.z, b.w); }
+};
+__device__ __forceinline__ f32x4 mm_mma(const MmFrag<kMmBf16>& w, const MmFrag<kMmBf16>& x, f32x4 c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[i], x.v[i], c, 0, 0, 0);
+    return c;
+}
+__device__ __forceinline__ f32x4 mm_mma(const MmFrag<kMmF32>& w, const MmFrag<kMmF32>& x, f32x4 c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(w.v[i / 4][i % 4], x.v[i / 4][i % 4], c, 0, 0, 0);
+    return c;
+}
+__device__ __forceinline__ f32x4 mm_mma(const MmFrag<kMmF8>& w, const MmFrag<kMmF8>& x, f32x4 c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x.v, c, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mm_mma(const MmFrag<kMmF8x>& w, const MmFrag<kMmF8x>& x, f32x4 c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[i], x.v[i], c, 0, 0, 0);
+    return c;
+}
+
+// ---- tiles in LDS ---------------------------------------------------------------------------
+// By rows: [R][128 bytes], chunk c of row r at c ^ key(r), so that 8 lanes that read one chunk of 8 rows meet
+// different banks. kFar: the tile's rows r come in fours that lie 2^kFar apart (the column order of W's tiles).
+// Turned: [steps][R elements].
+template <int kFar> __device__ __forceinline__ int mm_key(int r) { return (r & 3) | ((((r >> 2) ^ (r >> kFar)) & 1) << 2); }
+constexpr int kNear = 6;  // rows side by side
+template <int kFar> __device__ __forceinline__ int mm_at(int r, int c) { return r * kMmStep + ((c ^ mm_key<kFar>(r)) << 4); }
+
+// Turned: chunk c of 16 bytes of memory row k; XOR over units of 32 bytes spreads the 16 rows that a transposing read
+// meets (0-3, 8-11, 16-19, 24-27 of a half step) over the banks.
+template <int R, int E> __device__ __forceinline__ int mm_turn_key(int k) {
+    constexpr int kUnits = R * E / 32;
+    return (((k & 3) | ((k >> 3) & 3) << 2) & (kUnits - 1)) << 1;
+}
+template <int R, int E> __device__ __forceinline__ int mm_turn_at(int k, int c) { return k * R * E + ((c ^ mm_turn_key<R, E>(k)) << 4); }
+
+// The lane's two chunks of row r.
+template <int KIND, int kFar>
+__device__ __forceinline__ void mm_read(MmFrag<KIND>& f, const uint8_t* tile, int r) {
+    const int gq = threadIdx.x >> 4 & 3;
+    f.set(*reinterpret_cast<const u32x4*>(tile + mm_at<kFar>(r, gq)), *reinterpret_cast<const u32x4*>(tile + mm_at<kFar>(r, gq + 4)));
+}
+// The same from a turned tile of R rows, for 16 of them: r0 + far * g + i, lane ln = 4 g + i.
+template <int KIND, int R>
+__device__ __forceinline__ void mm_read_turned(MmFrag<KIND>& f, const uint8_t* tile, int r0, int far) {
+    const int ln = threadIdx.x & 15, gq = threadIdx.x >> 4 & 3;
+    if constexpr (KIND == kMmBf16) {
+        const int col = r0 + far * (ln & 3);  // four neighbouring columns of memory row k
+        u32x2 h[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int k = (q >> 1) * 32 + gq * 8 + (q & 1) * 4 + (ln >> 2);
+            h[q] = ds_read_tr16(reinterpret_cast<const bf16_t*>(tile + mm_turn_at<R, 2>(k, col >> 3) + (col & 7) * 2));
+        }
+        f.set(u32x4{h[0].x, h[0].y, h[1].x, h[1].y}, u32x4{h[2].x, h[2].y, h[3].x, h[3].y});
+    } else {
+        const int col = r0 + far * (ln >> 2) + (ln & 3);
+        u32x4 h[2];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int k = (q >> 2) * 16 + gq * 4 + (q & 3);
+            h[q >> 2][q & 3] = *reinterpret_cast<const uint32_t*>(tile + mm_turn_at<R, 4>(k, col >> 2) + (col & 3) * 4);
+        }
+        f.set(h[0], h[1]);
+    }
+}
+
+// ---- memory to LDS --------------------------------------------------------------------------
+// 16 bytes at p + off of a memory row of `limit` bytes, zeros behind it; at any address.
+template <int E>
+__device__ __forceinline__ u32x4 mm_chunk(const uint8_t* p, int64_t off, int64_t limit) {
+    u32x4 v = {0, 0, 0, 0};
+    if (off + 16 <= limit) {
+        __builtin_memcpy(&v, p + off, 16);
+    } else if (off < limit) {
+        const int n = (int)(limit - off);
+#pragma unroll
+        for (int i = 0; i < 16; i += E)
+            if (i < n) {
+                uint32_t x = 0;
+                __builtin_memcpy(&x, p + off + i, E);
+                v[i / 4] |= x << (8 * (i % 4));
+            }
+    }
+    return v;
+}
+
+// An operand's tile of R rows from row r0 on, in chunks: which memory row and byte a chunk has, and where it goes.
+// Rows behind the operand's last one repeat it (they reach outputs that are not stored); steps behind the contraction
+// are zeros.
+template <int E, int R, bool kTurned, int kFar>
+struct MmTile {
+    static constexpr int kChunks = R * 8;
+    static constexpr int kWide = R * E / 16;  // chunks of a turned memory row
+    static __device__ __forceinline__ int lds(int i) {
+        return kTurned ? mm_turn_at<R, E>(i / kWide, i % kWide) : mm_at<kFar>(i >> 3, i & 7);
+    }
+    static __device__ __forceinline__ u32x4 load(const uint8_t* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t K, int i) {
+        if constexpr (kTurned) {
+            const int64_t k = k0 + i / kWide;
+            return k < K ? mm_chunk<E>(p + k * ld, r0 * E + 16 * (i % kWide), rows * E) : u32x4{0, 0, 0, 0};
+        } else {
+            const int64_t r = r0 + (i >> 3);
+            return mm_chunk<E>(p + (r < rows ? r : rows - 1) * ld, k0 * E + 16 * (i & 7), K * E);
+        }
+    }
+};
+
+// ---- products -------------------------------------------------------------------------------
+enum MmScales { kMmPlain = 0, kMmBlock = 1, kMmGroup = 2, kMmRow = 3 };
+
+struct MmArgs {
+    const uint8_t* x[2];  // per segment of the contraction (dx: d_gate, d_up), or per output (dw)
+    const uint8_t* w[2];  // per segment, or gate and up side by side (the block's forward)
+    int64_t ldx, ldw;     // bytes between two memory rows
+    int64_t M, N, K;      // rows of X, of W (of each where there are two side by side), contraction of a segment
+    int32_t segs;         // segments of the contraction
+    int32_t outs;         // outputs, each with its x (dw)
+    const float* xs;      // scales of e4m3 operands: [M, kb] (row: [M])
+    const float* ws[2];   // block: [ceil(N/128), kb], group: [N, kb], row: [N]
+    int64_t kb;           // scales of a row: ceil(K / 128)
+    void* out[2];         // outputs [M, N] with ldo elements a row
+    int64_t ldo;
+    const void* d_h;      // [M, N]: the gradient that enters the block's backward
+    float* pre;           // [2, M, N] gate and up in fp32, or null
+    int32_t act;          // 1 silu, 2 gelu_tanh
+};
+
+// sigmoid and the slope of its argument: silu(a) = a sigmoid(a), gelu_tanh(a) = a sigmoid(2 c (a + 0.044715 a^3)).
+struct Act {
+    float f, df;  // activation and derivative
+    __device__ __forceinline__ Act(float a, int act, bool grad) {
+        constexpr float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+        const float a2 = a * a, p = act == 1 ? a : c * a * fmaf(0.044715f, a2, 1.f);
+        const float s = __builtin_amdgcn_rcpf(1.f + fast_exp(-p));
+        f = a * s;
+        if (grad) {
+            const float dp = act == 1 ? 1.f : c * fmaf(3.f * 0.044715f, a2, 1.f), t = s * (1.f - s);
+            df = t == 0.f ? s : fmaf(a * t, dp, s);  // (where s is 0 or 1 the slope may have overflowed)
+        } else {
+            df = 0.f;
+        }
+    }
+};
+
+// N consecutive outputs at p, of which those in front of `n` exist.
+template <typename T, int N>
+__device__ __forceinline__ void mm_store(T* p, const float (&v)[N], int64_t n) {
+    if (n >= N) {
+        Raw<T, N> r;
+        r.set(v);
+        store_raw<T, N>(p, r);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) p[i] = Elem<T>::from_f(v[i]);
+    }
+}
+template <typename T, int N>
+__device__ __forceinline__ void mm_load(const T* p, float (&v)[N], int64_t n) {
+    if (n >= N) {
+        const Raw<T, N> r = load_raw<T, N>(p);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = r.get(i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = i < n ? Elem<T>::to_f(p[i]) : 0.f;
+    }
+}
+
+// What is done with a lane's sums. kMmOut: y = sums (with kMmRow, times the rows' scales). kMmFfn: h = act(gate) up, and
+// gate and up themselves where `pre` is given. kMmFfnBwd: the gradients of gate and up from d_h.
+enum MmEpi { kMmOut = 0, kMmFfn = 1, kMmFfnBwd = 2 };
+
+// 8 columns of the block at (m, n).
+template <int EPI, typename T>
+__device__ __forceinline__ void mm_gate(const MmArgs& p, int64_t m, int64_t n, const float (&a)[8], const float (&u)[8]) {
+    const int64_t left = p.N - n;
+    if constexpr (EPI == kMmFfn) {
+        float h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = Act(a[i], p.act, false).f * u[i];
+        mm_store<T, 8>(static_cast<T*>(p.out[0]) + m * p.ldo + n, h, left);
+        if (p.pre) {
+            mm_store<float, 8>(p.pre + m * p.N + n, a, left);
+            mm_store<float, 8>(p.pre + (p.M + m) * p.N + n, u, left);
+        }
+    } else {
+        float d[8], da[8], du[8];
+        mm_load<T, 8>(static_cast<const T*>(p.d_h) + m * p.N + n, d, left);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const Act f(a[i], p.act, true);
+            da[i] = d[i] * u[i] * f.df;
+            du[i] = d[i] * f.f;
+        }
+        // rounded to the inputs' type: they are operands of the products behind
+        mm_store<T, 8>(static_cast<T*>(p.out[0]) + m * p.ldo + n, da, left);
+        mm_store<T, 8>(static_cast<T*>(p.out[1]) + m * p.ldo + n, du, left);
+    }
+}
+
+// The sums of a wave's MT x NT tiles, scaled where the operands are e4m3. Shared by the kernels below.
+template <int KIND, int SC, bool DUAL, int MT, int NT>
+struct MmSums {
+    static constexpr bool kScaled = SC == kMmBlock || SC == kMmGroup;
+    f32x4 acc[MT][NT] = {};
+    // One step: x and w fragments; sx[mt] the scale of the lane's X row, sw of W's rows: one for all (block; gate and
+    // up where there are two), or one for each of the lane's columns (group).
+    __device__ __forceinline__ void step(const MmFrag<KIND> (&x)[MT], const MmFrag<KIND> (&w)[NT], const float (&sx)[MT], const float (&sw)[NT][4]) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                if constexpr (kScaled) {
+                    const f32x4 c = mm_mma(w[j], x[t], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(c[i], SC == kMmBlock ? sx[t] * sw[j][0] : sx[t] * sw[j][i], acc[t][j][i]);
+                } else {
+                    acc[t][j] = mm_mma(w[j], x[t], acc[t][j]);
+                }
+            }
+    }
+    // Hands the lane's outputs on: X's row m0 + 16 t + ln, W's columns n0 + 64 g + 16 gq .. + 15 (two sides: n0 + 32 g
+    // + 8 gq .. + 7 of each).
+    template <int EPI, typename T>
+    __device__ __forceinline__ void finish(const MmArgs& p, T* out, int64_t m0, int64_t n0) const {
+        const int ln = threadIdx.x & 15, gq = threadIdx.x >> 4 & 3;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            const int64_t m = m0 + 16 * t + ln;
+            if (m >= p.M) continue;
+            const float sx = SC == kMmRow ? p.xs[m] : 1.f;
+#pragma unroll
+            for (int g = 0; g < NT / 4; ++g) {
+                float v[2][8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[j >> 1][(j & 1) * 4 + i] = acc[t][4 * g + j][i];
+                if constexpr (DUAL) {
+                    const int64_t n = n0 + 32 * g + 8 * gq;
+                    if (n < p.N) mm_gate<EPI, T>(p, m, n, v[0], v[1]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int64_t n = n0 + 64 * g + 16 * gq + 8 * h;
+                        if (SC == kMmRow)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[h][i] *= sx * p.ws[0][n + i < p.N ? n + i : p.N - 1];
+                        if (n < p.N) mm_store<T, 8>(out + m * p.ldo + n, v[h], p.N - n);
+                    }
+                }
+            }
+        }
+    }
+};
+
+// 128 x 128 outputs (two sides: 128 x 64 of each) by four waves of 64 x 64, any sizes and addresses: chunks go through
+// registers, one tile of each operand in LDS.
+template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
+__global__ __launch_bounds__(256) void k_mm_any(MmArgs p) {
+    constexpr int E = mm_size<KIND>(), kFar = DUAL ? 3 : 4, MT = 4, NT = 4;
+    constexpr int kSteps = kMmStep / E;  // of the contraction per step
+    constexpr int kCols = DUAL ? 64 : 128;
+    using X = MmTile<E, 128, XT, kNear>;
+    using W = MmTile<E, kCols, WT, kFar>;
+    __shared__ __align__(16) uint8_t xt[128 * kMmStep], wt[128 * kMmStep];
+    const int wave = wave_id(), wm = wave & 1, wn = wave >> 1;
+    const int ln = threadIdx.x & 15, gq = threadIdx.x >> 4 & 3;
+    const int64_t tm = (p.M + 127) / 128;
+    const int64_t m0 = (blockIdx.x % tm) * 128, n0 = (blockIdx.x / tm) * kCols;
+    const int z = p.outs > 1 ? (int)blockIdx.y : 0;
+    const int64_t per = (p.K + kSteps - 1) / kSteps;
+    MmSums<KIND, SC, DUAL, MT, NT> sums;
+    for (int64_t it = 0; it < per * p.segs; ++it) {
+        const int seg = (int)(it / per);
+        const int64_t kt = it % per, k0 = kt * kSteps;
+        u32x4 cx[4], cw[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cx[i] = X::load(p.x[XT ? z : seg], p.ldx, m0, p.M, k0, p.K, threadIdx.x + 256 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = threadIdx.x + 256 * i;
+            if constexpr (DUAL) cw[i] = W::load(p.w[i / 2], p.ldw, n0, p.N, k0, p.K, c - 512 * (i / 2));
+            else cw[i] = W::load(p.w[seg], p.ldw, n0, p.N, k0, p.K, c);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = threadIdx.x + 256 * i;
+            *reinterpret_cast<u32x4*>(xt + X::lds(c)) = cx[i];
+            if constexpr (DUAL) *reinterpret_cast<u32x4*>(wt + 64 * kMmStep * (i / 2) + W::lds(c - 512 * (i / 2))) = cw[i];
+            else *reinterpret_cast<u32x4*>(wt + W::lds(c)) = cw[i];
+        }
+        __syncthreads();
+        MmFrag<KIND> fx[MT], fw[NT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            if constexpr (XT) mm_read_turned<KIND, 128>(fx[t], xt, wm * 64 + 16 * t, 4);
+            else mm_read<KIND, kNear>(fx[t], xt, wm * 64 + 16 * t + ln);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            if constexpr (WT) mm_read_turned<KIND, 128>(fw[j], wt, wn * 64 + 4 * j, 16);
+            else if constexpr (DUAL) mm_read<KIND, kFar>(fw[j], wt + 64 * kMmStep * (j / 2), wn * 32 + 4 * (j % 2) + 8 * (ln >> 2) + (ln & 3));
+            else mm_read<KIND, kFar>(fw[j], wt, wn * 64 + 4 * j + 16 * (ln >> 2) + (ln & 3));
+        }
+        float sx[MT], sw[NT][4];
+        if constexpr (MmSums<KIND, SC, DUAL, MT, NT>::kScaled) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const int64_t m = m0 + wm * 64 + 16 * t + ln;
+                sx[t] = p.xs[(m < p.M ? m : p.M - 1) * p.kb + kt];
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t n = n0 + wn * 64 + 16 * gq + 4 * j + i;
+                    if (SC == kMmGroup) sw[j][i] = p.ws[0][(n < p.N ? n : p.N - 1) * p.kb + kt];
+                    else sw[j][i] = p.ws[DUAL ? j / 2 : 0][n0 / 128 * p.kb + kt];
+                }
+        }
+        sums.step(fx, fw, sx, sw);
+    }
+    sums.template finish<EPI, T>(p, static_cast<T*>(p.out[z]), m0 + wm * 64, n0 + wn * (kCols / 2));
+}
+
+inline int64_t mm_any_blocks(int64_t M, int64_t N, bool dual) { return ((M + 127) / 128) * ((N + (dual ? 63 : 127)) / (dual ? 64 : 128)); }
+
+}  // namespace gdn
