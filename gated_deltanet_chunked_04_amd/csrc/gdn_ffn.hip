@@ -33,6 +33,11 @@ MmArgs block_args(const FfnArgs& a, int64_t size) {
 
 template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
 hipError_t run(const MmArgs& p, hipStream_t st) {
+    if (mm_fits(p)) {
+        constexpr int BM = KIND == kMmF8x || KIND == kMmF32 ? 128 : 256;
+        hipLaunchKernelGGL((k_mm<KIND, SC, XT, WT, DUAL, EPI, T, BM>), dim3((unsigned)(mm_blocks(p.M, p.N, DUAL, BM) * p.outs)), dim3(512), 0, st, p);
+        return hipGetLastError();
+    }
     const int64_t blocks = mm_any_blocks(p.M, p.N, DUAL);
     if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((k_mm_any<KIND, SC, XT, WT, DUAL, EPI, T>), dim3((unsigned)blocks, (unsigned)p.outs), dim3(256), 0, st, p);
@@ -51,12 +56,12 @@ __global__ __launch_bounds__(256) void k_ffn_act_bwd(MmArgs p) {
     mm_gate<kMmFfnBwd, T>(p, m, n, a, u);
 }
 
-// memory rows of the gradients of gate and up in the workspace: whole vectors
-int64_t grad_ld(int64_t F, int64_t size) { return (F * size + 15) / 16 * 16 / size; }
+// columns of the gradients of gate and up in the workspace: whole vectors, zeros behind F
+int64_t grad_ld(int64_t F) { return (F + 7) / 8 * 8; }
 
 template <int KIND, typename T>
 hipError_t bwd(const FfnArgs& a, hipStream_t st) {
-    const int64_t size = sizeof(T), ldd = grad_ld(a.F, size);
+    const int64_t size = sizeof(T), ldd = grad_ld(a.F);
     void* d[2] = {a.ws, a.ws + align256((size_t)(a.M * ldd * size))};
     if (a.M) {
         MmArgs p = block_args(a, size);
@@ -123,7 +128,7 @@ hipError_t ffn8(const FfnArgs& a, void* h, hipStream_t st) {
 size_t ffn_fwd_ws(int64_t M, int64_t K, int64_t F, int dtype) { return 0; }
 size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
     const int64_t size = dtype == 1 ? 4 : 2;
-    return 2 * align256((size_t)(M * grad_ld(F, size) * size));
+    return 2 * align256((size_t)(M * grad_ld(F) * size));
 }
 size_t ffn8_ws(int64_t M, int64_t K, int64_t F, int dtype, bool quant) { return quant ? (size_t)(M * F * 4) : 0; }
 

@@ -248,12 +248,13 @@ __device__ __forceinline__ void mm_gate(const MmArgs& p, int64_t m, int64_t n, c
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const Act f(a[i], p.act, true);
-            da[i] = d[i] * u[i] * f.df;
-            du[i] = d[i] * f.f;
+            da[i] = i < left ? d[i] * u[i] * f.df : 0.f;
+            du[i] = i < left ? d[i] * f.f : 0.f;
         }
-        // rounded to the inputs' type: they are operands of the products behind
-        mm_store<T, 8>(static_cast<T*>(p.out[0]) + m * p.ldo + n, da, left);
-        mm_store<T, 8>(static_cast<T*>(p.out[1]) + m * p.ldo + n, du, left);
+        // rounded to the inputs' type: they are operands of the products behind, which take whole vectors of their rows
+        // (ldo is a multiple of 8) and multiply what lies behind column N by zero
+        mm_store<T, 8>(static_cast<T*>(p.out[0]) + m * p.ldo + n, da, 8);
+        mm_store<T, 8>(static_cast<T*>(p.out[1]) + m * p.ldo + n, du, 8);
     }
 }
 
@@ -262,21 +263,19 @@ template <int KIND, int SC, bool DUAL, int MT, int NT>
 struct MmSums {
     static constexpr bool kScaled = SC == kMmBlock || SC == kMmGroup;
     f32x4 acc[MT][NT] = {};
-    // One step: x and w fragments; sx[mt] the scale of the lane's X row, sw of W's rows: one for all (block; gate and
-    // up where there are two), or one for each of the lane's columns (group).
-    __device__ __forceinline__ void step(const MmFrag<KIND> (&x)[MT], const MmFrag<KIND> (&w)[NT], const float (&sx)[MT], const float (&sw)[NT][4]) {
+    // One step for X tile t; sx: the scale of the lane's X row, sw of W's rows: one for all (block; gate and up where
+    // there are two), or one for each of the lane's columns (group).
+    __device__ __forceinline__ void step(int t, const MmFrag<KIND>& x, const MmFrag<KIND> (&w)[NT], float sx, const float (&sw)[NT][4]) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j) {
+            if constexpr (kScaled) {
+                const f32x4 c = mm_mma(w[j], x, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                if constexpr (kScaled) {
-                    const f32x4 c = mm_mma(w[j], x[t], f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(c[i], SC == kMmBlock ? sx[t] * sw[j][0] : sx[t] * sw[j][i], acc[t][j][i]);
-                } else {
-                    acc[t][j] = mm_mma(w[j], x[t], acc[t][j]);
-                }
+                for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(c[i], SC == kMmBlock ? sx * sw[j][0] : sx * sw[j][i], acc[t][j][i]);
+            } else {
+                acc[t][j] = mm_mma(w[j], x, acc[t][j]);
             }
+        }
     }
     // Hands the lane's outputs on: X's row m0 + 16 t + ln, W's columns n0 + 64 g + 16 gq .. + 15 (two sides: n0 + 32 g
     // + 8 gq .. + 7 of each).
@@ -379,9 +378,201 @@ __global__ __launch_bounds__(256) void k_mm_any(MmArgs p) {
                     else sw[j][i] = p.ws[DUAL ? j / 2 : 0][n0 / 128 * p.kb + kt];
                 }
         }
-        sums.step(fx, fw, sx, sw);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) sums.step(t, fx[t], fw, sx[t], sw);
     }
     sums.template finish<EPI, T>(p, static_cast<T*>(p.out[z]), m0 + wm * 64, n0 + wn * (kCols / 2));
+}
+
+// ---- the same, memory to LDS without registers ----------------------------------------------
+// 16 (or 4) bytes of each lane from base + off to LDS at lds + 16 (4) lane. In assembly: the compiler takes the builtin for
+// a write that every later LDS read has to wait for. Counted by vmcnt like a load; no register is written. (M0 needs a
+// wait state before the load that uses it.)
+__device__ __forceinline__ uint64_t mm_uniform(const void* p) {
+    const uint64_t a = (uint64_t)(uintptr_t)p;
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a) | (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32;
+}
+__device__ __forceinline__ void mm_dma16(uint32_t lds, const uint8_t* base, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(off), "s"(mm_uniform(base)) : "memory");
+}
+__device__ __forceinline__ void mm_dma4(uint32_t lds, const void* base, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(off), "s"(mm_uniform(base)) : "memory");
+}
+// All of this wave's loads to LDS have landed and its LDS reads are done; then the workgroup meets.
+__device__ __forceinline__ void mm_meet() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+__device__ __forceinline__ uint32_t mm_lds(const void* p) { return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p; }
+
+// Which tile a workgroup takes. Workgroups go round robin over the 8 XCDs, each with an L2 of its own: an XCD gets a
+// run of tiles, in columns of 8 X tiles, so that the 32 tiles it works on at a time share 8 X and 4 W tiles.
+struct MmPlace {
+    int32_t m, n, rest;
+    __device__ __forceinline__ MmPlace(int32_t id, int32_t total, int32_t tm, int32_t tn) {
+        const int32_t xcd = id % 8, per = total / 8, more = total % 8;
+        int32_t l = xcd * per + min(xcd, more) + id / 8;
+        rest = l / (tm * tn);
+        l -= rest * tm * tn;
+        const int32_t group = l / (8 * tn), high = min(8, tm - 8 * group);
+        l -= group * 8 * tn;
+        m = 8 * group + l % high;
+        n = l / high;
+    }
+};
+
+// BM x 256 outputs (two sides: BM x 128 of each) by eight waves of BM/2 x 64; two steps' tiles in LDS, the next one on
+// its way while one is multiplied. Memory rows and addresses are multiples of 16 bytes, 256 rows within 2^31 bytes.
+template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T, int BM>
+__global__ __launch_bounds__(512) void k_mm(MmArgs p) {
+    constexpr int E = mm_size<KIND>(), kFar = DUAL ? 3 : 4, MT = BM / 32, NT = 4, BN = 256;
+    constexpr int kSteps = kMmStep / E;
+    constexpr int kCols = DUAL ? 128 : 256;
+    constexpr int kXB = BM * kMmStep, kWB = BN * kMmStep;
+    constexpr int kXC = BM * 8 / 512, kWC = 4;  // chunks of a thread
+    using Sums = MmSums<KIND, SC, DUAL, MT, NT>;
+    using X = MmTile<E, BM, XT, kNear>;
+    using W = MmTile<E, kCols, WT, kFar>;
+    constexpr int kSB = Sums::kScaled ? (BM + (SC == kMmGroup ? 256 : 0)) * 4 : 0;
+    constexpr int kStage = kXB + kWB + kSB;
+    __shared__ __align__(128) uint8_t sh[2 * kStage];
+    const int wave = wave_id(), lane = threadIdx.x & 63, wm = wave & 1, wn = wave >> 1;
+    const int ln = lane & 15, gq = lane >> 4;
+    const int32_t tm = (int32_t)((p.M + BM - 1) / BM), tn = (int32_t)((p.N + kCols - 1) / kCols);
+    const MmPlace at(blockIdx.x, gridDim.x, tm, tn);
+    const int64_t m0 = (int64_t)at.m * BM, n0 = (int64_t)at.n * kCols;
+    const int z = p.outs > 1 ? at.rest : 0;
+    const int32_t per = (int32_t)((p.K + kSteps - 1) / kSteps), total = per * p.segs;
+
+    // Chunks behind an operand's last row or column repeat its last one (which starts in it, so it lies at or behind the
+    // tile's start; a memory row is whole chunks).
+    // A thread's chunk i of a tile is chunk threadIdx.x + 512 i as LDS has them; which of memory's that is, is the XOR undone.
+    uint32_t xo[kXC], wo[kWC];
+    int xk[kXC], wk[kWC];  // its place along the contraction: bytes of a row, or rows
+#pragma unroll
+    for (int i = 0; i < kXC; ++i) {
+        const int c = threadIdx.x + 512 * i;
+        if constexpr (XT) {
+            const int k = c / X::kWide, b = ((c % X::kWide) ^ mm_turn_key<BM, E>(k)) * 16;
+            const int64_t col = m0 * E + b;
+            xk[i] = k;
+            xo[i] = (uint32_t)(k * p.ldx) + (uint32_t)(min(col, (p.M * E - 1) / 16 * 16) - m0 * E);
+        } else {
+            const int r = c >> 3, b = ((c & 7) ^ mm_key<kNear>(r)) * 16;
+            xk[i] = b;
+            xo[i] = (uint32_t)((m0 + r < p.M ? r : p.M - 1 - m0) * p.ldx) + b;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kWC; ++i) {
+        const int c = threadIdx.x + 512 * (DUAL ? i % 2 : i);
+        if constexpr (WT) {
+            const int k = c / W::kWide, b = ((c % W::kWide) ^ mm_turn_key<kCols, E>(k)) * 16;
+            const int64_t col = n0 * E + b;
+            wk[i] = k;
+            wo[i] = (uint32_t)(k * p.ldw) + (uint32_t)(min(col, (p.N * E - 1) / 16 * 16) - n0 * E);
+        } else {
+            const int r = c >> 3, b = ((c & 7) ^ mm_key<kFar>(r)) * 16;
+            wk[i] = b;
+            wo[i] = (uint32_t)((n0 + r < p.N ? r : p.N - 1 - n0) * p.ldw) + b;
+        }
+    }
+    uint32_t so = 0;
+    if constexpr (Sums::kScaled) {
+        const bool far = threadIdx.x >= BM;
+        const int r = threadIdx.x - (far ? BM : 0);
+        so = (uint32_t)((far ? (n0 + r < p.N ? r : p.N - 1 - n0) : (m0 + r < p.M ? r : p.M - 1 - m0)) * p.kb) * 4;
+    }
+    const uint32_t lds0 = mm_lds(sh) + wave * 1024;
+
+    auto fetch = [&](int32_t it) {
+        const int32_t seg = it >= per ? 1 : 0, kt = it - seg * per;
+        const int stage = it & 1;
+        const int64_t k0 = (int64_t)kt * kSteps;
+        const uint8_t* xb = p.x[XT ? z : seg] + (XT ? k0 * p.ldx + m0 * E : m0 * p.ldx + k0 * E);
+        const uint32_t xl = lds0 + stage * kStage, wl = xl + kXB;
+        auto base = [&](int side) { return p.w[DUAL ? side : seg] + (WT ? k0 * p.ldw + n0 * E : n0 * p.ldw + k0 * E); };
+        const int64_t left = p.K - k0;
+        if (left >= kSteps) {
+#pragma unroll
+            for (int i = 0; i < kXC; ++i) mm_dma16(xl + i * 8192, xb, xo[i]);
+#pragma unroll
+            for (int i = 0; i < kWC; ++i) mm_dma16(wl + i * 8192, base(i / 2), wo[i]);
+        } else {
+            // the contraction's end: zeros behind it
+            const int end = (int)left;
+            uint8_t* to = sh + stage * kStage + threadIdx.x * 16;
+#pragma unroll
+            for (int i = 0; i < kXC; ++i) {
+                if (xk[i] < (XT ? end : end * E)) mm_dma16(xl + i * 8192, xb, xo[i]);
+                else *reinterpret_cast<u32x4*>(to + i * 8192) = u32x4{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int i = 0; i < kWC; ++i) {
+                if (wk[i] < (WT ? end : end * E)) mm_dma16(wl + i * 8192, base(i / 2), wo[i]);
+                else *reinterpret_cast<u32x4*>(to + kXB + i * 8192) = u32x4{0, 0, 0, 0};
+            }
+        }
+        if constexpr (Sums::kScaled) {
+            const uint32_t sl = mm_lds(sh) + stage * kStage + kXB + kWB + wave * 256;
+            if (wave < BM / 64) mm_dma4(sl, p.xs + m0 * p.kb + kt, so);
+            else if (SC == kMmGroup && wave < BM / 64 + 4) mm_dma4(sl, p.ws[0] + n0 * p.kb + kt, so);
+        }
+    };
+
+    Sums sums;
+    if (total > 0) fetch(0);
+    for (int32_t it = 0; it < total; ++it) {
+        mm_meet();
+        const uint8_t* xt = sh + (it & 1) * kStage;
+        const uint8_t* wt = xt + kXB;
+        const float* sc = reinterpret_cast<const float*>(wt + kWB);
+        const int32_t kt = it >= per ? it - per : it;
+        MmFrag<KIND> fx[2], fw[NT];
+        float sx[2] = {}, sw[NT][4];
+        auto read = [&](int t) {
+            if constexpr (XT) mm_read_turned<KIND, BM>(fx[t & 1], xt, wm * (BM / 2) + 16 * t, 4);
+            else mm_read<KIND, kNear>(fx[t & 1], xt, wm * (BM / 2) + 16 * t + ln);
+            if constexpr (Sums::kScaled) sx[t & 1] = sc[wm * (BM / 2) + 16 * t + ln];
+        };
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            if constexpr (WT) mm_read_turned<KIND, BN>(fw[j], wt, wn * 64 + 4 * j, 16);
+            else if constexpr (DUAL) mm_read<KIND, kFar>(fw[j], wt + 128 * kMmStep * (j / 2), wn * 32 + 4 * (j % 2) + 8 * (ln >> 2) + (ln & 3));
+            else mm_read<KIND, kFar>(fw[j], wt, wn * 64 + 4 * j + 16 * (ln >> 2) + (ln & 3));
+        }
+        read(0);
+        if constexpr (Sums::kScaled) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                if constexpr (SC == kMmGroup) {
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(sc + BM + wn * 64 + 16 * gq + 4 * j);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sw[j][i] = v[i];
+                } else {
+                    const int64_t nb = DUAL ? n0 / 128 : min((n0 + wn * 64) / 128, (p.N - 1) / 128);
+                    const float v = p.ws[DUAL ? j / 2 : 0][nb * p.kb + kt];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sw[j][i] = v;
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (it + 1 < total) fetch(it + 1);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (t + 1 < MT) read(t + 1);
+            sums.step(t, fx[t & 1], fw, sx[t & 1], sw);
+        }
+    }
+    sums.template finish<EPI, T>(p, static_cast<T*>(p.out[z]), m0 + wm * (BM / 2), n0 + wn * (kCols / 4));
+}
+
+inline int64_t mm_blocks(int64_t M, int64_t N, bool dual, int BM) { return ((M + BM - 1) / BM) * ((N + (dual ? 127 : 255)) / (dual ? 128 : 256)); }
+
+// Whether k_mm takes the operands: `x`, `w` all pointers of a side.
+inline bool mm_fits(const MmArgs& p) {
+    uint64_t bits = (uint64_t)(p.ldx | p.ldw);
+    for (int i = 0; i < 2; ++i) bits |= (uint64_t)(uintptr_t)p.x[i] | (uint64_t)(uintptr_t)p.w[i];
+    return bits % 16 == 0 && p.ldx < (1 << 23) && p.ldw < (1 << 23) && p.kb < (1 << 21);
 }
 
 inline int64_t mm_any_blocks(int64_t M, int64_t N, bool dual) { return ((M + 127) / 128) * ((N + (dual ? 63 : 127)) / (dual ? 64 : 128)); }

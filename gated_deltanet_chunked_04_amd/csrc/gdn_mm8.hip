@@ -25,6 +25,11 @@ hipError_t mm8(const Mm8Args& a, hipStream_t st) {
     p.kb = (a.K + 127) / 128;
     p.out[0] = a.y;
     p.ldo = a.N;
+    if (mm_fits(p)) {
+        constexpr int BM = KIND == kMmF8x || KIND == kMmF32 ? 128 : 256;
+        hipLaunchKernelGGL((k_mm<KIND, SC, false, false, false, kMmOut, T, BM>), dim3((unsigned)mm_blocks(a.M, a.N, false, BM)), dim3(512), 0, st, p);
+        return hipGetLastError();
+    }
     const int64_t blocks = mm_any_blocks(a.M, a.N, false);
     if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((k_mm_any<KIND, SC, false, false, false, kMmOut, T>), dim3((unsigned)blocks), dim3(256), 0, st, p);
