@@ -79,8 +79,10 @@ __device__ __forceinline__ f32x4 mm_mma(const MmFrag<kMmF8x>& w, const MmFrag<kM
 // By rows: [R][128 bytes], chunk c of row r at c ^ key(r), so that 8 lanes that read one chunk of 8 rows meet
 // different banks. kFar: the tile's rows r come in fours that lie 2^kFar apart (the column order of W's tiles).
 // Turned: [steps][R elements].
-template <int kFar> __device__ __forceinline__ int mm_key(int r) { return (r & 3) | ((((r >> 2) ^ (r >> kFar)) & 1) << 2); }
-constexpr int kNear = 6;  // rows side by side
+constexpr int kNear = 0;  // rows side by side
+template <int kFar> __device__ __forceinline__ int mm_key(int r) {
+    return kFar == kNear ? r & 7 : (r & 3) | ((((r >> 2) ^ (r >> kFar)) & 1) << 2);
+}
 template <int kFar> __device__ __forceinline__ int mm_at(int r, int c) { return r * kMmStep + ((c ^ mm_key<kFar>(r)) << 4); }
 
 // Turned: chunk c of 16 bytes of memory row k; XOR over units of 32 bytes spreads the 16 rows that a transposing read
@@ -92,10 +94,28 @@ template <int R, int E> __device__ __forceinline__ int mm_turn_key(int k) {
 template <int R, int E> __device__ __forceinline__ int mm_turn_at(int k, int c) { return k * R * E + ((c ^ mm_turn_key<R, E>(k)) << 4); }
 
 // The lane's two chunks of row r.
+template <int kFar>
+__device__ __forceinline__ void mm_read(u32x4 (&raw)[2], const uint8_t* tile, int r) {
+    const int gq = threadIdx.x >> 4 & 3;
+    raw[0] = *reinterpret_cast<const u32x4*>(tile + mm_at<kFar>(r, gq));
+    raw[1] = *reinterpret_cast<const u32x4*>(tile + mm_at<kFar>(r, gq + 4));
+}
 template <int KIND, int kFar>
 __device__ __forceinline__ void mm_read(MmFrag<KIND>& f, const uint8_t* tile, int r) {
-    const int gq = threadIdx.x >> 4 & 3;
-    f.set(*reinterpret_cast<const u32x4*>(tile + mm_at<kFar>(r, gq)), *reinterpret_cast<const u32x4*>(tile + mm_at<kFar>(r, gq + 4)));
+    u32x4 raw[2];
+    mm_read<kFar>(raw, tile, r);
+    f.set(raw[0], raw[1]);
+}
+// The same for rows a whole number of 16 further on than the lane's row, whose two chunks lie at a and b: `by` bytes on.
+__device__ __forceinline__ void mm_read_at(u32x4 (&raw)[2], uint32_t a, uint32_t b, int by) {
+    typedef const __attribute__((address_space(3))) u32x4 lds_u32x4;
+    raw[0] = *(lds_u32x4*)(uintptr_t)(a + by);
+    raw[1] = *(lds_u32x4*)(uintptr_t)(b + by);
+}
+// A value that the compiler takes as new: offsets from it stay immediate offsets.
+__device__ __forceinline__ uint32_t mm_fresh(uint32_t x) {
+    asm volatile("" : "+v"(x));
+    return x;
 }
 // The same from a turned tile of R rows, for 16 of them: r0 + far * g + i, lane ln = 4 g + i.
 template <int KIND, int R>
@@ -206,7 +226,7 @@ __device__ __forceinline__ void mm_store(T* p, const float (&v)[N], int64_t n) {
     if (n >= N) {
         Raw<T, N> r;
         r.set(v);
-        store_raw<T, N>(p, r);
+        __builtin_memcpy(p, r.w, sizeof(T) * N);  // (not past the cache: it joins the parts of a line)
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -258,6 +278,19 @@ __device__ __forceinline__ void mm_gate(const MmArgs& p, int64_t m, int64_t n, c
     }
 }
 
+// Which of W's rows make up a wave's tile j of the register side: rows 4 g + i of the tile are rows
+// mm_row(j) + far g + i of W. kPair: a lane's columns in tiles 2 q and 2 q + 1 are 8 neighbours (one 16-byte store of
+// bf16, 64 bytes in a row by the four lane groups; gate and up: tiles 0, 1 and 2, 3); else 4 neighbours a tile (16
+// bytes of fp32; turned tiles, whose transposing reads want neighbouring columns).
+template <bool PAIR, bool DUAL> struct MmCols {
+    static constexpr int kFar = PAIR ? 3 : kNear;  // for mm_key
+    static constexpr int kStride = PAIR ? 8 : 4;
+    static __device__ __forceinline__ constexpr int row(int j) { return PAIR ? (DUAL ? 0 : 32 * (j / 2)) + 4 * (j % 2) : 16 * j; }
+    // the lane's first column of tile j
+    static __device__ __forceinline__ int col(int j, int gq) { return row(j) + kStride * gq; }
+};
+template <typename T, bool WT, bool DUAL> constexpr bool mm_pair() { return DUAL || (sizeof(T) == 2 && !WT); }
+
 // The sums of a wave's MT x NT tiles, scaled where the operands are e4m3. Shared by the kernels below.
 template <int KIND, int SC, bool DUAL, int MT, int NT>
 struct MmSums {
@@ -270,42 +303,43 @@ struct MmSums {
         for (int j = 0; j < NT; ++j) {
             if constexpr (kScaled) {
                 const f32x4 c = mm_mma(w[j], x, f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(c[i], SC == kMmBlock ? sx * sw[j][0] : sx * sw[j][i], acc[t][j][i]);
+                add(t, j, c, sx, sw[j]);
             } else {
                 acc[t][j] = mm_mma(w[j], x, acc[t][j]);
             }
         }
     }
-    // Hands the lane's outputs on: X's row m0 + 16 t + ln, W's columns n0 + 64 g + 16 gq .. + 15 (two sides: n0 + 32 g
-    // + 8 gq .. + 7 of each).
-    template <int EPI, typename T>
+    __device__ __forceinline__ void add(int t, int j, f32x4 c, float sx, const float (&sw)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(c[i], SC == kMmBlock ? sx * sw[0] : sx * sw[i], acc[t][j][i]);
+    }
+    // Hands the lane's outputs on: X's row m0 + 16 t + ln, the columns that MmCols names.
+    template <int EPI, typename T, bool PAIR>
     __device__ __forceinline__ void finish(const MmArgs& p, T* out, int64_t m0, int64_t n0) const {
+        using C = MmCols<PAIR, DUAL>;
         const int ln = threadIdx.x & 15, gq = threadIdx.x >> 4 & 3;
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             const int64_t m = m0 + 16 * t + ln;
             if (m >= p.M) continue;
             const float sx = SC == kMmRow ? p.xs[m] : 1.f;
+            constexpr int kRun = PAIR ? 8 : 4;
 #pragma unroll
-            for (int g = 0; g < NT / 4; ++g) {
-                float v[2][8];
+            for (int q = 0; q < NT; q += DUAL ? 4 : kRun / 4) {
+                const int64_t n = n0 + C::col(q, gq);
+                if (n >= p.N) continue;
+                float v[DUAL ? 2 : 1][kRun];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < (DUAL ? 4 : kRun / 4); ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[j >> 1][(j & 1) * 4 + i] = acc[t][4 * g + j][i];
+                    for (int i = 0; i < 4; ++i) v[DUAL ? j / 2 : 0][(j % (kRun / 4)) * 4 + i] = acc[t][q + j][i];
                 if constexpr (DUAL) {
-                    const int64_t n = n0 + 32 * g + 8 * gq;
-                    if (n < p.N) mm_gate<EPI, T>(p, m, n, v[0], v[1]);
+                    mm_gate<EPI, T>(p, m, n, v[0], v[1]);
                 } else {
+                    if (SC == kMmRow)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int64_t n = n0 + 64 * g + 16 * gq + 8 * h;
-                        if (SC == kMmRow)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) v[h][i] *= sx * p.ws[0][n + i < p.N ? n + i : p.N - 1];
-                        if (n < p.N) mm_store<T, 8>(out + m * p.ldo + n, v[h], p.N - n);
-                    }
+                        for (int i = 0; i < kRun; ++i) v[0][i] *= sx * p.ws[0][n + i < p.N ? n + i : p.N - 1];
+                    mm_store<T, kRun>(out + m * p.ldo + n, v[0], p.N - n);
                 }
             }
         }
@@ -316,11 +350,12 @@ struct MmSums {
 // registers, one tile of each operand in LDS.
 template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
 __global__ __launch_bounds__(256) void k_mm_any(MmArgs p) {
-    constexpr int E = mm_size<KIND>(), kFar = DUAL ? 3 : 4, MT = 4, NT = 4;
+    constexpr int E = mm_size<KIND>(), MT = 4, NT = 4;
+    using C = MmCols<mm_pair<T, WT, DUAL>(), DUAL>;
     constexpr int kSteps = kMmStep / E;  // of the contraction per step
     constexpr int kCols = DUAL ? 64 : 128;
     using X = MmTile<E, 128, XT, kNear>;
-    using W = MmTile<E, kCols, WT, kFar>;
+    using W = MmTile<E, kCols, WT, C::kFar>;
     __shared__ __align__(16) uint8_t xt[128 * kMmStep], wt[128 * kMmStep];
     const int wave = wave_id(), wm = wave & 1, wn = wave >> 1;
     const int ln = threadIdx.x & 15, gq = threadIdx.x >> 4 & 3;
@@ -358,9 +393,8 @@ __global__ __launch_bounds__(256) void k_mm_any(MmArgs p) {
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            if constexpr (WT) mm_read_turned<KIND, 128>(fw[j], wt, wn * 64 + 4 * j, 16);
-            else if constexpr (DUAL) mm_read<KIND, kFar>(fw[j], wt + 64 * kMmStep * (j / 2), wn * 32 + 4 * (j % 2) + 8 * (ln >> 2) + (ln & 3));
-            else mm_read<KIND, kFar>(fw[j], wt, wn * 64 + 4 * j + 16 * (ln >> 2) + (ln & 3));
+            if constexpr (WT) mm_read_turned<KIND, 128>(fw[j], wt, wn * 64 + C::row(j), C::kStride);
+            else mm_read<KIND, C::kFar>(fw[j], wt + (DUAL ? 64 * kMmStep * (j / 2) : 0), wn * (kCols / 2) + C::row(j) + C::kStride * (ln >> 2) + (ln & 3));
         }
         float sx[MT], sw[NT][4];
         if constexpr (MmSums<KIND, SC, DUAL, MT, NT>::kScaled) {
@@ -373,7 +407,7 @@ __global__ __launch_bounds__(256) void k_mm_any(MmArgs p) {
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int64_t n = n0 + wn * 64 + 16 * gq + 4 * j + i;
+                    const int64_t n = n0 + wn * 64 + C::col(j, gq) + i;
                     if (SC == kMmGroup) sw[j][i] = p.ws[0][(n < p.N ? n : p.N - 1) * p.kb + kt];
                     else sw[j][i] = p.ws[DUAL ? j / 2 : 0][n0 / 128 * p.kb + kt];
                 }
@@ -381,21 +415,21 @@ __global__ __launch_bounds__(256) void k_mm_any(MmArgs p) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) sums.step(t, fx[t], fw, sx[t], sw);
     }
-    sums.template finish<EPI, T>(p, static_cast<T*>(p.out[z]), m0 + wm * 64, n0 + wn * (kCols / 2));
+    sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, static_cast<T*>(p.out[z]), m0 + wm * 64, n0 + wn * (kCols / 2));
 }
 
 // ---- the same, memory to LDS without registers ----------------------------------------------
 // 16 (or 4) bytes of each lane from base + off to LDS at lds + 16 (4) lane. In assembly: the compiler takes the builtin for
 // a write that every later LDS read has to wait for. Counted by vmcnt like a load; no register is written. (M0 needs a
 // wait state before the load that uses it.)
-__device__ __forceinline__ uint64_t mm_uniform(const void* p) {
-    const uint64_t a = (uint64_t)(uintptr_t)p;
+__device__ __forceinline__ uint64_t mm_uniform(uint64_t a) {
     return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a) | (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32;
 }
-__device__ __forceinline__ void mm_dma16(uint32_t lds, const uint8_t* base, uint32_t off) {
+__device__ __forceinline__ uint64_t mm_uniform(const void* p) { return mm_uniform((uint64_t)(uintptr_t)p); }
+__device__ __forceinline__ void mm_dma16(uint32_t lds, uint64_t base, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(off), "s"(mm_uniform(base)) : "memory");
 }
-__device__ __forceinline__ void mm_dma4(uint32_t lds, const void* base, uint32_t off) {
+__device__ __forceinline__ void mm_dma4(uint32_t lds, uint64_t base, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(off), "s"(mm_uniform(base)) : "memory");
 }
 // All of this wave's loads to LDS have landed and its LDS reads are done; then the workgroup meets.
@@ -422,17 +456,18 @@ struct MmPlace {
 // its way while one is multiplied. Memory rows and addresses are multiples of 16 bytes, 256 rows within 2^31 bytes.
 template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T, int BM>
 __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
-    constexpr int E = mm_size<KIND>(), kFar = DUAL ? 3 : 4, MT = BM / 32, NT = 4, BN = 256;
+    constexpr int E = mm_size<KIND>(), MT = BM / 32, NT = 4, BN = 256;
+    using C = MmCols<mm_pair<T, WT, DUAL>(), DUAL>;
     constexpr int kSteps = kMmStep / E;
     constexpr int kCols = DUAL ? 128 : 256;
     constexpr int kXB = BM * kMmStep, kWB = BN * kMmStep;
     constexpr int kXC = BM * 8 / 512, kWC = 4;  // chunks of a thread
     using Sums = MmSums<KIND, SC, DUAL, MT, NT>;
     using X = MmTile<E, BM, XT, kNear>;
-    using W = MmTile<E, kCols, WT, kFar>;
-    constexpr int kSB = Sums::kScaled ? (BM + (SC == kMmGroup ? 256 : 0)) * 4 : 0;
-    constexpr int kStage = kXB + kWB + kSB;
-    __shared__ __align__(128) uint8_t sh[2 * kStage];
+    using W = MmTile<E, kCols, WT, C::kFar>;
+    constexpr int kStage = kXB + kWB;
+    constexpr int kSRows = Sums::kScaled ? BM + (SC == kMmGroup ? 256 : 2) : 0;  // rows of scales: X's, and W's or two of its blocks
+    __shared__ __align__(128) uint8_t sh[2 * (kStage + kSRows * 16)];
     const int wave = wave_id(), lane = threadIdx.x & 63, wm = wave & 1, wn = wave >> 1;
     const int ln = lane & 15, gq = lane >> 4;
     const int32_t tm = (int32_t)((p.M + BM - 1) / BM), tn = (int32_t)((p.N + kCols - 1) / kCols);
@@ -469,101 +504,167 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
             wk[i] = k;
             wo[i] = (uint32_t)(k * p.ldw) + (uint32_t)(min(col, (p.N * E - 1) / 16 * 16) - n0 * E);
         } else {
-            const int r = c >> 3, b = ((c & 7) ^ mm_key<kFar>(r)) * 16;
+            const int r = c >> 3, b = ((c & 7) ^ mm_key<C::kFar>(r)) * 16;
             wk[i] = b;
             wo[i] = (uint32_t)((n0 + r < p.N ? r : p.N - 1 - n0) * p.ldw) + b;
         }
     }
-    uint32_t so = 0;
+    // Scales pass through registers, those of four steps at a time: a thread has one row's, which lie side by side.
+    const float* srow = nullptr;
     if constexpr (Sums::kScaled) {
-        const bool far = threadIdx.x >= BM;
-        const int r = threadIdx.x - (far ? BM : 0);
-        so = (uint32_t)((far ? (n0 + r < p.N ? r : p.N - 1 - n0) : (m0 + r < p.M ? r : p.M - 1 - m0)) * p.kb) * 4;
+        const int r = threadIdx.x - BM;
+        if (r < 0) srow = p.xs + min(m0 + (int)threadIdx.x, p.M - 1) * p.kb;
+        else if (SC == kMmGroup && r < 256) srow = p.ws[0] + min(n0 + r, p.N - 1) * p.kb;
+        else if (SC == kMmBlock && r < 2) srow = (DUAL && r ? p.ws[1] : p.ws[0]) + (DUAL ? n0 / 128 : min(n0 / 128 + r, (p.N - 1) / 128)) * p.kb;
     }
+    f32x4* const sring = reinterpret_cast<f32x4*>(sh + 2 * kStage);
+    f32x4 snext = {};
+    auto fetch_scales = [&](int32_t k) {  // of steps k .. k + 3
+        if (srow) {
+            if (k + 4 <= p.kb) __builtin_memcpy(&snext, srow + k, 16);
+            else
+#pragma unroll
+                for (int i = 0; i < 4; ++i) snext[i] = srow[min((int64_t)k + i, p.kb - 1)];
+        }
+    };
+    auto keep_scales = [&](int32_t k) {
+        if (srow) sring[(k >> 2 & 1) * kSRows + threadIdx.x] = snext;
+    };
     const uint32_t lds0 = mm_lds(sh) + wave * 1024;
 
-    auto fetch = [&](int32_t it) {
-        const int32_t seg = it >= per ? 1 : 0, kt = it - seg * per;
-        const int stage = it & 1;
-        const int64_t k0 = (int64_t)kt * kSteps;
-        const uint8_t* xb = p.x[XT ? z : seg] + (XT ? k0 * p.ldx + m0 * E : m0 * p.ldx + k0 * E);
+    // Where the next step's tiles come from (scalars, whatever the compiler makes of the loop).
+    uint64_t xs = mm_uniform((XT ? (z ? p.x[1] : p.x[0]) : p.x[0]) + (XT ? m0 * E : m0 * p.ldx));
+    uint64_t ws0 = mm_uniform(p.w[0] + (WT ? n0 * E : n0 * p.ldw)), ws1 = mm_uniform(p.w[1] + (WT ? n0 * E : n0 * p.ldw));
+    const int64_t xstep = XT ? kSteps * p.ldx : kMmStep, wstep = WT ? kSteps * p.ldw : kMmStep;
+    const int32_t whole = (int32_t)(p.K / kSteps), rest = (int32_t)(p.K % kSteps);
+    int32_t kt = 0;
+    auto fetch = [&](int stage) {
         const uint32_t xl = lds0 + stage * kStage, wl = xl + kXB;
-        auto base = [&](int side) { return p.w[DUAL ? side : seg] + (WT ? k0 * p.ldw + n0 * E : n0 * p.ldw + k0 * E); };
-        const int64_t left = p.K - k0;
-        if (left >= kSteps) {
+        if (__builtin_expect(kt < whole, 1)) {
 #pragma unroll
-            for (int i = 0; i < kXC; ++i) mm_dma16(xl + i * 8192, xb, xo[i]);
+            for (int i = 0; i < kXC; ++i) mm_dma16(xl + i * 8192, xs, xo[i]);
 #pragma unroll
-            for (int i = 0; i < kWC; ++i) mm_dma16(wl + i * 8192, base(i / 2), wo[i]);
+            for (int i = 0; i < kWC; ++i) mm_dma16(wl + i * 8192, DUAL && i >= 2 ? ws1 : ws0, wo[i]);
         } else {
             // the contraction's end: zeros behind it
-            const int end = (int)left;
             uint8_t* to = sh + stage * kStage + threadIdx.x * 16;
 #pragma unroll
             for (int i = 0; i < kXC; ++i) {
-                if (xk[i] < (XT ? end : end * E)) mm_dma16(xl + i * 8192, xb, xo[i]);
+                if (xk[i] < (XT ? rest : rest * E)) mm_dma16(xl + i * 8192, xs, xo[i]);
                 else *reinterpret_cast<u32x4*>(to + i * 8192) = u32x4{0, 0, 0, 0};
             }
 #pragma unroll
             for (int i = 0; i < kWC; ++i) {
-                if (wk[i] < (WT ? end : end * E)) mm_dma16(wl + i * 8192, base(i / 2), wo[i]);
+                if (wk[i] < (WT ? rest : rest * E)) mm_dma16(wl + i * 8192, DUAL && i >= 2 ? ws1 : ws0, wo[i]);
                 else *reinterpret_cast<u32x4*>(to + kXB + i * 8192) = u32x4{0, 0, 0, 0};
             }
         }
-        if constexpr (Sums::kScaled) {
-            const uint32_t sl = mm_lds(sh) + stage * kStage + kXB + kWB + wave * 256;
-            if (wave < BM / 64) mm_dma4(sl, p.xs + m0 * p.kb + kt, so);
-            else if (SC == kMmGroup && wave < BM / 64 + 4) mm_dma4(sl, p.ws[0] + n0 * p.kb + kt, so);
+        xs += xstep;
+        ws0 += wstep;
+        if (DUAL) ws1 += wstep;
+        if (++kt == per && p.segs > 1) {
+            kt = 0;
+            xs = mm_uniform(p.x[1] + m0 * p.ldx);
+            ws0 = ws1;
         }
+        kt = __builtin_amdgcn_readfirstlane(kt);
     };
 
+    // The lane's chunks of its first X row; the rows of the next tiles lie whole numbers of 16 rows on, with the same keys.
+    const uint32_t xl0 = mm_at<kNear>(wm * (BM / 2) + ln, gq), xl1 = mm_at<kNear>(wm * (BM / 2) + ln, gq + 4);
     Sums sums;
-    if (total > 0) fetch(0);
+    if (total > 0) {
+        fetch(0);
+        if constexpr (Sums::kScaled) {
+            fetch_scales(0);
+            keep_scales(0);
+        }
+    }
     for (int32_t it = 0; it < total; ++it) {
         mm_meet();
+        if constexpr (Sums::kScaled) {
+            // (what was loaded has arrived with the step's tiles)
+            if ((it & 3) == 1 && it + 3 < total) keep_scales(it + 3);
+            if ((it & 3) == 0 && it + 4 < total) fetch_scales(it + 4);
+        }
         const uint8_t* xt = sh + (it & 1) * kStage;
         const uint8_t* wt = xt + kXB;
-        const float* sc = reinterpret_cast<const float*>(wt + kWB);
-        const int32_t kt = it >= per ? it - per : it;
+        const float* sc = reinterpret_cast<const float*>(sring + (it >> 2 & 1) * kSRows) + (it & 3);
+        // X's chunks are read a tile ahead; e4m3 that is widened two tiles, and widened one ahead
+        constexpr int kAhead = KIND == kMmF8x ? 2 : 1;
         MmFrag<KIND> fx[2], fw[NT];
-        float sx[2] = {}, sw[NT][4];
+        u32x4 raw[2][2], rw[NT][2];
+        f32x4 c[2][NT];
+        float sx[4] = {}, sw[NT][4];
+        typedef const __attribute__((address_space(3))) float lds_float;
+        const uint32_t xa = mm_fresh(mm_lds(xt) + xl0), xc = mm_fresh(mm_lds(xt) + xl1);
+        const uint32_t sa = Sums::kScaled ? mm_fresh(mm_lds(sc) + 16 * (wm * (BM / 2) + ln)) : 0;
         auto read = [&](int t) {
             if constexpr (XT) mm_read_turned<KIND, BM>(fx[t & 1], xt, wm * (BM / 2) + 16 * t, 4);
-            else mm_read<KIND, kNear>(fx[t & 1], xt, wm * (BM / 2) + 16 * t + ln);
-            if constexpr (Sums::kScaled) sx[t & 1] = sc[wm * (BM / 2) + 16 * t + ln];
+            else mm_read_at(raw[t & 1], xa, xc, 16 * kMmStep * t);
+            if constexpr (Sums::kScaled) sx[t & 3] = *(lds_float*)(uintptr_t)(sa + 256 * t);
+        };
+        auto ready = [&](int t) {
+            if constexpr (!XT) fx[t & 1].set(raw[t & 1][0], raw[t & 1][1]);
         };
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            if constexpr (WT) mm_read_turned<KIND, BN>(fw[j], wt, wn * 64 + 4 * j, 16);
-            else if constexpr (DUAL) mm_read<KIND, kFar>(fw[j], wt + 128 * kMmStep * (j / 2), wn * 32 + 4 * (j % 2) + 8 * (ln >> 2) + (ln & 3));
-            else mm_read<KIND, kFar>(fw[j], wt, wn * 64 + 4 * j + 16 * (ln >> 2) + (ln & 3));
+            if constexpr (WT) mm_read_turned<KIND, BN>(fw[j], wt, wn * 64 + C::row(j), C::kStride);
+            else mm_read<C::kFar>(rw[j], wt + (DUAL ? 128 * kMmStep * (j / 2) : 0), wn * (kCols / 4) + C::row(j) + C::kStride * (ln >> 2) + (ln & 3));
         }
-        read(0);
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) read(t);
         if constexpr (Sums::kScaled) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 if constexpr (SC == kMmGroup) {
-                    const f32x4 v = *reinterpret_cast<const f32x4*>(sc + BM + wn * 64 + 16 * gq + 4 * j);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sw[j][i] = v[i];
+                    for (int i = 0; i < 4; ++i) sw[j][i] = sc[4 * (BM + wn * 64 + C::col(j, gq) + i)];
                 } else {
-                    const int64_t nb = DUAL ? n0 / 128 : min((n0 + wn * 64) / 128, (p.N - 1) / 128);
-                    const float v = p.ws[DUAL ? j / 2 : 0][nb * p.kb + kt];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sw[j][i] = v;
+                    sw[j][0] = sc[4 * (BM + (DUAL ? j / 2 : wn / 2))];
                 }
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (it + 1 < total) fetch(it + 1);
+        if (it + 1 < total) fetch(~it & 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!WT)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) fw[j].set(rw[j][0], rw[j][1]);
+        ready(0);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            __builtin_amdgcn_sched_barrier(0);
-            if (t + 1 < MT) read(t + 1);
-            sums.step(t, fx[t & 1], fw, sx[t & 1], sw);
+            if constexpr (KIND != kMmF8x) __builtin_amdgcn_sched_barrier(0);
+            if (kAhead == 2 && t + 1 < MT) ready(t + 1);
+            if (t + kAhead < MT) read(t + kAhead);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                if constexpr (Sums::kScaled) {
+                    // a tile's sums are added while the next one is multiplied
+                    c[t & 1][j] = mm_mma(fw[j], fx[t & 1], f32x4{0.f, 0.f, 0.f, 0.f});
+                    if (t > 0) sums.add(t - 1, j, c[~t & 1][j], sx[(t - 1) & 3], sw[j]);
+                } else {
+                    sums.acc[t][j] = mm_mma(fw[j], fx[t & 1], sums.acc[t][j]);
+                }
+                // matrix instructions with vector ones between them
+                if constexpr (KIND == kMmF8x) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, SC == kMmGroup ? 4 : 3, 0);
+                    }
+                } else if constexpr (Sums::kScaled) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    if (t > 0) __builtin_amdgcn_sched_group_barrier(0x002, SC == kMmBlock ? 5 : 8, 0);
+                }
+            }
+            if (kAhead == 1 && t + 1 < MT) ready(t + 1);
         }
+        if constexpr (Sums::kScaled)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) sums.add(MT - 1, j, c[(MT - 1) & 1][j], sx[(MT - 1) & 3], sw[j]);
     }
-    sums.template finish<EPI, T>(p, static_cast<T*>(p.out[z]), m0 + wm * (BM / 2), n0 + wn * (kCols / 4));
+    sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, static_cast<T*>(p.out[z]), m0 + wm * (BM / 2), n0 + wn * (kCols / 4));
 }
 
 inline int64_t mm_blocks(int64_t M, int64_t N, bool dual, int BM) { return ((M + BM - 1) / BM) * ((N + (dual ? 127 : 255)) / (dual ? 128 : 256)); }
