@@ -31,19 +31,6 @@ MmArgs block_args(const FfnArgs& a, int64_t size) {
     return p;
 }
 
-template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
-hipError_t run(const MmArgs& p, hipStream_t st) {
-    if (mm_fits(p)) {
-        constexpr int BM = KIND == kMmF8x || KIND == kMmF32 ? 128 : 256;
-        hipLaunchKernelGGL((k_mm<KIND, SC, XT, WT, DUAL, EPI, T, BM>), dim3((unsigned)(mm_blocks(p.M, p.N, DUAL, BM) * p.outs)), dim3(512), 0, st, p);
-        return hipGetLastError();
-    }
-    const int64_t blocks = mm_any_blocks(p.M, p.N, DUAL);
-    if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_mm_any<KIND, SC, XT, WT, DUAL, EPI, T>), dim3((unsigned)blocks, (unsigned)p.outs), dim3(256), 0, st, p);
-    return hipGetLastError();
-}
-
 // gradients of gate and up from the forward's values, 8 at a time
 template <typename T>
 __global__ __launch_bounds__(256) void k_ffn_act_bwd(MmArgs p) {
@@ -53,7 +40,7 @@ __global__ __launch_bounds__(256) void k_ffn_act_bwd(MmArgs p) {
     float a[8], u[8];
     mm_load<float, 8>(p.pre + m * p.N + n, a, p.N - n);
     mm_load<float, 8>(p.pre + (p.M + m) * p.N + n, u, p.N - n);
-    mm_gate<kMmFfnBwd, T>(p, m, n, a, u);
+    mm_gate<kMmFfnBwd, T, 8>(p, m, n, a, u);
 }
 
 // columns of the gradients of gate and up in the workspace: whole vectors, zeros behind F
@@ -62,7 +49,8 @@ int64_t grad_ld(int64_t F) { return (F + 7) / 8 * 8; }
 template <int KIND, typename T>
 hipError_t bwd(const FfnArgs& a, hipStream_t st) {
     const int64_t size = sizeof(T), ldd = grad_ld(a.F);
-    void* d[2] = {a.ws, a.ws + align256((size_t)(a.M * ldd * size))};
+    const size_t bytes = align256((size_t)(a.M * ldd * size));
+    void *d[2] = {a.ws, a.ws + bytes}, *part = a.ws + 2 * bytes;
     if (a.M) {
         MmArgs p = block_args(a, size);
         p.out[0] = d[0];
@@ -73,7 +61,7 @@ hipError_t bwd(const FfnArgs& a, hipStream_t st) {
             const int64_t blocks = ((a.F + 7) / 8 * a.M + 255) / 256;
             if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
             hipLaunchKernelGGL(k_ffn_act_bwd<T>, dim3((unsigned)blocks), dim3(256), 0, st, p);
-        } else if (hipError_t e = run<KIND, kMmPlain, false, false, true, kMmFfnBwd, T>(p, st)) {
+        } else if (hipError_t e = mm_run<KIND, kMmPlain, false, false, true, kMmFfnBwd, T>(p, part, st)) {
             return e;
         }
     }
@@ -91,7 +79,7 @@ hipError_t bwd(const FfnArgs& a, hipStream_t st) {
         p.outs = 1;
         p.out[0] = a.dx;
         p.ldo = a.K;
-        if (hipError_t e = run<KIND, kMmPlain, false, true, false, kMmOut, T>(p, st)) return e;
+        if (hipError_t e = mm_run<KIND, kMmPlain, false, true, false, kMmOut, T>(p, part, st)) return e;
     }
     if (a.dwg) {
         MmArgs p{};
@@ -107,43 +95,49 @@ hipError_t bwd(const FfnArgs& a, hipStream_t st) {
         p.out[0] = a.dwg;
         p.out[1] = a.dwu;
         p.ldo = a.K;
-        if (hipError_t e = run<KIND, kMmPlain, true, true, false, kMmOut, T>(p, st)) return e;
+        if (hipError_t e = mm_run<KIND, kMmPlain, true, true, false, kMmOut, T>(p, part, st)) return e;
     }
     return hipGetLastError();
 }
 
 template <int KIND, typename T>
-hipError_t ffn8(const FfnArgs& a, void* h, hipStream_t st) {
+hipError_t ffn8(const FfnArgs& a, void* h, void* part, hipStream_t st) {
     MmArgs p = block_args(a, 1);
     p.xs = a.xs;
     p.ws[0] = a.gs;
     p.ws[1] = a.us;
     p.kb = (a.K + 127) / 128;
     p.out[0] = h;
-    return run<KIND, kMmBlock, false, false, true, kMmFfn, T>(p, st);
+    return mm_run<KIND, kMmBlock, false, false, true, kMmFfn, T>(p, part, st);
 }
 
 }  // namespace
 
-size_t ffn_fwd_ws(int64_t M, int64_t K, int64_t F, int dtype) { return 0; }
-size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
-    const int64_t size = dtype == 1 ? 4 : 2;
-    return 2 * align256((size_t)(M * grad_ld(F) * size));
+size_t ffn_fwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
+    return mm_plan(dtype == 1 ? kMmF32 : kMmBf16, M, F, K, 1, 1, false, true).bytes;
 }
-size_t ffn8_ws(int64_t M, int64_t K, int64_t F, int dtype, bool quant) { return quant ? (size_t)(M * F * 4) : 0; }
+size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
+    const int kind = dtype == 1 ? kMmF32 : kMmBf16;
+    const size_t again = mm_plan(kind, M, F, K, 1, 1, false, true).bytes, dx = mm_plan(kind, M, K, F, 2, 1, true, false).bytes;
+    return 2 * align256((size_t)(M * grad_ld(F) * (dtype == 1 ? 4 : 2))) + (again > dx ? again : dx);
+}
+// the block's fp32 output in front of its quantisation, and the parts
+size_t ffn8_ws(int64_t M, int64_t K, int64_t F, int dtype, bool quant) {
+    return (quant ? align256((size_t)(M * F * 4)) : 0) + mm_plan(quant || dtype == 1 ? kMmF8x : kMmF8, M, F, K, 1, 1, false, true).bytes;
+}
 
 hipError_t launch_ffn_fwd(const FfnArgs& a, int dtype, hipStream_t st) {
     if (a.M == 0) return hipSuccess;
-    if (dtype == 1) return run<kMmF32, kMmPlain, false, false, true, kMmFfn, float>(block_args(a, 4), st);
-    return run<kMmBf16, kMmPlain, false, false, true, kMmFfn, bf16_t>(block_args(a, 2), st);
+    if (dtype == 1) return mm_run<kMmF32, kMmPlain, false, false, true, kMmFfn, float>(block_args(a, 4), a.ws, st);
+    return mm_run<kMmBf16, kMmPlain, false, false, true, kMmFfn, bf16_t>(block_args(a, 2), a.ws, st);
 }
 hipError_t launch_ffn_bwd(const FfnArgs& a, int dtype, hipStream_t st) {
     return dtype == 1 ? bwd<kMmF32, float>(a, st) : bwd<kMmBf16, bf16_t>(a, st);
 }
 hipError_t launch_ffn8(const FfnArgs& a, int dtype, hipStream_t st) {
     if (a.M == 0) return hipSuccess;
-    if (!a.hs) return dtype == 1 ? ffn8<kMmF8x, float>(a, a.h, st) : ffn8<kMmF8, bf16_t>(a, a.h, st);
-    if (hipError_t e = ffn8<kMmF8x, float>(a, a.ws, st)) return e;
+    if (!a.hs) return dtype == 1 ? ffn8<kMmF8x, float>(a, a.h, a.ws, st) : ffn8<kMmF8, bf16_t>(a, a.h, a.ws, st);
+    if (hipError_t e = ffn8<kMmF8x, float>(a, a.ws, a.ws + align256((size_t)(a.M * a.F * 4)), st)) return e;
     const QuantArgs q{a.M, a.F, a.ws, static_cast<uint8_t*>(a.h), a.hs};
     return launch_quant(q, 1, 1, false, st);
 }

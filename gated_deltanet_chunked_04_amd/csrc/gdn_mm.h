@@ -144,20 +144,20 @@ __device__ __forceinline__ void mm_read_turned(MmFrag<KIND>& f, const uint8_t* t
 
 // ---- memory to LDS --------------------------------------------------------------------------
 // 16 bytes at p + off of a memory row of `limit` bytes, zeros behind it; at any address.
-template <int E>
 __device__ __forceinline__ u32x4 mm_chunk(const uint8_t* p, int64_t off, int64_t limit) {
     u32x4 v = {0, 0, 0, 0};
     if (off + 16 <= limit) {
         __builtin_memcpy(&v, p + off, 16);
     } else if (off < limit) {
-        const int n = (int)(limit - off);
-#pragma unroll
-        for (int i = 0; i < 16; i += E)
-            if (i < n) {
-                uint32_t x = 0;
-                __builtin_memcpy(&x, p + off + i, E);
-                v[i / 4] |= x << (8 * (i % 4));
-            }
+        unsigned __int128 x = 0;
+        if (limit >= 16) {  // the row's last 16 bytes, of which those in front of `off` go
+            __builtin_memcpy(&x, p + limit - 16, 16);
+            x >>= 8 * (int)(off + 16 - limit);
+        } else {
+#pragma unroll 1
+            for (int i = (int)(limit - off) - 1; i >= 0; --i) x = x << 8 | p[off + i];
+        }
+        v = __builtin_bit_cast(u32x4, x);
     }
     return v;
 }
@@ -175,10 +175,10 @@ struct MmTile {
     static __device__ __forceinline__ u32x4 load(const uint8_t* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t K, int i) {
         if constexpr (kTurned) {
             const int64_t k = k0 + i / kWide;
-            return k < K ? mm_chunk<E>(p + k * ld, r0 * E + 16 * (i % kWide), rows * E) : u32x4{0, 0, 0, 0};
+            return k < K ? mm_chunk(p + k * ld, r0 * E + 16 * (i % kWide), rows * E) : u32x4{0, 0, 0, 0};
         } else {
             const int64_t r = r0 + (i >> 3);
-            return mm_chunk<E>(p + (r < rows ? r : rows - 1) * ld, k0 * E + 16 * (i & 7), K * E);
+            return mm_chunk(p + (r < rows ? r : rows - 1) * ld, k0 * E + 16 * (i & 7), K * E);
         }
     }
 };
@@ -201,6 +201,9 @@ struct MmArgs {
     const void* d_h;      // [M, N]: the gradient that enters the block's backward
     float* pre;           // [2, M, N] gate and up in fp32, or null
     int32_t act;          // 1 silu, 2 gelu_tanh
+    float* part;          // where the contraction is split: sums of each part, [splits, sides, M, N]
+    int32_t splits;       // parts of the contraction (0: one, without part)
+    int32_t share;        // steps of a part
 };
 
 // sigmoid and the slope of its argument: silu(a) = a sigmoid(a), gelu_tanh(a) = a sigmoid(2 c (a + 0.044715 a^3)).
@@ -246,36 +249,78 @@ __device__ __forceinline__ void mm_load(const T* p, float (&v)[N], int64_t n) {
 }
 
 // What is done with a lane's sums. kMmOut: y = sums (with kMmRow, times the rows' scales). kMmFfn: h = act(gate) up, and
-// gate and up themselves where `pre` is given. kMmFfnBwd: the gradients of gate and up from d_h.
-enum MmEpi { kMmOut = 0, kMmFfn = 1, kMmFfnBwd = 2 };
+// gate and up themselves where `pre` is given. kMmFfnBwd: the gradients of gate and up from d_h. kMmPart: the sums of a
+// part of the contraction, for k_mm_join.
+enum MmEpi { kMmOut = 0, kMmFfn = 1, kMmFfnBwd = 2, kMmPart = 3 };
 
-// 8 columns of the block at (m, n).
-template <int EPI, typename T>
-__device__ __forceinline__ void mm_gate(const MmArgs& p, int64_t m, int64_t n, const float (&a)[8], const float (&u)[8]) {
+// R columns of the block at (m, n).
+template <int EPI, typename T, int R>
+__device__ __forceinline__ void mm_gate(const MmArgs& p, int64_t m, int64_t n, const float (&a)[R], const float (&u)[R]) {
     const int64_t left = p.N - n;
     if constexpr (EPI == kMmFfn) {
-        float h[8];
+        float h[R];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = Act(a[i], p.act, false).f * u[i];
-        mm_store<T, 8>(static_cast<T*>(p.out[0]) + m * p.ldo + n, h, left);
+        for (int i = 0; i < R; ++i) h[i] = Act(a[i], p.act, false).f * u[i];
+        mm_store<T, R>(static_cast<T*>(p.out[0]) + m * p.ldo + n, h, left);
         if (p.pre) {
-            mm_store<float, 8>(p.pre + m * p.N + n, a, left);
-            mm_store<float, 8>(p.pre + (p.M + m) * p.N + n, u, left);
+            mm_store<float, R>(p.pre + m * p.N + n, a, left);
+            mm_store<float, R>(p.pre + (p.M + m) * p.N + n, u, left);
         }
     } else {
-        float d[8], da[8], du[8];
-        mm_load<T, 8>(static_cast<const T*>(p.d_h) + m * p.N + n, d, left);
+        float d[R], da[R], du[R];
+        mm_load<T, R>(static_cast<const T*>(p.d_h) + m * p.N + n, d, left);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < R; ++i) {
             const Act f(a[i], p.act, true);
             da[i] = i < left ? d[i] * u[i] * f.df : 0.f;
             du[i] = i < left ? d[i] * f.f : 0.f;
         }
         // rounded to the inputs' type: they are operands of the products behind, which take whole vectors of their rows
         // (ldo is a multiple of 8) and multiply what lies behind column N by zero
-        mm_store<T, 8>(static_cast<T*>(p.out[0]) + m * p.ldo + n, da, 8);
-        mm_store<T, 8>(static_cast<T*>(p.out[1]) + m * p.ldo + n, du, 8);
+        mm_store<T, R>(static_cast<T*>(p.out[0]) + m * p.ldo + n, da, R);
+        mm_store<T, R>(static_cast<T*>(p.out[1]) + m * p.ldo + n, du, R);
     }
+}
+// Columns that an epilogue writes.
+template <int EPI> __device__ __forceinline__ int64_t mm_width(const MmArgs& p) { return EPI == kMmFfnBwd ? p.ldo : p.N; }
+
+// R columns of sums at (m, n): one side, or gate and up.
+template <int EPI, typename T, int SC, bool DUAL, int R>
+__device__ __forceinline__ void mm_finish(const MmArgs& p, void* out, int part, int64_t m, int64_t n, float (&v)[DUAL ? 2 : 1][R]) {
+    if constexpr (EPI == kMmPart) {
+#pragma unroll
+        for (int i = 0; i < (DUAL ? 2 : 1); ++i)
+            mm_store<float, R>(p.part + (((int64_t)part * (DUAL ? 2 : 1) + i) * p.M + m) * p.N + n, v[i], p.N - n);
+    } else if constexpr (DUAL) {
+        mm_gate<EPI, T, R>(p, m, n, v[0], v[1]);
+    } else {
+        if (SC == kMmRow) {
+            const float sx = p.xs[m];
+#pragma unroll
+            for (int i = 0; i < R; ++i) v[0][i] *= sx * p.ws[0][n + i < p.N ? n + i : p.N - 1];
+        }
+        mm_store<T, R>(static_cast<T*>(out) + m * p.ldo + n, v[0], p.N - n);
+    }
+}
+
+// Adds the parts in their order; 4 columns a thread.
+template <int SC, bool DUAL, int EPI, typename T>
+__global__ __launch_bounds__(256) void k_mm_join(MmArgs p) {
+    constexpr int kSides = DUAL ? 2 : 1;
+    const int64_t per = (mm_width<EPI>(p) + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= per * p.M) return;
+    const int64_t m = i / per, n = i % per * 4;
+    float v[kSides][4] = {};
+    if (n < p.N)
+        for (int s = 0; s < p.splits; ++s)
+#pragma unroll
+            for (int k = 0; k < kSides; ++k) {
+                float x[4];
+                mm_load<float, 4>(p.part + (((int64_t)s * kSides + k) * p.M + m) * p.N + n, x, p.N - n);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[k][j] += x[j];
+            }
+    mm_finish<EPI, T, SC, DUAL, 4>(p, p.out[0], 0, m, n, v);
 }
 
 // Which of W's rows make up a wave's tile j of the register side: rows 4 g + i of the tile are rows
@@ -296,86 +341,72 @@ template <int KIND, int SC, bool DUAL, int MT, int NT>
 struct MmSums {
     static constexpr bool kScaled = SC == kMmBlock || SC == kMmGroup;
     f32x4 acc[MT][NT] = {};
-    // One step for X tile t; sx: the scale of the lane's X row, sw of W's rows: one for all (block; gate and up where
-    // there are two), or one for each of the lane's columns (group).
-    __device__ __forceinline__ void step(int t, const MmFrag<KIND>& x, const MmFrag<KIND> (&w)[NT], float sx, const float (&sw)[NT][4]) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            if constexpr (kScaled) {
-                const f32x4 c = mm_mma(w[j], x, f32x4{0.f, 0.f, 0.f, 0.f});
-                add(t, j, c, sx, sw[j]);
-            } else {
-                acc[t][j] = mm_mma(w[j], x, acc[t][j]);
-            }
-        }
-    }
+    // A step's sums of X tile t and W tile j; sx: the scale of the lane's X row, sw of W's rows: one for all (block), or one
+    // for each of the lane's columns (group).
     __device__ __forceinline__ void add(int t, int j, f32x4 c, float sx, const float (&sw)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(c[i], SC == kMmBlock ? sx * sw[0] : sx * sw[i], acc[t][j][i]);
     }
     // Hands the lane's outputs on: X's row m0 + 16 t + ln, the columns that MmCols names.
     template <int EPI, typename T, bool PAIR>
-    __device__ __forceinline__ void finish(const MmArgs& p, T* out, int64_t m0, int64_t n0) const {
+    __device__ __forceinline__ void finish(const MmArgs& p, void* out, int part, int64_t m0, int64_t n0) const {
         using C = MmCols<PAIR, DUAL>;
+        constexpr int kRun = PAIR ? 8 : 4;
         const int ln = threadIdx.x & 15, gq = threadIdx.x >> 4 & 3;
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             const int64_t m = m0 + 16 * t + ln;
             if (m >= p.M) continue;
-            const float sx = SC == kMmRow ? p.xs[m] : 1.f;
-            constexpr int kRun = PAIR ? 8 : 4;
 #pragma unroll
             for (int q = 0; q < NT; q += DUAL ? 4 : kRun / 4) {
                 const int64_t n = n0 + C::col(q, gq);
-                if (n >= p.N) continue;
+                if (n >= mm_width<EPI>(p)) continue;
                 float v[DUAL ? 2 : 1][kRun];
 #pragma unroll
                 for (int j = 0; j < (DUAL ? 4 : kRun / 4); ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[DUAL ? j / 2 : 0][(j % (kRun / 4)) * 4 + i] = acc[t][q + j][i];
-                if constexpr (DUAL) {
-                    mm_gate<EPI, T>(p, m, n, v[0], v[1]);
-                } else {
-                    if (SC == kMmRow)
-#pragma unroll
-                        for (int i = 0; i < kRun; ++i) v[0][i] *= sx * p.ws[0][n + i < p.N ? n + i : p.N - 1];
-                    mm_store<T, kRun>(out + m * p.ldo + n, v[0], p.N - n);
-                }
+                mm_finish<EPI, T, SC, DUAL, kRun>(p, out, part, m, n, v);
             }
         }
     }
 };
 
 // 128 x 128 outputs (two sides: 128 x 64 of each) by four waves of 64 x 64, any sizes and addresses: chunks go through
-// registers, one tile of each operand in LDS.
+// registers, the next step's on their way while one is multiplied; one tile of each operand in LDS.
 template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
 __global__ __launch_bounds__(256) void k_mm_any(MmArgs p) {
     constexpr int E = mm_size<KIND>(), MT = 4, NT = 4;
     using C = MmCols<mm_pair<T, WT, DUAL>(), DUAL>;
     constexpr int kSteps = kMmStep / E;  // of the contraction per step
     constexpr int kCols = DUAL ? 64 : 128;
+    using Sums = MmSums<KIND, SC, DUAL, MT, NT>;
     using X = MmTile<E, 128, XT, kNear>;
     using W = MmTile<E, kCols, WT, C::kFar>;
     __shared__ __align__(16) uint8_t xt[128 * kMmStep], wt[128 * kMmStep];
     const int wave = wave_id(), wm = wave & 1, wn = wave >> 1;
     const int ln = threadIdx.x & 15, gq = threadIdx.x >> 4 & 3;
-    const int64_t tm = (p.M + 127) / 128;
-    const int64_t m0 = (blockIdx.x % tm) * 128, n0 = (blockIdx.x / tm) * kCols;
-    const int z = p.outs > 1 ? (int)blockIdx.y : 0;
-    const int64_t per = (p.K + kSteps - 1) / kSteps;
-    MmSums<KIND, SC, DUAL, MT, NT> sums;
-    for (int64_t it = 0; it < per * p.segs; ++it) {
-        const int seg = (int)(it / per);
-        const int64_t kt = it % per, k0 = kt * kSteps;
-        u32x4 cx[4], cw[4];
+    const int64_t tm = (p.M + 127) / 128, tn = (p.N + kCols - 1) / kCols;
+    const int64_t m0 = (blockIdx.x % tm) * 128, n0 = (blockIdx.x / tm % tn) * kCols;
+    const int rest = (int)(blockIdx.x / (tm * tn)), z = p.outs > 1 ? rest : 0, part = p.splits ? rest : 0;
+    const int32_t per = (int32_t)((p.K + kSteps - 1) / kSteps);
+    const int32_t begin = part * p.share, end = p.splits ? min(begin + p.share, per * p.segs) : per * p.segs;
+    Sums sums;
+    u32x4 cx[4], cw[4];
+    auto load = [&](int32_t it) {
+        const int seg = it >= per ? 1 : 0;
+        const int64_t k0 = (int64_t)(it - seg * per) * kSteps;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cx[i] = X::load(p.x[XT ? z : seg], p.ldx, m0, p.M, k0, p.K, threadIdx.x + 256 * i);
+        for (int i = 0; i < 4; ++i) cx[i] = X::load((XT ? z : seg) ? p.x[1] : p.x[0], p.ldx, m0, p.M, k0, p.K, threadIdx.x + 256 * i);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int c = threadIdx.x + 256 * i;
             if constexpr (DUAL) cw[i] = W::load(p.w[i / 2], p.ldw, n0, p.N, k0, p.K, c - 512 * (i / 2));
-            else cw[i] = W::load(p.w[seg], p.ldw, n0, p.N, k0, p.K, c);
+            else cw[i] = W::load(seg ? p.w[1] : p.w[0], p.ldw, n0, p.N, k0, p.K, c);
         }
+    };
+    if (begin < end) load(begin);
+    for (int32_t it = begin; it < end; ++it) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -385,37 +416,35 @@ __global__ __launch_bounds__(256) void k_mm_any(MmArgs p) {
             else *reinterpret_cast<u32x4*>(wt + W::lds(c)) = cw[i];
         }
         __syncthreads();
-        MmFrag<KIND> fx[MT], fw[NT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            if constexpr (XT) mm_read_turned<KIND, 128>(fx[t], xt, wm * 64 + 16 * t, 4);
-            else mm_read<KIND, kNear>(fx[t], xt, wm * 64 + 16 * t + ln);
-        }
+        if (it + 1 < end) load(it + 1);
+        MmFrag<KIND> fx, fw[NT];
+        float sw[NT][4];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             if constexpr (WT) mm_read_turned<KIND, 128>(fw[j], wt, wn * 64 + C::row(j), C::kStride);
             else mm_read<KIND, C::kFar>(fw[j], wt + (DUAL ? 64 * kMmStep * (j / 2) : 0), wn * (kCols / 2) + C::row(j) + C::kStride * (ln >> 2) + (ln & 3));
-        }
-        float sx[MT], sw[NT][4];
-        if constexpr (MmSums<KIND, SC, DUAL, MT, NT>::kScaled) {
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const int64_t m = m0 + wm * 64 + 16 * t + ln;
-                sx[t] = p.xs[(m < p.M ? m : p.M - 1) * p.kb + kt];
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
+            if constexpr (Sums::kScaled)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int64_t n = n0 + wn * 64 + C::col(j, gq) + i;
-                    if (SC == kMmGroup) sw[j][i] = p.ws[0][(n < p.N ? n : p.N - 1) * p.kb + kt];
-                    else sw[j][i] = p.ws[DUAL ? j / 2 : 0][n0 / 128 * p.kb + kt];
+                    if (SC == kMmGroup) sw[j][i] = p.ws[0][min(n0 + wn * 64 + C::col(j, gq) + i, p.N - 1) * p.kb + it];
+                    else sw[j][i] = p.ws[DUAL ? j / 2 : 0][n0 / 128 * p.kb + it];
                 }
         }
 #pragma unroll
-        for (int t = 0; t < MT; ++t) sums.step(t, fx[t], fw, sx[t], sw);
+        for (int t = 0; t < MT; ++t) {
+            if constexpr (XT) mm_read_turned<KIND, 128>(fx, xt, wm * 64 + 16 * t, 4);
+            else mm_read<KIND, kNear>(fx, xt, wm * 64 + 16 * t + ln);
+            if constexpr (Sums::kScaled) {
+                const float sx = p.xs[min(m0 + wm * 64 + 16 * t + ln, p.M - 1) * p.kb + it];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) sums.add(t, j, mm_mma(fw[j], fx, f32x4{0.f, 0.f, 0.f, 0.f}), sx, sw[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) sums.acc[t][j] = mm_mma(fw[j], fx, sums.acc[t][j]);
+            }
+        }
     }
-    sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, static_cast<T*>(p.out[z]), m0 + wm * 64, n0 + wn * (kCols / 2));
+    sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, z ? p.out[1] : p.out[0], part, m0 + wm * 64, n0 + wn * (kCols / 2));
 }
 
 // ---- the same, memory to LDS without registers ----------------------------------------------
@@ -473,8 +502,9 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
     const int32_t tm = (int32_t)((p.M + BM - 1) / BM), tn = (int32_t)((p.N + kCols - 1) / kCols);
     const MmPlace at(blockIdx.x, gridDim.x, tm, tn);
     const int64_t m0 = (int64_t)at.m * BM, n0 = (int64_t)at.n * kCols;
-    const int z = p.outs > 1 ? at.rest : 0;
-    const int32_t per = (int32_t)((p.K + kSteps - 1) / kSteps), total = per * p.segs;
+    const int z = p.outs > 1 ? at.rest : 0, part = p.splits ? at.rest : 0;
+    const int32_t per = (int32_t)((p.K + kSteps - 1) / kSteps);
+    const int32_t begin = part * p.share, end = p.splits ? min(begin + p.share, per * p.segs) : per * p.segs;
 
     // Chunks behind an operand's last row or column repeat its last one (which starts in it, so it lies at or behind the
     // tile's start; a memory row is whole chunks).
@@ -533,11 +563,12 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
     const uint32_t lds0 = mm_lds(sh) + wave * 1024;
 
     // Where the next step's tiles come from (scalars, whatever the compiler makes of the loop).
-    uint64_t xs = mm_uniform((XT ? (z ? p.x[1] : p.x[0]) : p.x[0]) + (XT ? m0 * E : m0 * p.ldx));
-    uint64_t ws0 = mm_uniform(p.w[0] + (WT ? n0 * E : n0 * p.ldw)), ws1 = mm_uniform(p.w[1] + (WT ? n0 * E : n0 * p.ldw));
     const int64_t xstep = XT ? kSteps * p.ldx : kMmStep, wstep = WT ? kSteps * p.ldw : kMmStep;
     const int32_t whole = (int32_t)(p.K / kSteps), rest = (int32_t)(p.K % kSteps);
-    int32_t kt = 0;
+    int32_t kt = begin >= per ? begin - per : begin;
+    const uint64_t second = mm_uniform(p.w[1] + (WT ? n0 * E : n0 * p.ldw));
+    uint64_t xs = mm_uniform((XT ? (z ? p.x[1] : p.x[0]) : (begin >= per ? p.x[1] : p.x[0])) + (XT ? m0 * E : m0 * p.ldx) + kt * xstep);
+    uint64_t ws0 = mm_uniform((begin >= per && !DUAL ? p.w[1] : p.w[0]) + (WT ? n0 * E : n0 * p.ldw) + kt * wstep), ws1 = second + kt * wstep;
     auto fetch = [&](int stage) {
         const uint32_t xl = lds0 + stage * kStage, wl = xl + kXB;
         if (__builtin_expect(kt < whole, 1)) {
@@ -565,7 +596,7 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
         if (++kt == per && p.segs > 1) {
             kt = 0;
             xs = mm_uniform(p.x[1] + m0 * p.ldx);
-            ws0 = ws1;
+            ws0 = second;
         }
         kt = __builtin_amdgcn_readfirstlane(kt);
     };
@@ -573,19 +604,19 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
     // The lane's chunks of its first X row; the rows of the next tiles lie whole numbers of 16 rows on, with the same keys.
     const uint32_t xl0 = mm_at<kNear>(wm * (BM / 2) + ln, gq), xl1 = mm_at<kNear>(wm * (BM / 2) + ln, gq + 4);
     Sums sums;
-    if (total > 0) {
-        fetch(0);
+    if (begin < end) {  // (a part begins with a multiple of four steps)
+        fetch(begin & 1);
         if constexpr (Sums::kScaled) {
-            fetch_scales(0);
-            keep_scales(0);
+            fetch_scales(begin);
+            keep_scales(begin);
         }
     }
-    for (int32_t it = 0; it < total; ++it) {
+    for (int32_t it = begin; it < end; ++it) {
         mm_meet();
         if constexpr (Sums::kScaled) {
             // (what was loaded has arrived with the step's tiles)
-            if ((it & 3) == 1 && it + 3 < total) keep_scales(it + 3);
-            if ((it & 3) == 0 && it + 4 < total) fetch_scales(it + 4);
+            if ((it & 3) == 1 && it + 3 < end) keep_scales(it + 3);
+            if ((it & 3) == 0 && it + 4 < end) fetch_scales(it + 4);
         }
         const uint8_t* xt = sh + (it & 1) * kStage;
         const uint8_t* wt = xt + kXB;
@@ -626,7 +657,7 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (it + 1 < total) fetch(~it & 1);
+        if (it + 1 < end) fetch(~it & 1);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (!WT)
 #pragma unroll
@@ -664,18 +695,204 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) sums.add(MT - 1, j, c[(MT - 1) & 1][j], sx[(MT - 1) & 3], sw[j]);
     }
-    sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, static_cast<T*>(p.out[z]), m0 + wm * (BM / 2), n0 + wn * (kCols / 4));
+    sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, z ? p.out[1] : p.out[0], part, m0 + wm * (BM / 2), n0 + wn * (kCols / 4));
 }
 
-inline int64_t mm_blocks(int64_t M, int64_t N, bool dual, int BM) { return ((M + BM - 1) / BM) * ((N + (dual ? 127 : 255)) / (dual ? 128 : 256)); }
+// ---- few rows of X ---------------------------------------------------------------------------
+// 16 W rows (of each side) by a workgroup whose waves share the contraction: W is read once, straight into the matrix
+// instructions' registers, several steps of a wave at a time; X (at most 16 MT rows) comes from the caches. The waves' sums
+// meet in LDS. WHOLE: memory rows are whole chunks.
+template <int KIND, int SC, bool DUAL, int EPI, typename T, int MT, int WAVES, bool WHOLE>
+__global__ __launch_bounds__(64 * WAVES) void k_mm_few(MmArgs p) {
+    constexpr int E = mm_size<KIND>(), kSides = DUAL ? 2 : 1;
+    // steps at a time: what the registers of 2 or 4 waves a SIMD hold
+    constexpr int kAt = !WHOLE ? 1 : (WAVES == 16 ? (MT + kSides <= 3 ? 2 : 1) : (MT == 4 ? 2 : 4));
+    constexpr int kSteps = kMmStep / E;
+    constexpr bool kScaled = SC == kMmBlock || SC == kMmGroup;
+    __shared__ f32x4 sh[WAVES][kSides * MT][64];
+    const int wave = wave_id(), lane = threadIdx.x & 63, ln = lane & 15, gq = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int32_t per = (int32_t)((p.K + kSteps - 1) / kSteps);
+    const uint8_t *wr[kSides], *xr[MT];
+#pragma unroll
+    for (int i = 0; i < kSides; ++i) wr[i] = p.w[i] + min(n0 + ln, p.N - 1) * p.ldw;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) xr[t] = p.x[0] + min((int64_t)16 * t + ln, p.M - 1) * p.ldx;
+    auto load = [&](const uint8_t* row, int64_t off) {
+        if constexpr (WHOLE) return off < p.K * E ? *reinterpret_cast<const u32x4*>(row + off) : u32x4{0, 0, 0, 0};
+        else return mm_chunk(row, off, p.K * E);
+    };
+    f32x4 acc[kSides][MT] = {};
+    for (int32_t first = wave; first < per; first += WAVES * kAt) {
+        u32x4 w[kAt][kSides][2], x[kAt][MT][2];
+        float sx[kAt][MT], sw[kAt][kSides][4];
+#pragma unroll
+        for (int a = 0; a < kAt; ++a) {
+            const int32_t kt = first + a * WAVES;
+            if (kt >= per) break;
+            const int64_t off = (int64_t)kt * kMmStep + 16 * gq;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int i = 0; i < kSides; ++i) w[a][i][h] = load(wr[i], off + 64 * h);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) x[a][t][h] = load(xr[t], off + 64 * h);
+            }
+            if constexpr (kScaled) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t) sx[a][t] = p.xs[min((int64_t)16 * t + ln, p.M - 1) * p.kb + kt];
+#pragma unroll
+                for (int i = 0; i < kSides; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        sw[a][i][j] = SC == kMmBlock ? p.ws[i][n0 / 128 * p.kb + kt] : p.ws[i][min(n0 + 4 * gq + j, p.N - 1) * p.kb + kt];
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < kAt; ++a) {
+            if (first + a * WAVES >= per) break;
+            MmFrag<KIND> fw[kSides];
+#pragma unroll
+            for (int i = 0; i < kSides; ++i) fw[i].set(w[a][i][0], w[a][i][1]);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                MmFrag<KIND> fx;
+                fx.set(x[a][t][0], x[a][t][1]);
+#pragma unroll
+                for (int i = 0; i < kSides; ++i) {
+                    if constexpr (kScaled) {
+                        const f32x4 c = mm_mma(fw[i], fx, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[i][t][j] = fmaf(c[j], sx[a][t] * sw[a][i][j], acc[i][t][j]);
+                    } else {
+                        acc[i][t] = mm_mma(fw[i], fx, acc[i][t]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kSides; ++i)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) sh[wave][i * MT + t][lane] = acc[i][t];
+    __syncthreads();
+    if (wave >= MT) return;
+    const int64_t m = 16 * wave + ln, n = n0 + 4 * gq;
+    if (m >= p.M || n >= mm_width<EPI>(p)) return;
+    float v[kSides][4] = {};
+#pragma unroll
+    for (int i = 0; i < kSides; ++i)
+#pragma unroll
+        for (int s = 0; s < WAVES; ++s) {
+            const f32x4 c = sh[s][i * MT + wave][lane];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] += c[j];
+        }
+    mm_finish<EPI, T, SC, DUAL, 4>(p, p.out[0], 0, m, n, v);
+}
 
-// Whether k_mm takes the operands: `x`, `w` all pointers of a side.
+// ---- which kernel ----------------------------------------------------------------------------
+inline int64_t mm_blocks(int64_t M, int64_t N, bool dual, int BM) { return ((M + BM - 1) / BM) * ((N + (dual ? 127 : 255)) / (dual ? 128 : 256)); }
+inline int64_t mm_any_blocks(int64_t M, int64_t N, bool dual) { return ((M + 127) / 128) * ((N + (dual ? 63 : 127)) / (dual ? 64 : 128)); }
+
+// Whether k_mm takes the operands.
 inline bool mm_fits(const MmArgs& p) {
     uint64_t bits = (uint64_t)(p.ldx | p.ldw);
     for (int i = 0; i < 2; ++i) bits |= (uint64_t)(uintptr_t)p.x[i] | (uint64_t)(uintptr_t)p.w[i];
-    return bits % 16 == 0 && p.ldx < (1 << 23) && p.ldw < (1 << 23) && p.kb < (1 << 21);
+    return bits % 16 == 0 && p.ldx < (1 << 23) && p.ldw < (1 << 23);
 }
 
-inline int64_t mm_any_blocks(int64_t M, int64_t N, bool dual) { return ((M + 127) / 128) * ((N + (dual ? 63 : 127)) / (dual ? 64 : 128)); }
+constexpr int kMmFew = 64;  // X rows of k_mm_few at most
+
+// What a product of these sizes runs as: by sizes alone, so that the workspace can be told beforehand (whatever the
+// operands' addresses: k_mm and k_mm_any split alike).
+struct MmPlan {
+    bool few;
+    int bm;
+    int splits, share;
+    size_t bytes;  // of the parts
+};
+inline MmPlan mm_plan(int kind, int64_t M, int64_t N, int64_t K, int segs, int outs, bool turned, bool dual) {
+    MmPlan r{};
+    const int steps = kMmStep / (kind == kMmBf16 ? 2 : (kind == kMmF32 ? 4 : 1));
+    r.few = !turned && segs == 1 && outs == 1 && M <= kMmFew;
+    if (r.few) return r;
+    const int64_t total = (K + steps - 1) / steps * segs;
+    r.bm = kind == kMmF8x || kind == kMmF32 || M <= 128 || mm_blocks(M, N, dual, 256) * outs < 256 ? 128 : 256;
+    const int64_t blocks = mm_blocks(M, N, dual, r.bm);
+    if (outs == 1 && blocks <= 128 && total >= 16) {
+        int64_t want = 256 / blocks, most = total / 8;
+        if (want > most) want = most;
+        if (want > 32) want = 32;
+        if (want > 1) {
+            r.share = (int)(((total + want - 1) / want + 3) / 4 * 4);
+            r.splits = (int)((total + r.share - 1) / r.share);
+            if (r.splits < 2) r.splits = r.share = 0;
+            r.bytes = (size_t)r.splits * (dual ? 2 : 1) * M * N * 4;
+        }
+    }
+    return r;
+}
+
+template <int KIND, int SC, bool DUAL, int EPI, typename T, int MT, bool WHOLE>
+hipError_t mm_few(const MmArgs& p, hipStream_t st) {
+    const int64_t blocks = ((EPI == kMmFfnBwd ? p.ldo : p.N) + 15) / 16;
+    const bool many = blocks <= 128 && p.K * mm_size<KIND>() >= 16 * kMmStep && MT * (DUAL ? 2 : 1) <= 4;
+    if (blocks > UINT32_MAX / 1024) return hipErrorInvalidConfiguration;
+    if constexpr (MT * (DUAL ? 2 : 1) <= 4)
+        if (many) {
+            hipLaunchKernelGGL((k_mm_few<KIND, SC, DUAL, EPI, T, MT, 16, WHOLE>), dim3((unsigned)blocks), dim3(1024), 0, st, p);
+            return hipGetLastError();
+        }
+    hipLaunchKernelGGL((k_mm_few<KIND, SC, DUAL, EPI, T, MT, 8, WHOLE>), dim3((unsigned)blocks), dim3(512), 0, st, p);
+    return hipGetLastError();
+}
+template <int KIND, int SC, bool DUAL, int EPI, typename T, int MT>
+hipError_t mm_few(const MmArgs& p, hipStream_t st) {
+    return mm_fits(p) ? mm_few<KIND, SC, DUAL, EPI, T, MT, true>(p, st) : mm_few<KIND, SC, DUAL, EPI, T, MT, false>(p, st);
+}
+
+template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
+hipError_t mm_tiles(const MmArgs& p, int bm, hipStream_t st) {
+    const int64_t times = p.splits ? p.splits : p.outs;
+    if (mm_fits(p)) {
+        const int64_t blocks = mm_blocks(p.M, p.N, DUAL, bm) * times;
+        if (blocks > UINT32_MAX / 512 || blocks > INT32_MAX) return hipErrorInvalidConfiguration;
+        if constexpr (KIND != kMmF8x && KIND != kMmF32 && EPI != kMmPart)
+            if (bm == 256) {
+                hipLaunchKernelGGL((k_mm<KIND, SC, XT, WT, DUAL, EPI, T, 256>), dim3((unsigned)blocks), dim3(512), 0, st, p);
+                return hipGetLastError();
+            }
+        hipLaunchKernelGGL((k_mm<KIND, SC, XT, WT, DUAL, EPI, T, 128>), dim3((unsigned)blocks), dim3(512), 0, st, p);
+        return hipGetLastError();
+    }
+    const int64_t blocks = mm_any_blocks(p.M, p.N, DUAL) * times;
+    if (blocks > UINT32_MAX / 256) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((k_mm_any<KIND, SC, XT, WT, DUAL, EPI, T>), dim3((unsigned)blocks), dim3(256), 0, st, p);
+    return hipGetLastError();
+}
+
+// `part`: the workspace that mm_plan asked for.
+template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
+hipError_t mm_run(MmArgs p, void* part, hipStream_t st) {
+    const MmPlan r = mm_plan(KIND, p.M, p.N, p.K, p.segs, p.outs, XT || WT, DUAL);
+    if constexpr (!XT && !WT)
+        if (r.few) {
+            if (p.M <= 16) return mm_few<KIND, SC, DUAL, EPI, T, 1>(p, st);
+            if (p.M <= 32) return mm_few<KIND, SC, DUAL, EPI, T, 2>(p, st);
+            return mm_few<KIND, SC, DUAL, EPI, T, 4>(p, st);
+        }
+    if constexpr (!XT)  // (dw has two outputs and is not split)
+        if (r.splits) {
+            p.splits = r.splits;
+            p.share = r.share;
+            p.part = static_cast<float*>(part);
+            if (hipError_t e = mm_tiles<KIND, SC, XT, WT, DUAL, kMmPart, T>(p, r.bm, st)) return e;
+            const int64_t blocks = (((EPI == kMmFfnBwd ? p.ldo : p.N) + 3) / 4 * p.M + 255) / 256;
+            hipLaunchKernelGGL((k_mm_join<SC, DUAL, EPI, T>), dim3((unsigned)blocks), dim3(256), 0, st, p);
+            return hipGetLastError();
+        }
+    return mm_tiles<KIND, SC, XT, WT, DUAL, EPI, T>(p, r.bm, st);
+}
 
 }  // namespace gdn

@@ -25,15 +25,7 @@ hipError_t mm8(const Mm8Args& a, hipStream_t st) {
     p.kb = (a.K + 127) / 128;
     p.out[0] = a.y;
     p.ldo = a.N;
-    if (mm_fits(p)) {
-        constexpr int BM = KIND == kMmF8x || KIND == kMmF32 ? 128 : 256;
-        hipLaunchKernelGGL((k_mm<KIND, SC, false, false, false, kMmOut, T, BM>), dim3((unsigned)mm_blocks(a.M, a.N, false, BM)), dim3(512), 0, st, p);
-        return hipGetLastError();
-    }
-    const int64_t blocks = mm_any_blocks(a.M, a.N, false);
-    if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_mm_any<KIND, SC, false, false, false, kMmOut, T>), dim3((unsigned)blocks), dim3(256), 0, st, p);
-    return hipGetLastError();
+    return mm_run<KIND, SC, false, false, false, kMmOut, T>(p, a.ws, st);
 }
 template <int KIND, typename T>
 hipError_t mm8_s(const Mm8Args& a, int scales, hipStream_t st) {
@@ -43,7 +35,9 @@ hipError_t mm8_s(const Mm8Args& a, int scales, hipStream_t st) {
 
 }  // namespace
 
-size_t mm8_ws(int64_t M, int64_t N, int64_t K, int out_dtype, int scales) { return 0; }
+size_t mm8_ws(int64_t M, int64_t N, int64_t K, int out_dtype) {
+    return mm_plan(out_dtype == 1 ? kMmF8x : kMmF8, M, N, K, 1, 1, false, false).bytes;
+}
 
 hipError_t launch_mm8(const Mm8Args& a, int out_dtype, int scales, hipStream_t st) {
     if (a.M == 0) return hipSuccess;
