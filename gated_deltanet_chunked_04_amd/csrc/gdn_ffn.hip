@@ -40,7 +40,7 @@ __global__ __launch_bounds__(256) void k_ffn_act_bwd(MmArgs p) {
     float a[8], u[8];
     mm_load<float, 8>(p.pre + m * p.N + n, a, p.N - n);
     mm_load<float, 8>(p.pre + (p.M + m) * p.N + n, u, p.N - n);
-    mm_gate<kMmFfnBwd, T, 8>(p, m, n, a, u);
+    mm_gate<kMmFfnBwd, T, 8, false>(p, m, n, a, u);
 }
 
 // columns of the gradients of gate and up in the workspace: whole vectors, zeros behind F
@@ -100,7 +100,7 @@ hipError_t bwd(const FfnArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <int KIND, typename T>
+template <int KIND, typename T, int EPI = kMmFfn>
 hipError_t ffn8(const FfnArgs& a, void* h, void* part, hipStream_t st) {
     MmArgs p = block_args(a, 1);
     p.xs = a.xs;
@@ -108,7 +108,8 @@ hipError_t ffn8(const FfnArgs& a, void* h, void* part, hipStream_t st) {
     p.ws[1] = a.us;
     p.kb = (a.K + 127) / 128;
     p.out[0] = h;
-    return mm_run<KIND, kMmBlock, false, false, true, kMmFfn, T>(p, part, st);
+    p.scale = a.hs;
+    return mm_run<KIND, kMmBlock, false, false, true, EPI, T>(p, part, st);
 }
 
 }  // namespace
@@ -118,12 +119,16 @@ size_t ffn_fwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
 }
 size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
     const int kind = dtype == 1 ? kMmF32 : kMmBf16;
-    const size_t again = mm_plan(kind, M, F, K, 1, 1, false, true).bytes, dx = mm_plan(kind, M, K, F, 2, 1, true, false).bytes;
-    return 2 * align256((size_t)(M * grad_ld(F) * (dtype == 1 ? 4 : 2))) + (again > dx ? again : dx);
+    size_t part = mm_plan(kind, M, F, K, 1, 1, false, true).bytes;
+    for (size_t b : {mm_plan(kind, M, K, F, 2, 1, true, false).bytes, mm_plan(kind, F, K, M, 1, 2, true, false).bytes})
+        if (b > part) part = b;
+    return 2 * align256((size_t)(M * grad_ld(F) * (dtype == 1 ? 4 : 2))) + part;
 }
-// the block's fp32 output in front of its quantisation, and the parts
+// Few rows, or a split contraction: the parts, and the block's fp32 output in front of its quantisation. Otherwise the
+// workgroup that has a row's 128 columns quantises them.
 size_t ffn8_ws(int64_t M, int64_t K, int64_t F, int dtype, bool quant) {
-    return (quant ? align256((size_t)(M * F * 4)) : 0) + mm_plan(quant || dtype == 1 ? kMmF8x : kMmF8, M, F, K, 1, 1, false, true).bytes;
+    const MmPlan r = mm_plan(quant || dtype == 1 ? kMmF8x : kMmF8, M, F, K, 1, 1, false, true);
+    return (quant && (r.few || r.splits) ? align256((size_t)(M * F * 4)) : 0) + r.bytes;
 }
 
 hipError_t launch_ffn_fwd(const FfnArgs& a, int dtype, hipStream_t st) {
@@ -137,6 +142,8 @@ hipError_t launch_ffn_bwd(const FfnArgs& a, int dtype, hipStream_t st) {
 hipError_t launch_ffn8(const FfnArgs& a, int dtype, hipStream_t st) {
     if (a.M == 0) return hipSuccess;
     if (!a.hs) return dtype == 1 ? ffn8<kMmF8x, float>(a, a.h, a.ws, st) : ffn8<kMmF8, bf16_t>(a, a.h, a.ws, st);
+    const MmPlan r = mm_plan(kMmF8x, a.M, a.F, a.K, 1, 1, false, true);
+    if (!r.few && !r.splits) return ffn8<kMmF8x, float, kMmFfn8>(a, a.h, nullptr, st);
     if (hipError_t e = ffn8<kMmF8x, float>(a, a.ws, a.ws + align256((size_t)(a.M * a.F * 4)), st)) return e;
     const QuantArgs q{a.M, a.F, a.ws, static_cast<uint8_t*>(a.h), a.hs};
     return launch_quant(q, 1, 1, false, st);

@@ -201,7 +201,8 @@ struct MmArgs {
     const void* d_h;      // [M, N]: the gradient that enters the block's backward
     float* pre;           // [2, M, N] gate and up in fp32, or null
     int32_t act;          // 1 silu, 2 gelu_tanh
-    float* part;          // where the contraction is split: sums of each part, [splits, sides, M, N]
+    float* scale;         // of an e4m3 output [M, ceil(N/128)]
+    float* part;          // where the contraction is split: sums of each part, [outs, splits, sides, M, N]
     int32_t splits;       // parts of the contraction (0: one, without part)
     int32_t share;        // steps of a part
 };
@@ -229,12 +230,27 @@ __device__ __forceinline__ void mm_store(T* p, const float (&v)[N], int64_t n) {
     if (n >= N) {
         Raw<T, N> r;
         r.set(v);
-        __builtin_memcpy(p, r.w, sizeof(T) * N);  // (not past the cache: it joins the parts of a line)
+        store_raw<T, N>(p, r);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (i < n) p[i] = Elem<T>::from_f(v[i]);
     }
+}
+// 32 neighbouring fp32 columns of a row, of which lane group gq holds 8 gq .. 8 gq + 7: the groups trade halves, so that
+// each of two stores writes 64 bytes in a row. p: the first of the 32. The four lanes of a row call it together.
+__device__ __forceinline__ void mm_store32(float* p, const float (&v)[8]) {
+    const int gq = threadIdx.x >> 4 & 3;
+    float a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[4 + i]), false, false);
+        const auto y = __builtin_amdgcn_permlane32_swap(x[0], x[1], false, false);
+        a[i] = __uint_as_float(y[0]);  // columns 4 gq + i
+        b[i] = __uint_as_float(y[1]);  // columns 16 + 4 gq + i
+    }
+    mm_store<float, 4>(p + 4 * gq, a, 4);
+    mm_store<float, 4>(p + 16 + 4 * gq, b, 4);
 }
 template <typename T, int N>
 __device__ __forceinline__ void mm_load(const T* p, float (&v)[N], int64_t n) {
@@ -250,11 +266,11 @@ __device__ __forceinline__ void mm_load(const T* p, float (&v)[N], int64_t n) {
 
 // What is done with a lane's sums. kMmOut: y = sums (with kMmRow, times the rows' scales). kMmFfn: h = act(gate) up, and
 // gate and up themselves where `pre` is given. kMmFfnBwd: the gradients of gate and up from d_h. kMmPart: the sums of a
-// part of the contraction, for k_mm_join.
-enum MmEpi { kMmOut = 0, kMmFfn = 1, kMmFfnBwd = 2, kMmPart = 3 };
+// part of the contraction, for k_mm_join. kMmFfn8: h in e4m3 with a scale for 128 columns (a tile's).
+enum MmEpi { kMmOut = 0, kMmFfn = 1, kMmFfnBwd = 2, kMmPart = 3, kMmFfn8 = 4 };
 
-// R columns of the block at (m, n).
-template <int EPI, typename T, int R>
+// R columns of the block at (m, n). SHARED: by a wave whose four lane groups hold 32 neighbouring columns of a row.
+template <int EPI, typename T, int R, bool SHARED>
 __device__ __forceinline__ void mm_gate(const MmArgs& p, int64_t m, int64_t n, const float (&a)[R], const float (&u)[R]) {
     const int64_t left = p.N - n;
     if constexpr (EPI == kMmFfn) {
@@ -263,6 +279,14 @@ __device__ __forceinline__ void mm_gate(const MmArgs& p, int64_t m, int64_t n, c
         for (int i = 0; i < R; ++i) h[i] = Act(a[i], p.act, false).f * u[i];
         mm_store<T, R>(static_cast<T*>(p.out[0]) + m * p.ldo + n, h, left);
         if (p.pre) {
+            if constexpr (R == 8) {
+                const int64_t first = n - (8 * (threadIdx.x >> 4 & 3));
+                if (SHARED && first + 32 <= p.N) {
+                    mm_store32(p.pre + m * p.N + first, a);
+                    mm_store32(p.pre + (p.M + m) * p.N + first, u);
+                    return;
+                }
+            }
             mm_store<float, R>(p.pre + m * p.N + n, a, left);
             mm_store<float, R>(p.pre + (p.M + m) * p.N + n, u, left);
         }
@@ -292,7 +316,7 @@ __device__ __forceinline__ void mm_finish(const MmArgs& p, void* out, int part, 
         for (int i = 0; i < (DUAL ? 2 : 1); ++i)
             mm_store<float, R>(p.part + (((int64_t)part * (DUAL ? 2 : 1) + i) * p.M + m) * p.N + n, v[i], p.N - n);
     } else if constexpr (DUAL) {
-        mm_gate<EPI, T, R>(p, m, n, v[0], v[1]);
+        mm_gate<EPI, T, R, R == 8>(p, m, n, v[0], v[1]);
     } else {
         if (SC == kMmRow) {
             const float sx = p.xs[m];
@@ -310,9 +334,10 @@ __global__ __launch_bounds__(256) void k_mm_join(MmArgs p) {
     const int64_t per = (mm_width<EPI>(p) + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= per * p.M) return;
     const int64_t m = i / per, n = i % per * 4;
+    const int z = blockIdx.y;
     float v[kSides][4] = {};
     if (n < p.N)
-        for (int s = 0; s < p.splits; ++s)
+        for (int s = z * p.splits; s < (z + 1) * p.splits; ++s)
 #pragma unroll
             for (int k = 0; k < kSides; ++k) {
                 float x[4];
@@ -320,7 +345,7 @@ __global__ __launch_bounds__(256) void k_mm_join(MmArgs p) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[k][j] += x[j];
             }
-    mm_finish<EPI, T, SC, DUAL, 4>(p, p.out[0], 0, m, n, v);
+    mm_finish<EPI, T, SC, DUAL, 4>(p, z ? p.out[1] : p.out[0], 0, m, n, v);
 }
 
 // Which of W's rows make up a wave's tile j of the register side: rows 4 g + i of the tile are rows
@@ -372,36 +397,84 @@ struct MmSums {
     }
 };
 
+// h in e4m3: 128 columns of a row, which share a scale, are those of the four waves side by side. top: [rows of the tile][4]
+// in LDS, row0 this wave's first row of it; all waves call it when they are done with the tiles.
+template <class Sums, int MT>
+__device__ __forceinline__ void mm_finish8(Sums& sums, const MmArgs& p, uint32_t* top, int row0, int wn, int64_t m0, int64_t n0) {
+    const int ln = threadIdx.x & 15, gq = threadIdx.x >> 4 & 3;
+    const int64_t n = n0 + 32 * wn + 8 * gq, left = p.N - n;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float h = Act(sums.acc[t][j][i], p.act, false).f * sums.acc[t][2 + j][i];
+                sums.acc[t][j][i] = h;
+                if (4 * j + i < left) m = max(m, abs_bits(h));
+            }
+        m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+        if (gq == 0) top[(row0 + 16 * t + ln) * 4 + wn] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const int64_t m = m0 + 16 * t + ln;
+        if (m >= p.M || left <= 0) continue;
+        const u32x4 a = *reinterpret_cast<const u32x4*>(top + (row0 + 16 * t + ln) * 4);
+        const float scale = scale_of(max(max(a.x, a.y), max(a.z, a.w)));
+        const Divisor by(scale);
+        uint32_t w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f32x4 h = sums.acc[t][j];
+            w[j] = pack_e4m3(by.quotient(h[0]), by.quotient(h[1]), by.quotient(h[2]), by.quotient(h[3]));
+        }
+        uint8_t* q = static_cast<uint8_t*>(p.out[0]) + m * p.N + n;
+        if (left >= 8) {
+            store_e4m3<false>(q, w[0], w[1], 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left) q[i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
+        }
+        if (wn == 0 && gq == 0) p.scale[m * ((p.N + 127) / 128) + n0 / 128] = scale;
+    }
+}
+
 // 128 x 128 outputs (two sides: 128 x 64 of each) by four waves of 64 x 64, any sizes and addresses: chunks go through
 // registers, the next step's on their way while one is multiplied; one tile of each operand in LDS.
-template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
-__global__ __launch_bounds__(256) void k_mm_any(MmArgs p) {
+template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T, int WN>
+__global__ __launch_bounds__(128 * WN) void k_mm_any(MmArgs p) {
     constexpr int E = mm_size<KIND>(), MT = 4, NT = 4;
     using C = MmCols<mm_pair<T, WT, DUAL>(), DUAL>;
     constexpr int kSteps = kMmStep / E;  // of the contraction per step
-    constexpr int kCols = DUAL ? 64 : 128;
+    constexpr int kRows = 64 * WN, kCols = DUAL ? kRows / 2 : kRows, kThreads = 128 * WN;
+    constexpr int kXC = 1024 / kThreads;
     using Sums = MmSums<KIND, SC, DUAL, MT, NT>;
     using X = MmTile<E, 128, XT, kNear>;
     using W = MmTile<E, kCols, WT, C::kFar>;
-    __shared__ __align__(16) uint8_t xt[128 * kMmStep], wt[128 * kMmStep];
+    __shared__ __align__(16) uint8_t xt[128 * kMmStep], wt[kRows * kMmStep];
     const int wave = wave_id(), wm = wave & 1, wn = wave >> 1;
     const int ln = threadIdx.x & 15, gq = threadIdx.x >> 4 & 3;
     const int64_t tm = (p.M + 127) / 128, tn = (p.N + kCols - 1) / kCols;
     const int64_t m0 = (blockIdx.x % tm) * 128, n0 = (blockIdx.x / tm % tn) * kCols;
-    const int rest = (int)(blockIdx.x / (tm * tn)), z = p.outs > 1 ? rest : 0, part = p.splits ? rest : 0;
+    const int rest = (int)(blockIdx.x / (tm * tn)), z = rest % p.outs, part = rest / p.outs;
     const int32_t per = (int32_t)((p.K + kSteps - 1) / kSteps);
     const int32_t begin = part * p.share, end = p.splits ? min(begin + p.share, per * p.segs) : per * p.segs;
     Sums sums;
-    u32x4 cx[4], cw[4];
+    u32x4 cx[kXC], cw[4];
     auto load = [&](int32_t it) {
         const int seg = it >= per ? 1 : 0;
         const int64_t k0 = (int64_t)(it - seg * per) * kSteps;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cx[i] = X::load((XT ? z : seg) ? p.x[1] : p.x[0], p.ldx, m0, p.M, k0, p.K, threadIdx.x + 256 * i);
+        for (int i = 0; i < kXC; ++i) cx[i] = X::load((XT ? z : seg) ? p.x[1] : p.x[0], p.ldx, m0, p.M, k0, p.K, threadIdx.x + kThreads * i);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int c = threadIdx.x + 256 * i;
-            if constexpr (DUAL) cw[i] = W::load(p.w[i / 2], p.ldw, n0, p.N, k0, p.K, c - 512 * (i / 2));
+            const int c = threadIdx.x + kThreads * i;
+            if constexpr (DUAL) cw[i] = W::load(p.w[i / 2], p.ldw, n0, p.N, k0, p.K, c - 2 * kThreads * (i / 2));
             else cw[i] = W::load(seg ? p.w[1] : p.w[0], p.ldw, n0, p.N, k0, p.K, c);
         }
     };
@@ -409,10 +482,11 @@ __global__ __launch_bounds__(256) void k_mm_any(MmArgs p) {
     for (int32_t it = begin; it < end; ++it) {
         __syncthreads();
 #pragma unroll
+        for (int i = 0; i < kXC; ++i) *reinterpret_cast<u32x4*>(xt + X::lds(threadIdx.x + kThreads * i)) = cx[i];
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int c = threadIdx.x + 256 * i;
-            *reinterpret_cast<u32x4*>(xt + X::lds(c)) = cx[i];
-            if constexpr (DUAL) *reinterpret_cast<u32x4*>(wt + 64 * kMmStep * (i / 2) + W::lds(c - 512 * (i / 2))) = cw[i];
+            const int c = threadIdx.x + kThreads * i;
+            if constexpr (DUAL) *reinterpret_cast<u32x4*>(wt + kCols * kMmStep * (i / 2) + W::lds(c - 2 * kThreads * (i / 2))) = cw[i];
             else *reinterpret_cast<u32x4*>(wt + W::lds(c)) = cw[i];
         }
         __syncthreads();
@@ -421,8 +495,8 @@ __global__ __launch_bounds__(256) void k_mm_any(MmArgs p) {
         float sw[NT][4];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            if constexpr (WT) mm_read_turned<KIND, 128>(fw[j], wt, wn * 64 + C::row(j), C::kStride);
-            else mm_read<KIND, C::kFar>(fw[j], wt + (DUAL ? 64 * kMmStep * (j / 2) : 0), wn * (kCols / 2) + C::row(j) + C::kStride * (ln >> 2) + (ln & 3));
+            if constexpr (WT) mm_read_turned<KIND, kRows>(fw[j], wt, wn * 64 + C::row(j), C::kStride);
+            else mm_read<KIND, C::kFar>(fw[j], wt + (DUAL ? kCols * kMmStep * (j / 2) : 0), wn * (kCols / WN) + C::row(j) + C::kStride * (ln >> 2) + (ln & 3));
             if constexpr (Sums::kScaled)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -444,7 +518,12 @@ __global__ __launch_bounds__(256) void k_mm_any(MmArgs p) {
             }
         }
     }
-    sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, z ? p.out[1] : p.out[0], part, m0 + wm * 64, n0 + wn * (kCols / 2));
+    if constexpr (EPI == kMmFfn8) {
+        __syncthreads();
+        mm_finish8<Sums, MT>(sums, p, reinterpret_cast<uint32_t*>(xt), wm * 64, wn, m0 + wm * 64, n0);
+    } else {
+        sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, z ? p.out[1] : p.out[0], z * p.splits + part, m0 + wm * 64, n0 + wn * (kCols / WN));
+    }
 }
 
 // ---- the same, memory to LDS without registers ----------------------------------------------
@@ -502,7 +581,7 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
     const int32_t tm = (int32_t)((p.M + BM - 1) / BM), tn = (int32_t)((p.N + kCols - 1) / kCols);
     const MmPlace at(blockIdx.x, gridDim.x, tm, tn);
     const int64_t m0 = (int64_t)at.m * BM, n0 = (int64_t)at.n * kCols;
-    const int z = p.outs > 1 ? at.rest : 0, part = p.splits ? at.rest : 0;
+    const int z = at.rest % p.outs, part = at.rest / p.outs;
     const int32_t per = (int32_t)((p.K + kSteps - 1) / kSteps);
     const int32_t begin = part * p.share, end = p.splits ? min(begin + p.share, per * p.segs) : per * p.segs;
 
@@ -695,7 +774,12 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) sums.add(MT - 1, j, c[(MT - 1) & 1][j], sx[(MT - 1) & 3], sw[j]);
     }
-    sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, z ? p.out[1] : p.out[0], part, m0 + wm * (BM / 2), n0 + wn * (kCols / 4));
+    if constexpr (EPI == kMmFfn8) {
+        mm_meet();
+        mm_finish8<Sums, MT>(sums, p, reinterpret_cast<uint32_t*>(sh), wm * (BM / 2), wn, m0 + wm * (BM / 2), n0);
+    } else {
+        sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, z ? p.out[1] : p.out[0], z * p.splits + part, m0 + wm * (BM / 2), n0 + wn * (kCols / 4));
+    }
 }
 
 // ---- few rows of X ---------------------------------------------------------------------------
@@ -818,17 +902,20 @@ inline MmPlan mm_plan(int kind, int64_t M, int64_t N, int64_t K, int segs, int o
     r.few = !turned && segs == 1 && outs == 1 && M <= kMmFew;
     if (r.few) return r;
     const int64_t total = (K + steps - 1) / steps * segs;
-    r.bm = kind == kMmF8x || kind == kMmF32 || M <= 128 || mm_blocks(M, N, dual, 256) * outs < 256 ? 128 : 256;
-    const int64_t blocks = mm_blocks(M, N, dual, r.bm);
-    if (outs == 1 && blocks <= 128 && total >= 16) {
-        int64_t want = 256 / blocks, most = total / 8;
+    // 256 rows of X a tile, or 128 where that is quicker: rounds of 256 workgroups, a step of the larger tile taking 8
+    // parts of time and one of the smaller 5
+    const int64_t large = mm_blocks(M, N, dual, 256) * outs, small = mm_blocks(M, N, dual, 128) * outs;
+    r.bm = kind == kMmF8x || kind == kMmF32 || 5 * ((small + 255) / 256) < 8 * ((large + 255) / 256) ? 128 : 256;
+    if (small <= 128 && total >= 16) {
+        int64_t want = 256 / small, most = total / 8;
         if (want > most) want = most;
         if (want > 32) want = 32;
         if (want > 1) {
+            r.bm = 128;
             r.share = (int)(((total + want - 1) / want + 3) / 4 * 4);
             r.splits = (int)((total + r.share - 1) / r.share);
             if (r.splits < 2) r.splits = r.share = 0;
-            r.bytes = (size_t)r.splits * (dual ? 2 : 1) * M * N * 4;
+            r.bytes = (size_t)outs * r.splits * (dual ? 2 : 1) * M * N * 4;
         }
     }
     return r;
@@ -854,7 +941,7 @@ hipError_t mm_few(const MmArgs& p, hipStream_t st) {
 
 template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
 hipError_t mm_tiles(const MmArgs& p, int bm, hipStream_t st) {
-    const int64_t times = p.splits ? p.splits : p.outs;
+    const int64_t times = (int64_t)p.outs * (p.splits ? p.splits : 1);
     if (mm_fits(p)) {
         const int64_t blocks = mm_blocks(p.M, p.N, DUAL, bm) * times;
         if (blocks > UINT32_MAX / 512 || blocks > INT32_MAX) return hipErrorInvalidConfiguration;
@@ -866,9 +953,10 @@ hipError_t mm_tiles(const MmArgs& p, int bm, hipStream_t st) {
         hipLaunchKernelGGL((k_mm<KIND, SC, XT, WT, DUAL, EPI, T, 128>), dim3((unsigned)blocks), dim3(512), 0, st, p);
         return hipGetLastError();
     }
-    const int64_t blocks = mm_any_blocks(p.M, p.N, DUAL) * times;
-    if (blocks > UINT32_MAX / 256) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_mm_any<KIND, SC, XT, WT, DUAL, EPI, T>), dim3((unsigned)blocks), dim3(256), 0, st, p);
+    constexpr int kWide = EPI == kMmFfn8 ? 4 : 2;  // (128 columns of h share a scale)
+    const int64_t blocks = (kWide == 4 ? mm_blocks(p.M, p.N, DUAL, 128) : mm_any_blocks(p.M, p.N, DUAL)) * times;
+    if (blocks > UINT32_MAX / 512) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((k_mm_any<KIND, SC, XT, WT, DUAL, EPI, T, kWide>), dim3((unsigned)blocks), dim3(128 * kWide), 0, st, p);
     return hipGetLastError();
 }
 
@@ -876,20 +964,20 @@ hipError_t mm_tiles(const MmArgs& p, int bm, hipStream_t st) {
 template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
 hipError_t mm_run(MmArgs p, void* part, hipStream_t st) {
     const MmPlan r = mm_plan(KIND, p.M, p.N, p.K, p.segs, p.outs, XT || WT, DUAL);
-    if constexpr (!XT && !WT)
+    if constexpr (!XT && !WT && EPI != kMmFfn8)
         if (r.few) {
             if (p.M <= 16) return mm_few<KIND, SC, DUAL, EPI, T, 1>(p, st);
             if (p.M <= 32) return mm_few<KIND, SC, DUAL, EPI, T, 2>(p, st);
             return mm_few<KIND, SC, DUAL, EPI, T, 4>(p, st);
         }
-    if constexpr (!XT)  // (dw has two outputs and is not split)
+    if constexpr (EPI != kMmFfn8)
         if (r.splits) {
             p.splits = r.splits;
             p.share = r.share;
             p.part = static_cast<float*>(part);
             if (hipError_t e = mm_tiles<KIND, SC, XT, WT, DUAL, kMmPart, T>(p, r.bm, st)) return e;
             const int64_t blocks = (((EPI == kMmFfnBwd ? p.ldo : p.N) + 3) / 4 * p.M + 255) / 256;
-            hipLaunchKernelGGL((k_mm_join<SC, DUAL, EPI, T>), dim3((unsigned)blocks), dim3(256), 0, st, p);
+            hipLaunchKernelGGL((k_mm_join<SC, DUAL, EPI, T>), dim3((unsigned)blocks, (unsigned)p.outs), dim3(256), 0, st, p);
             return hipGetLastError();
         }
     return mm_tiles<KIND, SC, XT, WT, DUAL, EPI, T>(p, r.bm, st);

@@ -45,21 +45,32 @@ __device__ __forceinline__ void pack8(const float (&v)[8], const Divisor& by, ui
     hi = pack_e4m3(by.quotient(v[4]), by.quotient(v[5]), by.quotient(v[6]), by.quotient(v[7]));
 }
 
-// 128 columns of a row: 16 lanes.
+// 128 columns of a row: 16 lanes, which take kGroups of them, a workgroup's width apart.
+constexpr int kGroups = 4;
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_quant_group(QuantArgs p) {
-    const int64_t groups = (p.cols + 127) / 128, i = (int64_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16;
-    const bool live = i < p.rows * groups;
-    const int64_t row = live ? i / groups : 0, c = (live ? i % groups : 0) * 128 + 8 * (threadIdx.x & 15);
-    float v[8];
-    load8(static_cast<const T*>(p.x) + row * p.cols, c, p.cols, v);
-    const float scale = scale_of(umax_ln(amax8(v)));
-    if (!live) return;
-    const Divisor by(scale);
-    uint32_t lo, hi;
-    pack8(v, by, lo, hi);
-    store8(p.q + row * p.cols, c, p.cols, lo, hi);
-    if ((threadIdx.x & 15) == 0) p.scale[i] = scale;
+    const int64_t groups = (p.cols + 127) / 128, total = p.rows * groups;
+    const int64_t first = (int64_t)blockIdx.x * (kThreads / 16 * kGroups) + threadIdx.x / 16;
+    float v[kGroups][8];
+    int64_t row[kGroups], c[kGroups];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        const int64_t i = min(first + g * (kThreads / 16), total - 1);
+        row[g] = i / groups;
+        c[g] = (i - row[g] * groups) * 128 + 8 * (threadIdx.x & 15);
+        load8(static_cast<const T*>(p.x) + row[g] * p.cols, c[g], p.cols, v[g]);
+    }
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        const int64_t i = first + g * (kThreads / 16);
+        const float scale = scale_of(umax_ln(amax8(v[g])));
+        if (i >= total) return;
+        const Divisor by(scale);
+        uint32_t lo, hi;
+        pack8(v[g], by, lo, hi);
+        store8(p.q + row[g] * p.cols, c[g], p.cols, lo, hi);
+        if ((threadIdx.x & 15) == 0) p.scale[i] = scale;
+    }
 }
 
 __device__ __forceinline__ uint32_t block_umax(uint32_t m, uint32_t* sh) {
@@ -94,22 +105,23 @@ __global__ __launch_bounds__(kThreads) void k_quant_row(QuantArgs p) {
     if (threadIdx.x == 0) p.scale[row] = scale;
 }
 
-// 128 x 128 values: a thread holds 8 columns of 8 rows, 16 rows apart. Turned: the 8-bit values go through LDS, a row of
-// the result (128 values of a column) in words of four.
+// 128 x 128 values: a thread holds 8 columns of 8 neighbouring rows. Turned: the 8 values of a column are 8 neighbours of
+// the result's row and go through LDS as such, at a place that spreads the 16 lanes of a row over the banks; a row of the
+// result leaves in pieces of 128 bytes.
 template <typename T, bool BLOCK, bool TURNED>
 __global__ __launch_bounds__(kThreads) void k_quant_tile(QuantArgs p) {
     __shared__ uint32_t sh[4];
-    __shared__ uint32_t top[16][129];
-    __shared__ __align__(16) uint8_t turn[TURNED ? 128 * 144 : 16];
+    __shared__ uint32_t top[BLOCK ? 1 : 16][128];
+    __shared__ __align__(16) float scales[BLOCK ? 4 : 128];
+    __shared__ u32x2 turn[TURNED ? 128 : 1][16];
     const int64_t tiles = (p.cols + 127) / 128, br = blockIdx.x / tiles, bc = blockIdx.x % tiles;
-    const int64_t c = bc * 128 + 8 * (threadIdx.x & 15);
-    const int r0 = threadIdx.x / 16;
+    const int l = threadIdx.x & 15, g = threadIdx.x >> 4;
+    const int64_t c = bc * 128 + 8 * l, r0 = br * 128 + 8 * g;
     float v[8][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int64_t r = br * 128 + r0 + 16 * i;
-        if (r < p.rows) {
-            load8(static_cast<const T*>(p.x) + r * p.cols, c, p.cols, v[i]);
+        if (r0 + i < p.rows) {
+            load8(static_cast<const T*>(p.x) + (r0 + i) * p.cols, c, p.cols, v[i]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
@@ -126,52 +138,55 @@ __global__ __launch_bounds__(kThreads) void k_quant_tile(QuantArgs p) {
         if (threadIdx.x == 0) p.scale[TURNED ? bc * ((p.rows + 127) / 128) + br : (int64_t)blockIdx.x] = s;
     } else {
         // the largest of each column over the tile's 128 rows
+        uint32_t m[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            uint32_t m = 0;
+            m[j] = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i][j]));
-            top[r0][8 * (threadIdx.x & 15) + j] = m;
+            for (int i = 0; i < 8; ++i) m[j] = max(m[j], abs_bits(v[i][j]));
+        }
+        *reinterpret_cast<u32x4*>(&top[g][8 * l]) = u32x4{m[0], m[1], m[2], m[3]};
+        *reinterpret_cast<u32x4*>(&top[g][8 * l + 4]) = u32x4{m[4], m[5], m[6], m[7]};
+        __syncthreads();
+        if (threadIdx.x < 128) {
+            uint32_t most = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) most = max(most, top[i][threadIdx.x]);
+            const float s = scale_of(most);
+            scales[threadIdx.x] = s;
+            const int64_t col = bc * 128 + threadIdx.x;
+            if (col < p.cols) p.scale[col * ((p.rows + 127) / 128) + br] = s;
         }
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) m = max(m, top[i][8 * (threadIdx.x & 15) + j]);
-            scale[j] = scale_of(m);
-        }
-        if (r0 == 0)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < p.cols) p.scale[(c + j) * ((p.rows + 127) / 128) + br] = scale[j];
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const Divisor by(scale[j]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i][j] = by.quotient(v[i][j]);
+        for (int j = 0; j < 8; ++j) scale[j] = scales[8 * l + j];
     }
     if constexpr (!TURNED) {
+        const Divisor by(scale[0]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int64_t r = br * 128 + r0 + 16 * i;
-            if (r < p.rows)
-                store8(p.q + r * p.cols, c, p.cols, pack_e4m3(v[i][0], v[i][1], v[i][2], v[i][3]), pack_e4m3(v[i][4], v[i][5], v[i][6], v[i][7]));
+            uint32_t lo, hi;
+            pack8(v[i], by, lo, hi);
+            if (r0 + i < p.rows) store8(p.q + (r0 + i) * p.cols, c, p.cols, lo, hi);
         }
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t lo = pack_e4m3(v[0][j], v[1][j], v[2][j], v[3][j]), hi = pack_e4m3(v[4][j], v[5][j], v[6][j], v[7][j]);
+            const Divisor by(scale[j]);
+            float column[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) turn[(8 * (threadIdx.x & 15) + j) * 144 + r0 + 16 * i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+            for (int i = 0; i < 8; ++i) column[i] = v[i][j];
+            uint32_t lo, hi;
+            pack8(column, by, lo, hi);
+            turn[8 * l + j][g ^ l] = u32x2{lo, hi};
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < 128 * 16; i += kThreads) {
-            const int64_t col = bc * 128 + i / 16, r = br * 128 + 8 * (i % 16);
-            if (col >= p.cols) break;
-            const u32x2 w = *reinterpret_cast<const u32x2*>(turn + (i / 16) * 144 + 8 * (i % 16));
-            store8(p.q + col * p.rows, r, p.rows, w.x, w.y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int k = 16 * i + g;
+            const int64_t col = bc * 128 + k;
+            const u32x2 w = turn[k][l ^ (k >> 3)];
+            if (col < p.cols) store8(p.q + col * p.rows, br * 128 + 8 * l, p.rows, w.x, w.y);
         }
     }
 }
@@ -181,7 +196,7 @@ hipError_t quant(const QuantArgs& a, int scales, bool turned, hipStream_t st) {
     const int64_t tiles = ((a.rows + 127) / 128) * ((a.cols + 127) / 128);
     int64_t blocks = tiles;
     if (scales == 0) blocks = a.rows;
-    else if (scales == 1 && !turned) blocks = (a.rows * ((a.cols + 127) / 128) + kThreads / 16 - 1) / (kThreads / 16);
+    else if (scales == 1 && !turned) blocks = (a.rows * ((a.cols + 127) / 128) + kThreads / 16 * kGroups - 1) / (kThreads / 16 * kGroups);
     if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)blocks), threads(kThreads);
     if (scales == 0) hipLaunchKernelGGL(k_quant_row<T>, grid, threads, 0, st, a);
