@@ -56,22 +56,24 @@ template <> struct MmFrag<kMmF8x> {
     }
     __device__ __forceinline__ void set(u32x4 a, u32x4 b) { widen(0, a.x, a.y), widen(1, a.z, a.w), widen(2, b.x, b.y), widen(3, b.z, b.w); }
 };
-__device__ __forceinline__ f32x4 mm_mma(const MmFrag<kMmBf16>& w, const MmFrag<kMmBf16>& x, f32x4 c) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[i], x.v[i], c, 0, 0, 0);
-    return c;
+// A step is mm_parts matrix instructions that add to one another.
+template <int KIND> constexpr int mm_parts() { return KIND == kMmBf16 ? 2 : (KIND == kMmF32 ? 8 : (KIND == kMmF8 ? 1 : 4)); }
+__device__ __forceinline__ f32x4 mm_part(int i, const MmFrag<kMmBf16>& w, const MmFrag<kMmBf16>& x, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[i], x.v[i], c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4 mm_mma(const MmFrag<kMmF32>& w, const MmFrag<kMmF32>& x, f32x4 c) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(w.v[i / 4][i % 4], x.v[i / 4][i % 4], c, 0, 0, 0);
-    return c;
+__device__ __forceinline__ f32x4 mm_part(int i, const MmFrag<kMmF32>& w, const MmFrag<kMmF32>& x, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(w.v[i / 4][i % 4], x.v[i / 4][i % 4], c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4 mm_mma(const MmFrag<kMmF8>& w, const MmFrag<kMmF8>& x, f32x4 c) {
+__device__ __forceinline__ f32x4 mm_part(int, const MmFrag<kMmF8>& w, const MmFrag<kMmF8>& x, f32x4 c) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x.v, c, 0, 0, 0, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4 mm_mma(const MmFrag<kMmF8x>& w, const MmFrag<kMmF8x>& x, f32x4 c) {
+__device__ __forceinline__ f32x4 mm_part(int i, const MmFrag<kMmF8x>& w, const MmFrag<kMmF8x>& x, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[i], x.v[i], c, 0, 0, 0);
+}
+template <int KIND>
+__device__ __forceinline__ f32x4 mm_mma(const MmFrag<KIND>& w, const MmFrag<KIND>& x, f32x4 c) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[i], x.v[i], c, 0, 0, 0);
+    for (int i = 0; i < mm_parts<KIND>(); ++i) c = mm_part(i, w, x, c);
     return c;
 }
 
@@ -747,25 +749,22 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
             if constexpr (KIND != kMmF8x) __builtin_amdgcn_sched_barrier(0);
             if (kAhead == 2 && t + 1 < MT) ready(t + 1);
             if (t + kAhead < MT) read(t + kAhead);
+            // A tile's parts one after the other, or the four tiles' in turn (widened e4m3, 6,144 x 2,048 x 32,768 by groups
+            // 1,045 us and 1,018; 16,384 x 16,384 x 2,048 by blocks 1,096 and 1,138).
+            constexpr bool kTurn = KIND == kMmF8x && SC == kMmGroup;
+            constexpr int kParts = mm_parts<KIND>();
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                if constexpr (Sums::kScaled) {
-                    // a tile's sums are added while the next one is multiplied
-                    c[t & 1][j] = mm_mma(fw[j], fx[t & 1], f32x4{0.f, 0.f, 0.f, 0.f});
-                    if (t > 0) sums.add(t - 1, j, c[~t & 1][j], sx[(t - 1) & 3], sw[j]);
-                } else {
-                    sums.acc[t][j] = mm_mma(fw[j], fx[t & 1], sums.acc[t][j]);
-                }
+            for (int k = 0; k < kParts * NT; ++k) {
+                const int i = kTurn ? k / NT : k % kParts, j = kTurn ? k % NT : k / kParts;
+                if constexpr (Sums::kScaled) c[t & 1][j] = mm_part(i, fw[j], fx[t & 1], i ? c[t & 1][j] : f32x4{0.f, 0.f, 0.f, 0.f});
+                else sums.acc[t][j] = mm_part(i, fw[j], fx[t & 1], sums.acc[t][j]);
+                // a tile's sums are added while the next one is multiplied
+                if (Sums::kScaled && i == (kTurn ? 0 : kParts - 1) && t > 0) sums.add(t - 1, j, c[~t & 1][j], sx[(t - 1) & 3], sw[j]);
                 // matrix instructions with vector ones between them
-                if constexpr (KIND == kMmF8x) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, SC == kMmGroup ? 4 : 3, 0);
-                    }
-                } else if constexpr (Sums::kScaled) {
+                if constexpr (Sums::kScaled) {
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                    if (t > 0) __builtin_amdgcn_sched_group_barrier(0x002, SC == kMmBlock ? 5 : 8, 0);
+                    if (KIND == kMmF8x) __builtin_amdgcn_sched_group_barrier(0x002, SC == kMmGroup ? 4 : 3, 0);
+                    else if (t > 0) __builtin_amdgcn_sched_group_barrier(0x002, SC == kMmBlock ? 5 : 8, 0);
                 }
             }
             if (kAhead == 1 && t + 1 < MT) ready(t + 1);
