@@ -115,19 +115,19 @@ hipError_t ffn8(const FfnArgs& a, void* h, void* part, hipStream_t st) {
 }  // namespace
 
 size_t ffn_fwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
-    return mm_plan(dtype == 1 ? kMmF32 : kMmBf16, M, F, K, 1, 1, false, true).bytes;
+    return mm_plan(dtype == 1 ? kMmF32 : kMmBf16, kMmPlain, M, F, K, 1, 1, false, true).bytes;
 }
 size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
     const int kind = dtype == 1 ? kMmF32 : kMmBf16;
-    size_t part = mm_plan(kind, M, F, K, 1, 1, false, true).bytes;
-    for (size_t b : {mm_plan(kind, M, K, F, 2, 1, true, false).bytes, mm_plan(kind, F, K, M, 1, 2, true, false).bytes})
+    size_t part = mm_plan(kind, kMmPlain, M, F, K, 1, 1, false, true).bytes;
+    for (size_t b : {mm_plan(kind, kMmPlain, M, K, F, 2, 1, true, false).bytes, mm_plan(kind, kMmPlain, F, K, M, 1, 2, true, false).bytes})
         if (b > part) part = b;
     return 2 * align256((size_t)(M * grad_ld(F) * (dtype == 1 ? 4 : 2))) + part;
 }
 // Few rows, or a split contraction: the parts, and the block's fp32 output in front of its quantisation. Otherwise the
 // workgroup that has a row's 128 columns quantises them.
 size_t ffn8_ws(int64_t M, int64_t K, int64_t F, int dtype, bool quant) {
-    const MmPlan r = mm_plan(quant || dtype == 1 ? kMmF8x : kMmF8, M, F, K, 1, 1, false, true);
+    const MmPlan r = mm_plan(quant || dtype == 1 ? kMmF8x : kMmF8, kMmBlock, M, F, K, 1, 1, false, true);
     return (quant && (r.few || r.splits) ? align256((size_t)(M * F * 4)) : 0) + r.bytes;
 }
 
@@ -142,7 +142,7 @@ hipError_t launch_ffn_bwd(const FfnArgs& a, int dtype, hipStream_t st) {
 hipError_t launch_ffn8(const FfnArgs& a, int dtype, hipStream_t st) {
     if (a.M == 0) return hipSuccess;
     if (!a.hs) return dtype == 1 ? ffn8<kMmF8x, float>(a, a.h, a.ws, st) : ffn8<kMmF8, bf16_t>(a, a.h, a.ws, st);
-    const MmPlan r = mm_plan(kMmF8x, a.M, a.F, a.K, 1, 1, false, true);
+    const MmPlan r = mm_plan(kMmF8x, kMmBlock, a.M, a.F, a.K, 1, 1, false, true);
     if (!r.few && !r.splits) return ffn8<kMmF8x, float, kMmFfn8>(a, a.h, nullptr, st);
     if (hipError_t e = ffn8<kMmF8x, float>(a, a.ws, a.ws + align256((size_t)(a.M * a.F * 4)), st)) return e;
     const QuantArgs q{a.M, a.F, a.ws, static_cast<uint8_t*>(a.h), a.hs};

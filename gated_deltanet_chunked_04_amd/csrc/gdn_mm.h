@@ -338,15 +338,25 @@ __global__ __launch_bounds__(256) void k_mm_join(MmArgs p) {
     const int64_t m = i / per, n = i % per * 4;
     const int z = blockIdx.y;
     float v[kSides][4] = {};
-    if (n < p.N)
-        for (int s = z * p.splits; s < (z + 1) * p.splits; ++s)
+    if (n < p.N) {
+        const float* from = p.part + ((int64_t)z * p.splits * kSides * p.M + m) * p.N + n;
+        const int64_t side = p.M * p.N, left = p.N - n;
+        constexpr int kAhead = 4;  // parts on their way together
+        for (int s = 0; s < p.splits; s += kAhead) {
+            float x[kAhead][kSides][4];
 #pragma unroll
-            for (int k = 0; k < kSides; ++k) {
-                float x[4];
-                mm_load<float, 4>(p.part + (((int64_t)s * kSides + k) * p.M + m) * p.N + n, x, p.N - n);
+            for (int a = 0; a < kAhead; ++a)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[k][j] += x[j];
-            }
+                for (int k = 0; k < kSides; ++k) mm_load<float, 4>(from + ((int64_t)min(s + a, p.splits - 1) * kSides + k) * side, x[a][k], left);
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+                if (s + a < p.splits)
+#pragma unroll
+                    for (int k = 0; k < kSides; ++k)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[k][j] += x[a][k][j];
+        }
+    }
     mm_finish<EPI, T, SC, DUAL, 4>(p, z ? p.out[1] : p.out[0], 0, m, n, v);
 }
 
@@ -446,20 +456,22 @@ __device__ __forceinline__ void mm_finish8(Sums& sums, const MmArgs& p, uint32_t
     }
 }
 
-// 128 x 128 outputs (two sides: 128 x 64 of each) by four waves of 64 x 64, any sizes and addresses: chunks go through
-// registers, the next step's on their way while one is multiplied; one tile of each operand in LDS.
-template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T, int WN>
-__global__ __launch_bounds__(128 * WN) void k_mm_any(MmArgs p) {
-    constexpr int E = mm_size<KIND>(), MT = 4, NT = 4;
+// 128 x 64 WN outputs (two sides: half of each) by WM x WN waves of 128 / WM x 64, any sizes and addresses: chunks go
+// through registers, the next step's on their way while one is multiplied; one tile of each operand in LDS. Eight waves,
+// two on a SIMD, so that one's LDS reads pass behind the other's products (1,003 x 777 x 1,001 in e4m3 19.4 us, with four
+// waves of 64 x 64 20.0).
+template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_mm_any(MmArgs p) {
+    constexpr int E = mm_size<KIND>(), MT = 8 / WM, NT = 4;
     using C = MmCols<mm_pair<T, WT, DUAL>(), DUAL>;
     constexpr int kSteps = kMmStep / E;  // of the contraction per step
-    constexpr int kRows = 64 * WN, kCols = DUAL ? kRows / 2 : kRows, kThreads = 128 * WN;
-    constexpr int kXC = 1024 / kThreads;
+    constexpr int kRows = 64 * WN, kCols = DUAL ? kRows / 2 : kRows, kThreads = 64 * WM * WN;
+    constexpr int kXC = 1024 / kThreads, kWC = kRows * 8 / kThreads;
     using Sums = MmSums<KIND, SC, DUAL, MT, NT>;
     using X = MmTile<E, 128, XT, kNear>;
     using W = MmTile<E, kCols, WT, C::kFar>;
     __shared__ __align__(16) uint8_t xt[128 * kMmStep], wt[kRows * kMmStep];
-    const int wave = wave_id(), wm = wave & 1, wn = wave >> 1;
+    const int wave = wave_id(), wm = wave % WM, wn = wave / WM;
     const int ln = threadIdx.x & 15, gq = threadIdx.x >> 4 & 3;
     const int64_t tm = (p.M + 127) / 128, tn = (p.N + kCols - 1) / kCols;
     const int64_t m0 = (blockIdx.x % tm) * 128, n0 = (blockIdx.x / tm % tn) * kCols;
@@ -467,16 +479,16 @@ __global__ __launch_bounds__(128 * WN) void k_mm_any(MmArgs p) {
     const int32_t per = (int32_t)((p.K + kSteps - 1) / kSteps);
     const int32_t begin = part * p.share, end = p.splits ? min(begin + p.share, per * p.segs) : per * p.segs;
     Sums sums;
-    u32x4 cx[kXC], cw[4];
+    u32x4 cx[kXC], cw[kWC];
     auto load = [&](int32_t it) {
         const int seg = it >= per ? 1 : 0;
         const int64_t k0 = (int64_t)(it - seg * per) * kSteps;
 #pragma unroll
         for (int i = 0; i < kXC; ++i) cx[i] = X::load((XT ? z : seg) ? p.x[1] : p.x[0], p.ldx, m0, p.M, k0, p.K, threadIdx.x + kThreads * i);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kWC; ++i) {
             const int c = threadIdx.x + kThreads * i;
-            if constexpr (DUAL) cw[i] = W::load(p.w[i / 2], p.ldw, n0, p.N, k0, p.K, c - 2 * kThreads * (i / 2));
+            if constexpr (DUAL) cw[i] = W::load(p.w[i / (kWC / 2)], p.ldw, n0, p.N, k0, p.K, c - kCols * 8 * (i / (kWC / 2)));
             else cw[i] = W::load(seg ? p.w[1] : p.w[0], p.ldw, n0, p.N, k0, p.K, c);
         }
     };
@@ -486,9 +498,9 @@ __global__ __launch_bounds__(128 * WN) void k_mm_any(MmArgs p) {
 #pragma unroll
         for (int i = 0; i < kXC; ++i) *reinterpret_cast<u32x4*>(xt + X::lds(threadIdx.x + kThreads * i)) = cx[i];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kWC; ++i) {
             const int c = threadIdx.x + kThreads * i;
-            if constexpr (DUAL) *reinterpret_cast<u32x4*>(wt + kCols * kMmStep * (i / 2) + W::lds(c - 2 * kThreads * (i / 2))) = cw[i];
+            if constexpr (DUAL) *reinterpret_cast<u32x4*>(wt + kCols * kMmStep * (i / (kWC / 2)) + W::lds(c - kCols * 8 * (i / (kWC / 2)))) = cw[i];
             else *reinterpret_cast<u32x4*>(wt + W::lds(c)) = cw[i];
         }
         __syncthreads();
@@ -508,10 +520,10 @@ __global__ __launch_bounds__(128 * WN) void k_mm_any(MmArgs p) {
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            if constexpr (XT) mm_read_turned<KIND, 128>(fx, xt, wm * 64 + 16 * t, 4);
-            else mm_read<KIND, kNear>(fx, xt, wm * 64 + 16 * t + ln);
+            if constexpr (XT) mm_read_turned<KIND, 128>(fx, xt, wm * (16 * MT) + 16 * t, 4);
+            else mm_read<KIND, kNear>(fx, xt, wm * (16 * MT) + 16 * t + ln);
             if constexpr (Sums::kScaled) {
-                const float sx = p.xs[min(m0 + wm * 64 + 16 * t + ln, p.M - 1) * p.kb + it];
+                const float sx = p.xs[min(m0 + wm * (16 * MT) + 16 * t + ln, p.M - 1) * p.kb + it];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) sums.add(t, j, mm_mma(fw[j], fx, f32x4{0.f, 0.f, 0.f, 0.f}), sx, sw[j]);
             } else {
@@ -522,9 +534,9 @@ __global__ __launch_bounds__(128 * WN) void k_mm_any(MmArgs p) {
     }
     if constexpr (EPI == kMmFfn8) {
         __syncthreads();
-        mm_finish8<Sums, MT>(sums, p, reinterpret_cast<uint32_t*>(xt), wm * 64, wn, m0 + wm * 64, n0);
+        mm_finish8<Sums, MT>(sums, p, reinterpret_cast<uint32_t*>(xt), wm * (16 * MT), wn, m0 + wm * (16 * MT), n0);
     } else {
-        sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, z ? p.out[1] : p.out[0], z * p.splits + part, m0 + wm * 64, n0 + wn * (kCols / WN));
+        sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, z ? p.out[1] : p.out[0], z * p.splits + part, m0 + wm * (16 * MT), n0 + wn * (kCols / WN));
     }
 }
 
@@ -887,36 +899,48 @@ inline bool mm_fits(const MmArgs& p) {
 
 constexpr int kMmFew = 64;  // X rows of k_mm_few at most
 
-// What a product of these sizes runs as: by sizes alone, so that the workspace can be told beforehand (whatever the
-// operands' addresses: k_mm and k_mm_any split alike).
+// What a product of these sizes runs as: by sizes and types alone, so that the workspace can be told beforehand (k_mm and
+// k_mm_any split alike, whichever the addresses ask for).
 struct MmPlan {
     bool few;
     int bm;
     int splits, share;
     size_t bytes;  // of the parts
 };
-inline MmPlan mm_plan(int kind, int64_t M, int64_t N, int64_t K, int segs, int outs, bool turned, bool dual) {
+inline MmPlan mm_plan(int kind, int sc, int64_t M, int64_t N, int64_t K, int segs, int outs, bool turned, bool dual) {
     MmPlan r{};
-    const int steps = kMmStep / (kind == kMmBf16 ? 2 : (kind == kMmF32 ? 4 : 1));
+    const int E = kind == kMmBf16 ? 2 : (kind == kMmF32 ? 4 : 1), steps = kMmStep / E;
     r.few = !turned && segs == 1 && outs == 1 && M <= kMmFew;
     if (r.few) return r;
     const int64_t total = (K + steps - 1) / steps * segs;
-    // 256 rows of X a tile, or 128 where that is quicker: rounds of 256 workgroups, a step of the larger tile taking 8
-    // parts of time and one of the smaller 5
-    const int64_t large = mm_blocks(M, N, dual, 256) * outs, small = mm_blocks(M, N, dual, 128) * outs;
-    r.bm = kind == kMmF8x || kind == kMmF32 || 5 * ((small + 255) / 256) < 8 * ((large + 255) / 256) ? 128 : 256;
-    if (small <= 128 && total >= 16) {
-        int64_t want = 256 / small, most = total / 8;
-        if (want > most) want = most;
-        if (want > 32) want = 32;
-        if (want > 1) {
+    // Memory rows that are no whole chunks go to k_mm_any (128 x 128, two workgroups a compute unit); others to k_mm with 256
+    // rows of X a tile or 128. The contraction is taken whole or in parts. Whatever is quickest by this count of microseconds:
+    // rounds of the workgroups that run at a time, what a step of a tile measured, and for parts another launch and what they
+    // write and read at 4 TB/s.
+    const bool odd = (turned ? N : K) * E % 16;
+    const double step = odd ? (kind == kMmF32 ? 3.2 : (kind == kMmF8x ? 2.8 : 1.6)) : (kind == kMmF32 ? 4.0 : (kind == kMmF8x ? 2.0 : (kind == kMmF8 ? 1.2 : 1.0)));
+    const int64_t tiles = (odd ? mm_any_blocks(M, N, dual) : mm_blocks(M, N, dual, 128)) * outs, slots = odd ? 512 : 256;
+    const double sums = 2e-6 * (double)M * (double)N * outs * (dual ? 2 : 1);
+    double best = step * ((tiles + slots - 1) / slots) * total;
+    r.bm = 128;
+    const int64_t large = mm_blocks(M, N, dual, 256) * outs;
+    const double large_us = (kind == kMmF8 ? 2.0 : 1.6) * ((large + 255) / 256) * total;
+    if (!odd && kind != kMmF8x && kind != kMmF32 && large_us <= best) {
+        r.bm = 256;
+        best = large_us;
+    }
+    const int unit = sc == kMmBlock || sc == kMmGroup ? 4 : 1;  // (scales come four steps at a time)
+    for (int64_t parts = 2; parts <= 32 && parts < total && parts * tiles <= 2 * slots; ++parts) {
+        const int64_t share = ((total + parts - 1) / parts + unit - 1) / unit * unit, got = (total + share - 1) / share;
+        const double t = step * ((tiles * got + slots - 1) / slots) * share + 5 + sums * got;
+        if (got > 1 && t < best) {
+            best = t;
             r.bm = 128;
-            r.share = (int)(((total + want - 1) / want + 3) / 4 * 4);
-            r.splits = (int)((total + r.share - 1) / r.share);
-            if (r.splits < 2) r.splits = r.share = 0;
-            r.bytes = (size_t)outs * r.splits * (dual ? 2 : 1) * M * N * 4;
+            r.share = (int)share;
+            r.splits = (int)got;
         }
     }
+    r.bytes = (size_t)outs * r.splits * (dual ? 2 : 1) * M * N * 4;
     return r;
 }
 
@@ -955,14 +979,14 @@ hipError_t mm_tiles(const MmArgs& p, int bm, hipStream_t st) {
     constexpr int kWide = EPI == kMmFfn8 ? 4 : 2;  // (128 columns of h share a scale)
     const int64_t blocks = (kWide == 4 ? mm_blocks(p.M, p.N, DUAL, 128) : mm_any_blocks(p.M, p.N, DUAL)) * times;
     if (blocks > UINT32_MAX / 512) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_mm_any<KIND, SC, XT, WT, DUAL, EPI, T, kWide>), dim3((unsigned)blocks), dim3(128 * kWide), 0, st, p);
+    hipLaunchKernelGGL((k_mm_any<KIND, SC, XT, WT, DUAL, EPI, T, 8 / kWide, kWide>), dim3((unsigned)blocks), dim3(512), 0, st, p);
     return hipGetLastError();
 }
 
 // `part`: the workspace that mm_plan asked for.
 template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
 hipError_t mm_run(MmArgs p, void* part, hipStream_t st) {
-    const MmPlan r = mm_plan(KIND, p.M, p.N, p.K, p.segs, p.outs, XT || WT, DUAL);
+    const MmPlan r = mm_plan(KIND, SC, p.M, p.N, p.K, p.segs, p.outs, XT || WT, DUAL);
     if constexpr (!XT && !WT && EPI != kMmFfn8)
         if (r.few) {
             if (p.M <= 16) return mm_few<KIND, SC, DUAL, EPI, T, 1>(p, st);

@@ -35,8 +35,14 @@ hipError_t mm8_s(const Mm8Args& a, int scales, hipStream_t st) {
 
 }  // namespace
 
-size_t mm8_ws(int64_t M, int64_t N, int64_t K, int out_dtype) {
-    return mm_plan(out_dtype == 1 ? kMmF8x : kMmF8, M, N, K, 1, 1, false, false).bytes;
+namespace {
+
+MmScales scales_of(int scales) { return scales == 2 ? kMmBlock : (scales == 1 ? kMmGroup : kMmRow); }
+
+}  // namespace
+
+size_t mm8_ws(int64_t M, int64_t N, int64_t K, int out_dtype, int scales) {
+    return mm_plan(out_dtype == 1 ? kMmF8x : kMmF8, scales_of(scales), M, N, K, 1, 1, false, false).bytes;
 }
 
 hipError_t launch_mm8(const Mm8Args& a, int out_dtype, int scales, hipStream_t st) {

@@ -74,7 +74,7 @@ gdn_status gdn_quant_e4m3(const gdn_quant_desc* desc, const void* x, void* q, fl
 gdn_status gdn_matmul_e4m3_workspace_size(const gdn_matmul_desc* desc, size_t* bytes) {
     if (!bytes) return GDN_ERR_INVALID_ARG;
     if (gdn_status s = check_matmul(desc)) return s;
-    *bytes = mm8_ws(desc->M, desc->N, desc->K, desc->out_dtype);
+    *bytes = mm8_ws(desc->M, desc->N, desc->K, desc->out_dtype, desc->scales);
     return GDN_OK;
 }
 
@@ -85,7 +85,7 @@ gdn_status gdn_matmul_e4m3(const gdn_matmul_desc* desc, const void* a, const flo
     if (desc->M && desc->K && (!a || !b)) return GDN_ERR_INVALID_ARG;
     // (without a contraction only the rows' own scales are read)
     if (desc->M && (desc->K || desc->scales == GDN_SCALE_ROW) && (!a_scale || !b_scale)) return GDN_ERR_INVALID_ARG;
-    if (gdn_status s = check_buf(workspace, mm8_ws(desc->M, desc->N, desc->K, desc->out_dtype), workspace_bytes)) return s;
+    if (gdn_status s = check_buf(workspace, mm8_ws(desc->M, desc->N, desc->K, desc->out_dtype, desc->scales), workspace_bytes)) return s;
     const Mm8Args m{desc->M, desc->N, desc->K, a, a_scale, b, b_scale, y, static_cast<unsigned char*>(workspace)};
     ProfScope ps(kKMatmul8, (hipStream_t)stream);
     return launched(launch_mm8(m, desc->out_dtype, desc->scales, (hipStream_t)stream));

@@ -25,7 +25,7 @@ struct Mm8Args {
     void* y;
     unsigned char* ws;
 };
-size_t mm8_ws(int64_t M, int64_t N, int64_t K, int out_dtype);
+size_t mm8_ws(int64_t M, int64_t N, int64_t K, int out_dtype, int scales);
 // scales as above, of b (a's are a row's where b's are, else of 128 columns)
 hipError_t launch_mm8(const Mm8Args& a, int out_dtype, int scales, hipStream_t st);
 

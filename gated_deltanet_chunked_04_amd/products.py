@@ -230,13 +230,13 @@ def gdn_gated_ffn_e4m3(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, activa
         raise TypeError("out_dtype: expected torch.bfloat16 or torch.float32")
     dev, lead, kb = x.device, x.shape[:-1], _blocks(K)
     F = _weight("w_gate", w_gate, K, E4M3, dev)
-    if w_up is None:
-        raise ValueError("w_up is required")
-    for name, t, shape, kind in (("w_up", w_up, (F, K), E4M3), ("x_scale", x_scale, (*lead, kb), torch.float32),
-                                 ("gate_scale", gate_scale, (_blocks(F), kb), torch.float32),
-                                 ("up_scale", up_scale, (_blocks(F), kb), torch.float32)):
-        if _like(name, t, shape, kind, dev) is None:
-            raise ValueError(f"{name} is required")
+    if w_up is None or x_scale is None or gate_scale is None or up_scale is None:
+        raise ValueError("w_up and all scales are required")
+    sshape = (-(-F // 128), kb)
+    pu = _like("w_up", w_up, w_gate.shape, E4M3, dev)
+    pxs = _like("x_scale", x_scale, (*lead, kb), torch.float32, dev)
+    pgs = _like("gate_scale", gate_scale, sshape, torch.float32, dev)
+    pus = _like("up_scale", up_scale, sshape, torch.float32, dev)
     ref, need = _ffn8_plan(rows, K, F, GDN_DTYPE_BF16 if quant else dtype, _gate(activation), GDN_OUT_E4M3 if quant else GDN_OUT_SAME)
     h, ph = _out("h", h, x, (*lead, F), E4M3 if quant else out_dtype, dev)
     if quant:
@@ -246,8 +246,7 @@ def gdn_gated_ffn_e4m3(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, activa
     else:
         psc = None
     pw, wb, ws = _scratch(need, x, workspace)
-    _run(load_library().gdn_gated_ffn_e4m3, dev, ref, x.data_ptr(), x_scale.data_ptr(), w_gate.data_ptr(), gate_scale.data_ptr(),
-         w_up.data_ptr(), up_scale.data_ptr(), ph, psc, pw, wb)
+    _run(load_library().gdn_gated_ffn_e4m3, dev, ref, x.data_ptr(), pxs, w_gate.data_ptr(), pgs, pu, pus, ph, psc, pw, wb)
     return h, scale
 
 
