@@ -255,14 +255,13 @@ def gdn_gated_ffn_e4m3(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, activa
 
 class _LinearE4m3(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight):
+    def forward(ctx, x, weight, need_dx, need_dw):
         q, s = gdn_quant_e4m3(x, quant="group")
         y = gdn_matmul_e4m3(q, s, *gdn_quant_e4m3(weight, quant="block"), out_dtype=x.dtype)
-        need_dx, need_dw = ctx.needs_input_grad
         # of x the backward needs what the weight gradient contracts: its columns, in e4m3
         turned = gdn_quant_e4m3(x, quant="group", transpose=True) if need_dw else (None, None)
         ctx.save_for_backward(weight if need_dx else None, *turned)
-        ctx.x_shape, ctx.w_dtype = x.shape, weight.dtype
+        ctx.w_dtype = weight.dtype
         return y
 
     @staticmethod
@@ -277,7 +276,7 @@ class _LinearE4m3(torch.autograd.Function):
         if xq is not None:
             q, s = gdn_quant_e4m3(d_y, quant="group", transpose=True)
             dw = gdn_matmul_e4m3(q, s, xq, xs, out_dtype=ctx.w_dtype)
-        return dx, dw
+        return dx, dw, None, None
 
 
 def linear_e4m3(x, weight):
@@ -291,7 +290,8 @@ def linear_e4m3(x, weight):
         raise ValueError(f"weight: expected [N, {K}]")
     if weight.device != x.device:
         raise ValueError(f"weight: expected a tensor on {x.device}")
-    return _LinearE4m3.apply(x, weight)
+    grad = torch.is_grad_enabled()
+    return _LinearE4m3.apply(x, weight, grad and x.requires_grad, grad and weight.requires_grad)
 
 
 class _GatedFfn(torch.autograd.Function):

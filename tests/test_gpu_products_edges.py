@@ -171,3 +171,46 @@ def test_ffn_beyond_32_bits(gpu_lib):
     # (other rows may be split otherwise: within the order of the additions)
     other = gdn.gdn_gated_ffn_bwd(x[few], wg, wu, h[few], pre=p2, need_dweight=False)["dx"]
     assert ((dx[few].float() - other.float()).norm() <= 2.0 ** -7 * other.float().norm()).item()
+
+
+def test_linear_does_what_is_asked(gpu_lib, monkeypatch):
+    """Nothing is prepared or computed for gradients that nobody can ask for."""
+    from gated_deltanet_chunked_04_amd import products
+
+    x, w = rnd(3, 70, 200, dtype=BF).cuda().requires_grad_(), rnd(130, 200, seed=1).cuda().requires_grad_()
+    kinds = []
+    quant = products.gdn_quant_e4m3
+
+    def counted(t, **kw):
+        kinds.append((kw["quant"], kw.get("transpose", False)))
+        return quant(t, **kw)
+
+    monkeypatch.setattr(products, "gdn_quant_e4m3", counted)
+    for mode in (torch.no_grad, torch.inference_mode):
+        kinds.clear()
+        with mode():
+            y = gdn.linear_e4m3(x, w)
+        assert kinds == [("group", False), ("block", False)] and not y.requires_grad
+    kinds.clear()
+    z = gdn.linear_e4m3(x, w)
+    assert torch.equal(z, y) and kinds == [("group", False), ("block", False), ("group", True)]
+    assert gdn.linear_e4m3(x.detach(), w.detach()).requires_grad is False and kinds[3:] == kinds[:2]
+    kinds.clear()
+    torch.autograd.grad(gdn.linear_e4m3(x, w.detach()).float().sum(), x)
+    assert kinds == [("group", False), ("block", False), ("group", False), ("block", True)]
+    kinds.clear()
+    dw = torch.autograd.grad(gdn.linear_e4m3(x.detach(), w).float().sum(), w)[0]
+    assert kinds == [("group", False), ("block", False), ("group", True), ("group", True)] and dw.dtype == F32
+
+
+def test_ffn_some_gradients(gpu_lib):
+    """gated_ffn's gradients one at a time are those asked for together."""
+    x, wg, wu, d = (t.cuda() for t in ffn_inputs(70, 96, 136, BF, seed=5))
+    leaves = [t.requires_grad_() for t in (x, wg, wu)]
+    for recompute in (False, True):
+        h = gdn.gated_ffn(*leaves, recompute=recompute)
+        all_of = torch.autograd.grad(h, leaves, d, retain_graph=True)
+        for i, leaf in enumerate(leaves):
+            assert torch.equal(torch.autograd.grad(h, leaf, d, retain_graph=True)[0], all_of[i])
+    with torch.no_grad():
+        assert torch.equal(gdn.gated_ffn(*leaves), h)
