@@ -76,36 +76,65 @@ __global__ __launch_bounds__(kThreads) void k_quant_group(QuantArgs p) {
     }
 }
 
+template <int THREADS>
 __device__ __forceinline__ uint32_t block_umax(uint32_t m, uint32_t* sh) {
     m = umax_ln(m);
     m = max(m, (uint32_t)__shfl_xor((int)m, 16));
     m = max(m, (uint32_t)__shfl_xor((int)m, 32));
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = m;
     __syncthreads();
-    return max(max(sh[0], sh[1]), max(sh[2], sh[3]));
+#pragma unroll
+    for (int i = 0; i < THREADS / 64; ++i) m = max(m, sh[i]);
+    return m;
 }
 
-// A row by a workgroup; read again for its values.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_quant_row(QuantArgs p) {
-    __shared__ uint32_t sh[4];
+// A row by a workgroup, in its registers up to 8 VECS columns a thread; a longer one (VECS 0) is read again for its values.
+template <typename T, int THREADS, int VECS>
+__global__ __launch_bounds__(THREADS) void k_quant_row(QuantArgs p) {
+    __shared__ uint32_t sh[THREADS / 64];
+    constexpr int kHeld = VECS ? VECS : 1;
     const int64_t row = blockIdx.x;
     const T* x = static_cast<const T*>(p.x) + row * p.cols;
-    float v[8];
-    uint32_t m = 0;
-    for (int64_t c = 8 * threadIdx.x; c < p.cols; c += 8 * kThreads) {
-        load8(x, c, p.cols, v);
-        m = max(m, amax8(v));
+    uint8_t* q = p.q + row * p.cols;
+    float v[kHeld][8];
+    uint32_t m = 0, lo, hi;
+    if constexpr (VECS) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) load8(x, 8 * ((int64_t)threadIdx.x + THREADS * i), p.cols, v[i]);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) m = max(m, amax8(v[i]));
+    } else {
+        for (int64_t c = 8 * threadIdx.x; c < p.cols; c += 8 * THREADS) {
+            load8(x, c, p.cols, v[0]);
+            m = max(m, amax8(v[0]));
+        }
     }
-    const float scale = scale_of(block_umax(m, sh));
+    const float scale = scale_of(block_umax<THREADS>(m, sh));
     const Divisor by(scale);
-    for (int64_t c = 8 * threadIdx.x; c < p.cols; c += 8 * kThreads) {
-        load8(x, c, p.cols, v);
-        uint32_t lo, hi;
-        pack8(v, by, lo, hi);
-        store8(p.q + row * p.cols, c, p.cols, lo, hi);
+    if constexpr (VECS) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            pack8(v[i], by, lo, hi);
+            store8(q, 8 * ((int64_t)threadIdx.x + THREADS * i), p.cols, lo, hi);
+        }
+    } else {
+        for (int64_t c = 8 * threadIdx.x; c < p.cols; c += 8 * THREADS) {
+            load8(x, c, p.cols, v[0]);
+            pack8(v[0], by, lo, hi);
+            store8(q, c, p.cols, lo, hi);
+        }
     }
     if (threadIdx.x == 0) p.scale[row] = scale;
+}
+// The smallest workgroup whose registers hold a row.
+template <typename T>
+void quant_row(const QuantArgs& a, hipStream_t st) {
+    const dim3 grid((unsigned)a.rows);
+    if (a.cols <= 2048) hipLaunchKernelGGL((k_quant_row<T, 256, 1>), grid, dim3(256), 0, st, a);
+    else if (a.cols <= 4096) hipLaunchKernelGGL((k_quant_row<T, 256, 2>), grid, dim3(256), 0, st, a);
+    else if (a.cols <= 8192) hipLaunchKernelGGL((k_quant_row<T, 256, 4>), grid, dim3(256), 0, st, a);
+    else if (a.cols <= 32768) hipLaunchKernelGGL((k_quant_row<T, 1024, 4>), grid, dim3(1024), 0, st, a);
+    else hipLaunchKernelGGL((k_quant_row<T, 1024, 0>), grid, dim3(1024), 0, st, a);
 }
 
 // 128 x 128 values: a thread holds 8 columns of 8 neighbouring rows. Turned: the 8 values of a column are 8 neighbours of
@@ -135,7 +164,7 @@ __global__ __launch_bounds__(kThreads) void k_quant_tile(QuantArgs p) {
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = max(m, amax8(v[i]));
-        const float s = scale_of(block_umax(m, sh));
+        const float s = scale_of(block_umax<kThreads>(m, sh));
 #pragma unroll
         for (int j = 0; j < 8; ++j) scale[j] = s;
         if (threadIdx.x == 0) p.scale[TURNED ? bc * ((p.rows + 127) / 128) + br : (int64_t)blockIdx.x] = s;
@@ -200,9 +229,9 @@ hipError_t quant(const QuantArgs& a, int scales, bool turned, hipStream_t st) {
     int64_t blocks = tiles;
     if (scales == 0) blocks = a.rows;
     else if (scales == 1 && !turned) blocks = (a.rows * ((a.cols + 127) / 128) + kThreads / 16 * kGroups - 1) / (kThreads / 16 * kGroups);
-    if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
+    if (!grid_fits(blocks, scales == 0 && a.cols > 8192 ? 1024 : kThreads)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)blocks), threads(kThreads);
-    if (scales == 0) hipLaunchKernelGGL(k_quant_row<T>, grid, threads, 0, st, a);
+    if (scales == 0) quant_row<T>(a, st);
     else if (scales == 1 && !turned) hipLaunchKernelGGL(k_quant_group<T>, grid, threads, 0, st, a);
     else if (scales == 1) hipLaunchKernelGGL((k_quant_tile<T, false, true>), grid, threads, 0, st, a);
     else if (turned) hipLaunchKernelGGL((k_quant_tile<T, true, true>), grid, threads, 0, st, a);

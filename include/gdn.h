@@ -490,7 +490,8 @@ typedef enum gdn_scales {
 /* Quantisation of x [rows, cols]: scale = max|x| / 448 over the values that share it (at least 2^-126;
  * 1 where all are zero), the 8-bit value is x / scale to nearest even. With transpose (not with
  * GDN_SCALE_ROW) q is [cols, rows], and the scales are those of that matrix: groups of 128 run along
- * x's rows. Values that share a scale with a NaN become NaN, beside an infinity the finite ones become 0. */
+ * x's rows. Values that share a scale with a NaN become NaN, beside an infinity the finite ones become 0.
+ * A scale per row: at most 16,777,215 rows, 4,194,303 of more than 8,192 columns (GDN_ERR_UNSUPPORTED). */
 typedef struct gdn_quant_desc {
     int64_t rows, cols;
     int32_t dtype;       /* gdn_dtype of x */

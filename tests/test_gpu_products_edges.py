@@ -214,3 +214,13 @@ def test_ffn_some_gradients(gpu_lib):
             assert torch.equal(torch.autograd.grad(h, leaf, d, retain_graph=True)[0], all_of[i])
     with torch.no_grad():
         assert torch.equal(gdn.gated_ffn(*leaves), h)
+
+
+# rows on both sides of what a workgroup's registers hold, its last vector whole and not
+@pytest.mark.parametrize("cols", [2047, 2048, 2049, 4096, 4101, 8192, 8193, 20000, 32768, 32769, 70003])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_quant_long_rows(cols, dt, gpu_lib):
+    x = rnd(5, cols, seed=cols, dtype=dt)
+    x[1, -1], x[2, 0], x[3] = 50.0, -60.0, 0.0
+    q, s = gdn.gdn_quant_e4m3(x.cuda(), quant="row")
+    check_quant(x, q, s, "row", "row")
