@@ -45,24 +45,32 @@ __device__ __forceinline__ void pack8(const float (&v)[8], const Divisor& by, ui
     hi = pack_e4m3(by.quotient(v[4]), by.quotient(v[5]), by.quotient(v[6]), by.quotient(v[7]));
 }
 
-// 128 columns of a row: 16 lanes, which take kGroups of them, a workgroup's width apart (32,768 x 2,048 bf16: one 40.4 us, two
-// 37.2, four 37.7, eight 45.8).
+// 128 columns of a row: 16 lanes, which take kGroups of them, a workgroup's width apart (32,768 x 2,048 bf16: one 35.4 us, two
+// 33.0, four 33.6). WHOLE: rows are whole groups, so the matrix is one run of them (with their row and column worked out 38.9).
 constexpr int kGroups = 2;
-template <typename T>
+template <typename T, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_quant_group(QuantArgs p) {
     const int64_t groups = (p.cols + 127) / 128, total = p.rows * groups;
     const int64_t begin = (int64_t)blockIdx.x * (kThreads / 16 * kGroups), first = begin + threadIdx.x / 16;
-    const int64_t row0 = begin / groups;  // (of the workgroup; what lies behind it is counted in 32 bits)
-    const uint32_t rest = (uint32_t)(begin - row0 * groups), per = (uint32_t)groups;
+    const int l = 8 * (threadIdx.x & 15);
     float v[kGroups][8];
-    int64_t row[kGroups], c[kGroups];
+    int64_t at[kGroups], left[kGroups];  // of the lane's values, and columns from there to the row's end
+    if constexpr (WHOLE) {
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-        const uint32_t i = rest + (uint32_t)(min(first + g * (kThreads / 16), total - 1) - begin), r = i / per;
-        row[g] = row0 + r;
-        c[g] = (int64_t)(i - r * per) * 128 + 8 * (threadIdx.x & 15);
-        load8(static_cast<const T*>(p.x) + row[g] * p.cols, c[g], p.cols, v[g]);
+        for (int g = 0; g < kGroups; ++g) at[g] = min(first + g * (kThreads / 16), total - 1) * 128 + l, left[g] = 8;
+    } else {
+        const int64_t row0 = begin / groups;  // (of the workgroup; what lies behind it is counted in 32 bits)
+        const uint32_t rest = (uint32_t)(begin - row0 * groups), per = (uint32_t)groups;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            const uint32_t i = rest + (uint32_t)(min(first + g * (kThreads / 16), total - 1) - begin), r = i / per;
+            const int64_t c = (int64_t)(i - r * per) * 128 + l;
+            at[g] = (row0 + r) * p.cols + c;
+            left[g] = p.cols - c;
+        }
     }
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) load8(static_cast<const T*>(p.x) + at[g], 0, left[g], v[g]);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
         const int64_t i = first + g * (kThreads / 16);
@@ -71,8 +79,8 @@ __global__ __launch_bounds__(kThreads) void k_quant_group(QuantArgs p) {
         const Divisor by(scale);
         uint32_t lo, hi;
         pack8(v[g], by, lo, hi);
-        store8(p.q + row[g] * p.cols, c[g], p.cols, lo, hi);
-        if ((threadIdx.x & 15) == 0) p.scale[i] = scale;
+        store8(p.q + at[g], 0, left[g], lo, hi);
+        if (l == 0) p.scale[i] = scale;
     }
 }
 
@@ -146,7 +154,8 @@ __global__ __launch_bounds__(kThreads) void k_quant_tile(QuantArgs p) {
     __shared__ uint32_t top[BLOCK ? 1 : 16][128];
     __shared__ __align__(16) float scales[BLOCK ? 4 : 128];
     __shared__ u32x2 turn[TURNED ? 128 : 1][16];
-    const int64_t tiles = (p.cols + 127) / 128, br = blockIdx.x / tiles, bc = blockIdx.x % tiles;
+    const uint32_t tiles = (uint32_t)((p.cols + 127) / 128);
+    const int64_t br = blockIdx.x / tiles, bc = blockIdx.x % tiles;
     const int l = threadIdx.x & 15, g = threadIdx.x >> 4;
     const int64_t c = bc * 128 + 8 * l, r0 = br * 128 + 8 * g;
     float v[8][8];
@@ -232,7 +241,8 @@ hipError_t quant(const QuantArgs& a, int scales, bool turned, hipStream_t st) {
     if (!grid_fits(blocks, scales == 0 && a.cols > 8192 ? 1024 : kThreads)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)blocks), threads(kThreads);
     if (scales == 0) quant_row<T>(a, st);
-    else if (scales == 1 && !turned) hipLaunchKernelGGL(k_quant_group<T>, grid, threads, 0, st, a);
+    else if (scales == 1 && !turned && a.cols % 128 == 0) hipLaunchKernelGGL((k_quant_group<T, true>), grid, threads, 0, st, a);
+    else if (scales == 1 && !turned) hipLaunchKernelGGL((k_quant_group<T, false>), grid, threads, 0, st, a);
     else if (scales == 1) hipLaunchKernelGGL((k_quant_tile<T, false, true>), grid, threads, 0, st, a);
     else if (turned) hipLaunchKernelGGL((k_quant_tile<T, true, true>), grid, threads, 0, st, a);
     else hipLaunchKernelGGL((k_quant_tile<T, true, false>), grid, threads, 0, st, a);
