@@ -35,6 +35,12 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(a), clamp_e4m3(b), 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(c), clamp_e4m3(d), w, true);
 }
+// The same for quotients by a scale of theirs, none of which lies above 448 by more than its rounding: half a step, 16, more
+// would be the next value.
+__device__ __forceinline__ uint32_t pack_e4m3_within(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
 __device__ __forceinline__ float scale_of(uint32_t amax_bits) {
     if (amax_bits == 0) return 1.f;
     const float s = __uint_as_float(amax_bits) / kE4m3Max;

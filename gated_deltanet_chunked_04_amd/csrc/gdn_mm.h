@@ -442,7 +442,7 @@ __device__ __forceinline__ void mm_finish8(Sums& sums, const MmArgs& p, uint32_t
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const f32x4 h = sums.acc[t][j];
-            w[j] = pack_e4m3(by.quotient(h[0]), by.quotient(h[1]), by.quotient(h[2]), by.quotient(h[3]));
+            w[j] = pack_e4m3_within(by.quotient(h[0]), by.quotient(h[1]), by.quotient(h[2]), by.quotient(h[3]));
         }
         uint8_t* q = static_cast<uint8_t*>(p.out[0]) + m * p.N + n;
         if (left >= 8) {
