@@ -45,18 +45,29 @@ __global__ __launch_bounds__(256) void k_ffn_act_bwd(MmArgs p) {
 
 // columns of the gradients of gate and up in the workspace: whole vectors, zeros behind F
 int64_t grad_ld(int64_t F) { return (F + 7) / 8 * 8; }
+// Whether bf16 gradients of gate and up are kept as two bf16 each, the rounded value and what that leaves (16 bits). One alone
+// adds as much to the results as their own rounding does, a factor of sqrt 2 in the 2-norm. That is the mean: where one of the
+// matrices has fewer than 65,536 values the factor itself scatters (16 x 4,096 with F = 16: up to 1.77; from 65,536 values on
+// within 0.02), and there the products are short.
+bool grad_pairs(int64_t M, int64_t K, int64_t F) {
+    const int64_t few = 65536;
+    return M * F < few || M * K < few || F * K < few;
+}
 
 template <int KIND, typename T>
 hipError_t bwd(const FfnArgs& a, hipStream_t st) {
     const int64_t size = sizeof(T), ldd = grad_ld(a.F);
     const size_t bytes = align256((size_t)(a.M * ldd * size));
-    void *d[2] = {a.ws, a.ws + bytes}, *part = a.ws + 2 * bytes;
+    const bool pairs = KIND == kMmBf16 && grad_pairs(a.M, a.K, a.F);
+    void *d[2] = {a.ws, a.ws + bytes}, *part = a.ws + (pairs ? 4 : 2) * bytes;
+    const int64_t low = pairs ? 2 * (int64_t)bytes : 0;
     if (a.M) {
         MmArgs p = block_args(a, size);
         p.out[0] = d[0];
         p.out[1] = d[1];
         p.ldo = ldd;
         p.d_h = a.d_h;
+        p.low = low;
         if (a.pre) {
             const int64_t blocks = ((a.F + 7) / 8 * a.M + 255) / 256;
             if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
@@ -75,7 +86,8 @@ hipError_t bwd(const FfnArgs& a, hipStream_t st) {
         p.M = a.M;
         p.N = a.K;
         p.K = a.F;
-        p.segs = 2;
+        p.segs = pairs ? 4 : 2;
+        p.low = low;
         p.outs = 1;
         p.out[0] = a.dx;
         p.ldo = a.K;
@@ -90,7 +102,8 @@ hipError_t bwd(const FfnArgs& a, hipStream_t st) {
         p.M = a.F;
         p.N = a.K;
         p.K = a.M;
-        p.segs = 1;
+        p.segs = pairs ? 2 : 1;
+        p.low = low;
         p.outs = 2;
         p.out[0] = a.dwg;
         p.out[1] = a.dwu;
@@ -119,10 +132,11 @@ size_t ffn_fwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
 }
 size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
     const int kind = dtype == 1 ? kMmF32 : kMmBf16;
+    const int n = kind == kMmBf16 && grad_pairs(M, K, F) ? 2 : 1;
     size_t part = mm_plan(kind, kMmPlain, M, F, K, 1, 1, false, true).bytes;
-    for (size_t b : {mm_plan(kind, kMmPlain, M, K, F, 2, 1, true, false).bytes, mm_plan(kind, kMmPlain, F, K, M, 1, 2, true, false).bytes})
+    for (size_t b : {mm_plan(kind, kMmPlain, M, K, F, 2 * n, 1, true, false).bytes, mm_plan(kind, kMmPlain, F, K, M, n, 2, true, false).bytes})
         if (b > part) part = b;
-    return 2 * align256((size_t)(M * grad_ld(F) * (dtype == 1 ? 4 : 2))) + part;
+    return 2 * n * align256((size_t)(M * grad_ld(F) * (dtype == 1 ? 4 : 2))) + part;
 }
 // Few rows, or a split contraction: the parts, and the block's fp32 output in front of its quantisation. Otherwise the
 // workgroup that has a row's 128 columns quantises them.

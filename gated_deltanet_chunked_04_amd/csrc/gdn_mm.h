@@ -191,9 +191,10 @@ enum MmScales { kMmPlain = 0, kMmBlock = 1, kMmGroup = 2, kMmRow = 3 };
 struct MmArgs {
     const uint8_t* x[2];  // per segment of the contraction (dx: d_gate, d_up), or per output (dw)
     const uint8_t* w[2];  // per segment, or gate and up side by side (the block's forward)
+    int64_t low;          // 0, or the bytes from x to what its rounding left (of d_gate and d_up): further segments
     int64_t ldx, ldw;     // bytes between two memory rows
     int64_t M, N, K;      // rows of X, of W (of each where there are two side by side), contraction of a segment
-    int32_t segs;         // segments of the contraction
+    int32_t segs;         // segments of the contraction, at most 4
     int32_t outs;         // outputs, each with its x (dw)
     const float* xs;      // scales of e4m3 operands: [M, kb] (row: [M])
     const float* ws[2];   // block: [ceil(N/128), kb], group: [N, kb], row: [N]
@@ -271,6 +272,13 @@ __device__ __forceinline__ void mm_load(const T* p, float (&v)[N], int64_t n) {
 // part of the contraction, for k_mm_join. kMmFfn8: h in e4m3 with a scale for 128 columns (a tile's).
 enum MmEpi { kMmOut = 0, kMmFfn = 1, kMmFfnBwd = 2, kMmPart = 3, kMmFfn8 = 4 };
 
+// What rounding to T leaves of a value (nothing of those that are not finite, or become so).
+template <typename T>
+__device__ __forceinline__ float mm_left(float v) {
+    const float d = v - Elem<T>::to_f(Elem<T>::from_f(v));
+    return fabsf(d) < INFINITY ? d : 0.f;
+}
+
 // R columns of the block at (m, n). SHARED: by a wave whose four lane groups hold 32 neighbouring columns of a row.
 template <int EPI, typename T, int R, bool SHARED>
 __device__ __forceinline__ void mm_gate(const MmArgs& p, int64_t m, int64_t n, const float (&a)[R], const float (&u)[R]) {
@@ -303,8 +311,16 @@ __device__ __forceinline__ void mm_gate(const MmArgs& p, int64_t m, int64_t n, c
         }
         // rounded to the inputs' type: they are operands of the products behind, which take whole vectors of their rows
         // (ldo is a multiple of 8) and multiply what lies behind column N by zero
-        mm_store<T, R>(static_cast<T*>(p.out[0]) + m * p.ldo + n, da, R);
-        mm_store<T, R>(static_cast<T*>(p.out[1]) + m * p.ldo + n, du, R);
+        T* const g = static_cast<T*>(p.out[0]) + m * p.ldo + n;
+        T* const v = static_cast<T*>(p.out[1]) + m * p.ldo + n;
+        mm_store<T, R>(g, da, R);
+        mm_store<T, R>(v, du, R);
+        if (p.low) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) da[i] = mm_left<T>(da[i]), du[i] = mm_left<T>(du[i]);
+            mm_store<T, R>(g + p.low / (int64_t)sizeof(T), da, R);
+            mm_store<T, R>(v + p.low / (int64_t)sizeof(T), du, R);
+        }
     }
 }
 // Columns that an epilogue writes.
@@ -371,6 +387,12 @@ template <bool PAIR, bool DUAL> struct MmCols {
     // the lane's first column of tile j
     static __device__ __forceinline__ int col(int j, int gq) { return row(j) + kStride * gq; }
 };
+// A segment of the contraction: which of the two X and W it takes, and whether what rounding left of X. Turned X (dw): the
+// output's x, then what is left of it; else both x, then what is left of both.
+template <bool XT> __device__ __forceinline__ const uint8_t* mm_x(const MmArgs& p, int seg, int z) {
+    return ((XT ? z : seg & 1) ? p.x[1] : p.x[0]) + ((XT ? seg : seg >> 1) ? p.low : 0);
+}
+template <bool XT> __device__ __forceinline__ const uint8_t* mm_w(const MmArgs& p, int seg) { return !XT && (seg & 1) ? p.w[1] : p.w[0]; }
 template <typename T, bool WT, bool DUAL> constexpr bool mm_pair() { return DUAL || (sizeof(T) == 2 && !WT); }
 
 // The sums of a wave's MT x NT tiles, scaled where the operands are e4m3. Shared by the kernels below.
@@ -481,15 +503,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm_any(MmArgs p) {
     Sums sums;
     u32x4 cx[kXC], cw[kWC];
     auto load = [&](int32_t it) {
-        const int seg = it >= per ? 1 : 0;
+        const int seg = (it >= per) + (it >= 2 * per) + (it >= 3 * per);
         const int64_t k0 = (int64_t)(it - seg * per) * kSteps;
 #pragma unroll
-        for (int i = 0; i < kXC; ++i) cx[i] = X::load((XT ? z : seg) ? p.x[1] : p.x[0], p.ldx, m0, p.M, k0, p.K, threadIdx.x + kThreads * i);
+        for (int i = 0; i < kXC; ++i) cx[i] = X::load(mm_x<XT>(p, seg, z), p.ldx, m0, p.M, k0, p.K, threadIdx.x + kThreads * i);
 #pragma unroll
         for (int i = 0; i < kWC; ++i) {
             const int c = threadIdx.x + kThreads * i;
             if constexpr (DUAL) cw[i] = W::load(p.w[i / (kWC / 2)], p.ldw, n0, p.N, k0, p.K, c - kCols * 8 * (i / (kWC / 2)));
-            else cw[i] = W::load(seg ? p.w[1] : p.w[0], p.ldw, n0, p.N, k0, p.K, c);
+            else cw[i] = W::load(mm_w<XT>(p, seg), p.ldw, n0, p.N, k0, p.K, c);
         }
     };
     if (begin < end) load(begin);
@@ -658,10 +680,13 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
     // Where the next step's tiles come from (scalars, whatever the compiler makes of the loop).
     const int64_t xstep = XT ? kSteps * p.ldx : kMmStep, wstep = WT ? kSteps * p.ldw : kMmStep;
     const int32_t whole = (int32_t)(p.K / kSteps), rest = (int32_t)(p.K % kSteps);
-    int32_t kt = begin >= per ? begin - per : begin;
-    const uint64_t second = mm_uniform(p.w[1] + (WT ? n0 * E : n0 * p.ldw));
-    uint64_t xs = mm_uniform((XT ? (z ? p.x[1] : p.x[0]) : (begin >= per ? p.x[1] : p.x[0])) + (XT ? m0 * E : m0 * p.ldx) + kt * xstep);
-    uint64_t ws0 = mm_uniform((begin >= per && !DUAL ? p.w[1] : p.w[0]) + (WT ? n0 * E : n0 * p.ldw) + kt * wstep), ws1 = second + kt * wstep;
+    const int64_t xat = XT ? m0 * E : m0 * p.ldx, wat = WT ? n0 * E : n0 * p.ldw;
+    // Whether there may be several segments. (Only the turned products have them, and the others are told so; not the one by
+    // groups of widened e4m3, whose schedule comes out 5% quicker with the test in it: 6,144 x 2,048 x 32,768 983 us, 1,035.)
+    constexpr bool kSegs = WT || (KIND == kMmF8x && SC == kMmGroup);
+    int32_t seg = kSegs ? (begin >= per) + (begin >= 2 * per) + (begin >= 3 * per) : 0, kt = begin - seg * per;
+    uint64_t xs = mm_uniform(mm_x<XT>(p, seg, z) + xat + kt * xstep);
+    uint64_t ws0 = mm_uniform((DUAL ? p.w[0] : mm_w<XT>(p, seg)) + wat + kt * wstep), ws1 = mm_uniform(p.w[1] + wat + kt * wstep);
     auto fetch = [&](int stage) {
         const uint32_t xl = lds0 + stage * kStage, wl = xl + kXB;
         if (__builtin_expect(kt < whole, 1)) {
@@ -686,10 +711,12 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
         xs += xstep;
         ws0 += wstep;
         if (DUAL) ws1 += wstep;
-        if (++kt == per && p.segs > 1) {
+        ++kt;
+        if (kSegs && kt == per && p.segs > 1) {
             kt = 0;
-            xs = mm_uniform(p.x[1] + m0 * p.ldx);
-            ws0 = second;
+            ++seg;
+            xs = mm_uniform(mm_x<XT>(p, seg, z) + xat);
+            ws0 = mm_uniform(mm_w<XT>(p, seg) + wat);
         }
         kt = __builtin_amdgcn_readfirstlane(kt);
     };
@@ -800,8 +827,9 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
 template <int KIND, int SC, bool DUAL, int EPI, typename T, int MT, int WAVES, bool WHOLE>
 __global__ __launch_bounds__(64 * WAVES) void k_mm_few(MmArgs p) {
     constexpr int E = mm_size<KIND>(), kSides = DUAL ? 2 : 1;
-    // steps at a time: what the registers of 2 or 4 waves a SIMD hold
-    constexpr int kAt = !WHOLE ? 1 : (WAVES == 16 ? (MT + kSides <= 3 ? 2 : 1) : (MT == 4 ? 2 : 4));
+    // Steps at a time: what the registers of 4 waves a SIMD hold (gate and up of 2,048 x 8,192 in e4m3, 20 rows, two steps 10.7 us,
+    // four, which leave room for 2 waves, 12.4; in fp32 at 5,648 x 5,952 124 and 118).
+    constexpr int kAt = !WHOLE ? 1 : (WAVES == 16 ? (MT + kSides <= 3 ? 2 : 1) : (MT * kSides >= 8 ? 1 : (MT * kSides >= 4 ? 2 : 4)));
     constexpr int kSteps = kMmStep / E;
     constexpr bool kScaled = SC == kMmBlock || SC == kMmGroup;
     __shared__ f32x4 sh[WAVES][kSides * MT][64];
@@ -897,7 +925,9 @@ inline bool mm_fits(const MmArgs& p) {
     return bits % 16 == 0 && p.ldx < (1 << 23) && p.ldw < (1 << 23);
 }
 
-constexpr int kMmFew = 64;  // X rows of k_mm_few at most
+// X rows of k_mm_few: 32, or 64 over short rows. Its workgroups read all of X each, so tiles pass it by as X grows (gate and up of
+// 2,048 x 8,192 in e4m3, 40 rows: 14.9 us and 17.0; 5,648 x 5,952: 28.0 and 25.8, in fp32 194 and 152).
+inline bool mm_is_few(int64_t M, int64_t row_bytes) { return M <= (row_bytes <= 3 * 1024 ? 64 : 32); }
 
 // What a product of these sizes runs as: by sizes and types alone, so that the workspace can be told beforehand (k_mm and
 // k_mm_any split alike, whichever the addresses ask for).
@@ -910,7 +940,7 @@ struct MmPlan {
 inline MmPlan mm_plan(int kind, int sc, int64_t M, int64_t N, int64_t K, int segs, int outs, bool turned, bool dual) {
     MmPlan r{};
     const int E = kind == kMmBf16 ? 2 : (kind == kMmF32 ? 4 : 1), steps = kMmStep / E;
-    r.few = !turned && segs == 1 && outs == 1 && M <= kMmFew;
+    r.few = !turned && segs == 1 && outs == 1 && mm_is_few(M, K * E);
     if (r.few) return r;
     const int64_t total = (K + steps - 1) / steps * segs;
     // Memory rows that are no whole chunks go to k_mm_any (128 x 128, two workgroups a compute unit); others to k_mm with 256

@@ -224,3 +224,46 @@ def test_quant_long_rows(cols, dt, gpu_lib):
     x[1, -1], x[2, 0], x[3] = 50.0, -60.0, 0.0
     q, s = gdn.gdn_quant_e4m3(x.cuda(), quant="row")
     check_quant(x, q, s, "row", "row")
+
+
+# bf16 gradients where they are few: all that rounds them to 8 bits is their own rounding, half a step a value at most (the
+# gradients of gate and up are kept to 16 bits).
+@pytest.mark.parametrize("M,K,F", [(1, 16, 16), (1, 1, 1), (16, 16, 2048), (16, 2048, 16), (3000, 16, 16), (1, 1024, 512), (129, 100, 70), (70, 1000, 333), (4096, 15, 64)])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_ffn_few_gradients(M, K, F, act, gpu_lib):
+    x, wg, wu, d = ffn_inputs(M, K, F, BF, seed=M + K)
+    dev = [t.cuda() for t in (x, wg, wu)]
+    pre = gdn.gdn_gated_ffn_pre(dev[0], dev[1])
+    gdn.gdn_gated_ffn_fwd(*dev, pre=pre, activation=act)
+    want = ref.ffn_bwd(x, wg, wu, d, act, F32)
+    for kept in (pre, None):
+        gr = gdn.gdn_gated_ffn_bwd(*dev, d.cuda(), pre=kept, activation=act)
+        for k, (v, e) in want.items():
+            err = (gr[k].cpu().double() - v).abs()
+            # half a step of bf16 each; of the products' terms 2^-16 for the pairs beside fp32's own bound
+            assert (err <= 2.0 ** -8 * v.abs() + 1.01 * e + 2.0 ** -15 * bound_of(x, wg, wu, d, act)[k]).all(), k
+
+
+def bound_of(x, wg, wu, d, act):
+    """Sums of the absolute terms of the gradients."""
+    from oracle import products as ref
+
+    x, wg, wu, d = (t.double() for t in (x, wg, wu, d))
+    a, u = x @ wg.t(), x @ wu.t()
+    f, df = ref._act(a, act)[:2]
+    da, du = (d * u * df).abs(), (d * f).abs()
+    return dict(dx=da @ wg.abs() + du @ wu.abs(), dw_gate=da.t() @ x.abs(), dw_up=du.t() @ x.abs())
+
+
+def test_ffn_pairs_infinite(gpu_lib):
+    """A gradient that bf16 has no value for is infinite, not NaN, and stays in its row of dx and its rows of the weights'."""
+    x, wg, wu, d = (t.cuda() for t in ffn_inputs(20, 16, 24, BF, seed=7))
+    d[3, 5] = 3.3e38
+    u = (x.float() @ wu.float().t())[3, 5]
+    x[3] *= (4 / u.abs()).to(BF)  # d_up up = 1.3e39
+    gr = gdn.gdn_gated_ffn_bwd(x, wg, wu, d)
+    rows = torch.arange(20, device="cuda") != 3
+    assert torch.isfinite(gr["dx"][rows]).all() and not torch.isfinite(gr["dx"][3]).all()
+    cols = torch.arange(24, device="cuda") != 5
+    assert torch.isfinite(gr["dw_gate"][cols]).all() and torch.isfinite(gr["dw_up"][cols]).all()
+    assert torch.isinf(gr["dw_gate"][5]).any() and not torch.isnan(gr["dw_gate"][5]).any()
