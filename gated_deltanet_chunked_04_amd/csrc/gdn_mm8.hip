@@ -2,7 +2,7 @@
 //   y[m, n] = sum over blocks kb of 128  a_scale[m, kb] b_scale[n, kb]  sum over k in kb of  a[m, k] b[n, k],
 // b_scale[n, kb] being one value for 128 rows n (block), or a row's own (group); or one scale a row for the whole
 // contraction in both (row). The scaled sums are kept in fp32: a step of the contraction is a block, its sum comes out
-// of the matrix cores unscaled and is added with one fused product.
+// of the matrix cores unscaled and is added with one fused product. Bounds and rates: at the tiles (gdn_mm.h).
 #include "gdn_layer.h"
 #include "gdn_mm.h"
 #include "gdn_products.h"

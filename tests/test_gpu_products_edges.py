@@ -267,3 +267,19 @@ def test_ffn_pairs_infinite(gpu_lib):
     cols = torch.arange(24, device="cuda") != 5
     assert torch.isfinite(gr["dw_gate"][cols]).all() and torch.isfinite(gr["dw_up"][cols]).all()
     assert torch.isinf(gr["dw_gate"][5]).any() and not torch.isnan(gr["dw_gate"][5]).any()
+
+
+# on both sides of what counts as few rows, over short rows and long ones
+@pytest.mark.parametrize("M", [32, 33, 48, 49, 64, 65])
+@pytest.mark.parametrize("K", [300, 3056, 3088, 3101])
+def test_few_rows_or_tiles(M, K, gpu_lib):
+    N = 200
+    a, sa = quantised(M, K, scales_for("block"), seed=M)
+    b, sb = quantised(N, K, "block", seed=K, scale=K ** -0.5)
+    y, s, bound = ref.matmul(a, sa, b, sb, "block")
+    bound = bound + 32 * 2 * ref.U * s
+    close(gdn.gdn_matmul_e4m3(*[t.cuda() for t in (a, sa, b, sb)], out_dtype=F32), (y, bound), "fp32")
+    x, wg, wu, _ = ffn_inputs(M, K // 2 // 8 * 8, 136, BF, seed=M)
+    h = ref.ffn_fwd(x, wg, wu, "silu")[0]
+    got = gdn.gdn_gated_ffn_fwd(x.cuda(), wg.cuda(), wu.cuda())
+    close(got, h, "h")
