@@ -194,7 +194,8 @@ def gdn_gated_ffn_bwd(x, w_gate, w_up, d_h, *, activation="silu", pre=None, need
                       workspace=None, out=None):
     """Gradients of <d_h, h>: dict(dx, dw_gate, dw_up) in x's type, None where not needed; `out` may hold them
     preallocated. pre: what gdn_gated_ffn_fwd(pre=...) wrote for these inputs, or None (gate and up are computed
-    again). The gradients of gate and up are rounded to x's type, the operands' type of the products behind."""
+    again). The gradients of gate and up are rounded to x's type, the operands' type of the products behind (bf16: to
+    a pair of bf16 where rows F, rows K or F K is below 65,536)."""
     ref, _, need, rows, K, F = _ffn_call(x, w_gate, w_up, activation)
     dev, shape = x.device, x.shape
     if d_h is None:

@@ -544,7 +544,8 @@ gdn_status gdn_gated_ffn_fwd(const gdn_ffn_desc* desc, const void* x, const void
                              void* h, float* pre, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Gradients of <d_h, h>. pre: what the forward of the same inputs wrote, or NULL (gate and up are computed
- * again). The gradients of gate and up are rounded to dtype, the operands' type of the products behind.
+ * again). The gradients of gate and up are rounded to dtype, the operands' type of the products behind (bf16: to a
+ * pair of bf16 where rows F, rows K or F K is below 65,536).
  *   d_h [rows,F]; dx [rows,K] or NULL (not written); dw_gate, dw_up [F,K], both or neither */
 gdn_status gdn_gated_ffn_bwd_workspace_size(const gdn_ffn_desc* desc, size_t* bytes);
 gdn_status gdn_gated_ffn_bwd(const gdn_ffn_desc* desc, const void* x, const void* w_gate, const void* w_up,
