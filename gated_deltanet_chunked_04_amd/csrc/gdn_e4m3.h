@@ -48,14 +48,28 @@ __device__ __forceinline__ float scale_of(uint32_t amax_bits) {
 }
 // y / scale to nearest, from the scale's reciprocal: y inv is off by up to 1.5 fp32 steps, which put values that lie on
 // an 8-bit tie to either side (0.2% of the values of rows of small whole numbers); what it leaves of y, times inv
-// again, makes it the nearest in three operations (32,768 x 2,048 80.8 us, one product alone 80.1). An infinite scale
+// again, makes it the nearest in three operations (32,768 x 2,048 80.8 us, one product alone 80.1). What it leaves has to
+// be an fp32 value itself: by scales near fp32's smallest normal one (below 2^-120 or so) it fell under 2^-149 and was lost, ties
+// with it; scales below 2^-100 and their values are taken 2^64 times as large. An infinite scale
 // has inv = 0, and its finite values are 0 / inf = 0: with 0 in place of the scale nothing is added to them.
 struct Divisor {
     float scale, inv;
-    __device__ __forceinline__ explicit Divisor(float s) : inv(1.f / s) { scale = inv == 0.f ? 0.f : s; }
-    __device__ __forceinline__ float quotient(float y) const {
-        const float q = y * inv;
-        return fmaf(fmaf(-q, scale, y), inv, q);
+    bool tiny;
+    __device__ __forceinline__ explicit Divisor(float s) : tiny(s < 0x1p-100f) {
+        if (tiny) s *= 0x1p64f;
+        inv = 1.f / s;
+        scale = inv == 0.f ? 0.f : s;
+    }
+    template <int N>
+    __device__ __forceinline__ void quotients(float (&y)[N]) const {
+        if (__builtin_expect(tiny, 0))
+#pragma unroll
+            for (int i = 0; i < N; ++i) y[i] *= 0x1p64f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float q = y[i] * inv;
+            y[i] = fmaf(fmaf(-q, scale, y[i]), inv, q);
+        }
     }
 };
 

@@ -463,8 +463,9 @@ __device__ __forceinline__ void mm_finish8(Sums& sums, const MmArgs& p, uint32_t
         uint32_t w[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const f32x4 h = sums.acc[t][j];
-            w[j] = pack_e4m3_within(by.quotient(h[0]), by.quotient(h[1]), by.quotient(h[2]), by.quotient(h[3]));
+            float h[4] = {sums.acc[t][j][0], sums.acc[t][j][1], sums.acc[t][j][2], sums.acc[t][j][3]};
+            by.quotients(h);
+            w[j] = pack_e4m3_within(h[0], h[1], h[2], h[3]);
         }
         uint8_t* q = static_cast<uint8_t*>(p.out[0]) + m * p.N + n;
         if (left >= 8) {

@@ -58,9 +58,10 @@ __device__ __forceinline__ uint32_t max_of(uint32_t m) {
 }
 template <typename T>
 __device__ __forceinline__ uint32_t amax8(const Raw<T, 8>& v) { return max_of<T>(max_words<T>(v)); }
-__device__ __forceinline__ void pack8(const float (&v)[8], const Divisor& by, uint32_t& lo, uint32_t& hi) {
-    lo = pack_e4m3_within(by.quotient(v[0]), by.quotient(v[1]), by.quotient(v[2]), by.quotient(v[3]));
-    hi = pack_e4m3_within(by.quotient(v[4]), by.quotient(v[5]), by.quotient(v[6]), by.quotient(v[7]));
+__device__ __forceinline__ void pack8(float (&v)[8], const Divisor& by, uint32_t& lo, uint32_t& hi) {
+    by.quotients(v);
+    lo = pack_e4m3_within(v[0], v[1], v[2], v[3]);
+    hi = pack_e4m3_within(v[4], v[5], v[6], v[7]);
 }
 
 template <typename T>

@@ -165,7 +165,8 @@ __global__ __launch_bounds__(threads_of<LANES>()) void k_rms_fwd(RmsArgs p) {
             const Divisor by(scale[v]);
             float q[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = by.quotient(r[v].get(i) * rstd * w[v].get(i));
+            for (int i = 0; i < 8; ++i) q[i] = r[v].get(i) * rstd * w[v].get(i);
+            by.quotients(q);
             if (live[v])
                 store_e4m3<kOdd>(static_cast<uint8_t*>(p.y) + base + at[v], pack_e4m3(q[0], q[1], q[2], q[3]),
                                  pack_e4m3(q[4], q[5], q[6], q[7]), skip[v]);
@@ -332,8 +333,9 @@ __global__ __launch_bounds__(kLoopThreads) void k_rms_fwd_loop(RmsArgs p) {
             const float scale = scale_of(m);
             const Divisor by(scale);
             for (int64_t c = g * G + id; c < c1; c += n) {
-                const float q = by.quotient(norm(c));
-                y[c] = (uint8_t)pack_e4m3(q, q, q, q);
+                float q[1] = {norm(c)};
+                by.quotients(q);
+                y[c] = (uint8_t)pack_e4m3(q[0], q[0], q[0], q[0]);
             }
             if (id == 0) p.scale[(int64_t)blockIdx.x * groups + g] = scale;
         }
