@@ -47,6 +47,7 @@ size_t mm8_ws(int64_t M, int64_t N, int64_t K, int out_dtype, int scales) {
 
 hipError_t launch_mm8(const Mm8Args& a, int out_dtype, int scales, hipStream_t st) {
     if (a.M == 0) return hipSuccess;
+    if (a.K == 0) scales = 2;  // zeros, whatever the rows' scales are: those of blocks are read with a block alone
     return out_dtype == 1 ? mm8_s<kMmF8x, float>(a, scales, st) : mm8_s<kMmF8, bf16_t>(a, scales, st);
 }
 

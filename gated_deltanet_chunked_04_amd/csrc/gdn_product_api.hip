@@ -82,9 +82,7 @@ gdn_status gdn_matmul_e4m3(const gdn_matmul_desc* desc, const void* a, const flo
                            const float* b_scale, void* y, void* workspace, size_t workspace_bytes, void* stream) {
     if (gdn_status s = check_matmul(desc)) return s;
     if (desc->M && (!y || y == a || y == b || y == a_scale || y == b_scale)) return GDN_ERR_INVALID_ARG;
-    if (desc->M && desc->K && (!a || !b)) return GDN_ERR_INVALID_ARG;
-    // (without a contraction only the rows' own scales are read)
-    if (desc->M && (desc->K || desc->scales == GDN_SCALE_ROW) && (!a_scale || !b_scale)) return GDN_ERR_INVALID_ARG;
+    if (desc->M && desc->K && (!a || !b || !a_scale || !b_scale)) return GDN_ERR_INVALID_ARG;
     if (gdn_status s = check_buf(workspace, mm8_ws(desc->M, desc->N, desc->K, desc->out_dtype, desc->scales), workspace_bytes)) return s;
     const Mm8Args m{desc->M, desc->N, desc->K, a, a_scale, b, b_scale, y, static_cast<unsigned char*>(workspace)};
     ProfScope ps(kKMatmul8, (hipStream_t)stream);

@@ -29,3 +29,14 @@ def test_quant_ties_by_small_scales(at, dt, kind, turned, gpu_lib):
         want, gap = ref.e4m3_nearest(v)
         assert (gap == 0).sum() == 127  # ties indeed
         assert torch.equal(q.cpu().double(), want), (m, (q.cpu().double() != want).sum())
+
+
+@pytest.mark.parametrize("M,N", [(5, 9), (70, 300)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_matmul_of_nothing_by_rows(M, N, dt, gpu_lib):
+    """A contraction of length zero is zero whatever the scales of its rows are."""
+    a, b = (torch.empty(n, 0).to(torch.float8_e4m3fn).cuda() for n in (M, N))
+    for bad in (float("nan"), float("inf"), 1.0):
+        y = gdn.gdn_matmul_e4m3(a, torch.full((M, 1), bad).cuda(), b, torch.full((N, 1), bad).cuda(), out_dtype=dt,
+                                y=torch.full((M, N), 3.0, dtype=dt).cuda())
+        assert (y == 0).all()
