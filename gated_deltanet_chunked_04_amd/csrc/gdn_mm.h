@@ -564,7 +564,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm_any(MmArgs p) {
 }
 
 // ---- the same, memory to LDS without registers ----------------------------------------------
-// 16 (or 4) bytes of each lane from base + off to LDS at lds + 16 (4) lane. In assembly: the compiler takes the builtin for
+// 16 bytes of each lane from base + off to LDS at lds + 16 lane. In assembly: the compiler takes the builtin for
 // a write that every later LDS read has to wait for. Counted by vmcnt like a load; no register is written. M0, which holds the
 // LDS address, is an operand, so that the compiler writes it and knows what it holds (as an instruction of the statement's own it
 // went unseen; the compiler takes no clobber of it). It needs a wait state before the load that uses it.
@@ -574,9 +574,6 @@ __device__ __forceinline__ uint64_t mm_uniform(uint64_t a) {
 __device__ __forceinline__ uint64_t mm_uniform(const void* p) { return mm_uniform((uint64_t)(uintptr_t)p); }
 __device__ __forceinline__ void mm_dma16(uint32_t lds, uint64_t base, uint32_t off) {
     asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(off), "s"(mm_uniform(base)) : "memory");
-}
-__device__ __forceinline__ void mm_dma4(uint32_t lds, uint64_t base, uint32_t off) {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, %2" ::"{m0}"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(off), "s"(mm_uniform(base)) : "memory");
 }
 // All of this wave's loads to LDS have landed and its LDS reads are done; then the workgroup meets.
 __device__ __forceinline__ void mm_meet() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }

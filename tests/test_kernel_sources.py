@@ -35,3 +35,9 @@ def test_assembly_leaves_m0_to_the_compiler(path):
         assert not re.search(r"\bm0\b", instructions, re.I), instructions
         if "load_lds" in instructions:
             assert '"{m0}"' in operands, instructions
+
+@pytest.mark.parametrize("path", FILES, ids=os.path.basename)
+def test_no_helper_without_a_caller(path):
+    everything = "\n".join(code(f) for f in FILES)
+    for name in re.findall(r"__device__ __forceinline__ [^;{}()=]*?(\w+)\(", code(path)):
+        assert len(re.findall(r"\b%s\b" % re.escape(name), everything)) > 1, name
