@@ -180,7 +180,7 @@ void quant_row(const QuantArgs& a, hipStream_t st) {
 template <typename T, bool BLOCK, bool TURNED>
 __global__ __launch_bounds__(kThreads) void k_quant_tile(QuantArgs p) {
     __shared__ uint32_t sh[4];
-    __shared__ uint32_t top[BLOCK ? 1 : 16][128];
+    __shared__ __align__(16) uint32_t top[BLOCK ? 1 : 16][128];
     __shared__ __align__(16) float scales[BLOCK ? 4 : 128];
     __shared__ u32x2 turn[TURNED ? 128 : 1][16];
     const uint32_t tiles = (uint32_t)((p.cols + 127) / 128);

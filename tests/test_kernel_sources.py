@@ -36,8 +36,20 @@ def test_assembly_leaves_m0_to_the_compiler(path):
         if "load_lds" in instructions:
             assert '"{m0}"' in operands, instructions
 
+
 @pytest.mark.parametrize("path", FILES, ids=os.path.basename)
 def test_no_helper_without_a_caller(path):
     everything = "\n".join(code(f) for f in FILES)
     for name in re.findall(r"__device__ __forceinline__ [^;{}()=]*?(\w+)\(", code(path)):
         assert len(re.findall(r"\b%s\b" % re.escape(name), everything)) > 1, name
+
+
+@pytest.mark.parametrize("path", FILES, ids=os.path.basename)
+def test_wide_lds_accesses_are_declared_aligned(path):
+    """An array in LDS that is read or written by 16 bytes says that it lies at a multiple of 16."""
+    text = code(path)
+    wide = set(re.findall(r"reinterpret_cast<(?:const )?(?:u32x4|f32x4)\s*\*>\(\s*&?\s*(\w+)\b", text))
+    for declaration in re.findall(r"__shared__[^;]*;", text):
+        for name in re.findall(r"(\w+)\s*\[", declaration):
+            if name in wide:
+                assert re.search(r"align(?:ed|__)\s*\(\s*\d+", declaration) or re.search(r"\b[uf]32x4\b", declaration), declaration
