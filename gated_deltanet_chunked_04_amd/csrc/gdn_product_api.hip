@@ -3,6 +3,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include "../../include/gdn.h"
 #include "gdn_kernels.h"
 #include "gdn_products.h"
@@ -21,6 +23,12 @@ bool zeros(const int32_t* r, int n) {
 }
 
 bool float_type(int32_t t) { return t == GDN_DTYPE_BF16 || t == GDN_DTYPE_FP32; }
+
+bool is_one_of(const void* out, std::initializer_list<const void*> inputs) {
+    for (const void* in : inputs)
+        if (out == in) return true;
+    return false;
+}
 
 gdn_status check_buf(const void* p, size_t need, size_t bytes) {
     if (!need) return GDN_OK;
@@ -107,7 +115,7 @@ gdn_status gdn_gated_ffn_fwd(const gdn_ffn_desc* desc, const void* x, const void
                              float* pre, void* workspace, size_t workspace_bytes, void* stream) {
     if (gdn_status s = check_ffn(desc, false)) return s;
     if (!w_gate || !w_up || (desc->rows && (!x || !h || h == x || h == w_gate || h == w_up))) return GDN_ERR_INVALID_ARG;
-    if (pre && (static_cast<void*>(pre) == h || static_cast<const void*>(pre) == x)) return GDN_ERR_INVALID_ARG;
+    if (pre && (static_cast<void*>(pre) == h || is_one_of(pre, {x, w_gate, w_up}))) return GDN_ERR_INVALID_ARG;
     if (gdn_status s = check_buf(workspace, ffn_fwd_ws(desc->rows, desc->K, desc->F, desc->dtype), workspace_bytes)) return s;
     FfnArgs a{};
     a.M = desc->rows;
@@ -163,9 +171,10 @@ gdn_status gdn_gated_ffn_e4m3(const gdn_ffn_desc* desc, const void* x, const flo
                               void* workspace, size_t workspace_bytes, void* stream) {
     if (gdn_status s = check_ffn(desc, true)) return s;
     if (!w_gate || !w_up || !gate_scale || !up_scale) return GDN_ERR_INVALID_ARG;
-    if (desc->rows && (!x || !x_scale || !h || h == x || h == w_gate || h == w_up)) return GDN_ERR_INVALID_ARG;
+    const std::initializer_list<const void*> inputs = {x, x_scale, w_gate, gate_scale, w_up, up_scale};
+    if (desc->rows && (!x || !x_scale || !h || is_one_of(h, inputs))) return GDN_ERR_INVALID_ARG;
     const bool quant = desc->out_type == GDN_OUT_E4M3;
-    if (quant ? (desc->rows && (!scale || scale == x_scale || static_cast<void*>(scale) == h)) : scale != nullptr) return GDN_ERR_INVALID_ARG;
+    if (quant ? (desc->rows && (!scale || static_cast<void*>(scale) == h || is_one_of(scale, inputs))) : scale != nullptr) return GDN_ERR_INVALID_ARG;
     if (gdn_status s = check_buf(workspace, ffn8_ws(desc->rows, desc->K, desc->F, desc->dtype, quant), workspace_bytes)) return s;
     FfnArgs a{};
     a.M = desc->rows;

@@ -1,0 +1,32 @@
+"""Outputs of the layer's products in the place of one of their inputs are refused before anything is launched (no GPU)."""
+import ctypes
+
+import pytest
+
+from test_product_abi import BIG, ffn_desc, lib  # noqa: F401
+
+ARGS = [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(10)]
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_ffn_pre_is_no_input(lib, dtype):  # noqa: F811
+    x, wg, wu, h, pre, ws = ARGS[:6]
+    need = ctypes.c_size_t()
+    d = ffn_desc(rows=0, dtype=dtype)
+    assert lib.gdn_gated_ffn_fwd_workspace_size(ctypes.byref(d), ctypes.byref(need)) == 0
+    assert lib.gdn_gated_ffn_fwd(ctypes.byref(d), x, wg, wu, h, pre, ws, BIG, None) == 0  # nothing to do
+    d = ffn_desc(dtype=dtype)
+    for taken in (x, wg, wu, h):
+        assert lib.gdn_gated_ffn_fwd(ctypes.byref(d), x, wg, wu, h, taken, ws, BIG, None) == 1
+
+
+def test_ffn8_outputs_are_no_inputs(lib):  # noqa: F811
+    x, xs, wg, gs, wu, us, h, hs, ws = ARGS[:9]
+    fn = lib.gdn_gated_ffn_e4m3
+    assert fn(ctypes.byref(ffn_desc(rows=0, out_type=1)), x, xs, wg, gs, wu, us, h, hs, ws, BIG, None) == 0
+    quant, plain = (ctypes.byref(ffn_desc(out_type=t)) for t in (1, 0))
+    for taken in (x, xs, wg, gs, wu, us):
+        assert fn(quant, x, xs, wg, gs, wu, us, taken, hs, ws, BIG, None) == 1
+        assert fn(plain, x, xs, wg, gs, wu, us, taken, None, ws, BIG, None) == 1
+        assert fn(quant, x, xs, wg, gs, wu, us, h, taken, ws, BIG, None) == 1
+    assert fn(quant, x, xs, wg, gs, wu, us, h, h, ws, BIG, None) == 1
