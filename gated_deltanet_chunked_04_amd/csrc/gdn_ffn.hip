@@ -47,29 +47,64 @@ __global__ __launch_bounds__(256) void k_ffn_act_bwd(MmArgs p) {
 
 // columns of the gradients of gate and up in the workspace: whole vectors, zeros behind F
 int64_t grad_ld(int64_t F) { return (F + 7) / 8 * 8; }
-// Whether bf16 gradients of gate and up are kept as two bf16 each, the rounded value and what that leaves (16 bits). One alone
-// adds as much to the results as their own rounding does, a factor of sqrt 2 in the 2-norm. That is the mean: where one of the
-// matrices has fewer than 65,536 values the factor itself scatters (16 x 4,096 with F = 16: up to 1.77; from 65,536 values on
-// within 0.02), and there the products are short.
+// Whether bf16 gradients of gate and up are kept as two bf16 each, the rounded value and what that leaves (16 bits), side by side
+// in a memory row. Rounded once, they make the error of dx and of the weights' gradients sqrt 2 times these results' own
+// rounding; in small matrices, where few of them weigh most, up to 2.4 times (16 values; 1.3 to 1.8 with 256, 1.33 to 1.50 with
+// 4,096, 1.40 to 1.43 with 65,536). As pairs they add nothing to it (1.00), for twice the matrix instructions and no second
+// read of the weights or of x (mm_pair_row). Below 65,536 values in one of the matrices that is no time lost: 7 x 8,192 x 8,192
+// all gradients 300 us, 8 rows, which are rounded once, 384; 32,768 x 8,192 with F = 7 648, with F = 9 870. Large ones would pay it
+// (8,192 x 2,048 x 8,192: dx and dw, 1,000 us, are the matrix cores').
 bool grad_pairs(int64_t M, int64_t K, int64_t F) {
     const int64_t few = 65536;
     return M * F < few || M * K < few || F * K < few;
 }
 
+// dx and both weights' gradients from the gradients of gate and up, d.
+template <int KIND, typename T, bool PAIRS>
+hipError_t bwd_products(const FfnArgs& a, void* const (&d)[2], int64_t ldd, void* part, hipStream_t st) {
+    MmArgs p{};
+    for (int i = 0; i < 2; ++i) p.x[i] = u8(d[i]);
+    p.low = PAIRS ? ldd * (int64_t)sizeof(T) : 0;
+    p.ldx = (PAIRS ? 2 : 1) * ldd * (int64_t)sizeof(T);
+    p.ldw = a.K * (int64_t)sizeof(T);
+    p.N = p.ldo = a.K;
+    if (a.dx && a.M) {
+        p.w[0] = u8(a.wg);
+        p.w[1] = u8(a.wu);
+        p.M = a.M;
+        p.K = a.F;
+        p.segs = 2;
+        p.outs = 1;
+        p.out[0] = a.dx;
+        if (hipError_t e = mm_run<KIND, kMmPlain, false, true, false, kMmOut, T, PAIRS>(p, part, st)) return e;
+    }
+    if (a.dwg) {
+        p.w[0] = u8(a.x);
+        p.w[1] = nullptr;
+        p.M = a.F;
+        p.K = a.M;
+        p.segs = 1;
+        p.outs = 2;
+        p.out[0] = a.dwg;
+        p.out[1] = a.dwu;
+        if (hipError_t e = mm_run<KIND, kMmPlain, true, true, false, kMmOut, T, PAIRS>(p, part, st)) return e;
+    }
+    return hipGetLastError();
+}
+
 template <int KIND, typename T>
 hipError_t bwd(const FfnArgs& a, hipStream_t st) {
     const int64_t size = sizeof(T), ldd = grad_ld(a.F);
-    const size_t bytes = align256((size_t)(a.M * ldd * size));
     const bool pairs = KIND == kMmBf16 && grad_pairs(a.M, a.K, a.F);
-    void *d[2] = {a.ws, a.ws + bytes}, *part = a.ws + (pairs ? 4 : 2) * bytes;
-    const int64_t low = pairs ? 2 * (int64_t)bytes : 0;
+    const size_t bytes = align256((size_t)((pairs ? 2 : 1) * a.M * ldd * size));
+    void *const d[2] = {a.ws, a.ws + bytes}, *const part = a.ws + 2 * bytes;
     if (a.M) {
         MmArgs p = block_args(a, size);
         p.out[0] = d[0];
         p.out[1] = d[1];
-        p.ldo = ldd;
+        p.ldo = (pairs ? 2 : 1) * ldd;
         p.d_h = a.d_h;
-        p.low = low;
+        p.low = pairs ? ldd * size : 0;
         if (a.pre) {
             const int64_t blocks = ((a.F + 7) / 8 * a.M + 255) / 256;
             if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
@@ -78,41 +113,9 @@ hipError_t bwd(const FfnArgs& a, hipStream_t st) {
             return e;
         }
     }
-    if (a.dx && a.M) {
-        MmArgs p{};
-        for (int i = 0; i < 2; ++i) p.x[i] = u8(d[i]);
-        p.w[0] = u8(a.wg);
-        p.w[1] = u8(a.wu);
-        p.ldx = ldd * size;
-        p.ldw = a.K * size;
-        p.M = a.M;
-        p.N = a.K;
-        p.K = a.F;
-        p.segs = pairs ? 4 : 2;
-        p.low = low;
-        p.outs = 1;
-        p.out[0] = a.dx;
-        p.ldo = a.K;
-        if (hipError_t e = mm_run<KIND, kMmPlain, false, true, false, kMmOut, T>(p, part, st)) return e;
-    }
-    if (a.dwg) {
-        MmArgs p{};
-        for (int i = 0; i < 2; ++i) p.x[i] = u8(d[i]);
-        p.w[0] = u8(a.x);
-        p.ldx = ldd * size;
-        p.ldw = a.K * size;
-        p.M = a.F;
-        p.N = a.K;
-        p.K = a.M;
-        p.segs = pairs ? 2 : 1;
-        p.low = low;
-        p.outs = 2;
-        p.out[0] = a.dwg;
-        p.out[1] = a.dwu;
-        p.ldo = a.K;
-        if (hipError_t e = mm_run<KIND, kMmPlain, true, true, false, kMmOut, T>(p, part, st)) return e;
-    }
-    return hipGetLastError();
+    if constexpr (KIND == kMmBf16)
+        if (pairs) return bwd_products<KIND, T, true>(a, d, ldd, part, st);
+    return bwd_products<KIND, T, false>(a, d, ldd, part, st);
 }
 
 template <int KIND, typename T, int EPI = kMmFfn>
@@ -134,11 +137,11 @@ size_t ffn_fwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
 }
 size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
     const int kind = dtype == 1 ? kMmF32 : kMmBf16;
-    const int n = kind == kMmBf16 && grad_pairs(M, K, F) ? 2 : 1;
+    const bool pairs = kind == kMmBf16 && grad_pairs(M, K, F);
     size_t part = mm_plan(kind, kMmPlain, M, F, K, 1, 1, false, true).bytes;
-    for (size_t b : {mm_plan(kind, kMmPlain, M, K, F, 2 * n, 1, true, false).bytes, mm_plan(kind, kMmPlain, F, K, M, n, 2, true, false).bytes})
+    for (size_t b : {mm_plan(kind, kMmPlain, M, K, F, 2, 1, true, false, pairs).bytes, mm_plan(kind, kMmPlain, F, K, M, 1, 2, true, false, pairs).bytes})
         if (b > part) part = b;
-    return 2 * n * align256((size_t)(M * grad_ld(F) * (dtype == 1 ? 4 : 2))) + part;
+    return 2 * align256((size_t)((pairs ? 2 : 1) * M * grad_ld(F) * (dtype == 1 ? 4 : 2))) + part;
 }
 // Few rows, or a split contraction: the parts, and the block's fp32 output in front of its quantisation. Otherwise the
 // workgroup that has a row's 128 columns quantises them.

@@ -167,19 +167,25 @@ __device__ __forceinline__ u32x4 mm_chunk(const uint8_t* p, int64_t off, int64_t
 // An operand's tile of R rows from row r0 on, in chunks: which memory row and byte a chunk has, and where it goes.
 // Rows behind the operand's last one repeat it (they reach outputs that are not stored); steps behind the contraction
 // are zeros.
-template <int E, int R, bool kTurned, int kFar>
+// PAIRS: X's values are pairs, what rounding left of a value `low` bytes behind it in its memory row. The tile's rows are then
+// 16 rows' values, the same rows' other halves, the next 16 rows' values, and so on: R / 2 rows, whose two halves meet one tile of W.
+__device__ __forceinline__ int mm_pair_row(int r) { return (r >> 5) * 16 + (r & 15); }
+__device__ __forceinline__ bool mm_pair_low(int r) { return r & 16; }
+template <int E, int R, bool kTurned, int kFar, bool PAIRS = false>
 struct MmTile {
     static constexpr int kChunks = R * 8;
     static constexpr int kWide = R * E / 16;  // chunks of a turned memory row
     static __device__ __forceinline__ int lds(int i) {
         return kTurned ? mm_turn_at<R, E>(i / kWide, i % kWide) : mm_at<kFar>(i >> 3, i & 7);
     }
-    static __device__ __forceinline__ u32x4 load(const uint8_t* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t K, int i) {
+    static __device__ __forceinline__ u32x4 load(const uint8_t* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t K, int i, int64_t low = 0) {
+        const int at = kTurned ? i % kWide * (16 / E) : i >> 3;  // the tile's row
+        if (PAIRS && mm_pair_low(at)) p += low;
         if constexpr (kTurned) {
             const int64_t k = k0 + i / kWide;
-            return k < K ? mm_chunk(p + k * ld, r0 * E + 16 * (i % kWide), rows * E) : u32x4{0, 0, 0, 0};
+            return k < K ? mm_chunk(p + k * ld, (r0 + (PAIRS ? mm_pair_row(at) : at)) * E, rows * E) : u32x4{0, 0, 0, 0};
         } else {
-            const int64_t r = r0 + (i >> 3);
+            const int64_t r = r0 + (PAIRS ? mm_pair_row(at) : at);
             return mm_chunk(p + (r < rows ? r : rows - 1) * ld, k0 * E + 16 * (i & 7), K * E);
         }
     }
@@ -191,10 +197,10 @@ enum MmScales { kMmPlain = 0, kMmBlock = 1, kMmGroup = 2, kMmRow = 3 };
 struct MmArgs {
     const uint8_t* x[2];  // per segment of the contraction (dx: d_gate, d_up), or per output (dw)
     const uint8_t* w[2];  // per segment, or gate and up side by side (the block's forward)
-    int64_t low;          // 0, or the bytes from x to what its rounding left (of d_gate and d_up): further segments
+    int64_t low;          // 0, or the bytes from a value to what its rounding left (of d_gate and d_up), in the same memory row
     int64_t ldx, ldw;     // bytes between two memory rows
     int64_t M, N, K;      // rows of X, of W (of each where there are two side by side), contraction of a segment
-    int32_t segs;         // segments of the contraction, at most 4
+    int32_t segs;         // segments of the contraction, 1 or 2
     int32_t outs;         // outputs, each with its x (dw)
     const float* xs;      // scales of e4m3 operands: [M, kb] (row: [M])
     const float* ws[2];   // block: [ceil(N/128), kb], group: [N, kb], row: [N]
@@ -310,7 +316,7 @@ __device__ __forceinline__ void mm_gate(const MmArgs& p, int64_t m, int64_t n, c
             du[i] = i < left ? d[i] * f.f : 0.f;
         }
         // rounded to the inputs' type: they are operands of the products behind, which take whole vectors of their rows
-        // (ldo is a multiple of 8) and multiply what lies behind column N by zero
+        // and multiply what lies behind column N by zero
         T* const g = static_cast<T*>(p.out[0]) + m * p.ldo + n;
         T* const v = static_cast<T*>(p.out[1]) + m * p.ldo + n;
         mm_store<T, R>(g, da, R);
@@ -323,8 +329,8 @@ __device__ __forceinline__ void mm_gate(const MmArgs& p, int64_t m, int64_t n, c
         }
     }
 }
-// Columns that an epilogue writes.
-template <int EPI> __device__ __forceinline__ int64_t mm_width(const MmArgs& p) { return EPI == kMmFfnBwd ? p.ldo : p.N; }
+// Columns that an epilogue writes: those of the gradients of gate and up to the end of their last vector.
+template <int EPI> __host__ __device__ __forceinline__ int64_t mm_width(const MmArgs& p) { return EPI == kMmFfnBwd ? (p.N + 7) / 8 * 8 : p.N; }
 
 // R columns of sums at (m, n): one side, or gate and up.
 template <int EPI, typename T, int SC, bool DUAL, int R>
@@ -387,12 +393,9 @@ template <bool PAIR, bool DUAL> struct MmCols {
     // the lane's first column of tile j
     static __device__ __forceinline__ int col(int j, int gq) { return row(j) + kStride * gq; }
 };
-// A segment of the contraction: which of the two X and W it takes, and whether what rounding left of X. Turned X (dw): the
-// output's x, then what is left of it; else both x, then what is left of both.
-template <bool XT> __device__ __forceinline__ const uint8_t* mm_x(const MmArgs& p, int seg, int z) {
-    return ((XT ? z : seg & 1) ? p.x[1] : p.x[0]) + ((XT ? seg : seg >> 1) ? p.low : 0);
-}
-template <bool XT> __device__ __forceinline__ const uint8_t* mm_w(const MmArgs& p, int seg) { return !XT && (seg & 1) ? p.w[1] : p.w[0]; }
+// Which of the two X and W a segment of the contraction takes. Turned X (dw): the output's.
+template <bool XT> __device__ __forceinline__ const uint8_t* mm_x(const MmArgs& p, int seg, int z) { return (XT ? z : seg) ? p.x[1] : p.x[0]; }
+template <bool XT> __device__ __forceinline__ const uint8_t* mm_w(const MmArgs& p, int seg) { return !XT && seg ? p.w[1] : p.w[0]; }
 template <typename T, bool WT, bool DUAL> constexpr bool mm_pair() { return DUAL || (sizeof(T) == 2 && !WT); }
 
 // The sums of a wave's MT x NT tiles, scaled where the operands are e4m3. Shared by the kernels below.
@@ -406,14 +409,16 @@ struct MmSums {
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(c[i], SC == kMmBlock ? sx * sw[0] : sx * sw[i], acc[t][j][i]);
     }
-    // Hands the lane's outputs on: X's row m0 + 16 t + ln, the columns that MmCols names.
-    template <int EPI, typename T, bool PAIR>
+    // Hands the lane's outputs on: X's row m0 + 16 t + ln, the columns that MmCols names. PAIRS: tiles 2 t and 2 t + 1 are the
+    // same rows'.
+    template <int EPI, typename T, bool PAIR, bool PAIRS = false>
     __device__ __forceinline__ void finish(const MmArgs& p, void* out, int part, int64_t m0, int64_t n0) const {
         using C = MmCols<PAIR, DUAL>;
         constexpr int kRun = PAIR ? 8 : 4;
         const int ln = threadIdx.x & 15, gq = threadIdx.x >> 4 & 3;
+        constexpr int kOf = PAIRS ? 2 : 1;
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
+        for (int t = 0; t < MT / kOf; ++t) {
             const int64_t m = m0 + 16 * t + ln;
             if (m >= p.M) continue;
 #pragma unroll
@@ -424,7 +429,11 @@ struct MmSums {
 #pragma unroll
                 for (int j = 0; j < (DUAL ? 4 : kRun / 4); ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[DUAL ? j / 2 : 0][(j % (kRun / 4)) * 4 + i] = acc[t][q + j][i];
+                    for (int i = 0; i < 4; ++i) {
+                        float& to = v[DUAL ? j / 2 : 0][(j % (kRun / 4)) * 4 + i];
+                        to = acc[kOf * t][q + j][i];
+                        if (PAIRS) to += acc[kOf * t + kOf - 1][q + j][i];
+                    }
                 mm_finish<EPI, T, SC, DUAL, kRun>(p, out, part, m, n, v);
             }
         }
@@ -483,7 +492,7 @@ __device__ __forceinline__ void mm_finish8(Sums& sums, const MmArgs& p, uint32_t
 // through registers, the next step's on their way while one is multiplied; one tile of each operand in LDS. Eight waves,
 // two on a SIMD, so that one's LDS reads pass behind the other's products (1,003 x 777 x 1,001 in e4m3 19.4 us, with four
 // waves of 64 x 64 20.0).
-template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T, int WM, int WN>
+template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T, int WM, int WN, bool PAIRS>
 __global__ __launch_bounds__(64 * WM * WN) void k_mm_any(MmArgs p) {
     constexpr int E = mm_size<KIND>(), MT = 8 / WM, NT = 4;
     using C = MmCols<mm_pair<T, WT, DUAL>(), DUAL>;
@@ -491,23 +500,24 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm_any(MmArgs p) {
     constexpr int kRows = 64 * WN, kCols = DUAL ? kRows / 2 : kRows, kThreads = 64 * WM * WN;
     constexpr int kXC = 1024 / kThreads, kWC = kRows * 8 / kThreads;
     using Sums = MmSums<KIND, SC, DUAL, MT, NT>;
-    using X = MmTile<E, 128, XT, kNear>;
+    using X = MmTile<E, 128, XT, kNear, PAIRS>;
     using W = MmTile<E, kCols, WT, C::kFar>;
+    constexpr int kOf = PAIRS ? 2 : 1, BM = 128 / kOf;  // rows of X
     __shared__ __align__(16) uint8_t xt[128 * kMmStep], wt[kRows * kMmStep];
     const int wave = wave_id(), wm = wave % WM, wn = wave / WM;
     const int ln = threadIdx.x & 15, gq = threadIdx.x >> 4 & 3;
-    const int64_t tm = (p.M + 127) / 128, tn = (p.N + kCols - 1) / kCols;
-    const int64_t m0 = (blockIdx.x % tm) * 128, n0 = (blockIdx.x / tm % tn) * kCols;
+    const int64_t tm = (p.M + BM - 1) / BM, tn = (p.N + kCols - 1) / kCols;
+    const int64_t m0 = (blockIdx.x % tm) * BM, n0 = (blockIdx.x / tm % tn) * kCols;
     const int rest = (int)(blockIdx.x / (tm * tn)), z = rest % p.outs, part = rest / p.outs;
     const int32_t per = (int32_t)((p.K + kSteps - 1) / kSteps);
     const int32_t begin = part * p.share, end = p.splits ? min(begin + p.share, per * p.segs) : per * p.segs;
     Sums sums;
     u32x4 cx[kXC], cw[kWC];
     auto load = [&](int32_t it) {
-        const int seg = (it >= per) + (it >= 2 * per) + (it >= 3 * per);
+        const int seg = it >= per;
         const int64_t k0 = (int64_t)(it - seg * per) * kSteps;
 #pragma unroll
-        for (int i = 0; i < kXC; ++i) cx[i] = X::load(mm_x<XT>(p, seg, z), p.ldx, m0, p.M, k0, p.K, threadIdx.x + kThreads * i);
+        for (int i = 0; i < kXC; ++i) cx[i] = X::load(mm_x<XT>(p, seg, z), p.ldx, m0, p.M, k0, p.K, threadIdx.x + kThreads * i, p.low);
 #pragma unroll
         for (int i = 0; i < kWC; ++i) {
             const int c = threadIdx.x + kThreads * i;
@@ -559,7 +569,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm_any(MmArgs p) {
         __syncthreads();
         mm_finish8<Sums, MT>(sums, p, reinterpret_cast<uint32_t*>(xt), wm * (16 * MT), wn, m0 + wm * (16 * MT), n0);
     } else {
-        sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, z ? p.out[1] : p.out[0], z * p.splits + part, m0 + wm * (16 * MT), n0 + wn * (kCols / WN));
+        sums.template finish<EPI, T, mm_pair<T, WT, DUAL>(), PAIRS>(p, z ? p.out[1] : p.out[0], z * p.splits + part, m0 + wm * (16 * MT / kOf), n0 + wn * (kCols / WN));
     }
 }
 
@@ -601,7 +611,7 @@ struct MmPlace {
 // matrix instructions need 2,048; without loads from memory 2,420 cycles, at a lower clock. e4m3 by blocks, 32,768 x 6,144 x
 // 2,048: 430 us (1.9 PFLOP/s), with a scaled sum for each 128 products on the vector ALUs. BM is 128 where widened operands
 // or fp32 leave no registers for 256, and where that fills the card better (mm_plan).
-template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T, int BM>
+template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T, int BM, bool PAIRS>
 __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
     constexpr int E = mm_size<KIND>(), MT = BM / 32, NT = 4, BN = 256;
     using C = MmCols<mm_pair<T, WT, DUAL>(), DUAL>;
@@ -617,9 +627,10 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
     __shared__ __align__(128) uint8_t sh[2 * (kStage + kSRows * 16)];
     const int wave = wave_id(), lane = threadIdx.x & 63, wm = wave & 1, wn = wave >> 1;
     const int ln = lane & 15, gq = lane >> 4;
-    const int32_t tm = (int32_t)((p.M + BM - 1) / BM), tn = (int32_t)((p.N + kCols - 1) / kCols);
+    constexpr int kOf = PAIRS ? 2 : 1, kXRows = BM / kOf;  // rows of X
+    const int32_t tm = (int32_t)((p.M + kXRows - 1) / kXRows), tn = (int32_t)((p.N + kCols - 1) / kCols);
     const MmPlace at(blockIdx.x, gridDim.x, tm, tn);
-    const int64_t m0 = (int64_t)at.m * BM, n0 = (int64_t)at.n * kCols;
+    const int64_t m0 = (int64_t)at.m * kXRows, n0 = (int64_t)at.n * kCols;
     const int z = at.rest % p.outs, part = at.rest / p.outs;
     const int32_t per = (int32_t)((p.K + kSteps - 1) / kSteps);
     const int32_t begin = part * p.share, end = p.splits ? min(begin + p.share, per * p.segs) : per * p.segs;
@@ -633,14 +644,16 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
     for (int i = 0; i < kXC; ++i) {
         const int c = threadIdx.x + 512 * i;
         if constexpr (XT) {
-            const int k = c / X::kWide, b = ((c % X::kWide) ^ mm_turn_key<BM, E>(k)) * 16;
-            const int64_t col = m0 * E + b;
+            const int k = c / X::kWide, r = ((c % X::kWide) ^ mm_turn_key<BM, E>(k)) * (16 / E);
+            const int64_t col = (m0 + (PAIRS ? mm_pair_row(r) : r)) * E;
             xk[i] = k;
             xo[i] = (uint32_t)(k * p.ldx) + (uint32_t)(min(col, (p.M * E - 1) / 16 * 16) - m0 * E);
+            if (PAIRS && mm_pair_low(r)) xo[i] += (uint32_t)p.low;
         } else {
-            const int r = c >> 3, b = ((c & 7) ^ mm_key<kNear>(r)) * 16;
+            const int r = c >> 3, b = ((c & 7) ^ mm_key<kNear>(r)) * 16, row = PAIRS ? mm_pair_row(r) : r;
             xk[i] = b;
-            xo[i] = (uint32_t)((m0 + r < p.M ? r : p.M - 1 - m0) * p.ldx) + b;
+            xo[i] = (uint32_t)((m0 + row < p.M ? row : p.M - 1 - m0) * p.ldx) + b;
+            if (PAIRS && mm_pair_low(r)) xo[i] += (uint32_t)p.low;
         }
     }
 #pragma unroll
@@ -684,10 +697,10 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
     const int64_t xstep = XT ? kSteps * p.ldx : kMmStep, wstep = WT ? kSteps * p.ldw : kMmStep;
     const int32_t whole = (int32_t)(p.K / kSteps), rest = (int32_t)(p.K % kSteps);
     const int64_t xat = XT ? m0 * E : m0 * p.ldx, wat = WT ? n0 * E : n0 * p.ldw;
-    // Whether there may be several segments. (Only the turned products have them, and the others are told so; not the one by
-    // groups of widened e4m3, whose schedule comes out 5% quicker with the test in it: 6,144 x 2,048 x 32,768 983 us, 1,035.)
-    constexpr bool kSegs = WT || (KIND == kMmF8x && SC == kMmGroup);
-    int32_t seg = kSegs ? (begin >= per) + (begin >= 2 * per) + (begin >= 3 * per) : 0, kt = begin - seg * per;
+    // Whether there may be two segments. (Only dx has them, and the others are told so; not the one by
+    // groups of widened e4m3, whose schedule comes out 4% quicker with the test in it: 6,144 x 2,048 x 32,768 971 us, 1,011.)
+    constexpr bool kSegs = (WT && !XT) || (KIND == kMmF8x && SC == kMmGroup);
+    int32_t seg = kSegs ? begin >= per : 0, kt = begin - seg * per;
     uint64_t xs = mm_uniform(mm_x<XT>(p, seg, z) + xat + kt * xstep);
     uint64_t ws0 = mm_uniform((DUAL ? p.w[0] : mm_w<XT>(p, seg)) + wat + kt * wstep), ws1 = mm_uniform(p.w[1] + wat + kt * wstep);
     auto fetch = [&](int stage) {
@@ -819,7 +832,7 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
         mm_meet();
         mm_finish8<Sums, MT>(sums, p, reinterpret_cast<uint32_t*>(sh), wm * (BM / 2), wn, m0 + wm * (BM / 2), n0);
     } else {
-        sums.template finish<EPI, T, mm_pair<T, WT, DUAL>()>(p, z ? p.out[1] : p.out[0], z * p.splits + part, m0 + wm * (BM / 2), n0 + wn * (kCols / 4));
+        sums.template finish<EPI, T, mm_pair<T, WT, DUAL>(), PAIRS>(p, z ? p.out[1] : p.out[0], z * p.splits + part, m0 + wm * (kXRows / 2), n0 + wn * (kCols / 4));
     }
 }
 
@@ -920,7 +933,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_mm_few(MmArgs p) {
 
 // ---- which kernel ----------------------------------------------------------------------------
 inline int64_t mm_blocks(int64_t M, int64_t N, bool dual, int BM) { return ((M + BM - 1) / BM) * ((N + (dual ? 127 : 255)) / (dual ? 128 : 256)); }
-inline int64_t mm_any_blocks(int64_t M, int64_t N, bool dual) { return ((M + 127) / 128) * ((N + (dual ? 63 : 127)) / (dual ? 64 : 128)); }
+inline int64_t mm_any_blocks(int64_t M, int64_t N, bool dual, int BM) { return ((M + BM - 1) / BM) * ((N + (dual ? 63 : 127)) / (dual ? 64 : 128)); }
 
 // Whether k_mm takes the operands.
 inline bool mm_fits(const MmArgs& p) {
@@ -941,7 +954,7 @@ struct MmPlan {
     int splits, share;
     size_t bytes;  // of the parts
 };
-inline MmPlan mm_plan(int kind, int sc, int64_t M, int64_t N, int64_t K, int segs, int outs, bool turned, bool dual) {
+inline MmPlan mm_plan(int kind, int sc, int64_t M, int64_t N, int64_t K, int segs, int outs, bool turned, bool dual, bool pairs = false) {
     MmPlan r{};
     const int E = kind == kMmBf16 ? 2 : (kind == kMmF32 ? 4 : 1), steps = kMmStep / E;
     r.few = !turned && segs == 1 && outs == 1 && mm_is_few(M, K * E);
@@ -953,13 +966,14 @@ inline MmPlan mm_plan(int kind, int sc, int64_t M, int64_t N, int64_t K, int seg
     // write and read at 4 TB/s.
     const bool odd = (turned ? N : K) * E % 16;
     const double step = odd ? (kind == kMmF32 ? 3.2 : (kind == kMmF8x ? 2.8 : 1.6)) : (kind == kMmF32 ? 4.0 : (kind == kMmF8x ? 2.0 : (kind == kMmF8 ? 1.2 : 1.0)));
-    const int64_t tiles = (odd ? mm_any_blocks(M, N, dual) : mm_blocks(M, N, dual, 128)) * outs, slots = odd ? 512 : 256;
+    const int rows = pairs ? 64 : 128;  // of X in a tile of 128
+    const int64_t tiles = (odd ? mm_any_blocks(M, N, dual, rows) : mm_blocks(M, N, dual, rows)) * outs, slots = odd ? 512 : 256;
     const double sums = 2e-6 * (double)M * (double)N * outs * (dual ? 2 : 1);
     double best = step * ((tiles + slots - 1) / slots) * total;
     r.bm = 128;
     const int64_t large = mm_blocks(M, N, dual, 256) * outs;
     const double large_us = (kind == kMmF8 ? 2.0 : 1.6) * ((large + 255) / 256) * total;
-    if (!odd && kind != kMmF8x && kind != kMmF32 && large_us <= best) {
+    if (!odd && !pairs && kind != kMmF8x && kind != kMmF32 && large_us <= best) {
         r.bm = 256;
         best = large_us;
     }
@@ -980,7 +994,7 @@ inline MmPlan mm_plan(int kind, int sc, int64_t M, int64_t N, int64_t K, int seg
 
 template <int KIND, int SC, bool DUAL, int EPI, typename T, int MT, bool WHOLE>
 hipError_t mm_few(const MmArgs& p, hipStream_t st) {
-    const int64_t blocks = ((EPI == kMmFfnBwd ? p.ldo : p.N) + 15) / 16;
+    const int64_t blocks = (mm_width<EPI>(p) + 15) / 16;
     const bool many = blocks <= 128 && p.K * mm_size<KIND>() >= 16 * kMmStep && MT * (DUAL ? 2 : 1) <= 4;
     if (blocks > UINT32_MAX / 1024) return hipErrorInvalidConfiguration;
     if constexpr (MT * (DUAL ? 2 : 1) <= 4)
@@ -996,31 +1010,32 @@ hipError_t mm_few(const MmArgs& p, hipStream_t st) {
     return mm_fits(p) ? mm_few<KIND, SC, DUAL, EPI, T, MT, true>(p, st) : mm_few<KIND, SC, DUAL, EPI, T, MT, false>(p, st);
 }
 
-template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
+template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T, bool PAIRS>
 hipError_t mm_tiles(const MmArgs& p, int bm, hipStream_t st) {
     const int64_t times = (int64_t)p.outs * (p.splits ? p.splits : 1);
+    constexpr int kOf = PAIRS ? 2 : 1;
     if (mm_fits(p)) {
-        const int64_t blocks = mm_blocks(p.M, p.N, DUAL, bm) * times;
+        const int64_t blocks = mm_blocks(p.M, p.N, DUAL, bm / kOf) * times;
         if (blocks > UINT32_MAX / 512 || blocks > INT32_MAX) return hipErrorInvalidConfiguration;
-        if constexpr (KIND != kMmF8x && KIND != kMmF32 && EPI != kMmPart)
+        if constexpr (KIND != kMmF8x && KIND != kMmF32 && EPI != kMmPart && !PAIRS)
             if (bm == 256) {
-                hipLaunchKernelGGL((k_mm<KIND, SC, XT, WT, DUAL, EPI, T, 256>), dim3((unsigned)blocks), dim3(512), 0, st, p);
+                hipLaunchKernelGGL((k_mm<KIND, SC, XT, WT, DUAL, EPI, T, 256, false>), dim3((unsigned)blocks), dim3(512), 0, st, p);
                 return hipGetLastError();
             }
-        hipLaunchKernelGGL((k_mm<KIND, SC, XT, WT, DUAL, EPI, T, 128>), dim3((unsigned)blocks), dim3(512), 0, st, p);
+        hipLaunchKernelGGL((k_mm<KIND, SC, XT, WT, DUAL, EPI, T, 128, PAIRS>), dim3((unsigned)blocks), dim3(512), 0, st, p);
         return hipGetLastError();
     }
     constexpr int kWide = EPI == kMmFfn8 ? 4 : 2;  // (128 columns of h share a scale)
-    const int64_t blocks = (kWide == 4 ? mm_blocks(p.M, p.N, DUAL, 128) : mm_any_blocks(p.M, p.N, DUAL)) * times;
+    const int64_t blocks = (kWide == 4 ? mm_blocks(p.M, p.N, DUAL, 128) : mm_any_blocks(p.M, p.N, DUAL, 128 / kOf)) * times;
     if (blocks > UINT32_MAX / 512) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_mm_any<KIND, SC, XT, WT, DUAL, EPI, T, 8 / kWide, kWide>), dim3((unsigned)blocks), dim3(512), 0, st, p);
+    hipLaunchKernelGGL((k_mm_any<KIND, SC, XT, WT, DUAL, EPI, T, 8 / kWide, kWide, PAIRS>), dim3((unsigned)blocks), dim3(512), 0, st, p);
     return hipGetLastError();
 }
 
 // `part`: the workspace that mm_plan asked for.
-template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T>
+template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T, bool PAIRS = false>
 hipError_t mm_run(MmArgs p, void* part, hipStream_t st) {
-    const MmPlan r = mm_plan(KIND, SC, p.M, p.N, p.K, p.segs, p.outs, XT || WT, DUAL);
+    const MmPlan r = mm_plan(KIND, SC, p.M, p.N, p.K, p.segs, p.outs, XT || WT, DUAL, PAIRS);
     if constexpr (!XT && !WT && EPI != kMmFfn8)
         if (r.few) {
             if (p.M <= 16) return mm_few<KIND, SC, DUAL, EPI, T, 1>(p, st);
@@ -1032,12 +1047,12 @@ hipError_t mm_run(MmArgs p, void* part, hipStream_t st) {
             p.splits = r.splits;
             p.share = r.share;
             p.part = static_cast<float*>(part);
-            if (hipError_t e = mm_tiles<KIND, SC, XT, WT, DUAL, kMmPart, T>(p, r.bm, st)) return e;
-            const int64_t blocks = (((EPI == kMmFfnBwd ? p.ldo : p.N) + 3) / 4 * p.M + 255) / 256;
+            if (hipError_t e = mm_tiles<KIND, SC, XT, WT, DUAL, kMmPart, T, PAIRS>(p, r.bm, st)) return e;
+            const int64_t blocks = ((mm_width<EPI>(p) + 3) / 4 * p.M + 255) / 256;
             hipLaunchKernelGGL((k_mm_join<SC, DUAL, EPI, T>), dim3((unsigned)blocks, (unsigned)p.outs), dim3(256), 0, st, p);
             return hipGetLastError();
         }
-    return mm_tiles<KIND, SC, XT, WT, DUAL, EPI, T>(p, r.bm, st);
+    return mm_tiles<KIND, SC, XT, WT, DUAL, EPI, T, PAIRS>(p, r.bm, st);
 }
 
 }  // namespace gdn

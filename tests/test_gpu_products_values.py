@@ -5,7 +5,8 @@ import torch
 
 import gated_deltanet_chunked_04_amd as gdn
 from oracle import products as ref
-from test_gpu_products import BF, F32
+from test_gpu_products import BF, F32, ffn_inputs
+from test_gpu_products_edges import bound_of
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,27 @@ def test_matmul_of_nothing_by_rows(M, N, dt, gpu_lib):
         y = gdn.gdn_matmul_e4m3(a, torch.full((M, 1), bad).cuda(), b, torch.full((N, 1), bad).cuda(), out_dtype=dt,
                                 y=torch.full((M, N), 3.0, dtype=dt).cuda())
         assert (y == 0).all()
+
+
+# few rows over large weights, few columns under many rows, several tiles of each operand; rows that are whole chunks and not
+@pytest.mark.parametrize("M,K,F", [(7, 8192, 1032), (1, 4104, 2056), (520, 120, 264), (65, 960, 136), (200, 72, 130), (9001, 264, 7), (130, 101, 99), (63, 1000, 1000)])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_ffn_pairs_in_tiles(M, K, F, act, gpu_lib):
+    """Gradients of gate and up kept as pairs of bf16: dx and the weights' gradients are off by their own rounding and 2^-15
+    of the products' terms, in every tile."""
+    x, wg, wu, d = ffn_inputs(M, K, F, BF, seed=M + K)
+    dev = [t.cuda() for t in (x, wg, wu)]
+    want = ref.ffn_bwd(x, wg, wu, d, act, F32)
+    terms = bound_of(x, wg, wu, d, act)
+    out = {k: torch.full((len(t) + 2, t.shape[1]), 9.0, dtype=BF).cuda() for k, t in (("dx", x), ("dw_gate", wg), ("dw_up", wu))}
+    for kept in (True, False):
+        pre = gdn.gdn_gated_ffn_pre(dev[0], dev[1]) if kept else None
+        if kept:
+            gdn.gdn_gated_ffn_fwd(*dev, pre=pre, activation=act)
+        gdn.gdn_gated_ffn_bwd(*dev, d.cuda(), pre=pre, activation=act, out={k: t[1:-1] for k, t in out.items()})
+        for k, (v, e) in want.items():
+            got = out[k][1:-1].cpu().double()
+            assert ((got - v).abs() <= 2.0 ** -8 * v.abs() + 1.01 * e + 2.0 ** -15 * terms[k]).all(), (k, kept)
+            # in the 2-norm: its own rounding is 2^-9.2 of it, and a lost half of the pairs would make that 2^-8.7
+            assert (got - v).norm() <= 1.12 * (v.to(BF).double() - v).norm() + 2.0 ** -15 * v.norm(), (k, kept)
+            assert (out[k][0] == 9).all() and (out[k][-1] == 9).all(), "rows around the output were written"
