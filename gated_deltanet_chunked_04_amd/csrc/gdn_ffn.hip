@@ -145,8 +145,8 @@ size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
 }
 // Few rows, or a split contraction: the parts, and the block's fp32 output in front of its quantisation. Otherwise the
 // workgroup that has a row's 128 columns quantises them.
-size_t ffn8_ws(int64_t M, int64_t K, int64_t F, int dtype, bool quant) {
-    const MmPlan r = mm_plan(quant || dtype == 1 ? kMmF8x : kMmF8, kMmBlock, M, F, K, 1, 1, false, true);
+size_t ffn8_ws(int64_t M, int64_t K, int64_t F, int dtype, bool quant, bool exact) {
+    const MmPlan r = mm_plan(quant || exact || dtype == 1 ? kMmF8x : kMmF8, kMmBlock, M, F, K, 1, 1, false, true);
     return (quant && (r.few || r.splits) ? align256((size_t)(M * F * 4)) : 0) + r.bytes;
 }
 
@@ -158,9 +158,10 @@ hipError_t launch_ffn_fwd(const FfnArgs& a, int dtype, hipStream_t st) {
 hipError_t launch_ffn_bwd(const FfnArgs& a, int dtype, hipStream_t st) {
     return dtype == 1 ? bwd<kMmF32, float>(a, st) : bwd<kMmBf16, bf16_t>(a, st);
 }
-hipError_t launch_ffn8(const FfnArgs& a, int dtype, hipStream_t st) {
+hipError_t launch_ffn8(const FfnArgs& a, int dtype, bool exact, hipStream_t st) {
     if (a.M == 0) return hipSuccess;
-    if (!a.hs) return dtype == 1 ? ffn8<kMmF8x, float>(a, a.h, a.ws, st) : ffn8<kMmF8, bf16_t>(a, a.h, a.ws, st);
+    if (!a.hs && dtype == 1) return ffn8<kMmF8x, float>(a, a.h, a.ws, st);
+    if (!a.hs) return exact ? ffn8<kMmF8x, bf16_t>(a, a.h, a.ws, st) : ffn8<kMmF8, bf16_t>(a, a.h, a.ws, st);
     const MmPlan r = mm_plan(kMmF8x, kMmBlock, a.M, a.F, a.K, 1, 1, false, true);
     if (!r.few && !r.splits) return ffn8<kMmF8x, float, kMmFfn8>(a, a.h, nullptr, st);
     if (hipError_t e = ffn8<kMmF8x, float>(a, a.ws, a.ws + align256((size_t)(a.M * a.F * 4)), st)) return e;

@@ -26,7 +26,8 @@ namespace gdn {
 // instruction adds products in groups of eight that it aligns to the largest of them and cuts about 13 bits below it
 // (measured: a product of 1 beside one of 448^2 in its group is lost; on quantised normal data its sums of 128 are off
 // by 1.5e-5 in the 2-norm, the widened ones by 1e-8). That is a hundredth of a bf16 output's own rounding, so kMmF8 is
-// for outputs in bf16 and kMmF8x for what is kept in 32 bits: fp32 outputs and the scales of an e4m3 output.
+// for outputs in bf16, and kMmF8x for what is kept in 32 bits (fp32 outputs and the scales of an e4m3 output) and for bf16
+// outputs of callers whose large products cancel, who ask for it (32,768 x 6,144 x 2,048 by blocks 430 us and 782).
 enum MmKind { kMmBf16 = 0, kMmF32 = 1, kMmF8 = 2, kMmF8x = 3 };
 template <int KIND> constexpr int mm_size() { return KIND == kMmBf16 ? 2 : (KIND == kMmF32 ? 4 : 1); }
 constexpr int kMmStep = 128;  // bytes of a row per step

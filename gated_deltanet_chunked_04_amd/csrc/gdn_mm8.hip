@@ -41,14 +41,15 @@ MmScales scales_of(int scales) { return scales == 2 ? kMmBlock : (scales == 1 ? 
 
 }  // namespace
 
-size_t mm8_ws(int64_t M, int64_t N, int64_t K, int out_dtype, int scales) {
-    return mm_plan(out_dtype == 1 ? kMmF8x : kMmF8, scales_of(scales), M, N, K, 1, 1, false, false).bytes;
+size_t mm8_ws(int64_t M, int64_t N, int64_t K, int out_dtype, int scales, bool exact) {
+    return mm_plan(out_dtype == 1 || exact ? kMmF8x : kMmF8, scales_of(scales), M, N, K, 1, 1, false, false).bytes;
 }
 
-hipError_t launch_mm8(const Mm8Args& a, int out_dtype, int scales, hipStream_t st) {
+hipError_t launch_mm8(const Mm8Args& a, int out_dtype, int scales, bool exact, hipStream_t st) {
     if (a.M == 0) return hipSuccess;
     if (a.K == 0) scales = 2;  // zeros, whatever the rows' scales are: those of blocks are read with a block alone
-    return out_dtype == 1 ? mm8_s<kMmF8x, float>(a, scales, st) : mm8_s<kMmF8, bf16_t>(a, scales, st);
+    if (out_dtype == 1) return mm8_s<kMmF8x, float>(a, scales, st);
+    return exact ? mm8_s<kMmF8x, bf16_t>(a, scales, st) : mm8_s<kMmF8, bf16_t>(a, scales, st);
 }
 
 }  // namespace gdn

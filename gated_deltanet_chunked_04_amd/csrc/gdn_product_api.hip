@@ -46,7 +46,7 @@ gdn_status check_quant(const gdn_quant_desc* d) {
 }
 
 gdn_status check_matmul(const gdn_matmul_desc* d) {
-    if (!d || d->flags || !zeros(d->reserved, 5) || !float_type(d->out_dtype)) return GDN_ERR_INVALID_ARG;
+    if (!d || (d->flags & ~GDN_FLAG_EXACT_SUMS) || !zeros(d->reserved, 5) || !float_type(d->out_dtype)) return GDN_ERR_INVALID_ARG;
     if (d->M < 0 || d->N < 1 || d->K < 0) return GDN_ERR_INVALID_ARG;
     if (d->scales < GDN_SCALE_ROW || d->scales > GDN_SCALE_BLOCK) return GDN_ERR_INVALID_ARG;
     if (d->M > kMaxRows || d->N > kMaxRows || d->K > kMaxRows) return GDN_ERR_UNSUPPORTED;
@@ -54,7 +54,7 @@ gdn_status check_matmul(const gdn_matmul_desc* d) {
 }
 
 gdn_status check_ffn(const gdn_ffn_desc* d, bool e4m3) {
-    if (!d || d->flags || !zeros(d->reserved, 4) || !float_type(d->dtype)) return GDN_ERR_INVALID_ARG;
+    if (!d || (d->flags & ~(e4m3 ? GDN_FLAG_EXACT_SUMS : 0)) || !zeros(d->reserved, 4) || !float_type(d->dtype)) return GDN_ERR_INVALID_ARG;
     if (d->rows < 0 || d->K < 1 || d->F < 1) return GDN_ERR_INVALID_ARG;
     if (d->activation != GDN_ACT_SILU && d->activation != GDN_ACT_GELU_TANH) return GDN_ERR_INVALID_ARG;
     if (d->out_type != GDN_OUT_SAME && (!e4m3 || d->out_type != GDN_OUT_E4M3)) return GDN_ERR_INVALID_ARG;
@@ -82,7 +82,7 @@ gdn_status gdn_quant_e4m3(const gdn_quant_desc* desc, const void* x, void* q, fl
 gdn_status gdn_matmul_e4m3_workspace_size(const gdn_matmul_desc* desc, size_t* bytes) {
     if (!bytes) return GDN_ERR_INVALID_ARG;
     if (gdn_status s = check_matmul(desc)) return s;
-    *bytes = mm8_ws(desc->M, desc->N, desc->K, desc->out_dtype, desc->scales);
+    *bytes = mm8_ws(desc->M, desc->N, desc->K, desc->out_dtype, desc->scales, desc->flags != 0);
     return GDN_OK;
 }
 
@@ -91,10 +91,10 @@ gdn_status gdn_matmul_e4m3(const gdn_matmul_desc* desc, const void* a, const flo
     if (gdn_status s = check_matmul(desc)) return s;
     if (desc->M && (!y || y == a || y == b || y == a_scale || y == b_scale)) return GDN_ERR_INVALID_ARG;
     if (desc->M && desc->K && (!a || !b || !a_scale || !b_scale)) return GDN_ERR_INVALID_ARG;
-    if (gdn_status s = check_buf(workspace, mm8_ws(desc->M, desc->N, desc->K, desc->out_dtype, desc->scales), workspace_bytes)) return s;
+    if (gdn_status s = check_buf(workspace, mm8_ws(desc->M, desc->N, desc->K, desc->out_dtype, desc->scales, desc->flags != 0), workspace_bytes)) return s;
     const Mm8Args m{desc->M, desc->N, desc->K, a, a_scale, b, b_scale, y, static_cast<unsigned char*>(workspace)};
     ProfScope ps(kKMatmul8, (hipStream_t)stream);
-    return launched(launch_mm8(m, desc->out_dtype, desc->scales, (hipStream_t)stream));
+    return launched(launch_mm8(m, desc->out_dtype, desc->scales, desc->flags != 0, (hipStream_t)stream));
 }
 
 gdn_status gdn_gated_ffn_fwd_workspace_size(const gdn_ffn_desc* desc, size_t* bytes) {
@@ -162,7 +162,7 @@ gdn_status gdn_gated_ffn_bwd(const gdn_ffn_desc* desc, const void* x, const void
 gdn_status gdn_gated_ffn_e4m3_workspace_size(const gdn_ffn_desc* desc, size_t* bytes) {
     if (!bytes) return GDN_ERR_INVALID_ARG;
     if (gdn_status s = check_ffn(desc, true)) return s;
-    *bytes = ffn8_ws(desc->rows, desc->K, desc->F, desc->dtype, desc->out_type == GDN_OUT_E4M3);
+    *bytes = ffn8_ws(desc->rows, desc->K, desc->F, desc->dtype, desc->out_type == GDN_OUT_E4M3, desc->flags != 0);
     return GDN_OK;
 }
 
@@ -175,7 +175,7 @@ gdn_status gdn_gated_ffn_e4m3(const gdn_ffn_desc* desc, const void* x, const flo
     if (desc->rows && (!x || !x_scale || !h || is_one_of(h, inputs))) return GDN_ERR_INVALID_ARG;
     const bool quant = desc->out_type == GDN_OUT_E4M3;
     if (quant ? (desc->rows && (!scale || static_cast<void*>(scale) == h || is_one_of(scale, inputs))) : scale != nullptr) return GDN_ERR_INVALID_ARG;
-    if (gdn_status s = check_buf(workspace, ffn8_ws(desc->rows, desc->K, desc->F, desc->dtype, quant), workspace_bytes)) return s;
+    if (gdn_status s = check_buf(workspace, ffn8_ws(desc->rows, desc->K, desc->F, desc->dtype, quant, desc->flags != 0), workspace_bytes)) return s;
     FfnArgs a{};
     a.M = desc->rows;
     a.K = desc->K;
@@ -191,7 +191,7 @@ gdn_status gdn_gated_ffn_e4m3(const gdn_ffn_desc* desc, const void* x, const flo
     a.hs = scale;
     a.ws = static_cast<unsigned char*>(workspace);
     ProfScope ps(kKFfn8, (hipStream_t)stream);
-    return launched(launch_ffn8(a, desc->dtype, (hipStream_t)stream));
+    return launched(launch_ffn8(a, desc->dtype, desc->flags != 0, (hipStream_t)stream));
 }
 
 }  // extern "C"

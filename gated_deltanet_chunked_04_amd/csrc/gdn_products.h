@@ -25,9 +25,10 @@ struct Mm8Args {
     void* y;
     unsigned char* ws;
 };
-size_t mm8_ws(int64_t M, int64_t N, int64_t K, int out_dtype, int scales);
+// exact: sums as in fp32 for an output in bf16 too (those of an output in fp32 always are)
+size_t mm8_ws(int64_t M, int64_t N, int64_t K, int out_dtype, int scales, bool exact);
 // scales as above, of b (a's are a row's where b's are, else of 128 columns)
-hipError_t launch_mm8(const Mm8Args& a, int out_dtype, int scales, hipStream_t st);
+hipError_t launch_mm8(const Mm8Args& a, int out_dtype, int scales, bool exact, hipStream_t st);
 
 struct FfnArgs {
     int64_t M, K, F;
@@ -50,9 +51,9 @@ struct FfnArgs {
 };
 size_t ffn_fwd_ws(int64_t M, int64_t K, int64_t F, int dtype);
 size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype);
-size_t ffn8_ws(int64_t M, int64_t K, int64_t F, int dtype, bool quant);
+size_t ffn8_ws(int64_t M, int64_t K, int64_t F, int dtype, bool quant, bool exact);
 hipError_t launch_ffn_fwd(const FfnArgs& a, int dtype, hipStream_t st);
 hipError_t launch_ffn_bwd(const FfnArgs& a, int dtype, hipStream_t st);
-hipError_t launch_ffn8(const FfnArgs& a, int dtype, hipStream_t st);
+hipError_t launch_ffn8(const FfnArgs& a, int dtype, bool exact, hipStream_t st);
 
 }  // namespace gdn

@@ -20,7 +20,7 @@ import functools
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._abi import (GDN_ACT_GELU_TANH, GDN_ACT_SILU, GDN_DTYPE_BF16, GDN_OUT_E4M3, GDN_OUT_SAME, GDN_SCALE_BLOCK,
+from ._abi import (GDN_ACT_GELU_TANH, GDN_ACT_SILU, GDN_DTYPE_BF16, GDN_FLAG_EXACT_SUMS, GDN_OUT_E4M3, GDN_OUT_SAME, GDN_SCALE_BLOCK,
                    GDN_SCALE_GROUP, GDN_SCALE_ROW, GdnFfnDesc, GdnMatmulDesc, GdnQuantDesc, load_library)
 from .layer import _DTYPES, _bytes, _dense, _dtype, _like, _out, _run, _scratch
 
@@ -92,19 +92,20 @@ def gdn_quant_e4m3(x, *, quant="group", transpose=False, q=None, scale=None):
 
 
 @functools.lru_cache(maxsize=1024)
-def _matmul_plan(M, N, K, out_dtype, scales):
+def _matmul_plan(M, N, K, out_dtype, scales, exact):
     """(descriptor, its workspace size)."""
-    desc = GdnMatmulDesc(M, N, K, out_dtype, scales)
+    desc = GdnMatmulDesc(M, N, K, out_dtype, scales, GDN_FLAG_EXACT_SUMS if exact else 0)
     return ctypes.byref(desc), _bytes("gdn_matmul_e4m3_workspace_size", desc)
 
 
-def gdn_matmul_e4m3(a, a_scale, b, b_scale, *, out_dtype=torch.bfloat16, y=None, workspace=None):
+def gdn_matmul_e4m3(a, a_scale, b, b_scale, *, out_dtype=torch.bfloat16, exact=False, y=None, workspace=None):
     """y = a b^T of quantised a [..., K] and b [N, K]: [..., N] in out_dtype, bf16 or fp32.
 
     b_scale is [ceil(N/128), ceil(K/128)] or [N, ceil(K/128)] with a_scale [..., ceil(K/128)], or [N, 1] with
     a_scale [..., 1] (what gdn_quant_e4m3 and gdn_rmsnorm_fwd give). With fp32 the products and sums are fp32's;
     bf16 takes the 8-bit matrix instruction, whose sums of eight products drop what lies about 2^-13 below the
-    largest of them (include/gdn.h): twice as fast, and for activations and weights far below bf16's rounding."""
+    largest of them (include/gdn.h): twice as fast, and for activations and weights far below bf16's rounding. Where
+    large products cancel, exact=True gives fp32's products and sums, rounded to bf16 at the end."""
     M, K = _matrix("a", a)
     if a.dtype != E4M3:
         raise TypeError("a: expected torch.float8_e4m3fn")
@@ -126,7 +127,7 @@ def gdn_matmul_e4m3(a, a_scale, b, b_scale, *, out_dtype=torch.bfloat16, y=None,
     else:
         raise ValueError(f"scales {ashape} and {bshape} fit no kind: a [..., {kb}] with b [{_blocks(N)}, {kb}] or [{N}, {kb}], "
                          f"or a [..., 1] with b [{N}, 1]")
-    ref, need = _matmul_plan(M, N, K, out, kind)
+    ref, need = _matmul_plan(M, N, K, out, kind, bool(exact))
     y, py = _out("y", y, a, (*lead, N), out_dtype, dev)
     pw, wb, ws = _scratch(need, a, workspace)
     _run(load_library().gdn_matmul_e4m3, dev, ref, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), py, pw, wb)
@@ -145,8 +146,8 @@ def _ffn_plan(rows, K, F, dtype, activation):
 
 
 @functools.lru_cache(maxsize=1024)
-def _ffn8_plan(rows, K, F, dtype, activation, out_type):
-    desc = GdnFfnDesc(rows, K, F, dtype, activation, out_type)
+def _ffn8_plan(rows, K, F, dtype, activation, out_type, exact):
+    desc = GdnFfnDesc(rows, K, F, dtype, activation, out_type, GDN_FLAG_EXACT_SUMS if exact else 0)
     return ctypes.byref(desc), _bytes("gdn_gated_ffn_e4m3_workspace_size", desc)
 
 
@@ -217,10 +218,11 @@ def gdn_gated_ffn_bwd(x, w_gate, w_up, d_h, *, activation="silu", pre=None, need
 
 
 def gdn_gated_ffn_e4m3(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, activation="silu", quant=None,
-                       out_dtype=torch.bfloat16, h=None, scale=None, workspace=None):
+                       out_dtype=torch.bfloat16, exact=False, h=None, scale=None, workspace=None):
     """The block on quantised x [..., K] (scales per 128 columns) and weights [F, K] (scales per 128 x 128). Returns
-    (h, scale or None): h [..., F] in out_dtype (bf16 by the 8-bit matrix instruction, fp32 with fp32's products; see
-    gdn_matmul_e4m3), or with quant='group' in e4m3 with scales per 128 columns, quantised from its fp32 values."""
+    (h, scale or None): h [..., F] in out_dtype (bf16 by the 8-bit matrix instruction, or with exact=True and in fp32
+    with fp32's products and sums; see gdn_matmul_e4m3), or with quant='group' in e4m3 with scales per 128 columns,
+    quantised from its fp32 values."""
     rows, K = _matrix("x", x)
     if x.dtype != E4M3:
         raise TypeError("x: expected torch.float8_e4m3fn")
@@ -238,7 +240,8 @@ def gdn_gated_ffn_e4m3(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, activa
     pxs = _like("x_scale", x_scale, (*lead, kb), torch.float32, dev)
     pgs = _like("gate_scale", gate_scale, sshape, torch.float32, dev)
     pus = _like("up_scale", up_scale, sshape, torch.float32, dev)
-    ref, need = _ffn8_plan(rows, K, F, GDN_DTYPE_BF16 if quant else dtype, _gate(activation), GDN_OUT_E4M3 if quant else GDN_OUT_SAME)
+    ref, need = _ffn8_plan(rows, K, F, GDN_DTYPE_BF16 if quant else dtype, _gate(activation), GDN_OUT_E4M3 if quant else GDN_OUT_SAME,
+                           bool(exact))
     h, ph = _out("h", h, x, (*lead, F), E4M3 if quant else out_dtype, dev)
     if quant:
         scale, psc = _out("scale", scale, x, (*lead, _blocks(F)), torch.float32, dev)
@@ -256,13 +259,13 @@ def gdn_gated_ffn_e4m3(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, activa
 
 class _LinearE4m3(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, need_dx, need_dw):
+    def forward(ctx, x, weight, need_dx, need_dw, exact):
         q, s = gdn_quant_e4m3(x, quant="group")
-        y = gdn_matmul_e4m3(q, s, *gdn_quant_e4m3(weight, quant="block"), out_dtype=x.dtype)
+        y = gdn_matmul_e4m3(q, s, *gdn_quant_e4m3(weight, quant="block"), out_dtype=x.dtype, exact=exact)
         # of x the backward needs what the weight gradient contracts: its columns, in e4m3
         turned = gdn_quant_e4m3(x, quant="group", transpose=True) if need_dw else (None, None)
         ctx.save_for_backward(weight if need_dx else None, *turned)
-        ctx.w_dtype = weight.dtype
+        ctx.w_dtype, ctx.exact = weight.dtype, exact
         return y
 
     @staticmethod
@@ -273,26 +276,27 @@ class _LinearE4m3(torch.autograd.Function):
         dx = dw = None
         if weight is not None:
             q, s = gdn_quant_e4m3(d_y, quant="group")
-            dx = gdn_matmul_e4m3(q, s, *gdn_quant_e4m3(weight, quant="block", transpose=True), out_dtype=d_y.dtype)
+            dx = gdn_matmul_e4m3(q, s, *gdn_quant_e4m3(weight, quant="block", transpose=True), out_dtype=d_y.dtype, exact=ctx.exact)
         if xq is not None:
             q, s = gdn_quant_e4m3(d_y, quant="group", transpose=True)
-            dw = gdn_matmul_e4m3(q, s, xq, xs, out_dtype=ctx.w_dtype)
-        return dx, dw, None, None
+            dw = gdn_matmul_e4m3(q, s, xq, xs, out_dtype=ctx.w_dtype, exact=ctx.exact)
+        return dx, dw, None, None, None
 
 
-def linear_e4m3(x, weight):
+def linear_e4m3(x, weight, *, exact=False):
     """y = x weight^T through e4m3, with autograd (x, weight): y [..., N] in x's type.
 
     x [..., K] and weight [N, K], each bf16 or fp32, are quantised on the way (x per 128 columns, weight per 128 x
     128), and so is the gradient that comes back (per 128 columns for dx, per 128 tokens for the weight's). Held for
-    the backward: x in e4m3, quantised along its tokens."""
+    the backward: x in e4m3, quantised along its tokens. exact: sums as in fp32 in the three products' bf16 outputs
+    too (gdn_matmul_e4m3)."""
     rows, K = _matrix("x", x)
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2 or weight.shape[1] != K:
         raise ValueError(f"weight: expected [N, {K}]")
     if weight.device != x.device:
         raise ValueError(f"weight: expected a tensor on {x.device}")
     grad = torch.is_grad_enabled()
-    return _LinearE4m3.apply(x, weight, grad and x.requires_grad, grad and weight.requires_grad)
+    return _LinearE4m3.apply(x, weight, grad and x.requires_grad, grad and weight.requires_grad, bool(exact))
 
 
 class _GatedFfn(torch.autograd.Function):

@@ -510,12 +510,15 @@ gdn_status gdn_quant_e4m3(const gdn_quant_desc* desc, const void* x, void* q, fl
  *   GDN_DTYPE_BF16: by the 8-bit matrix instruction, at about twice the rate: it adds products in groups
  *   of eight (neighbours along K) aligned to the largest of them, and drops what lies about 2^-13 below
  *   it. On quantised activations and weights that is 1.5e-5 of the result in the 2-norm, a hundredth
- *   of the rounding to bf16; where large products cancel, ask for fp32. */
+ *   of the rounding to bf16. Where large products cancel it is more, up to all that is left: ask for
+ *   GDN_FLAG_EXACT_SUMS, with which the products and sums are those of fp32 and rounded to bf16 at the
+ *   end (the flag says nothing new for an output in fp32). */
+#define GDN_FLAG_EXACT_SUMS 256
 typedef struct gdn_matmul_desc {
     int64_t M, N, K;
     int32_t out_dtype;   /* gdn_dtype of y */
     int32_t scales;      /* gdn_scales of b */
-    int32_t flags;       /* must be zero */
+    int32_t flags;       /* 0 or GDN_FLAG_EXACT_SUMS */
     int32_t reserved[5]; /* must be zero */
 } gdn_matmul_desc;
 
@@ -533,7 +536,7 @@ typedef struct gdn_ffn_desc {
     int32_t dtype;       /* gdn_dtype of x, the weights, h and their gradients (gdn_gated_ffn_e4m3: of h) */
     int32_t activation;  /* GDN_ACT_SILU or GDN_ACT_GELU_TANH */
     int32_t out_type;    /* gdn_out_type of h: GDN_OUT_E4M3 with gdn_gated_ffn_e4m3 alone */
-    int32_t flags;       /* must be zero */
+    int32_t flags;       /* 0, or with gdn_gated_ffn_e4m3 GDN_FLAG_EXACT_SUMS */
     int32_t reserved[4]; /* must be zero */
 } gdn_ffn_desc;
 
@@ -553,8 +556,9 @@ gdn_status gdn_gated_ffn_bwd(const gdn_ffn_desc* desc, const void* x, const void
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* Forward on quantised x (GDN_SCALE_GROUP) and weights (GDN_SCALE_BLOCK). h [rows,F] in dtype (scale
- * NULL; a bf16 h by the 8-bit matrix instruction, see gdn_matmul_e4m3), or with GDN_OUT_E4M3 quantised
- * from its fp32 values, scale [rows, ceil(F/128)] (GDN_SCALE_GROUP; dtype is then ignored). */
+ * NULL; a bf16 h by the 8-bit matrix instruction unless GDN_FLAG_EXACT_SUMS is set, see gdn_matmul_e4m3),
+ * or with GDN_OUT_E4M3 quantised from its fp32 values, scale [rows, ceil(F/128)] (GDN_SCALE_GROUP; dtype is
+ * then ignored). */
 gdn_status gdn_gated_ffn_e4m3_workspace_size(const gdn_ffn_desc* desc, size_t* bytes);
 gdn_status gdn_gated_ffn_e4m3(const gdn_ffn_desc* desc, const void* x, const float* x_scale,
                               const void* w_gate, const float* gate_scale, const void* w_up,

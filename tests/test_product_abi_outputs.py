@@ -3,7 +3,7 @@ import ctypes
 
 import pytest
 
-from test_product_abi import BIG, ffn_desc, lib  # noqa: F401
+from test_product_abi import BIG, ffn_desc, lib, mm_desc  # noqa: F401
 
 ARGS = [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(10)]
 
@@ -30,3 +30,13 @@ def test_ffn8_outputs_are_no_inputs(lib):  # noqa: F811
         assert fn(plain, x, xs, wg, gs, wu, us, taken, None, ws, BIG, None) == 1
         assert fn(quant, x, xs, wg, gs, wu, us, h, taken, ws, BIG, None) == 1
     assert fn(quant, x, xs, wg, gs, wu, us, h, h, ws, BIG, None) == 1
+
+
+def test_flags(lib):  # noqa: F811
+    """Exact sums may be asked for where the operands are e4m3, and nothing else."""
+    n = ctypes.byref(ctypes.c_size_t())
+    for flags, code in ((0, 0), (256, 0), (128, 1), (257, 1), (-1, 1)):
+        assert lib.gdn_matmul_e4m3_workspace_size(ctypes.byref(mm_desc(flags=flags)), n) == code
+        assert lib.gdn_gated_ffn_e4m3_workspace_size(ctypes.byref(ffn_desc(flags=flags)), n) == code
+        assert lib.gdn_gated_ffn_fwd_workspace_size(ctypes.byref(ffn_desc(flags=flags)), n) == (1 if flags else 0)
+        assert lib.gdn_gated_ffn_bwd_workspace_size(ctypes.byref(ffn_desc(flags=flags)), n) == (1 if flags else 0)
