@@ -29,7 +29,8 @@ def test_matmul_split(M, N, K, kind, gpu_lib):
     near(got, y, 2.0 ** -9 + 2.0 ** -13, "bf16")
 
 
-# tiles of 128 and 256 rows and columns met and passed by one, one step of the contraction and a bit, several tiles a side
+# tiles of 128 rows and 256 columns met and passed by one, one step of the contraction and a bit, several tiles a side (tiles of
+# 256 rows: test_gpu_products_tiles.py)
 @pytest.mark.parametrize("M,N,K", [(255, 257, 128), (256, 256, 256), (257, 255, 144), (511, 513, 400), (1025, 129, 16), (129, 1025, 1008), (640, 2304, 512)])
 def test_matmul_tiles(M, N, K, gpu_lib):
     for kind in ("block", "group", "row"):
