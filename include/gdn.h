@@ -505,7 +505,9 @@ gdn_status gdn_quant_e4m3(const gdn_quant_desc* desc, const void* x, void* q, fl
 
 /* y = a b^T of quantised matrices a [M,K] and b [N,K], y [M,N] in out_dtype. desc->scales is the kind of
  * b's scales: GDN_SCALE_BLOCK or GDN_SCALE_GROUP with a_scale in groups [M, ceil(K/128)], GDN_SCALE_ROW
- * with a_scale [M]. The scaled sums are fp32. K may be 0 (y is 0, and no scale is read).
+ * with a_scale [M]. The scaled sums are fp32, and so is the product of two scales that a sum is
+ * multiplied by: below 2^-126 it loses bits, below 2^-149 the sum counts as 0 (values near 1e-17 in
+ * both operands, or near 1e-32 in one beside 0.1 in the other). K may be 0 (y is 0, and no scale is read).
  *   GDN_DTYPE_FP32: products and sums as in fp32.
  *   GDN_DTYPE_BF16: by the 8-bit matrix instruction, at about twice the rate: it adds products in groups
  *   of eight (neighbours along K) aligned to the largest of them, and drops what lies about 2^-13 below
