@@ -18,7 +18,7 @@ CP_MODES = {"auto": 0, "off": 1, "on": 2, "exact": 3, "warmup": 4, "pages": 5}
 GDN_FLAG_KEEP_FORWARD, GDN_FLAG_REUSE_FORWARD, GDN_FLAG_QK_L2NORM, GDN_FLAG_BWD_ADJOINT_PASS = 1, 2, 4, 8
 GDN_FLAG_FWD_FUSED, GDN_FLAG_FWD_SPLIT, GDN_FLAG_REUSE_CP = 16, 32, 64
 GDN_FLAG_ZERO_OUTSIDE = 128
-GDN_FLAG_EXACT_SUMS = 256
+GDN_FLAG_EXACT_SUMS, GDN_FLAG_GRAD_PAIRS = 256, 512
 GDN_ABI_VERSION = 10
 GDN_NOALLOC_SCRATCH_BYTES = 128 << 20
 

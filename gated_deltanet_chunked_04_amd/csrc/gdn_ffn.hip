@@ -52,8 +52,8 @@ int64_t grad_ld(int64_t F) { return (F + 7) / 8 * 8; }
 // rounding; in small matrices, where few of them weigh most, up to 2.4 times (16 values; 1.3 to 1.8 with 256, 1.33 to 1.50 with
 // 4,096, 1.40 to 1.43 with 65,536). As pairs they add nothing to it (1.00), for twice the matrix instructions and no second
 // read of the weights or of x (mm_pair_row). Below 65,536 values in one of the matrices that is no time lost: 7 x 8,192 x 8,192
-// all gradients 300 us, 8 rows, which are rounded once, 384; 32,768 x 8,192 with F = 7 648, with F = 9 870. Large ones would pay it
-// (8,192 x 2,048 x 8,192: dx and dw, 1,000 us, are the matrix cores').
+// all gradients 300 us, 8 rows, which are rounded once, 384; 32,768 x 8,192 with F = 7 648, with F = 9 870. Large ones pay it
+// where the caller asks (8,192 x 2,048 x 8,192: all gradients 1,040 us, as pairs 2,690, for tiles of 64 rows too).
 bool grad_pairs(int64_t M, int64_t K, int64_t F) {
     const int64_t few = 65536;
     return M * F < few || M * K < few || F * K < few;
@@ -95,7 +95,7 @@ hipError_t bwd_products(const FfnArgs& a, void* const (&d)[2], int64_t ldd, void
 template <int KIND, typename T>
 hipError_t bwd(const FfnArgs& a, hipStream_t st) {
     const int64_t size = sizeof(T), ldd = grad_ld(a.F);
-    const bool pairs = KIND == kMmBf16 && grad_pairs(a.M, a.K, a.F);
+    const bool pairs = KIND == kMmBf16 && (a.pairs || grad_pairs(a.M, a.K, a.F));
     const size_t bytes = align256((size_t)((pairs ? 2 : 1) * a.M * ldd * size));
     void *const d[2] = {a.ws, a.ws + bytes}, *const part = a.ws + 2 * bytes;
     if (a.M) {
@@ -135,9 +135,9 @@ hipError_t ffn8(const FfnArgs& a, void* h, void* part, hipStream_t st) {
 size_t ffn_fwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
     return mm_plan(dtype == 1 ? kMmF32 : kMmBf16, kMmPlain, M, F, K, 1, 1, false, true).bytes;
 }
-size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype) {
+size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype, bool pairs) {
     const int kind = dtype == 1 ? kMmF32 : kMmBf16;
-    const bool pairs = kind == kMmBf16 && grad_pairs(M, K, F);
+    pairs = kind == kMmBf16 && (pairs || grad_pairs(M, K, F));
     size_t part = mm_plan(kind, kMmPlain, M, F, K, 1, 1, false, true).bytes;
     for (size_t b : {mm_plan(kind, kMmPlain, M, K, F, 2, 1, true, false, pairs).bytes, mm_plan(kind, kMmPlain, F, K, M, 1, 2, true, false, pairs).bytes})
         if (b > part) part = b;

@@ -53,8 +53,9 @@ gdn_status check_matmul(const gdn_matmul_desc* d) {
     return GDN_OK;
 }
 
-gdn_status check_ffn(const gdn_ffn_desc* d, bool e4m3) {
-    if (!d || (d->flags & ~(e4m3 ? GDN_FLAG_EXACT_SUMS : 0)) || !zeros(d->reserved, 4) || !float_type(d->dtype)) return GDN_ERR_INVALID_ARG;
+// flags: which the call takes
+gdn_status check_ffn(const gdn_ffn_desc* d, bool e4m3, int32_t flags = 0) {
+    if (!d || (d->flags & ~flags) || !zeros(d->reserved, 4) || !float_type(d->dtype)) return GDN_ERR_INVALID_ARG;
     if (d->rows < 0 || d->K < 1 || d->F < 1) return GDN_ERR_INVALID_ARG;
     if (d->activation != GDN_ACT_SILU && d->activation != GDN_ACT_GELU_TANH) return GDN_ERR_INVALID_ARG;
     if (d->out_type != GDN_OUT_SAME && (!e4m3 || d->out_type != GDN_OUT_E4M3)) return GDN_ERR_INVALID_ARG;
@@ -106,8 +107,8 @@ gdn_status gdn_gated_ffn_fwd_workspace_size(const gdn_ffn_desc* desc, size_t* by
 
 gdn_status gdn_gated_ffn_bwd_workspace_size(const gdn_ffn_desc* desc, size_t* bytes) {
     if (!bytes) return GDN_ERR_INVALID_ARG;
-    if (gdn_status s = check_ffn(desc, false)) return s;
-    *bytes = ffn_bwd_ws(desc->rows, desc->K, desc->F, desc->dtype);
+    if (gdn_status s = check_ffn(desc, false, GDN_FLAG_GRAD_PAIRS)) return s;
+    *bytes = ffn_bwd_ws(desc->rows, desc->K, desc->F, desc->dtype, desc->flags != 0);
     return GDN_OK;
 }
 
@@ -135,17 +136,18 @@ gdn_status gdn_gated_ffn_fwd(const gdn_ffn_desc* desc, const void* x, const void
 gdn_status gdn_gated_ffn_bwd(const gdn_ffn_desc* desc, const void* x, const void* w_gate, const void* w_up,
                              const float* pre, const void* d_h, void* dx, void* dw_gate, void* dw_up, void* workspace,
                              size_t workspace_bytes, void* stream) {
-    if (gdn_status s = check_ffn(desc, false)) return s;
+    if (gdn_status s = check_ffn(desc, false, GDN_FLAG_GRAD_PAIRS)) return s;
     if (!w_gate || !w_up || (desc->rows && (!x || !d_h)) || (!dw_gate) != (!dw_up)) return GDN_ERR_INVALID_ARG;
     if (dw_gate && (dw_gate == dw_up || dw_gate == dx || dw_up == dx)) return GDN_ERR_INVALID_ARG;
     for (const void* out : {dx, dw_gate, dw_up})
         if (out && (out == x || out == w_gate || out == w_up || out == d_h || out == pre)) return GDN_ERR_INVALID_ARG;
-    if (gdn_status s = check_buf(workspace, ffn_bwd_ws(desc->rows, desc->K, desc->F, desc->dtype), workspace_bytes)) return s;
+    if (gdn_status s = check_buf(workspace, ffn_bwd_ws(desc->rows, desc->K, desc->F, desc->dtype, desc->flags != 0), workspace_bytes)) return s;
     FfnArgs a{};
     a.M = desc->rows;
     a.K = desc->K;
     a.F = desc->F;
     a.act = desc->activation;
+    a.pairs = desc->flags != 0;
     a.x = x;
     a.wg = w_gate;
     a.wu = w_up;
@@ -161,7 +163,7 @@ gdn_status gdn_gated_ffn_bwd(const gdn_ffn_desc* desc, const void* x, const void
 
 gdn_status gdn_gated_ffn_e4m3_workspace_size(const gdn_ffn_desc* desc, size_t* bytes) {
     if (!bytes) return GDN_ERR_INVALID_ARG;
-    if (gdn_status s = check_ffn(desc, true)) return s;
+    if (gdn_status s = check_ffn(desc, true, GDN_FLAG_EXACT_SUMS)) return s;
     *bytes = ffn8_ws(desc->rows, desc->K, desc->F, desc->dtype, desc->out_type == GDN_OUT_E4M3, desc->flags != 0);
     return GDN_OK;
 }
@@ -169,7 +171,7 @@ gdn_status gdn_gated_ffn_e4m3_workspace_size(const gdn_ffn_desc* desc, size_t* b
 gdn_status gdn_gated_ffn_e4m3(const gdn_ffn_desc* desc, const void* x, const float* x_scale, const void* w_gate,
                               const float* gate_scale, const void* w_up, const float* up_scale, void* h, float* scale,
                               void* workspace, size_t workspace_bytes, void* stream) {
-    if (gdn_status s = check_ffn(desc, true)) return s;
+    if (gdn_status s = check_ffn(desc, true, GDN_FLAG_EXACT_SUMS)) return s;
     if (!w_gate || !w_up || !gate_scale || !up_scale) return GDN_ERR_INVALID_ARG;
     const std::initializer_list<const void*> inputs = {x, x_scale, w_gate, gate_scale, w_up, up_scale};
     if (desc->rows && (!x || !x_scale || !h || is_one_of(h, inputs))) return GDN_ERR_INVALID_ARG;

@@ -33,6 +33,7 @@ hipError_t launch_mm8(const Mm8Args& a, int out_dtype, int scales, bool exact, h
 struct FfnArgs {
     int64_t M, K, F;
     int32_t act;
+    bool pairs;  // gradients of gate and up as pairs of bf16 at any size
     const void* x;
     const void* wg;
     const void* wu;
@@ -50,7 +51,7 @@ struct FfnArgs {
     unsigned char* ws;
 };
 size_t ffn_fwd_ws(int64_t M, int64_t K, int64_t F, int dtype);
-size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype);
+size_t ffn_bwd_ws(int64_t M, int64_t K, int64_t F, int dtype, bool pairs);
 size_t ffn8_ws(int64_t M, int64_t K, int64_t F, int dtype, bool quant, bool exact);
 hipError_t launch_ffn_fwd(const FfnArgs& a, int dtype, hipStream_t st);
 hipError_t launch_ffn_bwd(const FfnArgs& a, int dtype, hipStream_t st);

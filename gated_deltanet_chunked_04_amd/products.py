@@ -20,7 +20,7 @@ import functools
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._abi import (GDN_ACT_GELU_TANH, GDN_ACT_SILU, GDN_DTYPE_BF16, GDN_FLAG_EXACT_SUMS, GDN_OUT_E4M3, GDN_OUT_SAME, GDN_SCALE_BLOCK,
+from ._abi import (GDN_ACT_GELU_TANH, GDN_ACT_SILU, GDN_DTYPE_BF16, GDN_FLAG_EXACT_SUMS, GDN_FLAG_GRAD_PAIRS, GDN_OUT_E4M3, GDN_OUT_SAME, GDN_SCALE_BLOCK,
                    GDN_SCALE_GROUP, GDN_SCALE_ROW, GdnFfnDesc, GdnMatmulDesc, GdnQuantDesc, load_library)
 from .layer import _DTYPES, _bytes, _dense, _dtype, _like, _out, _run, _scratch
 
@@ -138,11 +138,10 @@ def gdn_matmul_e4m3(a, a_scale, b, b_scale, *, out_dtype=torch.bfloat16, exact=F
 
 
 @functools.lru_cache(maxsize=1024)
-def _ffn_plan(rows, K, F, dtype, activation):
-    """(descriptor, its forward's and its backward's workspace sizes)."""
-    desc = GdnFfnDesc(rows, K, F, dtype, activation, GDN_OUT_SAME)
-    return (ctypes.byref(desc), _bytes("gdn_gated_ffn_fwd_workspace_size", desc),
-            _bytes("gdn_gated_ffn_bwd_workspace_size", desc))
+def _ffn_plan(rows, K, F, dtype, activation, backward, pairs):
+    """(descriptor, its workspace size) of one of the two directions."""
+    desc = GdnFfnDesc(rows, K, F, dtype, activation, GDN_OUT_SAME, GDN_FLAG_GRAD_PAIRS if pairs else 0)
+    return ctypes.byref(desc), _bytes("gdn_gated_ffn_bwd_workspace_size" if backward else "gdn_gated_ffn_fwd_workspace_size", desc)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -158,15 +157,15 @@ def _gate(activation) -> int:
     return code
 
 
-def _ffn_call(x, w_gate, w_up, activation):
-    """(descriptor, workspace bytes forward and backward, rows, K, F)."""
+def _ffn_call(x, w_gate, w_up, activation, backward=False, pairs=False):
+    """(descriptor, workspace bytes, rows, K, F)."""
     rows, K = _matrix("x", x)
     dtype = _dtype(x)
     F = _weight("w_gate", w_gate, K, x.dtype, x.device)
     _like("w_up", w_up, (F, K), x.dtype, x.device)
     if w_up is None:
         raise ValueError("w_up is required")
-    return (*_ffn_plan(rows, K, F, dtype, _gate(activation)), rows, K, F)
+    return (*_ffn_plan(rows, K, F, dtype, _gate(activation), backward, pairs), rows, K, F)
 
 
 def gdn_gated_ffn_pre(x, w_gate):
@@ -182,7 +181,7 @@ def gdn_gated_ffn_fwd(x, w_gate, w_up, *, activation="silu", h=None, pre=None, w
 
     x [..., K] bf16 or fp32; w_gate, w_up [F, K] in x's type; activation 'silu' or 'gelu_tanh'. pre (see
     gdn_gated_ffn_pre) receives what gdn_gated_ffn_bwd needs of the forward."""
-    ref, need, _, rows, K, F = _ffn_call(x, w_gate, w_up, activation)
+    ref, need, rows, K, F = _ffn_call(x, w_gate, w_up, activation)
     dev = x.device
     h, ph = _out("h", h, x, (*x.shape[:-1], F), x.dtype, dev)
     pp = _like("pre", pre, (2, rows, F), torch.float32, dev)
@@ -192,12 +191,13 @@ def gdn_gated_ffn_fwd(x, w_gate, w_up, *, activation="silu", h=None, pre=None, w
 
 
 def gdn_gated_ffn_bwd(x, w_gate, w_up, d_h, *, activation="silu", pre=None, need_dx=True, need_dweight=True,
-                      workspace=None, out=None):
+                      pairs=False, workspace=None, out=None):
     """Gradients of <d_h, h>: dict(dx, dw_gate, dw_up) in x's type, None where not needed; `out` may hold them
     preallocated. pre: what gdn_gated_ffn_fwd(pre=...) wrote for these inputs, or None (gate and up are computed
-    again). The gradients of gate and up are rounded to x's type, the operands' type of the products behind (bf16: to
-    a pair of bf16 where rows F, rows K or F K is below 65,536)."""
-    ref, _, need, rows, K, F = _ffn_call(x, w_gate, w_up, activation)
+    again). The gradients of gate and up are rounded to x's type, the operands' type of the products behind, which in
+    bf16 makes the error sqrt 2 times the results' own rounding; to a pair of bf16, which adds nothing to it, where rows
+    F, rows K or F K is below 65,536, and with pairs=True at any size (8,192 x 2,048 x 8,192: 1,040 us to 2,690)."""
+    ref, need, rows, K, F = _ffn_call(x, w_gate, w_up, activation, True, bool(pairs))
     dev, shape = x.device, x.shape
     if d_h is None:
         raise ValueError("d_h is required")
@@ -301,11 +301,11 @@ def linear_e4m3(x, weight, *, exact=False):
 
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, activation, keep):
+    def forward(ctx, x, w_gate, w_up, activation, keep, pairs):
         pre = gdn_gated_ffn_pre(x, w_gate) if keep else None
         h = gdn_gated_ffn_fwd(x, w_gate, w_up, activation=activation, pre=pre)
         ctx.save_for_backward(x, w_gate, w_up, pre)
-        ctx.activation = activation
+        ctx.activation, ctx.pairs = activation, pairs
         return h
 
     @staticmethod
@@ -314,12 +314,12 @@ class _GatedFfn(torch.autograd.Function):
         x, w_gate, w_up, pre = ctx.saved_tensors
         need = ctx.needs_input_grad
         gr = gdn_gated_ffn_bwd(x, w_gate, w_up, _dense(d_h), activation=ctx.activation, pre=pre, need_dx=need[0],
-                               need_dweight=need[1] or need[2])
-        return gr["dx"], gr["dw_gate"] if need[1] else None, gr["dw_up"] if need[2] else None, None, None
+                               need_dweight=need[1] or need[2], pairs=ctx.pairs)
+        return gr["dx"], gr["dw_gate"] if need[1] else None, gr["dw_up"] if need[2] else None, None, None, None
 
 
-def gated_ffn(x, w_gate, w_up, *, activation="silu", recompute=False):
+def gated_ffn(x, w_gate, w_up, *, activation="silu", recompute=False, pairs=False):
     """gdn_gated_ffn_fwd with autograd (x, w_gate, w_up): h [..., F] in x's type. gate and up are held in fp32 for
-    the backward (8 bytes per value of h), or with recompute computed again there."""
+    the backward (8 bytes per value of h), or with recompute computed again there. pairs: see gdn_gated_ffn_bwd."""
     keep = not recompute and torch.is_grad_enabled() and any(t.requires_grad for t in (x, w_gate, w_up))
-    return _GatedFfn.apply(x, w_gate, w_up, activation, keep)
+    return _GatedFfn.apply(x, w_gate, w_up, activation, keep, bool(pairs))

@@ -1,11 +1,13 @@
-"""bf16 outputs of e4m3 operands with sums as in fp32: products that cancel beside small ones, and the fp32 outputs' values
-rounded once."""
+"""What a caller may ask for beyond the defaults: bf16 outputs of e4m3 operands with sums as in fp32 (products that cancel
+beside small ones, and the fp32 outputs' values rounded once), and the gated block's bf16 gradients from gradients of gate and up
+that are pairs of bf16 at any size."""
 import pytest
 import torch
 
 import gated_deltanet_chunked_04_amd as gdn
 from oracle import products as ref
-from test_gpu_products import BF, E4M3, F32, close, quantised, rnd, scales_for
+from test_gpu_products import BF, E4M3, F32, close, ffn_inputs, quantised, rnd, scales_for
+from test_gpu_products_edges import bound_of
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +100,26 @@ def test_exact_in_a_graph(gpu_lib):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, step())), k
         torch.cuda.synchronize()
+
+
+# all matrices of 65,536 values and more: rounded once, unless asked for
+@pytest.mark.parametrize("M,K,F", [(300, 264, 520), (1000, 300, 257), (513, 1025, 130), (4101, 600, 331)])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_ffn_pairs_asked_for(M, K, F, act, gpu_lib):
+    assert min(M * K, M * F, K * F) >= 65536
+    x, wg, wu, d = ffn_inputs(M, K, F, BF, seed=M)
+    leaves = [t.cuda().requires_grad_() for t in (x, wg, wu)]
+    want = ref.ffn_bwd(x, wg, wu, d, act, F32)
+    terms = bound_of(x, wg, wu, d, act)
+    for recompute in (False, True):
+        grads = torch.autograd.grad(gdn.gated_ffn(*leaves, activation=act, recompute=recompute, pairs=True), leaves, d.cuda())
+        for got, (k, (v, e)) in zip(grads, want.items()):
+            got = got.cpu().double()
+            own = (v.to(BF).double() - v).norm()
+            assert ((got - v).abs() <= 2.0 ** -8 * v.abs() + 1.01 * e + 2.0 ** -15 * terms[k]).all(), k
+            # its own rounding alone; rounded once it is 1.35 to 1.44 of that
+            assert (got - v).norm() <= 1.12 * own + 2.0 ** -15 * v.norm(), k
+    # (in fp32 there is nothing to ask for)
+    dev = [t.detach().float() for t in leaves]
+    a, b = (gdn.gdn_gated_ffn_bwd(*dev, d.cuda().float(), activation=act, pairs=p) for p in (False, True))
+    assert all(torch.equal(a[k], b[k]) for k in a)

@@ -40,3 +40,21 @@ def test_flags(lib):  # noqa: F811
         assert lib.gdn_gated_ffn_e4m3_workspace_size(ctypes.byref(ffn_desc(flags=flags)), n) == code
         assert lib.gdn_gated_ffn_fwd_workspace_size(ctypes.byref(ffn_desc(flags=flags)), n) == (1 if flags else 0)
         assert lib.gdn_gated_ffn_bwd_workspace_size(ctypes.byref(ffn_desc(flags=flags)), n) == (1 if flags else 0)
+
+
+def test_flag_of_pairs(lib):  # noqa: F811
+    """Pairs of bf16 at any size may be asked of the block's backward, and of nothing else; they want a larger workspace."""
+    n = ctypes.c_size_t()
+    sizes = {}
+    for dtype in (0, 1):
+        for flags in (0, 512):
+            d = ffn_desc(rows=700, K=800, F=900, dtype=dtype, flags=flags)
+            assert lib.gdn_gated_ffn_bwd_workspace_size(ctypes.byref(d), ctypes.byref(n)) == 0
+            sizes[dtype, flags] = n.value
+            assert lib.gdn_gated_ffn_fwd_workspace_size(ctypes.byref(d), ctypes.byref(n)) == (1 if flags else 0)
+            assert lib.gdn_gated_ffn_e4m3_workspace_size(ctypes.byref(d), ctypes.byref(n)) == (1 if flags else 0)
+    assert sizes[0, 512] >= sizes[0, 0] + 2 * 700 * 900 * 2 and sizes[1, 512] == sizes[1, 0]
+    assert lib.gdn_gated_ffn_bwd_workspace_size(ctypes.byref(ffn_desc(flags=513)), ctypes.byref(n)) == 1
+    x, wg, wu, d_h, dx, ws = ARGS[:6]
+    d = ffn_desc(rows=700, K=800, F=900, flags=512)
+    assert lib.gdn_gated_ffn_bwd(ctypes.byref(d), x, wg, wu, None, d_h, dx, None, None, ws, ctypes.c_size_t(sizes[0, 512] - 1), None) == 3
