@@ -2,7 +2,7 @@
 //   dg = d_h u act'(g), du = d_h act(g),  dx = dg Wg + du Wu,  dWg = dg^T x, dWu = du^T x.
 // Gate and up are computed side by side by the same waves, so h is made where both sums are and neither is written
 // (`pre` keeps them in fp32 for the backward, which otherwise computes them again). 8,192 x 2,048 x 8,192 bf16: forward with pre
-// 674 us (550 GFLOP, 0.8 GB written), dx 480, both weights' gradients 520: see the tiles (gdn_mm.h) for what bounds them.
+// 681 us (550 GFLOP, 0.8 GB written), dx 474, both weights' gradients 517: see the tiles (gdn_mm.h) for what bounds them.
 #include "gdn_layer.h"
 #include "gdn_mm.h"
 #include "gdn_products.h"

@@ -491,8 +491,8 @@ __device__ __forceinline__ void mm_finish8(Sums& sums, const MmArgs& p, uint32_t
 
 // 128 x 64 WN outputs (two sides: half of each) by WM x WN waves of 128 / WM x 64, any sizes and addresses: chunks go
 // through registers, the next step's on their way while one is multiplied; one tile of each operand in LDS. Eight waves,
-// two on a SIMD, so that one's LDS reads pass behind the other's products (1,003 x 777 x 1,001 in e4m3 19.4 us, with four
-// waves of 64 x 64 20.0).
+// two on a SIMD, so that one's LDS reads pass behind the other's products (1,003 x 777 x 1,001 in e4m3, when the two were compared,
+// 19.4 us, with four waves of 64 x 64 20.0; 16.3 now).
 template <int KIND, int SC, bool XT, bool WT, bool DUAL, int EPI, typename T, int WM, int WN, bool PAIRS>
 __global__ __launch_bounds__(64 * WM * WN) void k_mm_any(MmArgs p) {
     constexpr int E = mm_size<KIND>(), MT = 8 / WM, NT = 4;
