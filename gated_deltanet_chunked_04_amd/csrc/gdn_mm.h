@@ -698,9 +698,7 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
     const int64_t xstep = XT ? kSteps * p.ldx : kMmStep, wstep = WT ? kSteps * p.ldw : kMmStep;
     const int32_t whole = (int32_t)(p.K / kSteps), rest = (int32_t)(p.K % kSteps);
     const int64_t xat = XT ? m0 * E : m0 * p.ldx, wat = WT ? n0 * E : n0 * p.ldw;
-    // Whether there may be two segments. (Only dx has them, and the others are told so; not the one by
-    // groups of widened e4m3, whose schedule comes out 4% quicker with the test in it: 6,144 x 2,048 x 32,768 971 us, 1,011.)
-    constexpr bool kSegs = (WT && !XT) || (KIND == kMmF8x && SC == kMmGroup);
+    constexpr bool kSegs = WT && !XT;  // there may be two segments (dx)
     int32_t seg = kSegs ? begin >= per : 0, kt = begin - seg * per;
     uint64_t xs = mm_uniform(mm_x<XT>(p, seg, z) + xat + kt * xstep);
     uint64_t ws0 = mm_uniform((DUAL ? p.w[0] : mm_w<XT>(p, seg)) + wat + kt * wstep), ws1 = mm_uniform(p.w[1] + wat + kt * wstep);
@@ -806,7 +804,7 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
             if (kAhead == 2 && t + 1 < MT) ready(t + 1);
             if (t + kAhead < MT) read(t + kAhead);
             // A tile's parts one after the other, or the four tiles' in turn (widened e4m3, 6,144 x 2,048 x 32,768 by groups
-            // 1,045 us and 1,018; 16,384 x 16,384 x 2,048 by blocks 1,096 and 1,138).
+            // 1,031 us and 1,010; 16,384 x 16,384 x 2,048 by blocks 1,096 and 1,138).
             constexpr bool kTurn = KIND == kMmF8x && SC == kMmGroup;
             constexpr int kParts = mm_parts<KIND>();
 #pragma unroll
@@ -816,10 +814,11 @@ __global__ __launch_bounds__(512) void k_mm(MmArgs p) {
                 else sums.acc[t][j] = mm_part(i, fw[j], fx[t & 1], sums.acc[t][j]);
                 // a tile's sums are added while the next one is multiplied
                 if (Sums::kScaled && i == (kTurn ? 0 : kParts - 1) && t > 0) sums.add(t - 1, j, c[~t & 1][j], sx[(t - 1) & 3], sw[j]);
-                // matrix instructions with vector ones between them
+                // matrix instructions with vector ones between them (widened e4m3: three; by groups, 6,144 x 2,048 x 32,768, three
+                // 969 us, four 1,010, five 990)
                 if constexpr (Sums::kScaled) {
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                    if (KIND == kMmF8x) __builtin_amdgcn_sched_group_barrier(0x002, SC == kMmGroup ? 4 : 3, 0);
+                    if (KIND == kMmF8x) __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
                     else if (t > 0) __builtin_amdgcn_sched_group_barrier(0x002, SC == kMmBlock ? 5 : 8, 0);
                 }
             }
